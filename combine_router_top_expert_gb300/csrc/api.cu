@@ -253,6 +253,29 @@ bool routing_ok(const mok_routing* r, int32_t T = 1) {
            (T == 0 || (r->topk_idx && r->topk_w && r->row_src && r->slot_row));
 }
 
+// Rows of the pre-norm: whole 16-byte vectors, a row held by one CTA.
+bool norm_dims_ok(int T, int H) { return T >= 0 && H >= 8 && H % 8 == 0 && H <= 65536; }
+
+// The 8-bit checkpoint of the training context: codes and scales of x, G|U
+// and the partials.
+struct CkptLayout {
+    size_t x, x_sf, gu, gu_sf, y, y_sf, total;
+};
+
+CkptLayout ckpt_layout(const mok_problem* p) {
+    CkptLayout L{};
+    const int64_t R = (int64_t)p->T * p->k, W = 2 * (int64_t)p->I;
+    size_t o = 0;
+    L.x = o; o += align_up((int64_t)p->T * p->H, 256);
+    L.x_sf = o; o += align_up((int64_t)p->T * p->H / 32, 256);
+    L.gu = o; o += align_up(R * W, 256);
+    L.gu_sf = o; o += align_up(R * W / 32, 256);
+    L.y = o; o += align_up(R * p->H, 256);
+    L.y_sf = o; o += align_up(R * p->H / 32, 256);
+    L.total = std::max<size_t>(o, 256);
+    return L;
+}
+
 // Requires an sm_103-class device for the tensor-core kernels.
 bool device_ok() {
     int dev = 0;
@@ -702,6 +725,107 @@ mok_status mok_moe_backward(const mok_problem* p, const mok_bwd_args* a, const m
         e = launch_bwd_small(a->dY, sv + FL.spart, r.topk_w, r.topk_idx, a->x, WrT, da, T, H, E, k, gw, dl, dl_full,
                              part, a->dX, a->dW_r, 1, s);
     return cuda_status(e);
+}
+
+mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream) {
+    if (!a || !norm_dims_ok(T, H)) return MOK_ERR_INVALID;
+    if (T > 0 && !a->sum && !a->y && !a->y_q && !a->sum_q && !a->rstd) return MOK_ERR_INVALID;
+    if ((a->y_q != nullptr) != (a->y_sf != nullptr) || (a->sum_q != nullptr) != (a->sum_sf != nullptr))
+        return MOK_ERR_INVALID;
+    if ((a->y_q || a->sum_q) && H % 32) return MOK_ERR_INVALID;
+    if (!(a->eps >= 0.f) || a->ldx < H || a->ldx % 8 || (a->residual && (a->ldr < H || a->ldr % 8)))
+        return MOK_ERR_INVALID;
+    if (T > 0 && (!a->x || !a->gain)) return MOK_ERR_INVALID;
+    if (!aligned(a->x, 16) || !aligned(a->residual, 16) || !aligned(a->gain, 16) || !aligned(a->sum, 16) ||
+        !aligned(a->y, 16) || !aligned(a->y_q, 16) || !aligned(a->sum_q, 16) || !aligned(a->rstd, 4))
+        return MOK_ERR_INVALID;
+    // in place only where a row's reads and writes are the same bytes
+    for (const void* o : {(const void*)a->sum, (const void*)a->y})
+        if (o && ((o == a->x && a->ldx != H) || (o == a->residual && a->ldr != H))) return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (T == 0) return MOK_OK;
+    return cuda_status(launch_rmsnorm(T, H, *a, (cudaStream_t)stream));
+}
+
+size_t mok_rmsnorm_bwd_workspace_size(int32_t T, int32_t H) {
+    if (!norm_dims_ok(T, H)) return 0;
+    return (size_t)std::max(rmsnorm_bwd_partials(T), 1) * H * 4;
+}
+
+mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args* a, mok_stream_t stream) {
+    if (!a || !norm_dims_ok(T, H) || !a->dgain || !a->workspace) return MOK_ERR_INVALID;
+    if ((a->sum_q != nullptr) != (a->sum_sf != nullptr) || (a->sum_q && (a->sum || H % 32)))
+        return MOK_ERR_INVALID;
+    if (T > 0 && (!a->dy || (!a->sum && !a->sum_q) || !a->rstd || !a->gain || !a->dx)) return MOK_ERR_INVALID;
+    if (!aligned(a->dy, 16) || !aligned(a->sum, 16) || !aligned(a->sum_q, 16) || !aligned(a->dsum, 16) ||
+        !aligned(a->rstd, 4) || !aligned(a->gain, 16) || !aligned(a->dx, 16) || !aligned(a->dgain, 4) ||
+        !aligned(a->workspace, 16))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (a->ws_bytes < mok_rmsnorm_bwd_workspace_size(T, H)) return MOK_ERR_INVALID;
+    if (T == 0) return cuda_status(cudaMemsetAsync(a->dgain, 0, (size_t)H * 4, (cudaStream_t)stream));
+    return cuda_status(launch_rmsnorm_backward(T, H, *a, (cudaStream_t)stream));
+}
+
+mok_status mok_dequantize_rows(const void* x_q, const void* x_sf, int32_t T, int32_t H, void* x,
+                               mok_stream_t stream) {
+    if (T < 0 || H <= 0 || H % 32) return MOK_ERR_INVALID;
+    if (T > 0 && (!x_q || !x_sf || !x)) return MOK_ERR_INVALID;
+    if (!aligned(x_q, 16) || !aligned(x, 16)) return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (T == 0) return MOK_OK;
+    return cuda_status(launch_dequantize_rows(x_q, x_sf, T, H, x, (cudaStream_t)stream));
+}
+
+size_t mok_checkpoint_size(const mok_problem* p) {
+    if (!problem_ok(p)) return 0;
+    return ckpt_layout(p).total;
+}
+
+static CheckpointParams ckpt_params(const mok_problem* p, const mok_routing* r, void* ckpt, void* saved) {
+    const CkptLayout C = ckpt_layout(p);
+    const FwdLayout L = fwd_layout(p, true);
+    uint8_t* c = static_cast<uint8_t*>(ckpt);
+    char* sv = static_cast<char*>(saved);
+    CheckpointParams q{};
+    q.T = p->T; q.H = p->H; q.I = p->I; q.E = p->E; q.k = p->k;
+    q.counts = r->counts;
+    q.offsets = r->offsets;
+    q.row_src = r->row_src;
+    q.x_q = c + C.x; q.x_sf = c + C.x_sf;
+    q.gu_q = c + C.gu; q.gu_sf = c + C.gu_sf;
+    q.y_q = c + C.y; q.y_sf = c + C.y_sf;
+    q.A_out = reinterpret_cast<__nv_bfloat16*>(sv + L.sA);
+    q.gu_out = reinterpret_cast<float*>(sv + L.sGU);
+    q.h_out = reinterpret_cast<__nv_bfloat16*>(sv + L.sh);
+    q.partials_out = reinterpret_cast<__nv_bfloat16*>(sv + L.spart);
+    q.gu = q.gu_out;
+    q.partials = q.partials_out;
+    return q;
+}
+
+mok_status mok_checkpoint_save(const mok_problem* p, const void* x, const mok_routing* routing, const void* saved,
+                               void* ckpt, size_t ckpt_bytes, mok_stream_t stream) {
+    if (!problem_ok(p) || !routing_ok(routing, p->T) || !saved || !ckpt || (p->T > 0 && !x)) return MOK_ERR_INVALID;
+    if (ckpt_bytes < ckpt_layout(p).total || !aligned(ckpt, 256) || !aligned(saved, 1024) || !aligned(x, 16))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (p->T == 0) return MOK_OK;
+    CheckpointParams q = ckpt_params(p, routing, ckpt, const_cast<void*>(saved));
+    q.x = static_cast<const __nv_bfloat16*>(x);
+    return cuda_status(launch_checkpoint_save(q, (cudaStream_t)stream));
+}
+
+mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ckpt_bytes, const mok_routing* routing,
+                               void* x, void* saved, mok_stream_t stream) {
+    if (!problem_ok(p) || !routing_ok(routing, p->T) || !saved || !ckpt || (p->T > 0 && !x)) return MOK_ERR_INVALID;
+    if (ckpt_bytes < ckpt_layout(p).total || !aligned(ckpt, 256) || !aligned(saved, 1024) || !aligned(x, 16))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (p->T == 0) return MOK_OK;
+    CheckpointParams q = ckpt_params(p, routing, const_cast<void*>(ckpt), saved);
+    q.x_out = static_cast<__nv_bfloat16*>(x);
+    return cuda_status(launch_checkpoint_load(q, (cudaStream_t)stream));
 }
 
 mok_status mok_route_test_hook(int32_t withhold_copy, int32_t timeout_ms) {

@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "moves.cuh"
+#include "quant.cuh"
 #include "tc.cuh"
 
 namespace mok {
@@ -43,45 +44,6 @@ __device__ __forceinline__ int find_expert(const int32_t* poff, int E, int pr) {
 // ---------------------------------------------------------------------------
 // Pull-dispatch: one warp per padded row.
 // ---------------------------------------------------------------------------
-// One 32-element MXFP8 block: E8M0 code of its amax, E4M3 bytes of x / scale.
-// Every quantiser of the library goes through quantize32.
-__device__ __forceinline__ uint32_t quantize32(const float (&f)[32], uint4& o0, uint4& o1) {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    const uint32_t code = e8m0_code(amax);
-    const float inv = e8m0_inv_scale(code);
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i] = f32x2_to_e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
-               (f32x2_to_e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
-    o0 = make_uint4(w[0], w[1], w[2], w[3]);
-    o1 = make_uint4(w[4], w[5], w[6], w[7]);
-    return code;
-}
-
-// 32 BF16 values (four 16-byte words) to fp32.
-__device__ __forceinline__ void unpack32(const uint4 (&v)[4], float (&f)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[8 * i + 0] = bf16_lo(v[i].x); f[8 * i + 1] = bf16_hi(v[i].x);
-        f[8 * i + 2] = bf16_lo(v[i].y); f[8 * i + 3] = bf16_hi(v[i].y);
-        f[8 * i + 4] = bf16_lo(v[i].z); f[8 * i + 5] = bf16_hi(v[i].z);
-        f[8 * i + 6] = bf16_lo(v[i].w); f[8 * i + 7] = bf16_hi(v[i].w);
-    }
-}
-
-__device__ __forceinline__ uint32_t quantize_block32(const __nv_bfloat16* src, uint4& o0, uint4& o1) {
-    const uint4* s4 = reinterpret_cast<const uint4*>(src);
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldg(s4 + i);
-    float f[32];
-    unpack32(v, f);
-    return quantize32(f, o0, o1);
-}
-
 // Row-wise MXFP8 quantisation of x (warp per row; the codes the dispatch
 // writes): x_q [T, H] E4M3, x_sf bytes [T, H/32] (= words [T, H/128], byte j
 // of word c = scale of 32-block 4c + j).

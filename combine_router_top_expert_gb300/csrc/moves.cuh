@@ -57,6 +57,35 @@ inline int down_tile_n(int H, bool mx) {
     return H % 256 == 0 ? 256 : 128;
 }
 
+// norm.cu
+int rmsnorm_bwd_partials(int T);   // partial rows of dgain that the backward's workspace holds
+cudaError_t launch_rmsnorm(int T, int H, const mok_rmsnorm_args& a, cudaStream_t s);
+cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a, cudaStream_t s);
+cudaError_t launch_dequantize_rows(const void* q, const void* sf, int T, int H, void* x, cudaStream_t s);
+
+// checkpoint.cu: the training context in 8 bits. Save reads x, gu and partials
+// (and counts, offsets) and writes the MXFP8 rows; load reads those (and
+// row_src) and writes the *_out arrays.
+struct CheckpointParams {
+    int T, H, I, E, k;
+    const int32_t* counts;    // [E]
+    const int32_t* offsets;   // [E+1]
+    const int32_t* row_src;   // [T*k]
+    const __nv_bfloat16* x;         // [T, H]
+    const float* gu;                // [padded rows, 2I]
+    const __nv_bfloat16* partials;  // [T*k, H]
+    uint8_t *x_q, *x_sf;      // [T, H], [T, H/32]
+    uint8_t *gu_q, *gu_sf;    // [T*k, 2I] in expert order, [T*k, 2I/32]
+    uint8_t *y_q, *y_sf;      // [T*k, H] in slot order, [T*k, H/32]
+    __nv_bfloat16* x_out;
+    __nv_bfloat16* A_out;     // [padded rows, H]
+    float* gu_out;            // [padded rows, 2I]
+    __nv_bfloat16* h_out;     // [padded rows, I]
+    __nv_bfloat16* partials_out;
+};
+cudaError_t launch_checkpoint_save(const CheckpointParams& p, cudaStream_t s);
+cudaError_t launch_checkpoint_load(const CheckpointParams& p, cudaStream_t s);
+
 // gemm.cu
 // Raise a kernel's dynamic shared memory limit (per device) to at least `bytes`.
 void ensure_smem_attr(const void* func, int bytes);

@@ -28,7 +28,8 @@ EXPORTS = ["mok_route_workspace_size", "mok_route_layout", "mok_packed_weights_s
            "mok_version", "mok_route_layout_static", "mok_workspace_size_batches", "mok_moe_forward_batches",
            "mok_quantize_rows", "mok_dispatch_quantized", "mok_route_test_hook", "mok_ep_workspace_size",
            "mok_ep_dispatch", "mok_ep_push", "mok_packed_weights_bwd_size", "mok_pack_weights_bwd",
-           "mok_dispatch_tokens"]
+           "mok_dispatch_tokens", "mok_rmsnorm", "mok_rmsnorm_bwd_workspace_size", "mok_rmsnorm_backward",
+           "mok_dequantize_rows", "mok_checkpoint_size", "mok_checkpoint_save", "mok_checkpoint_load"]
 
 FLAG_MEGAKERNEL = 1
 FLAG_GEMM_PAIRS = 2
@@ -83,6 +84,20 @@ class EpPeer(ctypes.Structure):
                 ("partials", ctypes.c_void_p), ("T", ctypes.c_int32)]
 
 
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("ldr", ctypes.c_int64), ("gain", ctypes.c_void_p), ("eps", ctypes.c_float), ("sum", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_q", ctypes.c_void_p), ("y_sf", ctypes.c_void_p),
+                ("sum_q", ctypes.c_void_p), ("sum_sf", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class RmsNormBwdArgs(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("sum_q", ctypes.c_void_p),
+                ("sum_sf", ctypes.c_void_p), ("dsum", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("gain", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dgain", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 EP_MAX_RANKS = 8
 _lock = threading.Lock()
 _lib = None
@@ -134,13 +149,23 @@ def lib():
             L.mok_ep_dispatch.argtypes = [I32, I32, I32, I32, I32, ctypes.POINTER(EpPeer), P, P, ctypes.c_int64, P, P,
                                           P, P, P, P, SZ, P]
             L.mok_ep_push.argtypes = [I32, I32, I32, I32, ctypes.POINTER(EpPeer), P, ctypes.c_int64, P, P, P, P]
+            L.mok_rmsnorm.argtypes = [I32, I32, ctypes.POINTER(RmsNormArgs), P]
+            L.mok_rmsnorm_bwd_workspace_size.argtypes = [I32, I32]
+            L.mok_rmsnorm_bwd_workspace_size.restype = SZ
+            L.mok_rmsnorm_backward.argtypes = [I32, I32, ctypes.POINTER(RmsNormBwdArgs), P]
+            L.mok_dequantize_rows.argtypes = [P, P, I32, I32, P, P]
+            L.mok_checkpoint_size.argtypes = [PP]
+            L.mok_checkpoint_size.restype = SZ
+            L.mok_checkpoint_save.argtypes = [PP, P, PR, P, P, SZ, P]
+            L.mok_checkpoint_load.argtypes = [PP, P, SZ, PR, P, P, P]
             L.mok_status_string.argtypes = [I32]
             L.mok_status_string.restype = ctypes.c_char_p
             L.mok_version.restype = ctypes.c_char_p
             for name in ("mok_route_layout", "mok_route_layout_static", "mok_pack_weights", "mok_moe_forward",
                          "mok_moe_forward_batches", "mok_dispatch", "mok_quantize_rows", "mok_dispatch_quantized",
                          "mok_expert_ffn", "mok_combine", "mok_moe_backward", "mok_device_status", "mok_route_test_hook",
-                         "mok_ep_dispatch", "mok_ep_push", "mok_pack_weights_bwd", "mok_dispatch_tokens"):
+                         "mok_ep_dispatch", "mok_ep_push", "mok_pack_weights_bwd", "mok_dispatch_tokens", "mok_rmsnorm",
+                         "mok_rmsnorm_backward", "mok_dequantize_rows", "mok_checkpoint_save", "mok_checkpoint_load"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -368,6 +393,102 @@ def expert_ffn(p: Problem, A, A_sf, packed, routing, h, h_sf, partials, workspac
 def combine(p: Problem, partials, topk_w, out, shared=None, stream=None):
     rc = lib().mok_combine(ctypes.byref(p), _ptr(partials), _ptr(topk_w), _ptr(shared), _ptr(out), _stream(stream))
     _check(rc, "mok_combine")
+
+
+# --------------------------------------------------------------------------- pre-norm
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(T, H, dtype, **tensors):
+    """The given tensors (None allowed) are contiguous CUDA tensors [T, H] of one dtype."""
+    for name, t in tensors.items():
+        if t is not None:
+            assert t.is_cuda and t.dtype == dtype and t.shape == (T, H) and t.is_contiguous(), \
+                f"{name}: contiguous {dtype} CUDA tensor [{T}, {H}] expected"
+
+
+def _f32(n, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            assert t.is_cuda and t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous(), \
+                f"{name}: contiguous float32 CUDA tensor [{n}] expected"
+
+
+def _rows(name, t, T, H):
+    """bf16 rows of any pitch: the elements of a row are adjacent."""
+    assert t.is_cuda and t.dtype == torch.bfloat16 and t.shape == (T, H) and (t.stride(1) == 1 or H == 1), \
+        f"{name}: bf16 CUDA tensor [{T}, {H}] with adjacent row elements expected"
+    return t.stride(0) if T > 1 else max(t.stride(0), H)
+
+
+def rmsnorm(x, gain, residual=None, eps=1e-6, sum=None, y=None, y_q=None, y_sf=None, sum_q=None, sum_sf=None,
+            rstd=None, stream=None):
+    """Residual's addition and root-mean-square norm, into the outputs given
+    (see mok_rmsnorm). x and residual may be row-strided views."""
+    T, H = x.shape
+    _dense(T, H, torch.bfloat16, sum=sum, y=y)
+    _dense(T, H, torch.uint8, y_q=y_q, sum_q=sum_q)
+    _dense(T, H // 32, torch.uint8, y_sf=y_sf, sum_sf=sum_sf)
+    _f32(H, gain=gain)
+    _f32(T, rstd=rstd)
+    a = RmsNormArgs(x.data_ptr(), _rows("x", x, T, H), _addr(residual),
+                    0 if residual is None else _rows("residual", residual, T, H), gain.data_ptr(), eps, _addr(sum),
+                    _addr(y), _addr(y_q), _addr(y_sf), _addr(sum_q), _addr(sum_sf), _addr(rstd))
+    _check(lib().mok_rmsnorm(T, H, ctypes.byref(a), _stream(stream)), "mok_rmsnorm")
+
+
+def rmsnorm_bwd_workspace_size(T, H) -> int:
+    return int(lib().mok_rmsnorm_bwd_workspace_size(T, H))
+
+
+def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_sf=None, dsum=None, stream=None):
+    """Gradients of rmsnorm from the forward's sum, in BF16 (s) or as MXFP8 rows (s_q, s_sf)."""
+    T, H = dy.shape
+    _dense(T, H, torch.bfloat16, dy=dy, dx=dx, s=s, dsum=dsum)
+    _dense(T, H, torch.uint8, s_q=s_q)
+    _dense(T, H // 32, torch.uint8, s_sf=s_sf)
+    _f32(H, gain=gain, dgain=dgain)
+    _f32(T, rstd=rstd)
+    a = RmsNormBwdArgs(dy.data_ptr(), _addr(s), _addr(s_q), _addr(s_sf), _addr(dsum), rstd.data_ptr(),
+                       gain.data_ptr(), dx.data_ptr(), dgain.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _check(lib().mok_rmsnorm_backward(T, H, ctypes.byref(a), _stream(stream)), "mok_rmsnorm_backward")
+
+
+def dequantize_rows(x_q, x_sf, x, stream=None):
+    """BF16 values of MXFP8 rows (the way back from quantize_rows)."""
+    T, H = x.shape
+    _dense(T, H, torch.bfloat16, x=x)
+    _dense(T, H, torch.uint8, x_q=x_q)
+    _dense(T, H // 32, torch.uint8, x_sf=x_sf)
+    _check(lib().mok_dequantize_rows(_ptr(x_q), _ptr(x_sf), T, H, _ptr(x), _stream(stream)), "mok_dequantize_rows")
+
+
+# --------------------------------------------------------------------------- 8-bit training context
+
+def checkpoint_size(p: Problem) -> int:
+    return int(lib().mok_checkpoint_size(ctypes.byref(p)))
+
+
+def checkpoint_save(p: Problem, x, routing, saved, ckpt, stream=None):
+    """MXFP8 copy of a training forward's context (x, pre-activations, partials)."""
+    _dense(p.T, p.H, torch.bfloat16, x=x)
+    if saved.numel() < saved_size(p):
+        raise MokError(ERR_INVALID, "mok_checkpoint_save: saved")
+    rs = routing_struct(routing)
+    _check(lib().mok_checkpoint_save(ctypes.byref(p), _ptr(x), ctypes.byref(rs), _ptr(saved), _ptr(ckpt),
+                                     ckpt.numel(), _stream(stream)), "mok_checkpoint_save")
+
+
+def checkpoint_load(p: Problem, ckpt, routing, x, saved, stream=None):
+    """x and the saved context, restored for moe_backward."""
+    _dense(p.T, p.H, torch.bfloat16, x=x)
+    if saved.numel() < saved_size(p):
+        raise MokError(ERR_INVALID, "mok_checkpoint_load: saved")
+    rs = routing_struct(routing)
+    _check(lib().mok_checkpoint_load(ctypes.byref(p), _ptr(ckpt), ckpt.numel(), ctypes.byref(rs), _ptr(x),
+                                     _ptr(saved), _stream(stream)), "mok_checkpoint_load")
 
 
 def megakernel_trace(workspace, n_ctas):

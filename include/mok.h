@@ -224,7 +224,11 @@ typedef struct {
 size_t mok_workspace_size(const mok_problem* p, const mok_config* cfg);
 /* Workspace bytes of mok_moe_forward_batches for nbatch macro-batches. */
 size_t mok_workspace_size_batches(const mok_problem* p, int32_t nbatch, const mok_config* cfg);
-/* Bytes of the saved context (BF16 training forward only). */
+/* Bytes of the saved context of a training forward. Four arrays, each starting
+ * on a 1024-byte boundary, with R = mok_padded_rows_max rounded up to a multiple
+ * of 128: the gathered rows A [R,H] bf16, the pre-activations G|U [R,2I] f32,
+ * h [R,I] bf16 (all three in the padded expert-contiguous layout), and the
+ * partials [T*k,H] bf16 (slot order). */
 size_t mok_saved_size(const mok_problem* p);
 
 /* The layer forward: pull-gather (+MXFP8 quantisation) of each routed row
@@ -380,6 +384,93 @@ mok_status mok_pack_weights_bwd(int32_t E, int32_t H, int32_t I, int32_t dtype, 
  * expert (I_shared > 0) has no backward here: MOK_ERR_UNSUPPORTED. */
 mok_status mok_moe_backward(const mok_problem* p, const mok_bwd_args* a,
                             const mok_config* cfg, mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* The layer's pre-norm: root-mean-square norm with the residual's addition,   */
+/* and its backward pass. The pages have no counterpart: these stand directly  */
+/* before the layer in every block that uses it.                               */
+/* ------------------------------------------------------------------------- */
+
+typedef struct {
+    const void* x;         /* [T,H] bf16, row pitch ldx elements */
+    int64_t ldx;           /* >= H, a multiple of 8 */
+    const void* residual;  /* [T,H] bf16, row pitch ldr, or NULL (no addition) */
+    int64_t ldr;
+    const float* gain;     /* [H] */
+    float eps;             /* >= 0 */
+    /* outputs, contiguous; each may be NULL, at least one is given */
+    void* sum;             /* [T,H] bf16: bf16(x + residual), the residual stream carried on */
+    void* y;               /* [T,H] bf16 */
+    void* y_q;             /* [T,H] E4M3 and */
+    void* y_sf;            /* [T,H/32] E8M0: the bytes of mok_quantize_rows on y */
+    void* sum_q;           /* [T,H] E4M3 and */
+    void* sum_sf;          /* [T,H/32] E8M0: the bytes of mok_quantize_rows on sum (8-bit checkpoint) */
+    float* rstd;           /* [T] */
+} mok_rmsnorm_args;
+
+/* s = x + residual (fp32, not rounded), rstd = 1/sqrt(mean(s^2) + eps),
+ * y = bf16(s * rstd * gain). Needs H % 8 == 0 (H % 32 == 0 for the MXFP8
+ * outputs), 8 <= H <= 65536, pointers 16-byte aligned (rstd 4, y_sf and
+ * sum_sf 1). sum or y may be x's or residual's own buffer when that buffer's
+ * pitch is H; otherwise outputs overlap no input and no other output. A row
+ * that holds a NaN or an infinity gives NaN in y (its MXFP8 bytes are then
+ * unspecified). T == 0 is a no-op. */
+mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream);
+
+typedef struct {
+    const void* dy;        /* [T,H] bf16: gradient of y */
+    const void* sum;       /* [T,H] bf16: the forward's sum, or NULL and */
+    const void* sum_q;     /* its MXFP8 rows: [T,H] E4M3, */
+    const void* sum_sf;    /* [T,H/32] E8M0 */
+    const void* dsum;      /* [T,H] bf16: gradient that reaches the sum past the norm, or NULL */
+    const float* rstd;     /* [T]: the forward's */
+    const float* gain;     /* [H] */
+    void* dx;              /* [T,H] bf16: gradient of x and of the residual; may be dy's or dsum's buffer */
+    float* dgain;          /* [H] */
+    void* workspace;       /* mok_rmsnorm_bwd_workspace_size bytes, 16-byte aligned */
+    size_t ws_bytes;
+} mok_rmsnorm_bwd_args;
+
+/* Workspace bytes of mok_rmsnorm_backward on the current device (0: invalid). */
+size_t mok_rmsnorm_bwd_workspace_size(int32_t T, int32_t H);
+
+/* With xh = sum * rstd and a = gain * dy:
+ * dx = bf16(dsum + rstd * (a - xh * mean(a * xh))), dgain = sum_t dy * xh, in
+ * fp32 and in a fixed order (bitwise the same in every run on one device).
+ * The sum comes in BF16 or as the 8-bit checkpoint, exactly one of the two.
+ * Sizes and alignment as mok_rmsnorm. T == 0 zeroes dgain. */
+mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args* a, mok_stream_t stream);
+
+/* The values that MXFP8 rows stand for, as BF16 (exact: a block's elements have
+ * four significant bits): x [T,H] from x_q and x_sf as mok_quantize_rows writes
+ * them. Needs H % 32 == 0, x and x_q 16-byte aligned. */
+mok_status mok_dequantize_rows(const void* x_q, const void* x_sf, int32_t T, int32_t H, void* x,
+                               mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* The training context in 8 bits: save it after the training forward, free or */
+/* reuse `saved` for the next layer, and restore it before the backward.       */
+/* ------------------------------------------------------------------------- */
+
+/* Bytes of the checkpoint (0: invalid problem): x [T,H], the pre-activations
+ * G|U [T*k,2I] and the partials [T*k,H], as E4M3 elements with one E8M0 scale
+ * per 32 along each row. About a quarter of mok_saved_size for BF16. */
+size_t mok_checkpoint_size(const mok_problem* p);
+
+/* Quantise the context of a training forward (any dtype) into ckpt
+ * (mok_checkpoint_size bytes, 256-byte aligned): x as the forward read it, and
+ * the G|U rows and partials of `saved`. The values must be finite. The routing
+ * is not part of the checkpoint: keep its arrays until the load. */
+mok_status mok_checkpoint_save(const mok_problem* p, const void* x, const mok_routing* routing,
+                               const void* saved, void* ckpt, size_t ckpt_bytes, mok_stream_t stream);
+
+/* Restore what mok_moe_backward reads: x [T,H] bf16 and `saved`
+ * (mok_saved_size bytes, 1024-byte aligned) with the values that the
+ * checkpoint's bytes stand for, h = bf16(silu(G) * U) formed from the restored
+ * G and U, pad rows zero. Bytes of `saved` past the last padded row are left
+ * as they are (the backward reads none of them). */
+mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ckpt_bytes,
+                               const mok_routing* routing, void* x, void* saved, mok_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* Expert parallelism across ranks ([K-ja] 02: experts spread over GPUs, the  */
