@@ -253,6 +253,11 @@ bool routing_ok(const mok_routing* r, int32_t T = 1) {
            (T == 0 || (r->topk_idx && r->topk_w && r->row_src && r->slot_row));
 }
 
+// The few-token path's limits.
+bool few_ok(const mok_problem* p) {
+    return problem_ok(p) && p->T <= kFewMaxTokens && (int64_t)p->T * p->k <= kFewMaxPairs;
+}
+
 // Rows of the pre-norm: whole 16-byte vectors, a row held by one CTA.
 bool norm_dims_ok(int T, int H) { return T >= 0 && H >= 8 && H % 8 == 0 && H <= 65536; }
 
@@ -725,6 +730,47 @@ mok_status mok_moe_backward(const mok_problem* p, const mok_bwd_args* a, const m
         e = launch_bwd_small(a->dY, sv + FL.spart, r.topk_w, r.topk_idx, a->x, WrT, da, T, H, E, k, gw, dl, dl_full,
                              part, a->dX, a->dW_r, 1, s);
     return cuda_status(e);
+}
+
+size_t mok_few_workspace_size(const mok_problem* p, const mok_config* cfg) {
+    if (!few_ok(p)) return 0;
+    return few_workspace_bytes(p, make_common(nullptr, cfg).num_sms);
+}
+
+mok_status mok_moe_few(const mok_problem* p, const mok_few_args* a, const mok_config* cfg, mok_stream_t stream) {
+    if (!few_ok(p) || !a || !a->packed || !a->workspace) return MOK_ERR_INVALID;
+    if (p->T > 0 && (!a->x || !a->W_r || !a->out)) return MOK_ERR_INVALID;
+    if ((p->I_shared > 0) != (a->packed_shared != nullptr)) return MOK_ERR_INVALID;
+    if (!aligned(a->x, 16) || !aligned(a->W_r, 4) || !aligned(a->bias, 4) || !aligned(a->packed, 256) ||
+        !aligned(a->packed_shared, 256) || !aligned(a->out, 16) || !aligned(a->topk_idx, 4) || !aligned(a->topk_w, 4) ||
+        !aligned(a->workspace, 256))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (a->ws_bytes < mok_few_workspace_size(p, cfg)) return MOK_ERR_INVALID;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (p->T == 0) return cuda_status(cudaMemsetAsync(a->workspace, 0, kStatusBytes, s));
+    const bool mx = p->dtype == MOK_MXFP8;
+    const PackedLayout L = packed_layout(p->E, p->H, p->I, p->dtype);
+    const char* pk = static_cast<const char*>(a->packed);
+    FewLaunch f{};
+    f.p = p;
+    f.x = a->x;
+    f.W_r = a->W_r;
+    f.bias = a->bias;
+    f.gu = pk + L.gu;
+    f.dn = pk + L.dn;
+    f.gu_sf = mx ? reinterpret_cast<const uint8_t*>(pk + L.gu_sf) : nullptr;
+    f.dn_sf = mx ? reinterpret_cast<const uint8_t*>(pk + L.dn_sf) : nullptr;
+    if (p->I_shared > 0) {
+        const PackedLayout SL = packed_layout(1, p->H, p->I_shared, MOK_BF16);
+        f.sgu = static_cast<const char*>(a->packed_shared) + SL.gu;
+        f.sdn = static_cast<const char*>(a->packed_shared) + SL.dn;
+    }
+    f.topk_idx = a->topk_idx;
+    f.topk_w = a->topk_w;
+    f.out = a->out;
+    f.workspace = a->workspace;
+    return cuda_status(launch_few(f, make_common(a->workspace, cfg, p->dtype), s));
 }
 
 mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream) {

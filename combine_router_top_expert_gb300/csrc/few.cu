@@ -1,0 +1,1000 @@
+// few.cu - the whole routed layer for a few tokens (T <= 128) in two kernels:
+// router logits, then everything else (top-k, both expert GEMMs, weighted sum,
+// shared expert).
+//
+// With few tokens the layer is bound by reading each selected expert's weights
+// once: a 128-row tile of packed weights takes longer to arrive than its
+// product with up to 128 token columns takes on the tensor cores. So the
+// weights are the M side of the MMAs and all T tokens are the N side, for every
+// active expert: no gather, no per-expert token lists, no padding of rows. A
+// token's result from an expert that it did not select is dropped (gate/up: the
+// row is never read with a weight; down: the accumulation skips the column).
+//
+//   phase 1   h_e = SwiGLU(W_gu[e] x^T)       units: (expert, row tile, K block)
+//   phase 2   out = sum_e w_e * (W_dn[e] h_e^T)   units: (row tile, expert, K block)
+//
+// Each phase's K blocks form one sequence that is cut into equal contiguous
+// ranges, one per CTA, so every SM streams the same number of weight bytes at
+// any T. A row tile cut between CTAs goes through fp32 partial sums in the
+// workspace; the last CTA to arrive (an atomic count) adds them in CTA order,
+// so the order of additions, and with it every bit, does not depend on timing.
+// Phase 2 multiplies each expert's accumulator by the routing weight in fp32 and
+// adds it up in registers; nothing between h and the output is rounded.
+//
+// CTA layout (one per SM, cooperative launch: phase 2 waits for other CTAs'
+// phase 1 through per-expert counters):
+//   warp 0      TMA of the weight boxes (and their block scales)
+//   warp 1      allocates tensor memory, issues tcgen05.mma
+//   warp 2      TMA of the token boxes; in phase 2 it first waits for the
+//               expert's h, while warp 0 is already a ring of weights ahead
+//   warps 3-10  epilogue: two warps per TMEM lane quadrant, half the token
+//               columns each
+// Every wait is bounded (StatusBlock); nothing traps.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "gemm.cuh"
+#include "moves.cuh"
+#include "quant.cuh"
+
+namespace mok {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Kernel 1: router logits in the fixed order of the routing kernels (32 fma
+// chains, chain c over h = 256 i + 8 c + m, then adds at distance 16, 8, 4, 2,
+// 1, then the bias), the MXFP8 rows of x, and the zeroed counters of kernel 2.
+//
+// A cluster of 8 CTAs takes 8 tokens x 32 experts; CTA r holds the chains
+// 4r .. 4r+3, i.e. 32 consecutive h of every 256, so its share of W_r and x is
+// contiguous per 256-chunk and all of it (H <= 8192: one pass) is in flight at
+// once. Warp w runs chain 4r + w % 4 for 4 of the tokens, one expert a lane. The
+// chain sums meet in the first CTA's shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kLgThreads = 256;
+constexpr int kLgTokens = 8;       // tokens per cluster
+constexpr int kLgCluster = 8;
+constexpr int kLgChunks = 32;      // 256-wide h chunks per pass
+constexpr int kLgWBytes = kLgChunks * 32 * 32 * 4;
+constexpr int kLgXBytes = kLgChunks * kLgTokens * 32 * 2;
+constexpr int kLgRedBytes = 32 * kLgTokens * 32 * 4;
+constexpr int kLgSmem = kLgWBytes + kLgXBytes + kLgRedBytes;
+
+struct FewLogitsParams {
+    const __nv_bfloat16* x;
+    const float* W_r;
+    const float* bias;
+    int T, H, E;
+    float* logits;        // [T, E]
+    uint8_t* xq;          // MXFP8: [T, H] E4M3, else NULL
+    uint8_t* xsf;         // chunk order, one 512-byte chunk per 128 columns
+    int* zero;            // status block and counters of kernel 2
+    int zero_words;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    const int n = valid ? 16 : 0;   // 0: the destination is filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__global__ void __cluster_dims__(kLgCluster, 1, 1) __launch_bounds__(kLgThreads)
+few_logits_kernel(const FewLogitsParams p) {
+    extern __shared__ __align__(128) unsigned char lg_smem[];
+    float* ws = reinterpret_cast<float*>(lg_smem);                                   // [chunk][32 h][32 experts]
+    unsigned char* xs = lg_smem + kLgWBytes;                                         // [chunk][token][32 h] bf16
+    float* red = reinterpret_cast<float*>(lg_smem + kLgWBytes + kLgXBytes);          // [chain][token][expert]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)tc::cluster_ctarank();
+    const int e0 = ((int)blockIdx.x / kLgCluster) * 32, t0 = (int)blockIdx.y * kLgTokens;
+    const int ntok = min(kLgTokens, p.T - t0);
+    const int nchunks = ceil_div(p.H, 256);
+    const int cl = warp & 3, th = warp >> 2;          // chain of this CTA's four, token half
+    const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.W_r) & 15) == 0;
+
+    pdl_wait();
+    pdl_allow_next();
+    tc::cluster_sync();   // every CTA of the cluster runs before any writes to the first one's shared memory
+
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < nchunks; c0 += kLgChunks) {
+        const int nc = min(kLgChunks, nchunks - c0);
+        if (c0 > 0) __syncthreads();
+        if (vec) {
+            for (int i = 0; i < nc; ++i) {   // 32 rows x 8 vectors = 256 copies a chunk
+                const int r = tid >> 3, v = tid & 7;
+                const int h = 256 * (c0 + i) + 32 * rank + r, e = e0 + 4 * v;
+                const bool in = h < p.H && e < p.E;
+                cp_async16(tc::smem_u32(ws + (i * 32 + r) * 32 + 4 * v), in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+            }
+        } else {
+            for (int j = tid; j < nc * 1024; j += kLgThreads) {
+                const int i = j >> 10, r = (j >> 5) & 31, v = j & 31;
+                const int h = 256 * (c0 + i) + 32 * rank + r, e = e0 + v;
+                const bool in = h < p.H && e < p.E;
+                cp_async4(tc::smem_u32(ws + (i * 32 + r) * 32 + v), in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+            }
+        }
+        for (int j = tid; j < nc * kLgTokens * 4; j += kLgThreads) {
+            const int i = j / (kLgTokens * 4), t = (j >> 2) & (kLgTokens - 1), v = j & 3;
+            const int h = 256 * (c0 + i) + 32 * rank + 8 * v;
+            const bool in = h < p.H && t < ntok;
+            cp_async16(tc::smem_u32(xs + ((i * kLgTokens + t) * 32 + 8 * v) * 2),
+                       in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
+        }
+        if (c0 == 0) {
+            // while the copies are in flight: counters of kernel 2, and x in
+            // 8 bits (one block of 32 a thread; the bytes of mok_quantize_rows)
+            const int cta = ((int)blockIdx.y * (int)gridDim.x + (int)blockIdx.x);
+            for (int i = cta * kLgThreads + tid; i < p.zero_words; i += (int)(gridDim.x * gridDim.y) * kLgThreads)
+                p.zero[i] = 0;
+            if (p.xq && e0 == 0) {
+                const int nb = p.H / 32;
+                for (int j = rank * kLgThreads + tid; j < ntok * nb; j += kLgCluster * kLgThreads) {
+                    const int t = t0 + j / nb, b = j % nb;
+                    uint4 o0, o1;
+                    const uint32_t code = quantize_block32(p.x + (int64_t)t * p.H + b * 32, o0, o1);
+                    uint4* dst = reinterpret_cast<uint4*>(p.xq + (int64_t)t * p.H + b * 32);
+                    dst[0] = o0;
+                    dst[1] = o1;
+                    p.xsf[(b >> 2) * 512 + sf_chunk_offset(t, b & 3)] = (uint8_t)code;
+                }
+            }
+        }
+        cp_async_wait_all();
+        __syncthreads();
+        for (int i = 0; i < nc; ++i) {
+            if (256 * (c0 + i) + 32 * rank + 8 * cl >= p.H) break;
+            float w[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) w[m] = ws[(i * 32 + 8 * cl + m) * 32 + lane];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (4 * th + u < ntok) {
+                    float f[8];
+                    unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + 4 * th + u) * 32 + 8 * cl) * 2), f);
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) acc[u] = fmaf(f[m], w[m], acc[u]);
+                }
+            }
+        }
+    }
+    const uint32_t dst = tc::mapa_shared(tc::smem_u32(red), 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t a = dst + (uint32_t)((((4 * rank + cl) * kLgTokens + 4 * th + u) * 32 + lane) * 4);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(acc[u]) : "memory");
+    }
+    tc::cluster_sync();
+    if (rank == 0) {
+        const int t = warp, e = e0 + lane;   // 8 warps: 8 tokens
+        float s[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = red[(c * kLgTokens + t) * 32 + lane];
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1)
+#pragma unroll
+            for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
+        if (t < ntok && e < p.E) p.logits[(int64_t)(t0 + t) * p.E + e] = p.bias ? s[0] + p.bias[e] : s[0];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Kernel 2
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 352;
+constexpr int kFewEpi = 256;      // epilogue threads
+constexpr int kFewEpiBar = 1;     // their named barrier
+
+struct FewParams {
+    int T, H, I, E, k, Is;
+    int R1, R2, Rs1;              // packed weight rows per tile: gate/up, down, shared gate/up
+    const float* logits;
+    int32_t* topk_idx;            // outputs, or NULL
+    float* topk_w;
+    const uint8_t* gu_sf;
+    const uint8_t* dn_sf;
+    const uint8_t* xsf;
+    void* h;                      // [active experts * T, I]
+    uint8_t* hsf;                 // [active experts][I / 128] chunks of 512 bytes
+    __nv_bfloat16* hs;            // [T, Is]
+    float* part;                  // [2 phases][CTAs][2][T][256]
+    int* hready;                  // [E + 1] finished gate/up tiles per active expert (the shared one last)
+    int* cnt1;                    // arrivals per gate/up tile
+    int* cnt2;                    // arrivals per down tile
+    __nv_bfloat16* out;
+    StatusBlock* status;
+    unsigned long long timeout_ns;
+};
+
+template <bool MX, int NT>
+struct FewCfg {
+    static constexpr int kBK = MX ? 128 : 64;              // K elements per block of 128 bytes
+    static constexpr int kBytesA = 256 * 128;
+    static constexpr int kBytesB = NT * 128;
+    static constexpr int kSf = MX ? 3 * 512 : 0;           // two weight chunks, one token chunk
+    static constexpr int kStage = kBytesA + kBytesB;
+    static constexpr int kFixed = 1024 /* alignment */ + 512 /* barriers */ + kFewMaxPairs * 5 + 256 * 2 + 2 * 128 * 4;
+    static constexpr int kLimit = 227 * 1024 - 256 /* the kernel's static shared memory */;
+    static constexpr int kStagesFit = (kLimit - kFixed) / (kStage + kSf);
+    static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
+    static constexpr int kSfOffset = kStages * kStage;
+    static constexpr int kBarOffset = kSfOffset + kStages * kSf;
+    static constexpr int kTabOffset = kBarOffset + 512;
+    static constexpr int kSmem = kBarOffset + kFixed;
+    static constexpr int kAccCols = 2 * NT;
+    static constexpr int kTmemNeed = kAccCols + (MX ? 12 * kStages : 0);
+    static constexpr int kTmemCols = kTmemNeed <= 32 ? 32 : kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128
+                                   : kTmemNeed <= 256 ? 256 : 512;
+    static_assert(kStages >= 3 && kSmem <= kLimit && kTmemNeed <= 512, "few-token kernel budget");
+};
+
+// The layer's work as two sequences of K blocks, and this CTA's part of each.
+struct FewWork {
+    int A;                       // active routed experts
+    int t1, kb1, ts1, kbs1;      // gate/up: tiles per expert and K blocks per tile, routed and shared
+    int t2, kb2, kbs2;           // down: tiles, K blocks per tile and expert, routed and shared
+    int64_t U1, U2;              // units of the phases
+    int G1, G2;                  // CTAs that share them
+};
+
+struct FewJob {
+    int phase;       // 0 gate/up, 1 down
+    int a;           // active expert (A: the shared one)
+    int tile;        // gate/up: row tile of the expert; down: row tile
+    int gtile;       // index of the tile's arrival counter
+    int kb, n;       // K blocks kb .. kb + n - 1
+    int64_t u0, u1;  // unit range of the whole tile (the partial sums' scope)
+    bool last;       // this CTA's last job of the tile
+    bool first;      // and its first
+};
+
+__device__ __forceinline__ int64_t few_start(int64_t U, int G, int c) { return U * c / G; }
+__device__ __forceinline__ int few_owner(int64_t U, int G, int64_t u) { return (int)(((u + 1) * G - 1) / U); }
+
+// Calls f(job) for this CTA's jobs in order; stops when it returns false.
+template <typename F>
+__device__ __forceinline__ void few_jobs(const FewWork& w, F&& f) {
+    const int c = (int)blockIdx.x;
+    FewJob j;
+    if (c < w.G1) {
+        int64_t u = few_start(w.U1, w.G1, c);
+        const int64_t end = few_start(w.U1, w.G1, c + 1);
+        const int64_t routed = (int64_t)w.A * w.t1 * w.kb1;
+        j.phase = 0;
+        j.first = j.last = true;
+        while (u < end) {
+            const bool sh = u >= routed;
+            const int kbt = sh ? w.kbs1 : w.kb1;
+            const int64_t v = sh ? u - routed : u;
+            const int g = (int)(v / kbt);
+            j.kb = (int)(v % kbt);
+            j.u0 = u - j.kb;
+            j.u1 = j.u0 + kbt;
+            j.n = (int)(min(end, j.u1) - u);
+            j.a = sh ? w.A : g / w.t1;
+            j.tile = sh ? g : g % w.t1;
+            j.gtile = sh ? w.A * w.t1 + g : g;
+            u += j.n;
+            if (!f(j)) return;
+        }
+    }
+    if (c < w.G2) {
+        int64_t u = few_start(w.U2, w.G2, c);
+        const int64_t end = few_start(w.U2, w.G2, c + 1);
+        const int upt = w.A * w.kb2 + w.kbs2;
+        j.phase = 1;
+        j.first = true;
+        while (u < end) {
+            j.tile = (int)(u / upt);
+            j.gtile = j.tile;
+            j.u0 = (int64_t)j.tile * upt;
+            j.u1 = j.u0 + upt;
+            const int r = (int)(u - j.u0);
+            const bool sh = r >= w.A * w.kb2;
+            j.a = sh ? w.A : r / w.kb2;
+            j.kb = sh ? r - w.A * w.kb2 : r % w.kb2;
+            const int left = (sh ? w.kbs2 : w.kb2) - j.kb;
+            j.n = (int)min((int64_t)left, end - u);
+            u += j.n;
+            j.last = u == end || u == j.u1;
+            if (!f(j)) return;
+            j.first = j.last;
+        }
+    }
+}
+
+__device__ __forceinline__ int few_ld_acquire(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void few_red_release(int* p) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+
+// Bounded wait until *p >= target (acquire). False: gave up (recorded).
+__device__ bool few_wait_counter(const int* p, int target, StatusBlock* st, uint64_t tmo) {
+    if (few_ld_acquire(p) >= target) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (few_ld_acquire(p) >= target) return true;
+        if ((it & 31) == 0) {
+            if (abort_requested(st)) return false;
+            if (globaltimer_ns() - t0 > tmo) {
+                record_failure(st, MOK_ERR_TIMEOUT, kSiteCounter);
+                return false;
+            }
+        }
+    }
+}
+
+// Wait, whatever the abort flag says, until copies or MMAs in flight have
+// landed, at most tmo.
+__device__ void few_drain(uint32_t bar, uint32_t parity, uint64_t tmo) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!tc::mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < tmo) {
+    }
+}
+
+// AND over the epilogue's threads (all of them call it), so that they leave a
+// loop together.
+__device__ __forceinline__ bool epi_and(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "n"(kFewEpiBar), "n"(kFewEpi)
+        : "memory");
+    __syncwarp();
+    return r != 0;
+}
+__device__ __forceinline__ void epi_sync() {
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"n"(kFewEpiBar), "n"(kFewEpi) : "memory");
+}
+
+// CH (8 or 16) consecutive 32-bit columns of this warp's 32 lanes.
+template <int CH>
+__device__ __forceinline__ void few_tmem_ld(uint32_t a, float (&v)[CH]) {
+    uint32_t r[CH];
+    if constexpr (CH == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(a)
+                     : "memory");
+    } else {
+        static_assert(CH == 16, "columns per load");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
+            " %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(a)
+            : "memory");
+    }
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <bool MX, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXq,
+               const __grid_constant__ CUtensorMap tmGU, const __grid_constant__ CUtensorMap tmDN,
+               const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmSGU,
+               const __grid_constant__ CUtensorMap tmSDN, const __grid_constant__ CUtensorMap tmHs,
+               const FewParams p) {
+    using C = FewCfg<MX, NT>;
+    constexpr int S = C::kStages;
+    extern __shared__ __align__(1024) unsigned char few_smem[];
+    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_hit[kMaxE / 32];
+    __shared__ int s_active, s_last;
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(few_smem) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = tc::smem_u32(smem);
+    const uint32_t bar = base + C::kBarOffset;
+    auto fullA = [&](int s) { return bar + 8u * s; };
+    auto fullB = [&](int s) { return bar + 8u * (S + s); };
+    auto empty = [&](int s) { return bar + 8u * (2 * S + s); };
+    const uint32_t accf = bar + 8u * (3 * S), acce = bar + 8u * (3 * S + 1), drain = bar + 8u * (3 * S + 2);
+    auto a_tile = [&](int s) { return base + s * C::kStage; };
+    auto b_tile = [&](int s) { return base + s * C::kStage + C::kBytesA; };
+    auto sf_tile = [&](int s) { return base + C::kSfOffset + s * C::kSf; };
+    float* s_w = reinterpret_cast<float*>(smem + C::kTabOffset);              // [T*k] routing weights
+    uint8_t* s_idx = smem + C::kTabOffset + kFewMaxPairs * 4;                 // [T*k] experts
+    uint16_t* s_act = reinterpret_cast<uint16_t*>(smem + C::kTabOffset + kFewMaxPairs * 5);   // [A] active experts
+    float* s_row = reinterpret_cast<float*>(smem + C::kTabOffset + kFewMaxPairs * 5 + 512);   // [2][128]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    StatusBlock* st = p.status;
+    const uint64_t tmo = p.timeout_ns;
+    const int T = p.T, E = p.E, k = p.k;
+
+    if (threadIdx.x < kMaxE / 32) s_hit[threadIdx.x] = 0;
+    if (threadIdx.x == 64) {
+        for (int s = 0; s < S; ++s) {
+            tc::mbar_init(fullA(s), 1);
+            tc::mbar_init(fullB(s), 1);
+            tc::mbar_init(empty(s), 1);
+        }
+        tc::mbar_init(accf, 1);
+        tc::mbar_init(acce, kFewEpi);
+        tc::mbar_init(drain, 1);
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tc::smem_u32(&s_tmem), C::kTmemCols);
+        tc::tmem_relinquish();
+    }
+    __syncthreads();
+
+    // top-k of every token, in each CTA for itself: a warp per token, experts
+    // lane, lane + 32, ...; keys order like the logits (-0 = +0), 0 is "taken"
+    for (int t = warp; t < T; t += kFewThreads / 32) {
+        uint32_t key[kMaxE / 32];
+#pragma unroll
+        for (int q = 0; q < kMaxE / 32; ++q) {
+            const int e = lane + 32 * q;
+            key[q] = 0;
+            if (e < E) {
+                const uint32_t b = __float_as_uint(p.logits[(int64_t)t * E + e] + 0.0f);
+                key[q] = max(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u), 1u);
+            }
+        }
+        float l0 = 0.f, den = 0.f;
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = key[0];
+            int be = lane;
+#pragma unroll
+            for (int q = 1; q < kMaxE / 32; ++q)
+                if (key[q] > best) {
+                    best = key[q];
+                    be = lane + 32 * q;
+                }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)be : 0xffffu);
+#pragma unroll
+            for (int q = 0; q < kMaxE / 32; ++q)
+                if (e == lane + 32 * q) key[q] = 0;
+            const float l = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
+            if (j == 0) l0 = l;
+            den += expf(l - l0);   // j ascending; identical in every lane
+            if (lane == 0) {
+                s_idx[t * k + j] = (uint8_t)e;
+                s_w[t * k + j] = l;
+                atomicOr(&s_hit[e >> 5], 1u << (e & 31));
+            }
+        }
+        __syncwarp();
+        for (int j = lane; j < k; j += 32) {
+            const float w = expf(s_w[t * k + j] - l0) / den;
+            s_w[t * k + j] = w;
+            if (blockIdx.x == 0) {
+                if (p.topk_idx) p.topk_idx[t * k + j] = s_idx[t * k + j];
+                if (p.topk_w) p.topk_w[t * k + j] = w;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {   // the active experts, ascending
+        int n = 0;
+        for (int q = 0; 32 * q < E; ++q) {
+            const uint32_t m = s_hit[q];
+            if ((m >> lane) & 1u) s_act[n + __popc(m & ((1u << lane) - 1))] = (uint16_t)(32 * q + lane);
+            n += __popc(m);
+        }
+        if (lane == 0) s_active = n;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+
+    FewWork w;
+    w.A = s_active;
+    w.t1 = 2 * p.I / p.R1;
+    w.kb1 = p.H / C::kBK;
+    w.ts1 = p.Is ? 2 * p.Is / p.Rs1 : 0;
+    w.kbs1 = p.Is ? p.H / 64 : 0;
+    w.t2 = p.H / p.R2;
+    w.kb2 = p.I / C::kBK;
+    w.kbs2 = p.Is / 64;
+    w.U1 = (int64_t)w.A * w.t1 * w.kb1 + (int64_t)w.ts1 * w.kbs1;
+    w.U2 = (int64_t)w.t2 * (w.A * w.kb2 + w.kbs2);
+    w.G1 = (int)min((int64_t)gridDim.x, w.U1);
+    w.G2 = (int)min((int64_t)gridDim.x, w.U2);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ weights
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int last_par[S];
+            for (int i = 0; i < S; ++i) last_par[i] = -1;
+            few_jobs(w, [&](const FewJob& j) {
+                const bool sh = j.a == w.A;
+                const int e = sh ? 0 : s_act[j.a];
+                const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
+                const int row0 = (j.phase ? e * p.H : e * 2 * p.I) + j.tile * rows;
+                const CUtensorMap* tm = j.phase ? (sh ? &tmSDN : &tmDN) : (sh ? &tmSGU : &tmGU);
+                const int bk = sh ? 64 : C::kBK;
+                for (int i = 0; i < j.n; ++i) {
+                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) {
+                        for (int q = 0; q < S; ++q)
+                            if (last_par[q] >= 0) few_drain(fullA(q), (uint32_t)last_par[q], tmo);
+                        return false;
+                    }
+                    const int kb = j.kb + i;
+                    uint32_t bytes = (uint32_t)rows * 128u;
+                    if constexpr (MX) {
+                        if (!sh) bytes += 512u * (uint32_t)ceil_div(rows, 128);
+                    }
+                    tc::mbar_expect_tx(fullA(s), bytes);
+                    tc::tma_load_2d(a_tile(s), tm, fullA(s), kb * bk, row0);
+                    if constexpr (MX) {
+                        if (!sh) {
+                            if (rows == 224) {   // scales packed per 224-row tile: two chunks side by side
+                                tc::bulk_load(sf_tile(s), p.dn_sf + ((int64_t)(row0 / 224) * (p.I / 128) + kb) * 1024, 1024,
+                                              fullA(s));
+                            } else {
+                                const uint8_t* sf = j.phase ? p.dn_sf : p.gu_sf;
+                                const int nkc = (j.phase ? p.I : p.H) / 128;
+                                for (int b = 0; b < rows / 128; ++b)
+                                    tc::bulk_load(sf_tile(s) + 512 * b, sf + ((int64_t)(row0 / 128 + b) * nkc + kb) * 512, 512,
+                                                  fullA(s));
+                            }
+                        }
+                    }
+                    last_par[s] = (int)ph;
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+                return true;
+            });
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ tokens
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            int last_par[S];
+            for (int i = 0; i < S; ++i) last_par[i] = -1;
+            int ready = -1;   // the expert whose h is known to be complete
+            auto give_up = [&]() {
+                for (int q = 0; q < S; ++q)
+                    if (last_par[q] >= 0) few_drain(fullB(q), (uint32_t)last_par[q], tmo);
+                return false;
+            };
+            few_jobs(w, [&](const FewJob& j) {
+                const bool sh = j.a == w.A;
+                if (j.phase && ready != j.a) {
+                    if (!few_wait_counter(p.hready + j.a, sh ? w.ts1 : w.t1, st, tmo)) return give_up();
+                    tc::fence_proxy_async_global();
+                    ready = j.a;
+                }
+                const CUtensorMap* tm = j.phase ? (sh ? &tmHs : &tmH) : (MX && !sh ? &tmXq : &tmX);
+                const int row0 = j.phase && !sh ? j.a * T : 0;
+                const int bk = sh ? 64 : C::kBK;
+                for (int i = 0; i < j.n; ++i) {
+                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) return give_up();
+                    const int kb = j.kb + i;
+                    tc::mbar_expect_tx(fullB(s), (uint32_t)C::kBytesB + (MX && !sh ? 512u : 0u));
+                    tc::tma_load_2d(b_tile(s), tm, fullB(s), kb * bk, row0);
+                    if constexpr (MX) {
+                        if (!sh)
+                            tc::bulk_load(sf_tile(s) + 1024,
+                                          j.phase ? p.hsf + ((int64_t)j.a * (p.I / 128) + kb) * 512 : p.xsf + (int64_t)kb * 512,
+                                          512, fullB(s));
+                    }
+                    last_par[s] = (int)ph;
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+                return true;
+            });
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, acc_ph = 0;
+            bool issued = false;
+            auto give_up = [&]() {
+                if (issued) {   // the MMAs issued so far end before tensor memory is freed
+                    tc::mma_commit(drain);
+                    few_drain(drain, 0, tmo);
+                }
+                return false;
+            };
+            few_jobs(w, [&](const FewJob& j) {
+                const bool sh = j.a == w.A;
+                const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
+                const int nb = ceil_div(rows, 128);
+                if (!tc::mbar_wait(acce, acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return give_up();
+                tc::fence_after_sync();
+                for (int i = 0; i < j.n; ++i) {
+                    if (!tc::mbar_wait(fullA(s), ph, st, tmo, kSiteMmaFull)) return give_up();
+                    if (!tc::mbar_wait(fullB(s), ph, st, tmo, kSiteMmaFull)) return give_up();
+                    tc::fence_after_sync();
+                    const uint32_t sf = tmem + (uint32_t)(C::kAccCols + 12 * s);
+                    if constexpr (MX) {
+                        if (!sh) {
+                            for (int b = 0; b < nb; ++b)
+                                tc::tmem_cp_32x128b_warpx4(sf + 4 * b, tc::make_sdesc(sf_tile(s) + 512 * b, 0, 128, tc::kLayoutNone));
+                            tc::tmem_cp_32x128b_warpx4(sf + 8, tc::make_sdesc(sf_tile(s) + 1024, 0, 128, tc::kLayoutNone));
+                        }
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t bd = tc::make_sdesc(b_tile(s) + kk * 32, 16, 1024, tc::kLayoutSW128);
+                        const uint32_t on = (i > 0 || kk > 0) ? 1u : 0u;
+                        for (int b = 0; b < nb; ++b) {
+                            const uint64_t ad = tc::make_sdesc(a_tile(s) + b * 16384 + kk * 32, 16, 1024, tc::kLayoutSW128);
+                            if (MX && !sh)
+                                tc::mma_mxf8(tmem + b * NT, ad, bd, tc::idesc_mxf8(128, NT, kk, kk), sf + 4 * b, sf + 8, on);
+                            else
+                                tc::mma_bf16(tmem + b * NT, ad, bd, tc::idesc_bf16(128, NT, false, false), on);
+                        }
+                    }
+                    issued = true;
+                    tc::mma_commit(empty(s));
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+                tc::mma_commit(accf);
+                acc_ph ^= 1u;
+                return true;
+            });
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        constexpr int NC = NT / 2;                  // token columns of a thread
+        constexpr int CH = NC < 16 ? NC : 16;       // columns at a time
+        const int q = warp & 3;                     // TMEM lane quadrant of this warp
+        const int half = (warp - 3) >> 2;
+        const int et = threadIdx.x - 96;            // 0 .. 255
+        const int row = 32 * q + lane;              // row in each 128-row block
+        const int col0 = half * NC;                 // first token column of this thread
+        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
+        const int c_me = (int)blockIdx.x;
+        uint32_t ph = 0;
+        int wbuf = 0;
+        float acc[2][NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) acc[0][i] = acc[1][i] = 0.f;
+
+        auto slot = [&](int phase, int c, int64_t u0, int64_t U, int G) -> float* {
+            const int which = few_start(U, G, c) >= u0 ? 0 : 1;
+            return p.part + (((int64_t)phase * gridDim.x + c) * 2 + which) * (256 * (int64_t)T);
+        };
+        // SwiGLU of CH columns: v[0], v[1] are the tile's two row blocks
+        auto store_h = [&](const FewJob& j, int cc, const float (&v0)[CH], const float (&v1)[CH]) {
+            const bool sh = j.a == w.A;
+            if (MX && !sh) {
+                // gate rows 0..127, up rows 128..255 of the same features
+                uint8_t* hq = static_cast<uint8_t*>(p.h);
+                const int f = j.tile * 128 + row;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int t = col0 + cc + i;
+                    if (t < T) {
+                        const float hv = silu_f(v0[i]) * v1[i];
+                        const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(hv)));
+                        const uint32_t code = e8m0_code(__uint_as_float(am));
+                        hq[((int64_t)j.a * T + t) * p.I + f] = (uint8_t)f32x2_to_e4m3x2(hv * e8m0_inv_scale(code), 0.f);
+                        if (lane == 0)
+                            p.hsf[((int64_t)j.a * (p.I / 128) + j.tile) * 512 + sf_chunk_offset(t, q)] = (uint8_t)code;
+                    }
+                }
+            } else {
+                // lanes 0-15 gate, 16-31 up of the same 16 features: the lower
+                // half forms the first CH/2 columns, the upper half the others
+                const int rows = sh ? p.Rs1 : p.R1, ld = sh ? p.Is : p.I;
+                __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)j.a * T * p.I;
+                const bool lower = lane < 16;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (128 * b >= rows) continue;
+                    const int f = j.tile * (rows / 2) + 64 * b + 16 * q + (lane & 15);
+#pragma unroll
+                    for (int i = 0; i < CH / 2; ++i) {
+                        const float lo = b ? v1[i] : v0[i], hi = b ? v1[CH / 2 + i] : v0[CH / 2 + i];
+                        const float other = __shfl_xor_sync(0xffffffffu, lower ? hi : lo, 16);
+                        const int t = col0 + cc + (lower ? i : CH / 2 + i);
+                        const float hv = silu_f(lower ? lo : other) * (lower ? other : hi);
+                        if (t < T) hb[(int64_t)t * ld + f] = __float2bfloat16_rn(hv);
+                    }
+                }
+            }
+        };
+        // write a partial tile of CH columns, or add up all of them
+        auto put_part = [&](float* dst, int nb, int cc, const float (&v0)[CH], const float (&v1)[CH]) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int t = col0 + cc + i;
+                if (t < T) {
+                    __stcg(dst + (int64_t)t * 256 + row, v0[i]);
+                    if (nb > 1) __stcg(dst + (int64_t)t * 256 + 128 + row, v1[i]);
+                }
+            }
+        };
+        // every thread's partial is written: count this CTA in; true in the last one
+        auto arrive_last = [&](int* cnt, int n) {
+            epi_sync();
+            if (et == 0) {
+                __threadfence();
+                s_last = atomicAdd(cnt, 1) == n - 1;
+                __threadfence();
+            }
+            epi_sync();
+            return s_last != 0;
+        };
+        auto sum_parts = [&](int phase, const FewJob& j, int64_t U, int G, int c0, int c1, int nb, int cc, float (&v0)[CH],
+                             float (&v1)[CH]) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) v0[i] = v1[i] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+                const float* src = slot(phase, c, j.u0, U, G);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int t = col0 + cc + i;
+                    if (t < T) {
+                        v0[i] += __ldcg(src + (int64_t)t * 256 + row);
+                        if (nb > 1) v1[i] += __ldcg(src + (int64_t)t * 256 + 128 + row);
+                    }
+                }
+            }
+        };
+
+        few_jobs(w, [&](const FewJob& j) {
+            const bool sh = j.a == w.A;
+            const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
+            const int nb = ceil_div(rows, 128);
+            const int64_t U = j.phase ? w.U2 : w.U1;
+            const int G = j.phase ? w.G2 : w.G1;
+            const int c0 = few_owner(U, G, j.u0), c1 = few_owner(U, G, j.u1 - 1);
+            if (j.phase && et < T) {
+                // this expert's routing weights per token; -1: not selected
+                float wt = -1.f;
+                if (sh) wt = 1.f;
+                else
+                    for (int i = 0; i < k; ++i)
+                        if (s_idx[et * k + i] == s_act[j.a]) wt = s_w[et * k + i];
+                s_row[wbuf * 128 + et] = wt;
+            }
+            if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
+            ph ^= 1u;
+            tc::fence_after_sync();
+            if (j.phase == 0) {
+                const bool whole = c0 == c1;
+                float* mine = slot(0, c_me, j.u0, U, G);
+#pragma unroll 1
+                for (int cc = 0; cc < NC; cc += CH) {
+                    float v0[CH], v1[CH];
+                    few_tmem_ld<CH>(tq + cc, v0);
+                    few_tmem_ld<CH>(tq + NT + cc, v1);
+                    if (col0 + cc < T) {
+                        if (whole) store_h(j, cc, v0, v1);
+                        else put_part(mine, nb, cc, v0, v1);
+                    }
+                }
+                tc::fence_before_sync();
+                tc::mbar_arrive(acce);
+                bool done = whole;
+                if (!whole && arrive_last(p.cnt1 + j.gtile, c1 - c0 + 1)) {
+                    done = true;
+#pragma unroll 1
+                    for (int cc = 0; cc < NC; cc += CH) {
+                        if (col0 + cc >= T) break;
+                        float v0[CH], v1[CH];
+                        sum_parts(0, j, U, G, c0, c1, nb, cc, v0, v1);
+                        store_h(j, cc, v0, v1);
+                    }
+                }
+                if (done) {   // publish the tile of h
+                    __threadfence();
+                    tc::fence_proxy_async_global();
+                    epi_sync();
+                    if (et == 0) few_red_release(p.hready + j.a);
+                }
+            } else {
+                const float* wr = s_row + wbuf * 128 + col0;
+                wbuf ^= 1;
+#pragma unroll
+                for (int cc = 0; cc < NC; cc += CH) {
+                    float v0[CH], v1[CH];
+                    few_tmem_ld<CH>(tq + cc, v0);
+                    few_tmem_ld<CH>(tq + NT + cc, v1);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const float wt = col0 + cc + i < T ? wr[cc + i] : -1.f;
+                        if (wt >= 0.f) {
+                            acc[0][cc + i] = fmaf(wt, v0[i], acc[0][cc + i]);
+                            acc[1][cc + i] = fmaf(wt, v1[i], acc[1][cc + i]);
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+                tc::mbar_arrive(acce);
+                if (j.last) {
+                    const bool whole = c0 == c1;
+                    auto store_out = [&](int cc, const float (&v0)[CH], const float (&v1)[CH]) {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            const int t = col0 + cc + i;
+                            if (t < T) {
+                                __nv_bfloat16* o = p.out + (int64_t)t * p.H + j.tile * rows;
+                                o[row] = __float2bfloat16_rn(v0[i]);
+                                if (128 + row < rows) o[128 + row] = __float2bfloat16_rn(v1[i]);
+                            }
+                        }
+                    };
+                    float* mine = slot(1, c_me, j.u0, U, G);
+#pragma unroll
+                    for (int cc = 0; cc < NC; cc += CH) {
+                        float v0[CH], v1[CH];
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            v0[i] = acc[0][cc + i];
+                            v1[i] = acc[1][cc + i];
+                            acc[0][cc + i] = acc[1][cc + i] = 0.f;
+                        }
+                        if (whole) store_out(cc, v0, v1);
+                        else put_part(mine, nb, cc, v0, v1);
+                    }
+                    if (!whole && arrive_last(p.cnt2 + j.gtile, c1 - c0 + 1)) {
+#pragma unroll 1
+                        for (int cc = 0; cc < NC; cc += CH) {
+                            if (col0 + cc >= T) break;
+                            float v0[CH], v1[CH];
+                            sum_parts(1, j, U, G, c0, c1, nb, cc, v0, v1);
+                            store_out(cc, v0, v1);
+                        }
+                    }
+                }
+            }
+            return true;
+        });
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+int few_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+struct FewLayout {
+    size_t counters, logits, xq, xsf, h, hsf, hs, part, total;
+    int n_counters, n1;   // ints: E + 1 ready counts, n1 gate/up tiles, down tiles
+};
+
+int gu_rows(int I) { return std::min(256, 2 * I); }
+
+FewLayout few_layout(const mok_problem* p, int ctas) {
+    FewLayout L{};
+    const bool mx = p->dtype == MOK_MXFP8;
+    const int64_t T = p->T, H = p->H, I = p->I;
+    const int64_t act = std::min<int64_t>(p->E, T * p->k);
+    const int r2 = down_tile_n(p->H, mx);
+    L.n1 = (int)(act * (2 * I / gu_rows(p->I))) + (p->I_shared ? 2 * p->I_shared / gu_rows(p->I_shared) : 0);
+    L.n_counters = p->E + 1 + L.n1 + (int)(H / r2);
+    size_t o = kStatusBytes;
+    L.counters = o; o += align_up((int64_t)L.n_counters * 4, 256);
+    L.logits = o; o += align_up(T * p->E * 4, 256);
+    L.xq = o; if (mx) o += align_up(T * H, 256);
+    L.xsf = o; if (mx) o += H / 128 * 512;
+    L.h = o; o += align_up(act * T * I * (mx ? 1 : 2), 256);
+    L.hsf = o; if (mx) o += act * (I / 128) * 512;
+    L.hs = o; o += align_up(T * p->I_shared * 2, 256);
+    L.part = o; o += (size_t)2 * ctas * 2 * 256 * T * 4;
+    L.total = o;
+    return L;
+}
+
+template <bool MX, int NT>
+cudaError_t run_ffn(const CUtensorMap* tm, const FewParams& p, int grid, cudaStream_t s) {
+    using C = FewCfg<MX, NT>;
+    auto kern = few_ffn_kernel<MX, NT>;
+    ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmem);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], tm[6], tm[7], p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool MX>
+cudaError_t run_ffn(const CUtensorMap* tm, const FewParams& p, int grid, cudaStream_t s) {
+    switch (few_columns(p.T)) {
+        case 16: return run_ffn<MX, 16>(tm, p, grid, s);
+        case 32: return run_ffn<MX, 32>(tm, p, grid, s);
+        case 64: return run_ffn<MX, 64>(tm, p, grid, s);
+        default: return run_ffn<MX, 128>(tm, p, grid, s);
+    }
+}
+
+}  // namespace
+
+size_t few_workspace_bytes(const mok_problem* p, int ctas) { return few_layout(p, ctas).total; }
+
+cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) {
+    const mok_problem* q = a.p;
+    const bool mx = q->dtype == MOK_MXFP8;
+    const int T = q->T, H = q->H, I = q->I, E = q->E, Is = q->I_shared;
+    const FewLayout L = few_layout(q, c.num_sms);
+    char* ws = static_cast<char*>(a.workspace);
+    const int64_t act = std::min<int64_t>(E, (int64_t)T * q->k);
+
+    FewLogitsParams lp{};
+    lp.x = static_cast<const __nv_bfloat16*>(a.x);
+    lp.W_r = a.W_r;
+    lp.bias = a.bias;
+    lp.T = T;
+    lp.H = H;
+    lp.E = E;
+    lp.logits = reinterpret_cast<float*>(ws + L.logits);
+    lp.xq = mx ? reinterpret_cast<uint8_t*>(ws + L.xq) : nullptr;
+    lp.xsf = mx ? reinterpret_cast<uint8_t*>(ws + L.xsf) : nullptr;
+    lp.zero = reinterpret_cast<int*>(ws);
+    lp.zero_words = (int)(kStatusBytes / 4) + L.n_counters;
+
+    FewParams p{};
+    p.T = T; p.H = H; p.I = I; p.E = E; p.k = q->k; p.Is = Is;
+    p.R1 = gu_rows(I);
+    p.R2 = down_tile_n(H, mx);
+    p.Rs1 = Is ? gu_rows(Is) : 0;
+    p.logits = lp.logits;
+    p.topk_idx = a.topk_idx;
+    p.topk_w = a.topk_w;
+    p.gu_sf = a.gu_sf;
+    p.dn_sf = a.dn_sf;
+    p.xsf = lp.xsf;
+    p.h = ws + L.h;
+    p.hsf = mx ? reinterpret_cast<uint8_t*>(ws + L.hsf) : nullptr;
+    p.hs = reinterpret_cast<__nv_bfloat16*>(ws + L.hs);
+    p.part = reinterpret_cast<float*>(ws + L.part);
+    p.hready = reinterpret_cast<int*>(ws + L.counters);
+    p.cnt1 = p.hready + E + 1;
+    p.cnt2 = p.cnt1 + L.n1;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.status = c.status;
+    p.timeout_ns = c.timeout_ns;
+
+    CUtensorMap tm[8];
+    const int NT = few_columns(T), eb = mx ? 1 : 2, bk = 128 / eb;
+    bool ok = make_tmap_swizzled(&tm[0], a.x, T, H, 2, 64, NT) &&
+              make_tmap_swizzled(&tm[2], a.gu, (int64_t)E * 2 * I, H, eb, bk, p.R1) &&
+              make_tmap_swizzled(&tm[3], a.dn, (int64_t)E * H, I, eb, bk, p.R2) &&
+              make_tmap_swizzled(&tm[4], p.h, act * T, I, eb, bk, NT);
+    tm[1] = tm[0];
+    if (ok && mx) ok = make_tmap_swizzled(&tm[1], lp.xq, T, H, 1, 128, NT);
+    tm[5] = tm[2];
+    tm[6] = tm[3];
+    tm[7] = tm[4];
+    if (ok && Is)
+        ok = make_tmap_swizzled(&tm[5], a.sgu, 2 * (int64_t)Is, H, 2, 64, p.Rs1) &&
+             make_tmap_swizzled(&tm[6], a.sdn, H, Is, 2, 64, p.R2) && make_tmap_swizzled(&tm[7], p.hs, T, Is, 2, 64, NT);
+    if (!ok) return cudaErrorInvalidValue;
+
+    ensure_smem_attr(reinterpret_cast<const void*>(few_logits_kernel), kLgSmem);
+    cudaError_t e = launch_after(few_logits_kernel, dim3(kLgCluster * ceil_div(E, 32), ceil_div(T, kLgTokens)),
+                                 dim3(kLgThreads), kLgSmem, s, lp);
+    if (e != cudaSuccess) return e;
+    return mx ? run_ffn<true>(tm, p, c.num_sms, s) : run_ffn<false>(tm, p, c.num_sms, s);
+}
+
+}  // namespace mok

@@ -10,6 +10,10 @@ namespace mok {
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem_bytes, int box_cols,
                     int box_rows);
 
+// The same with a 128-byte swizzle (box_cols * elem_bytes == 128).
+bool make_tmap_swizzled(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem_bytes, int box_cols,
+                        int box_rows);
+
 // route.cu
 size_t route_workspace_bytes(int T, int H, int E, int k);
 cudaError_t launch_route_layout(const void* x, const float* W_r, const float* bias, int T, int H, int E, int k,
@@ -98,6 +102,26 @@ struct GemmCommon {
     int cluster;   // 2: grouped GEMMs run as 2-SM CTA pairs (tcgen05 cta_group::2, B rows split
                    // between the two CTAs, no multicast loads; the BF16 default); 1: single CTAs
 };
+// few.cu: the whole layer for at most kFewMaxTokens tokens and kFewMaxPairs
+// (token, slot) pairs.
+constexpr int kFewMaxTokens = 128;
+constexpr int kFewMaxPairs = 2048;
+struct FewLaunch {
+    const mok_problem* p;
+    const void* x;
+    const float* W_r;
+    const float* bias;
+    const void *gu, *dn;        // packed routed experts and their block scales (MXFP8)
+    const uint8_t *gu_sf, *dn_sf;
+    const void *sgu, *sdn;      // packed shared expert (BF16), or NULL
+    int32_t* topk_idx;
+    float* topk_w;
+    void* out;
+    void* workspace;            // few_workspace_bytes for c.num_sms CTAs
+};
+size_t few_workspace_bytes(const mok_problem* p, int ctas);
+cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s);
+
 // Forward gate/up GEMM + SwiGLU. A: [rows, H] (bf16 or E4M3 + tile scales);
 // packed B: [E * 2I, H] (interleaved gate/up per il = BN/2 columns).
 // identity_rows > 0: A is a plain [identity_rows, H] matrix (shared expert;

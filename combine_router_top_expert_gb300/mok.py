@@ -29,7 +29,8 @@ EXPORTS = ["mok_route_workspace_size", "mok_route_layout", "mok_packed_weights_s
            "mok_quantize_rows", "mok_dispatch_quantized", "mok_route_test_hook", "mok_ep_workspace_size",
            "mok_ep_dispatch", "mok_ep_push", "mok_packed_weights_bwd_size", "mok_pack_weights_bwd",
            "mok_dispatch_tokens", "mok_rmsnorm", "mok_rmsnorm_bwd_workspace_size", "mok_rmsnorm_backward",
-           "mok_dequantize_rows", "mok_checkpoint_size", "mok_checkpoint_save", "mok_checkpoint_load"]
+           "mok_dequantize_rows", "mok_checkpoint_size", "mok_checkpoint_save", "mok_checkpoint_load",
+           "mok_few_workspace_size", "mok_moe_few"]
 
 FLAG_MEGAKERNEL = 1
 FLAG_GEMM_PAIRS = 2
@@ -98,7 +99,16 @@ class RmsNormBwdArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class FewArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("W_r", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("packed", ctypes.c_void_p), ("packed_shared", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("topk_idx", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("ws_bytes", ctypes.c_size_t)]
+
+
 EP_MAX_RANKS = 8
+FEW_MAX_TOKENS = 128   # MOK_FEW_MAX_TOKENS
+FEW_MAX_PAIRS = 2048   # MOK_FEW_MAX_PAIRS
 _lock = threading.Lock()
 _lib = None
 
@@ -158,6 +168,9 @@ def lib():
             L.mok_checkpoint_size.restype = SZ
             L.mok_checkpoint_save.argtypes = [PP, P, PR, P, P, SZ, P]
             L.mok_checkpoint_load.argtypes = [PP, P, SZ, PR, P, P, P]
+            L.mok_few_workspace_size.argtypes = [PP, PC]
+            L.mok_few_workspace_size.restype = SZ
+            L.mok_moe_few.argtypes = [PP, ctypes.POINTER(FewArgs), PC, P]
             L.mok_status_string.argtypes = [I32]
             L.mok_status_string.restype = ctypes.c_char_p
             L.mok_version.restype = ctypes.c_char_p
@@ -165,7 +178,8 @@ def lib():
                          "mok_moe_forward_batches", "mok_dispatch", "mok_quantize_rows", "mok_dispatch_quantized",
                          "mok_expert_ffn", "mok_combine", "mok_moe_backward", "mok_device_status", "mok_route_test_hook",
                          "mok_ep_dispatch", "mok_ep_push", "mok_pack_weights_bwd", "mok_dispatch_tokens", "mok_rmsnorm",
-                         "mok_rmsnorm_backward", "mok_dequantize_rows", "mok_checkpoint_save", "mok_checkpoint_load"):
+                         "mok_rmsnorm_backward", "mok_dequantize_rows", "mok_checkpoint_save", "mok_checkpoint_load",
+                         "mok_moe_few"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -463,6 +477,27 @@ def dequantize_rows(x_q, x_sf, x, stream=None):
     _dense(T, H, torch.uint8, x_q=x_q)
     _dense(T, H // 32, torch.uint8, x_sf=x_sf)
     _check(lib().mok_dequantize_rows(_ptr(x_q), _ptr(x_sf), T, H, _ptr(x), _stream(stream)), "mok_dequantize_rows")
+
+
+# --------------------------------------------------------------------------- the layer for a few tokens
+
+def few_workspace_size(p: Problem, cfg: Config | None = None) -> int:
+    return int(lib().mok_few_workspace_size(ctypes.byref(p), ctypes.byref(cfg) if cfg else None))
+
+
+def moe_few(p: Problem, x, W_r, packed, out, workspace, bias=None, packed_shared=None, topk_idx=None, topk_w=None,
+            cfg: Config | None = None, stream=None):
+    """The whole layer for p.T <= FEW_MAX_TOKENS tokens (p.T * p.k <= FEW_MAX_PAIRS)."""
+    _dense(p.T, p.H, torch.bfloat16, x=x, out=out)
+    _dense(p.H, p.E, torch.float32, W_r=W_r)
+    _dense(p.T, p.k, torch.int32, topk_idx=topk_idx)
+    _dense(p.T, p.k, torch.float32, topk_w=topk_w)
+    _f32(p.E, bias=bias)
+    a = FewArgs(x.data_ptr(), W_r.data_ptr(), _addr(bias), packed.data_ptr(), _addr(packed_shared), out.data_ptr(),
+                _addr(topk_idx), _addr(topk_w), workspace.data_ptr(), workspace.numel())
+    _check(lib().mok_moe_few(ctypes.byref(p), ctypes.byref(a), ctypes.byref(cfg) if cfg else None, _stream(stream)),
+           "mok_moe_few")
+    return out
 
 
 # --------------------------------------------------------------------------- 8-bit training context

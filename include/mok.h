@@ -386,6 +386,42 @@ mok_status mok_moe_backward(const mok_problem* p, const mok_bwd_args* a,
                             const mok_config* cfg, mok_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* The whole layer for a few tokens (decoding): routing, expert FFNs, weighted */
+/* sum and shared expert in two kernels.                                       */
+/* ------------------------------------------------------------------------- */
+
+#define MOK_FEW_MAX_TOKENS 128
+#define MOK_FEW_MAX_PAIRS 2048   /* T * k */
+
+typedef struct {
+    const void* x;              /* [T,H] bf16 */
+    const float* W_r;           /* [H,E] */
+    const float* bias;          /* [E] or NULL */
+    const void* packed;         /* routed experts, from mok_pack_weights (the layer's own copy) */
+    const void* packed_shared;  /* shared expert (E=1, BF16) or NULL; needs I_shared > 0 */
+    void* out;                  /* [T,H] bf16; may not overlap x */
+    int32_t* topk_idx;          /* [T,k] or NULL: the routing, as mok_route_layout's */
+    float* topk_w;              /* [T,k] or NULL */
+    void* workspace;            /* mok_few_workspace_size bytes, 256-B aligned, any content */
+    size_t ws_bytes;
+} mok_few_args;
+
+/* Workspace bytes of mok_moe_few on the current device (0: invalid problem, or
+ * more tokens or pairs than the limits above). */
+size_t mok_few_workspace_size(const mok_problem* p, const mok_config* cfg);
+
+/* out[t] = bf16(sum_j w[t,j] * y[t,j] (+ shared[t])): the layer of
+ * mok_route_layout and mok_moe_forward, with the same routing bits and the same
+ * operand roundings (h to BF16, or x and h to MXFP8), but the expert outputs y
+ * stay in fp32 (mok_moe_forward rounds each to BF16), and the sum runs over
+ * experts in ascending order. Bitwise the same in every run with one num_sms.
+ * The second kernel is one cooperative launch with a CTA on each of
+ * cfg->num_sms SMs (0: all); it fails with MOK_ERR_CUDA if they cannot all be
+ * resident. Of cfg only num_sms and timeout_ms are read. Device-side waits are
+ * bounded: mok_device_status on the workspace reports MOK_ERR_TIMEOUT. */
+mok_status mok_moe_few(const mok_problem* p, const mok_few_args* a, const mok_config* cfg, mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* The layer's pre-norm: root-mean-square norm with the residual's addition,   */
 /* and its backward pass. The pages have no counterpart: these stand directly  */
 /* before the layer in every block that uses it.                               */
