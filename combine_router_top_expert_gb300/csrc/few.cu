@@ -1,6 +1,6 @@
 // few.cu - the whole routed layer for a few tokens (T <= 128) in two kernels:
-// router logits, then everything else (top-k, both expert GEMMs, weighted sum,
-// shared expert).
+// the router (logits, top-k), then everything else (both expert GEMMs, weighted
+// sum, shared expert).
 //
 // With few tokens the layer is bound by reading each selected expert's weights
 // once: a 128-row tile of packed weights takes longer to arrive than its
@@ -16,8 +16,9 @@
 // Each phase's K blocks form one sequence that is cut into equal contiguous
 // ranges, one per CTA, so every SM streams the same number of weight bytes at
 // any T. A row tile cut between CTAs goes through fp32 partial sums in the
-// workspace; the last CTA to arrive (an atomic count) adds them in CTA order,
-// so the order of additions, and with it every bit, does not depend on timing.
+// workspace: at the end of the phase each CTA that shares the tile waits for the
+// others' partials and adds up its own part of the token columns, always in CTA
+// order, so no bit depends on timing and the additions are spread over the SMs.
 // Phase 2 multiplies each expert's accumulator by the routing weight in fp32 and
 // adds it up in registers; nothing between h and the output is rounded.
 //
@@ -45,29 +46,40 @@ namespace {
 // ---------------------------------------------------------------------------
 // Kernel 1: router logits in the fixed order of the routing kernels (32 fma
 // chains, chain c over h = 256 i + 8 c + m, then adds at distance 16, 8, 4, 2,
-// 1, then the bias), the MXFP8 rows of x, and the zeroed counters of kernel 2.
+// 1, then the bias), the top-k with its weights, the MXFP8 rows of x, and the
+// zeroed counters of kernel 2.
 //
-// A cluster of 8 CTAs takes 8 tokens x 32 experts; CTA r holds the chains
-// 4r .. 4r+3, i.e. 32 consecutive h of every 256, so its share of W_r and x is
-// contiguous per 256-chunk and all of it (H <= 8192: one pass) is in flight at
-// once. Warp w runs chain 4r + w % 4 for 4 of the tokens, one expert a lane. The
-// chain sums meet in the first CTA's shared memory.
+// A cluster of 8 CTAs takes 8 tokens and all experts, 32 at a time. CTA r holds
+// the chains r, r + 8, r + 16, r + 24, so two levels of the adding tree stay
+// inside it and one value per (token, expert) goes to the first CTA. Warp w runs
+// chain r + 8 (w % 4) for four of the tokens, one expert a lane. The work is a
+// few hundred KB of W_r per CTA: what counts is to have the loads in flight
+// early, so W_r and x stream through a ring of cp.async stages.
 // ---------------------------------------------------------------------------
 constexpr int kLgThreads = 256;
 constexpr int kLgTokens = 8;       // tokens per cluster
 constexpr int kLgCluster = 8;
-constexpr int kLgChunks = 32;      // 256-wide h chunks per pass
+constexpr int kLgChunks = 4;       // 256-wide h chunks per stage
+constexpr int kLgStages = 5;
 constexpr int kLgWBytes = kLgChunks * 32 * 32 * 4;
 constexpr int kLgXBytes = kLgChunks * kLgTokens * 32 * 2;
-constexpr int kLgRedBytes = 32 * kLgTokens * 32 * 4;
-constexpr int kLgSmem = kLgWBytes + kLgXBytes + kLgRedBytes;
+constexpr int kLgStageBytes = kLgWBytes + kLgXBytes;
+// after the ring: the four chains' sums of this CTA, the 8 CTAs' sums (written
+// by all of them in the first one), the logits
+constexpr int kLgPartOffset = kLgStages * kLgStageBytes;
+constexpr int kLgRedOffset = kLgPartOffset + 4 * kLgTokens * 32 * 4;
+constexpr int kLgLogOffset = kLgRedOffset + kLgCluster * kLgTokens * 32 * 4;
+constexpr int kLgSmem = kLgLogOffset + kLgTokens * kMaxE * 4;
 
 struct FewLogitsParams {
     const __nv_bfloat16* x;
     const float* W_r;
     const float* bias;
-    int T, H, E;
-    float* logits;        // [T, E]
+    int T, H, E, k;
+    int32_t* idx;         // [T, k]
+    float* w;             // [T, k]
+    int32_t* topk_idx;    // the caller's copies, or NULL
+    float* topk_w;
     uint8_t* xq;          // MXFP8: [T, H] E4M3, else NULL
     uint8_t* xsf;         // chunk order, one 512-byte chunk per 128 columns
     int* zero;            // status block and counters of kernel 2
@@ -82,106 +94,186 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool va
     const int n = valid ? 4 : 0;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Top-k of one token by one warp (larger logit first, lower expert on ties,
+// -0 = +0): experts lane, lane + 32, ...; keys order like the logits, 0 is
+// "taken". The weights are the softmax over the selected logits.
+__device__ __forceinline__ void few_topk(const float* lg, const FewLogitsParams& p, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    const int nq = ceil_div(p.E, 32);
+    uint32_t key[kMaxE / 32];
+#pragma unroll
+    for (int q = 0; q < kMaxE / 32; ++q) {
+        key[q] = 0;
+        if (q < nq && lane + 32 * q < p.E) {
+            const uint32_t b = __float_as_uint(lg[lane + 32 * q] + 0.0f);
+            key[q] = max(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u), 1u);
+        }
+    }
+    float l0 = 0.f, den = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+        uint32_t best = key[0];
+        int be = lane;
+#pragma unroll
+        for (int q = 1; q < kMaxE / 32; ++q)
+            if (q < nq && key[q] > best) {
+                best = key[q];
+                be = lane + 32 * q;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)be : 0xffffu);
+#pragma unroll
+        for (int q = 0; q < kMaxE / 32; ++q)
+            if (e == lane + 32 * q) key[q] = 0;
+        const float l = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
+        if (j == 0) l0 = l;
+        den += expf(l - l0);   // j ascending; identical in every lane
+        if (lane == 0) {
+            p.idx[t * p.k + j] = e;
+            if (p.topk_idx) p.topk_idx[t * p.k + j] = e;
+        }
+    }
+    __syncwarp();
+    for (int j = lane; j < p.k; j += 32) {
+        const float w = expf(lg[p.idx[t * p.k + j]] - l0) / den;
+        p.w[t * p.k + j] = w;
+        if (p.topk_w) p.topk_w[t * p.k + j] = w;
+    }
+}
 
 __global__ void __cluster_dims__(kLgCluster, 1, 1) __launch_bounds__(kLgThreads)
 few_logits_kernel(const FewLogitsParams p) {
     extern __shared__ __align__(128) unsigned char lg_smem[];
-    float* ws = reinterpret_cast<float*>(lg_smem);                                   // [chunk][32 h][32 experts]
-    unsigned char* xs = lg_smem + kLgWBytes;                                         // [chunk][token][32 h] bf16
-    float* red = reinterpret_cast<float*>(lg_smem + kLgWBytes + kLgXBytes);          // [chain][token][expert]
+    float* part = reinterpret_cast<float*>(lg_smem + kLgPartOffset);   // [chain of four][token][expert]
+    float* red = reinterpret_cast<float*>(lg_smem + kLgRedOffset);     // [CTA][token][expert]
+    float* lg = reinterpret_cast<float*>(lg_smem + kLgLogOffset);      // [token][kMaxE]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)tc::cluster_ctarank();
-    const int e0 = ((int)blockIdx.x / kLgCluster) * 32, t0 = (int)blockIdx.y * kLgTokens;
+    const int t0 = ((int)blockIdx.x / kLgCluster) * kLgTokens;
     const int ntok = min(kLgTokens, p.T - t0);
     const int nchunks = ceil_div(p.H, 256);
-    const int cl = warp & 3, th = warp >> 2;          // chain of this CTA's four, token half
+    const int per = ceil_div(nchunks, kLgChunks);        // stages per 32 experts
+    const int total = per * ceil_div(p.E, 32);
+    const int cl = warp & 3, th = warp >> 2;             // chain of this CTA's four, token half
     const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.W_r) & 15) == 0;
 
     pdl_wait();
     pdl_allow_next();
+
+    // row r (0..31) of a chunk's share: chain rank + 8 (r / 8), h = 256 i + 8 chain + r % 8
+    auto h_of = [&](int i, int r) { return 256 * i + 8 * (rank + 8 * (r >> 3)) + (r & 7); };
+    auto issue = [&](int n) {
+        if (n < total) {
+            const int e0 = (n / per) * 32, c0 = (n % per) * kLgChunks;
+            unsigned char* st = lg_smem + (n % kLgStages) * kLgStageBytes;
+            const uint32_t ws = tc::smem_u32(st), xs = ws + kLgWBytes;
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < kLgChunks; ++i) {   // 32 rows x 8 vectors a chunk
+                    const int r = tid >> 3, v = tid & 7;
+                    const int h = h_of(c0 + i, r), e = e0 + 4 * v;
+                    const bool in = h < p.H && e < p.E;
+                    cp_async16(ws + ((i * 32 + r) * 32 + 4 * v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+                }
+            } else {
+                for (int j = tid; j < kLgChunks * 1024; j += kLgThreads) {
+                    const int i = j >> 10, r = (j >> 5) & 31, v = j & 31;
+                    const int h = h_of(c0 + i, r), e = e0 + v;
+                    const bool in = h < p.H && e < p.E;
+                    cp_async4(ws + ((i * 32 + r) * 32 + v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+                }
+            }
+            if (tid < kLgChunks * kLgTokens * 4) {      // [chunk][token][chain of four][8 h]
+                const int i = tid / (kLgTokens * 4), t = (tid >> 2) & (kLgTokens - 1), v = tid & 3;
+                const int h = h_of(c0 + i, 8 * v);
+                const bool in = h < p.H && t < ntok;
+                cp_async16(xs + ((i * kLgTokens + t) * 32 + 8 * v) * 2, in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
+            }
+        }
+        cp_async_commit();   // one group per stage, empty past the end
+    };
+    for (int n = 0; n < kLgStages - 1; ++n) issue(n);
+
+    // while the first copies are in flight: the counters of kernel 2, and x in
+    // 8 bits (one block of 32 a thread; the bytes of mok_quantize_rows)
+    for (int i = (int)blockIdx.x * kLgThreads + tid; i < p.zero_words; i += (int)gridDim.x * kLgThreads) p.zero[i] = 0;
+    if (p.xq) {
+        const int nb = p.H / 32;
+        for (int j = rank * kLgThreads + tid; j < ntok * nb; j += kLgCluster * kLgThreads) {
+            const int t = t0 + j / nb, b = j % nb;
+            uint4 o0, o1;
+            const uint32_t code = quantize_block32(p.x + (int64_t)t * p.H + b * 32, o0, o1);
+            uint4* dst = reinterpret_cast<uint4*>(p.xq + (int64_t)t * p.H + b * 32);
+            dst[0] = o0;
+            dst[1] = o1;
+            p.xsf[(b >> 2) * 512 + sf_chunk_offset(t, b & 3)] = (uint8_t)code;
+        }
+    }
     tc::cluster_sync();   // every CTA of the cluster runs before any writes to the first one's shared memory
 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 0; c0 < nchunks; c0 += kLgChunks) {
-        const int nc = min(kLgChunks, nchunks - c0);
-        if (c0 > 0) __syncthreads();
-        if (vec) {
-            for (int i = 0; i < nc; ++i) {   // 32 rows x 8 vectors = 256 copies a chunk
-                const int r = tid >> 3, v = tid & 7;
-                const int h = 256 * (c0 + i) + 32 * rank + r, e = e0 + 4 * v;
-                const bool in = h < p.H && e < p.E;
-                cp_async16(tc::smem_u32(ws + (i * 32 + r) * 32 + 4 * v), in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
-            }
-        } else {
-            for (int j = tid; j < nc * 1024; j += kLgThreads) {
-                const int i = j >> 10, r = (j >> 5) & 31, v = j & 31;
-                const int h = 256 * (c0 + i) + 32 * rank + r, e = e0 + v;
-                const bool in = h < p.H && e < p.E;
-                cp_async4(tc::smem_u32(ws + (i * 32 + r) * 32 + v), in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
-            }
-        }
-        for (int j = tid; j < nc * kLgTokens * 4; j += kLgThreads) {
-            const int i = j / (kLgTokens * 4), t = (j >> 2) & (kLgTokens - 1), v = j & 3;
-            const int h = 256 * (c0 + i) + 32 * rank + 8 * v;
-            const bool in = h < p.H && t < ntok;
-            cp_async16(tc::smem_u32(xs + ((i * kLgTokens + t) * 32 + 8 * v) * 2),
-                       in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
-        }
-        if (c0 == 0) {
-            // while the copies are in flight: counters of kernel 2, and x in
-            // 8 bits (one block of 32 a thread; the bytes of mok_quantize_rows)
-            const int cta = ((int)blockIdx.y * (int)gridDim.x + (int)blockIdx.x);
-            for (int i = cta * kLgThreads + tid; i < p.zero_words; i += (int)(gridDim.x * gridDim.y) * kLgThreads)
-                p.zero[i] = 0;
-            if (p.xq && e0 == 0) {
-                const int nb = p.H / 32;
-                for (int j = rank * kLgThreads + tid; j < ntok * nb; j += kLgCluster * kLgThreads) {
-                    const int t = t0 + j / nb, b = j % nb;
-                    uint4 o0, o1;
-                    const uint32_t code = quantize_block32(p.x + (int64_t)t * p.H + b * 32, o0, o1);
-                    uint4* dst = reinterpret_cast<uint4*>(p.xq + (int64_t)t * p.H + b * 32);
-                    dst[0] = o0;
-                    dst[1] = o1;
-                    p.xsf[(b >> 2) * 512 + sf_chunk_offset(t, b & 3)] = (uint8_t)code;
+    for (int n = 0; n < total; ++n) {
+        cp_async_wait<kLgStages - 2>();
+        __syncthreads();              // stage n has landed for every thread; stage n - 1 is consumed
+        issue(n + kLgStages - 1);
+        const int c0 = (n % per) * kLgChunks;
+        const float* ws = reinterpret_cast<const float*>(lg_smem + (n % kLgStages) * kLgStageBytes);
+        const unsigned char* xs = lg_smem + (n % kLgStages) * kLgStageBytes + kLgWBytes;
+#pragma unroll
+        for (int i = 0; i < kLgChunks; ++i) {
+            if (h_of(c0 + i, 8 * cl) < p.H) {
+                float w[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) w[m] = ws[(i * 32 + 8 * cl + m) * 32 + lane];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (4 * th + u < ntok) {
+                        float f[8];
+                        unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + 4 * th + u) * 32 + 8 * cl) * 2), f);
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) acc[u] = fmaf(f[m], w[m], acc[u]);
+                    }
                 }
             }
         }
-        cp_async_wait_all();
-        __syncthreads();
-        for (int i = 0; i < nc; ++i) {
-            if (256 * (c0 + i) + 32 * rank + 8 * cl >= p.H) break;
-            float w[8];
-#pragma unroll
-            for (int m = 0; m < 8; ++m) w[m] = ws[(i * 32 + 8 * cl + m) * 32 + lane];
+        if (n % per == per - 1) {
+            // the tree over the 32 chains: distances 16 and 8 here, 4, 2 and 1
+            // over the CTAs
+            const int e0 = (n / per) * 32;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (4 * th + u < ntok) {
-                    float f[8];
-                    unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + 4 * th + u) * 32 + 8 * cl) * 2), f);
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) acc[u] = fmaf(f[m], w[m], acc[u]);
-                }
+                part[(cl * kLgTokens + 4 * th + u) * 32 + lane] = acc[u];
+                acc[u] = 0.f;
             }
+            __syncthreads();
+            const int o = warp * 32 + lane;             // token = warp
+            constexpr int P = kLgTokens * 32;
+            const float v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
+            const uint32_t dst = tc::mapa_shared(tc::smem_u32(red + rank * P + o), 0);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+            tc::cluster_sync();
+            if (rank == 0) {
+                float s[kLgCluster];
+#pragma unroll
+                for (int c = 0; c < kLgCluster; ++c) s[c] = red[c * P + o];
+#pragma unroll
+                for (int d = kLgCluster / 2; d >= 1; d >>= 1)
+#pragma unroll
+                    for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
+                const int e = e0 + lane;
+                if (e < p.E) lg[warp * kMaxE + e] = p.bias ? s[0] + p.bias[e] : s[0];
+            }
+            if (n + 1 < total) tc::cluster_sync();      // red is read before the next 32 experts' sums arrive
         }
     }
-    const uint32_t dst = tc::mapa_shared(tc::smem_u32(red), 0);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const uint32_t a = dst + (uint32_t)((((4 * rank + cl) * kLgTokens + 4 * th + u) * 32 + lane) * 4);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(acc[u]) : "memory");
-    }
-    tc::cluster_sync();
-    if (rank == 0) {
-        const int t = warp, e = e0 + lane;   // 8 warps: 8 tokens
-        float s[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = red[(c * kLgTokens + t) * 32 + lane];
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-            for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
-        if (t < ntok && e < p.E) p.logits[(int64_t)(t0 + t) * p.E + e] = p.bias ? s[0] + p.bias[e] : s[0];
+    if (rank == 0 && warp < ntok) {
+        __syncwarp();
+        few_topk(lg + warp * kMaxE, p, t0 + warp);
     }
 }
 
@@ -195,9 +287,8 @@ constexpr int kFewEpiBar = 1;     // their named barrier
 struct FewParams {
     int T, H, I, E, k, Is;
     int R1, R2, Rs1;              // packed weight rows per tile: gate/up, down, shared gate/up
-    const float* logits;
-    int32_t* topk_idx;            // outputs, or NULL
-    float* topk_w;
+    const int32_t* idx;           // [T, k] routing of kernel 1
+    const float* w;
     const uint8_t* gu_sf;
     const uint8_t* dn_sf;
     const uint8_t* xsf;
@@ -205,7 +296,7 @@ struct FewParams {
     uint8_t* hsf;                 // [active experts][I / 128] chunks of 512 bytes
     __nv_bfloat16* hs;            // [T, Is]
     float* part;                  // [2 phases][CTAs][2][T][256]
-    int* hready;                  // [E + 1] finished gate/up tiles per active expert (the shared one last)
+    int* hready;                  // [E + 1] finished (gate/up tile, token) rows per active expert (the shared one last)
     int* cnt1;                    // arrivals per gate/up tile
     int* cnt2;                    // arrivals per down tile
     __nv_bfloat16* out;
@@ -221,7 +312,7 @@ struct FewCfg {
     static constexpr int kSf = MX ? 3 * 512 : 0;           // two weight chunks, one token chunk
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kFixed = 1024 /* alignment */ + 512 /* barriers */ + kFewMaxPairs * 5 + 256 * 2 + 2 * 128 * 4;
-    static constexpr int kLimit = 227 * 1024 - 256 /* the kernel's static shared memory */;
+    static constexpr int kLimit = 227 * 1024 - 1024 /* the kernel's static shared memory */;
     static constexpr int kStagesFit = (kLimit - kFixed) / (kStage + kSf);
     static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
     static constexpr int kSfOffset = kStages * kStage;
@@ -252,62 +343,76 @@ struct FewJob {
     int kb, n;       // K blocks kb .. kb + n - 1
     int64_t u0, u1;  // unit range of the whole tile (the partial sums' scope)
     bool last;       // this CTA's last job of the tile
-    bool first;      // and its first
+};
+
+// A row tile that this CTA shares with others, to be finished at the end of
+// the phase.
+struct FewShared {
+    int a, tile, gtile;
+    int c0, c1;      // the CTAs that share it
+    int64_t u0;
 };
 
 __device__ __forceinline__ int64_t few_start(int64_t U, int G, int c) { return U * c / G; }
 __device__ __forceinline__ int few_owner(int64_t U, int G, int64_t u) { return (int)(((u + 1) * G - 1) / U); }
 
-// Calls f(job) for this CTA's jobs in order; stops when it returns false.
+// Calls f(job) for this CTA's jobs of a phase in order; false as soon as f
+// returns false.
+template <typename F>
+__device__ __forceinline__ bool few_jobs_up(const FewWork& w, F&& f) {
+    const int c = (int)blockIdx.x;
+    if (c >= w.G1) return true;
+    int64_t u = few_start(w.U1, w.G1, c);
+    const int64_t end = few_start(w.U1, w.G1, c + 1);
+    const int64_t routed = (int64_t)w.A * w.t1 * w.kb1;
+    FewJob j;
+    j.phase = 0;
+    j.last = true;
+    while (u < end) {
+        const bool sh = u >= routed;
+        const int kbt = sh ? w.kbs1 : w.kb1;
+        const int64_t v = sh ? u - routed : u;
+        const int g = (int)(v / kbt);
+        j.kb = (int)(v % kbt);
+        j.u0 = u - j.kb;
+        j.u1 = j.u0 + kbt;
+        j.n = (int)(min(end, j.u1) - u);
+        j.a = sh ? w.A : g / w.t1;
+        j.tile = sh ? g : g % w.t1;
+        j.gtile = sh ? w.A * w.t1 + g : g;
+        u += j.n;
+        if (!f(j)) return false;
+    }
+    return true;
+}
+template <typename F>
+__device__ __forceinline__ bool few_jobs_down(const FewWork& w, F&& f) {
+    const int c = (int)blockIdx.x;
+    if (c >= w.G2) return true;
+    int64_t u = few_start(w.U2, w.G2, c);
+    const int64_t end = few_start(w.U2, w.G2, c + 1);
+    const int upt = w.A * w.kb2 + w.kbs2;
+    FewJob j;
+    j.phase = 1;
+    while (u < end) {
+        j.tile = (int)(u / upt);
+        j.gtile = j.tile;
+        j.u0 = (int64_t)j.tile * upt;
+        j.u1 = j.u0 + upt;
+        const int r = (int)(u - j.u0);
+        const bool sh = r >= w.A * w.kb2;
+        j.a = sh ? w.A : r / w.kb2;
+        j.kb = sh ? r - w.A * w.kb2 : r % w.kb2;
+        j.n = (int)min((int64_t)((sh ? w.kbs2 : w.kb2) - j.kb), end - u);
+        u += j.n;
+        j.last = u == end || u == j.u1;
+        if (!f(j)) return false;
+    }
+    return true;
+}
 template <typename F>
 __device__ __forceinline__ void few_jobs(const FewWork& w, F&& f) {
-    const int c = (int)blockIdx.x;
-    FewJob j;
-    if (c < w.G1) {
-        int64_t u = few_start(w.U1, w.G1, c);
-        const int64_t end = few_start(w.U1, w.G1, c + 1);
-        const int64_t routed = (int64_t)w.A * w.t1 * w.kb1;
-        j.phase = 0;
-        j.first = j.last = true;
-        while (u < end) {
-            const bool sh = u >= routed;
-            const int kbt = sh ? w.kbs1 : w.kb1;
-            const int64_t v = sh ? u - routed : u;
-            const int g = (int)(v / kbt);
-            j.kb = (int)(v % kbt);
-            j.u0 = u - j.kb;
-            j.u1 = j.u0 + kbt;
-            j.n = (int)(min(end, j.u1) - u);
-            j.a = sh ? w.A : g / w.t1;
-            j.tile = sh ? g : g % w.t1;
-            j.gtile = sh ? w.A * w.t1 + g : g;
-            u += j.n;
-            if (!f(j)) return;
-        }
-    }
-    if (c < w.G2) {
-        int64_t u = few_start(w.U2, w.G2, c);
-        const int64_t end = few_start(w.U2, w.G2, c + 1);
-        const int upt = w.A * w.kb2 + w.kbs2;
-        j.phase = 1;
-        j.first = true;
-        while (u < end) {
-            j.tile = (int)(u / upt);
-            j.gtile = j.tile;
-            j.u0 = (int64_t)j.tile * upt;
-            j.u1 = j.u0 + upt;
-            const int r = (int)(u - j.u0);
-            const bool sh = r >= w.A * w.kb2;
-            j.a = sh ? w.A : r / w.kb2;
-            j.kb = sh ? r - w.A * w.kb2 : r % w.kb2;
-            const int left = (sh ? w.kbs2 : w.kb2) - j.kb;
-            j.n = (int)min((int64_t)left, end - u);
-            u += j.n;
-            j.last = u == end || u == j.u1;
-            if (!f(j)) return;
-            j.first = j.last;
-        }
-    }
+    if (few_jobs_up(w, f)) few_jobs_down(w, f);
 }
 
 __device__ __forceinline__ int few_ld_acquire(const int* p) {
@@ -315,8 +420,8 @@ __device__ __forceinline__ int few_ld_acquire(const int* p) {
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void few_red_release(int* p) {
-    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+__device__ __forceinline__ void few_red_release(int* p, int v) {
+    asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 // Bounded wait until *p >= target (acquire). False: gave up (recorded).
@@ -399,7 +504,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     extern __shared__ __align__(1024) unsigned char few_smem[];
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_hit[kMaxE / 32];
-    __shared__ int s_active, s_last;
+    __shared__ int s_active;
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(few_smem) + 1023) & ~uintptr_t(1023));
     const uint32_t base = tc::smem_u32(smem);
     const uint32_t bar = base + C::kBarOffset;
@@ -437,52 +542,11 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
     __syncthreads();
 
-    // top-k of every token, in each CTA for itself: a warp per token, experts
-    // lane, lane + 32, ...; keys order like the logits (-0 = +0), 0 is "taken"
-    for (int t = warp; t < T; t += kFewThreads / 32) {
-        uint32_t key[kMaxE / 32];
-#pragma unroll
-        for (int q = 0; q < kMaxE / 32; ++q) {
-            const int e = lane + 32 * q;
-            key[q] = 0;
-            if (e < E) {
-                const uint32_t b = __float_as_uint(p.logits[(int64_t)t * E + e] + 0.0f);
-                key[q] = max(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u), 1u);
-            }
-        }
-        float l0 = 0.f, den = 0.f;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = key[0];
-            int be = lane;
-#pragma unroll
-            for (int q = 1; q < kMaxE / 32; ++q)
-                if (key[q] > best) {
-                    best = key[q];
-                    be = lane + 32 * q;
-                }
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-            const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)be : 0xffffu);
-#pragma unroll
-            for (int q = 0; q < kMaxE / 32; ++q)
-                if (e == lane + 32 * q) key[q] = 0;
-            const float l = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
-            if (j == 0) l0 = l;
-            den += expf(l - l0);   // j ascending; identical in every lane
-            if (lane == 0) {
-                s_idx[t * k + j] = (uint8_t)e;
-                s_w[t * k + j] = l;
-                atomicOr(&s_hit[e >> 5], 1u << (e & 31));
-            }
-        }
-        __syncwarp();
-        for (int j = lane; j < k; j += 32) {
-            const float w = expf(s_w[t * k + j] - l0) / den;
-            s_w[t * k + j] = w;
-            if (blockIdx.x == 0) {
-                if (p.topk_idx) p.topk_idx[t * k + j] = s_idx[t * k + j];
-                if (p.topk_w) p.topk_w[t * k + j] = w;
-            }
-        }
+    for (int i = threadIdx.x; i < T * k; i += kFewThreads) {
+        const int e = p.idx[i];
+        s_idx[i] = (uint8_t)e;
+        s_w[i] = p.w[i];
+        atomicOr(&s_hit[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
     if (warp == 0) {   // the active experts, ascending
@@ -576,7 +640,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             few_jobs(w, [&](const FewJob& j) {
                 const bool sh = j.a == w.A;
                 if (j.phase && ready != j.a) {
-                    if (!few_wait_counter(p.hready + j.a, sh ? w.ts1 : w.t1, st, tmo)) return give_up();
+                    if (!few_wait_counter(p.hready + j.a, (sh ? w.ts1 : w.t1) * T, st, tmo)) return give_up();
                     tc::fence_proxy_async_global();
                     ready = j.a;
                 }
@@ -616,31 +680,39 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             few_jobs(w, [&](const FewJob& j) {
                 const bool sh = j.a == w.A;
                 const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
-                const int nb = ceil_div(rows, 128);
+                const bool two = rows > 128;   // two 128-row blocks
                 if (!tc::mbar_wait(acce, acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return give_up();
                 tc::fence_after_sync();
                 for (int i = 0; i < j.n; ++i) {
                     if (!tc::mbar_wait(fullA(s), ph, st, tmo, kSiteMmaFull)) return give_up();
                     if (!tc::mbar_wait(fullB(s), ph, st, tmo, kSiteMmaFull)) return give_up();
                     tc::fence_after_sync();
-                    const uint32_t sf = tmem + (uint32_t)(C::kAccCols + 12 * s);
-                    if constexpr (MX) {
-                        if (!sh) {
-                            for (int b = 0; b < nb; ++b)
-                                tc::tmem_cp_32x128b_warpx4(sf + 4 * b, tc::make_sdesc(sf_tile(s) + 512 * b, 0, 128, tc::kLayoutNone));
-                            tc::tmem_cp_32x128b_warpx4(sf + 8, tc::make_sdesc(sf_tile(s) + 1024, 0, 128, tc::kLayoutNone));
-                        }
-                    }
+                    // descriptors of the stage; K step kk starts 32 bytes (2
+                    // descriptor units) further, row block b 16 KB
+                    const uint64_t ad = tc::make_sdesc(a_tile(s), 16, 1024, tc::kLayoutSW128);
+                    const uint64_t bd = tc::make_sdesc(b_tile(s), 16, 1024, tc::kLayoutSW128);
+                    const uint32_t on = i > 0 ? 1u : 0u;
+                    if (MX && !sh) {
+                        const uint32_t sf = tmem + (uint32_t)(C::kAccCols + 12 * s);
+                        const uint64_t sd = tc::make_sdesc(sf_tile(s), 0, 128, tc::kLayoutNone);
+                        tc::tmem_cp_32x128b_warpx4(sf, sd);
+                        if (two) tc::tmem_cp_32x128b_warpx4(sf + 4, sd + 32);
+                        tc::tmem_cp_32x128b_warpx4(sf + 8, sd + 64);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t bd = tc::make_sdesc(b_tile(s) + kk * 32, 16, 1024, tc::kLayoutSW128);
-                        const uint32_t on = (i > 0 || kk > 0) ? 1u : 0u;
-                        for (int b = 0; b < nb; ++b) {
-                            const uint64_t ad = tc::make_sdesc(a_tile(s) + b * 16384 + kk * 32, 16, 1024, tc::kLayoutSW128);
-                            if (MX && !sh)
-                                tc::mma_mxf8(tmem + b * NT, ad, bd, tc::idesc_mxf8(128, NT, kk, kk), sf + 4 * b, sf + 8, on);
-                            else
-                                tc::mma_bf16(tmem + b * NT, ad, bd, tc::idesc_bf16(128, NT, false, false), on);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            tc::mma_mxf8(tmem, ad + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk), sf, sf + 8,
+                                         kk ? 1u : on);
+                            if (two)
+                                tc::mma_mxf8(tmem + NT, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk),
+                                             sf + 4, sf + 8, kk ? 1u : on);
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            tc::mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false), kk ? 1u : on);
+                            if (two)
+                                tc::mma_bf16(tmem + NT, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false),
+                                             kk ? 1u : on);
                         }
                     }
                     issued = true;
@@ -655,7 +727,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     } else {
         // ------------------------------------------------------------ epilogue
         constexpr int NC = NT / 2;                  // token columns of a thread
-        constexpr int CH = NC < 16 ? NC : 16;       // columns at a time
+        constexpr int CH = NC == 8 || NC == 64 ? 8 : 16;   // columns at a time (NC = 64: what the registers allow)
         const int q = warp & 3;                     // TMEM lane quadrant of this warp
         const int half = (warp - 3) >> 2;
         const int et = threadIdx.x - 96;            // 0 .. 255
@@ -669,100 +741,165 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < NC; ++i) acc[0][i] = acc[1][i] = 0.f;
 
-        auto slot = [&](int phase, int c, int64_t u0, int64_t U, int G) -> float* {
-            const int which = few_start(U, G, c) >= u0 ? 0 : 1;
-            return p.part + (((int64_t)phase * gridDim.x + c) * 2 + which) * (256 * (int64_t)T);
+        // this CTA's two shared tiles of a phase: the one its range starts
+        // in (0) and the one it ends in (1)
+        FewShared pend[2];
+        int n_pend = 0;
+        const int64_t part_stride = 256 * (int64_t)T;
+        auto slots = [&](int phase) { return p.part + (int64_t)phase * gridDim.x * 2 * part_stride; };
+        // CTA c's partial of a tile whose first unit is u0: only the first
+        // sharer may have started before the tile
+        auto slot_of = [&](int phase, int c, bool began_before) {
+            return slots(phase) + (2 * (int64_t)c + (began_before ? 1 : 0)) * part_stride;
         };
-        // SwiGLU of CH columns: v[0], v[1] are the tile's two row blocks
-        auto store_h = [&](const FewJob& j, int cc, const float (&v0)[CH], const float (&v1)[CH]) {
-            const bool sh = j.a == w.A;
+
+        // SwiGLU of one token column: v0, v1 are this thread's values in the
+        // tile's two row blocks (all lanes of the warp call it)
+        auto store_h = [&](int a, int tile, int t, float v0, float v1) {
+            const bool sh = a == w.A;
             if (MX && !sh) {
                 // gate rows 0..127, up rows 128..255 of the same features
-                uint8_t* hq = static_cast<uint8_t*>(p.h);
-                const int f = j.tile * 128 + row;
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int t = col0 + cc + i;
-                    if (t < T) {
-                        const float hv = silu_f(v0[i]) * v1[i];
-                        const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(hv)));
-                        const uint32_t code = e8m0_code(__uint_as_float(am));
-                        hq[((int64_t)j.a * T + t) * p.I + f] = (uint8_t)f32x2_to_e4m3x2(hv * e8m0_inv_scale(code), 0.f);
-                        if (lane == 0)
-                            p.hsf[((int64_t)j.a * (p.I / 128) + j.tile) * 512 + sf_chunk_offset(t, q)] = (uint8_t)code;
-                    }
-                }
+                const float hv = silu_f(v0) * v1;
+                const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(hv)));
+                const uint32_t code = e8m0_code(__uint_as_float(am));
+                const int64_t r = (int64_t)a * T + t;
+                static_cast<uint8_t*>(p.h)[r * p.I + tile * 128 + row] =
+                    (uint8_t)f32x2_to_e4m3x2(hv * e8m0_inv_scale(code), 0.f);
+                if (lane == 0) p.hsf[((int64_t)a * (p.I / 128) + tile) * 512 + sf_chunk_offset(t, q)] = (uint8_t)code;
             } else {
-                // lanes 0-15 gate, 16-31 up of the same 16 features: the lower
-                // half forms the first CH/2 columns, the upper half the others
+                // lanes 0-15 hold gate rows, 16-31 the up rows of the same 16
+                // features: the lower half forms h of the first row block, the
+                // upper half that of the second
                 const int rows = sh ? p.Rs1 : p.R1, ld = sh ? p.Is : p.I;
-                __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)j.a * T * p.I;
                 const bool lower = lane < 16;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (128 * b >= rows) continue;
-                    const int f = j.tile * (rows / 2) + 64 * b + 16 * q + (lane & 15);
-#pragma unroll
-                    for (int i = 0; i < CH / 2; ++i) {
-                        const float lo = b ? v1[i] : v0[i], hi = b ? v1[CH / 2 + i] : v0[CH / 2 + i];
-                        const float other = __shfl_xor_sync(0xffffffffu, lower ? hi : lo, 16);
-                        const int t = col0 + cc + (lower ? i : CH / 2 + i);
-                        const float hv = silu_f(lower ? lo : other) * (lower ? other : hi);
-                        if (t < T) hb[(int64_t)t * ld + f] = __float2bfloat16_rn(hv);
-                    }
+                const float other = __shfl_xor_sync(0xffffffffu, lower ? v1 : v0, 16);
+                const float hv = silu_f(lower ? v0 : other) * (lower ? other : v1);
+                if (lower || rows > 128) {
+                    __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)a * T * p.I;
+                    const int f = tile * (rows / 2) + (lower ? 0 : 64) + 16 * q + (lane & 15);
+                    hb[(int64_t)t * ld + f] = __float2bfloat16_rn(hv);
                 }
             }
         };
-        // write a partial tile of CH columns, or add up all of them
-        auto put_part = [&](float* dst, int nb, int cc, const float (&v0)[CH], const float (&v1)[CH]) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int t = col0 + cc + i;
-                if (t < T) {
-                    __stcg(dst + (int64_t)t * 256 + row, v0[i]);
-                    if (nb > 1) __stcg(dst + (int64_t)t * 256 + 128 + row, v1[i]);
-                }
-            }
+        auto store_out = [&](int tile, int t, float v0, float v1) {
+            __nv_bfloat16* o = p.out + (int64_t)t * p.H + tile * p.R2;
+            o[row] = __float2bfloat16_rn(v0);
+            if (128 + row < p.R2) o[128 + row] = __float2bfloat16_rn(v1);
         };
-        // every thread's partial is written: count this CTA in; true in the last one
-        auto arrive_last = [&](int* cnt, int n) {
+        // n token rows of an expert's h tile are written: publish them
+        auto publish_h = [&](int a, int n) {
+            __threadfence();
+            tc::fence_proxy_async_global();
+            epi_sync();
+            if (et == 0) few_red_release(p.hready + a, n);
+        };
+        // this CTA's partial of a shared tile is written: count it in and
+        // remember the tile
+        auto share = [&](const FewJob& j, int c0, int c1) {
             epi_sync();
             if (et == 0) {
                 __threadfence();
-                s_last = atomicAdd(cnt, 1) == n - 1;
-                __threadfence();
+                few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
             }
-            epi_sync();
-            return s_last != 0;
+            const FewShared f{j.a, j.tile, j.gtile, c0, c1, j.u0};
+            if (n_pend == 0) pend[0] = f;
+            else pend[1] = f;
+            ++n_pend;
         };
-        auto sum_parts = [&](int phase, const FewJob& j, int64_t U, int G, int c0, int c1, int nb, int cc, float (&v0)[CH],
-                             float (&v1)[CH]) {
+        // end of a phase: of each shared tile, sharer i of n adds up the
+        // partials of the tokens T i / n .. T (i + 1) / n in CTA order
+        auto finish = [&](int phase) {
+            const int64_t U = phase ? w.U2 : w.U1;
+            const int G = phase ? w.G2 : w.G1;
+#pragma unroll 1
+            for (int i = 0; i < n_pend; ++i) {
+                const FewShared f = i == 0 ? pend[0] : pend[1];
+                const int n = f.c1 - f.c0 + 1, me = c_me - f.c0;
+                const int ta = T * me / n, tb = T * (me + 1) / n;
+                if (ta == tb) continue;
+                bool ok = true;
+                if (et == 0) ok = few_wait_counter((phase ? p.cnt2 : p.cnt1) + f.gtile, n, st, tmo);
+                if (!epi_and(ok)) return false;
+                __threadfence();
+                const int rows = phase ? p.R2 : f.a == w.A ? p.Rs1 : p.R1;
+                const bool two = rows > 128;
+                const int lead = few_start(U, G, f.c0) < f.u0 ? 1 : 0;
+                const float* src0 = slots(phase) + (2 * (int64_t)f.c0 + lead) * part_stride + row;
+                const float* src = slots(phase) + 2 * (int64_t)f.c0 * part_stride + row;
+#pragma unroll 1
+                for (int t0 = ta + half; t0 < tb; t0 += 8) {
+                    float v0[4], v1[4];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) v0[i] = v1[i] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-                const float* src = slot(phase, c, j.u0, U, G);
+                    for (int u = 0; u < 4; ++u) {
+                        const int t = t0 + 2 * u;
+                        v0[u] = t < tb ? __ldcg(src0 + t * 256) : 0.f;
+                        v1[u] = t < tb && two ? __ldcg(src0 + t * 256 + 128) : 0.f;
+                    }
+#pragma unroll 4
+                    for (int c = 1; c < n; ++c) {
+                        const float* sc = src + 2 * (int64_t)c * part_stride;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = t0 + 2 * u;
+                            if (t < tb) {
+                                v0[u] += __ldcg(sc + t * 256);
+                                if (two) v1[u] += __ldcg(sc + t * 256 + 128);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int t = t0 + 2 * u;
+                        if (t < tb) {
+                            if (phase) store_out(f.tile, t, v0[u], v1[u]);
+                            else store_h(f.a, f.tile, t, v0[u], v1[u]);
+                        }
+                    }
+                }
+                if (!phase) publish_h(f.a, tb - ta);
+            }
+            n_pend = 0;
+            return true;
+        };
+
+        bool ok = few_jobs_up(w, [&](const FewJob& j) {
+            const int c0 = few_owner(w.U1, w.G1, j.u0), c1 = few_owner(w.U1, w.G1, j.u1 - 1);
+            const bool whole = c0 == c1;
+            const bool two = (j.a == w.A ? p.Rs1 : p.R1) > 128;
+            float* mine = slot_of(0, c_me, few_start(w.U1, w.G1, c_me) < j.u0);
+            if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
+            ph ^= 1u;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int cc = 0; cc < NC && col0 + cc < T; cc += CH) {
+                float v0[CH], v1[CH];
+                few_tmem_ld<CH>(tq + cc, v0);
+                few_tmem_ld<CH>(tq + NT + cc, v1);
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
                     const int t = col0 + cc + i;
                     if (t < T) {
-                        v0[i] += __ldcg(src + (int64_t)t * 256 + row);
-                        if (nb > 1) v1[i] += __ldcg(src + (int64_t)t * 256 + 128 + row);
+                        if (whole) {
+                            store_h(j.a, j.tile, t, v0[i], v1[i]);
+                        } else {
+                            __stcg(mine + t * 256 + row, v0[i]);
+                            if (two) __stcg(mine + t * 256 + 128 + row, v1[i]);
+                        }
                     }
                 }
             }
-        };
-
-        few_jobs(w, [&](const FewJob& j) {
-            const bool sh = j.a == w.A;
-            const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
-            const int nb = ceil_div(rows, 128);
-            const int64_t U = j.phase ? w.U2 : w.U1;
-            const int G = j.phase ? w.G2 : w.G1;
-            const int c0 = few_owner(U, G, j.u0), c1 = few_owner(U, G, j.u1 - 1);
-            if (j.phase && et < T) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(acce);
+            if (whole) publish_h(j.a, T);
+            else share(j, c0, c1);
+            return true;
+        });
+        ok = ok && finish(0);
+        ok = ok && few_jobs_down(w, [&](const FewJob& j) {
+            if (et < T) {
                 // this expert's routing weights per token; -1: not selected
                 float wt = -1.f;
-                if (sh) wt = 1.f;
+                if (j.a == w.A) wt = 1.f;
                 else
                     for (int i = 0; i < k; ++i)
                         if (s_idx[et * k + i] == s_act[j.a]) wt = s_w[et * k + i];
@@ -771,43 +908,11 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
             ph ^= 1u;
             tc::fence_after_sync();
-            if (j.phase == 0) {
-                const bool whole = c0 == c1;
-                float* mine = slot(0, c_me, j.u0, U, G);
-#pragma unroll 1
-                for (int cc = 0; cc < NC; cc += CH) {
-                    float v0[CH], v1[CH];
-                    few_tmem_ld<CH>(tq + cc, v0);
-                    few_tmem_ld<CH>(tq + NT + cc, v1);
-                    if (col0 + cc < T) {
-                        if (whole) store_h(j, cc, v0, v1);
-                        else put_part(mine, nb, cc, v0, v1);
-                    }
-                }
-                tc::fence_before_sync();
-                tc::mbar_arrive(acce);
-                bool done = whole;
-                if (!whole && arrive_last(p.cnt1 + j.gtile, c1 - c0 + 1)) {
-                    done = true;
-#pragma unroll 1
-                    for (int cc = 0; cc < NC; cc += CH) {
-                        if (col0 + cc >= T) break;
-                        float v0[CH], v1[CH];
-                        sum_parts(0, j, U, G, c0, c1, nb, cc, v0, v1);
-                        store_h(j, cc, v0, v1);
-                    }
-                }
-                if (done) {   // publish the tile of h
-                    __threadfence();
-                    tc::fence_proxy_async_global();
-                    epi_sync();
-                    if (et == 0) few_red_release(p.hready + j.a);
-                }
-            } else {
-                const float* wr = s_row + wbuf * 128 + col0;
-                wbuf ^= 1;
+            const float* wr = s_row + wbuf * 128 + col0;
+            wbuf ^= 1;
 #pragma unroll
-                for (int cc = 0; cc < NC; cc += CH) {
+            for (int cc = 0; cc < NC; cc += CH) {
+                if (col0 + cc < T) {
                     float v0[CH], v1[CH];
                     few_tmem_ld<CH>(tq + cc, v0);
                     few_tmem_ld<CH>(tq + NT + cc, v1);
@@ -820,47 +925,32 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         }
                     }
                 }
-                tc::fence_before_sync();
-                tc::mbar_arrive(acce);
-                if (j.last) {
-                    const bool whole = c0 == c1;
-                    auto store_out = [&](int cc, const float (&v0)[CH], const float (&v1)[CH]) {
+            }
+            tc::fence_before_sync();
+            tc::mbar_arrive(acce);
+            if (j.last) {
+                const int c0 = few_owner(w.U2, w.G2, j.u0), c1 = few_owner(w.U2, w.G2, j.u1 - 1);
+                const bool whole = c0 == c1;
+                const bool two = p.R2 > 128;
+                float* mine = slot_of(1, c_me, few_start(w.U2, w.G2, c_me) < j.u0);
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const int t = col0 + cc + i;
-                            if (t < T) {
-                                __nv_bfloat16* o = p.out + (int64_t)t * p.H + j.tile * rows;
-                                o[row] = __float2bfloat16_rn(v0[i]);
-                                if (128 + row < rows) o[128 + row] = __float2bfloat16_rn(v1[i]);
-                            }
-                        }
-                    };
-                    float* mine = slot(1, c_me, j.u0, U, G);
-#pragma unroll
-                    for (int cc = 0; cc < NC; cc += CH) {
-                        float v0[CH], v1[CH];
-#pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            v0[i] = acc[0][cc + i];
-                            v1[i] = acc[1][cc + i];
-                            acc[0][cc + i] = acc[1][cc + i] = 0.f;
-                        }
-                        if (whole) store_out(cc, v0, v1);
-                        else put_part(mine, nb, cc, v0, v1);
-                    }
-                    if (!whole && arrive_last(p.cnt2 + j.gtile, c1 - c0 + 1)) {
-#pragma unroll 1
-                        for (int cc = 0; cc < NC; cc += CH) {
-                            if (col0 + cc >= T) break;
-                            float v0[CH], v1[CH];
-                            sum_parts(1, j, U, G, c0, c1, nb, cc, v0, v1);
-                            store_out(cc, v0, v1);
+                for (int i = 0; i < NC; ++i) {
+                    const int t = col0 + i;
+                    if (t < T) {
+                        if (whole) {
+                            store_out(j.tile, t, acc[0][i], acc[1][i]);
+                        } else {
+                            __stcg(mine + t * 256 + row, acc[0][i]);
+                            if (two) __stcg(mine + t * 256 + 128 + row, acc[1][i]);
                         }
                     }
+                    acc[0][i] = acc[1][i] = 0.f;
                 }
+                if (!whole) share(j, c0, c1);
             }
             return true;
         });
+        if (ok) finish(1);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -871,7 +961,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 int few_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
 struct FewLayout {
-    size_t counters, logits, xq, xsf, h, hsf, hs, part, total;
+    size_t counters, idx, w, xq, xsf, h, hsf, hs, part, total;
     int n_counters, n1;   // ints: E + 1 ready counts, n1 gate/up tiles, down tiles
 };
 
@@ -887,7 +977,8 @@ FewLayout few_layout(const mok_problem* p, int ctas) {
     L.n_counters = p->E + 1 + L.n1 + (int)(H / r2);
     size_t o = kStatusBytes;
     L.counters = o; o += align_up((int64_t)L.n_counters * 4, 256);
-    L.logits = o; o += align_up(T * p->E * 4, 256);
+    L.idx = o; o += align_up(T * p->k * 4, 256);
+    L.w = o; o += align_up(T * p->k * 4, 256);
     L.xq = o; if (mx) o += align_up(T * H, 256);
     L.xsf = o; if (mx) o += H / 128 * 512;
     L.h = o; o += align_up(act * T * I * (mx ? 1 : 2), 256);
@@ -946,7 +1037,11 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     lp.T = T;
     lp.H = H;
     lp.E = E;
-    lp.logits = reinterpret_cast<float*>(ws + L.logits);
+    lp.k = q->k;
+    lp.idx = reinterpret_cast<int32_t*>(ws + L.idx);
+    lp.w = reinterpret_cast<float*>(ws + L.w);
+    lp.topk_idx = a.topk_idx;
+    lp.topk_w = a.topk_w;
     lp.xq = mx ? reinterpret_cast<uint8_t*>(ws + L.xq) : nullptr;
     lp.xsf = mx ? reinterpret_cast<uint8_t*>(ws + L.xsf) : nullptr;
     lp.zero = reinterpret_cast<int*>(ws);
@@ -957,9 +1052,8 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     p.R1 = gu_rows(I);
     p.R2 = down_tile_n(H, mx);
     p.Rs1 = Is ? gu_rows(Is) : 0;
-    p.logits = lp.logits;
-    p.topk_idx = a.topk_idx;
-    p.topk_w = a.topk_w;
+    p.idx = lp.idx;
+    p.w = lp.w;
     p.gu_sf = a.gu_sf;
     p.dn_sf = a.dn_sf;
     p.xsf = lp.xsf;
@@ -991,7 +1085,7 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     if (!ok) return cudaErrorInvalidValue;
 
     ensure_smem_attr(reinterpret_cast<const void*>(few_logits_kernel), kLgSmem);
-    cudaError_t e = launch_after(few_logits_kernel, dim3(kLgCluster * ceil_div(E, 32), ceil_div(T, kLgTokens)),
+    cudaError_t e = launch_after(few_logits_kernel, dim3(kLgCluster * ceil_div(T, kLgTokens)),
                                  dim3(kLgThreads), kLgSmem, s, lp);
     if (e != cudaSuccess) return e;
     return mx ? run_ffn<true>(tm, p, c.num_sms, s) : run_ffn<false>(tm, p, c.num_sms, s);
