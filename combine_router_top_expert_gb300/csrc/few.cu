@@ -737,9 +737,6 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const int c_me = (int)blockIdx.x;
         uint32_t ph = 0;
         int wbuf = 0;
-        float acc[2][NC];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) acc[0][i] = acc[1][i] = 0.f;
 
         // this CTA's two shared tiles of a phase: the one its range starts
         // in (0) and the one it ends in (1)
@@ -821,38 +818,74 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 if (et == 0) ok = few_wait_counter((phase ? p.cnt2 : p.cnt1) + f.gtile, n, st, tmo);
                 if (!epi_and(ok)) return false;
                 __threadfence();
-                const int rows = phase ? p.R2 : f.a == w.A ? p.Rs1 : p.R1;
-                const bool two = rows > 128;
+                const bool sh = f.a == w.A;
+                const int rows = phase ? p.R2 : sh ? p.Rs1 : p.R1;
+                // a warp per token; this lane's two groups of four rows: down 8
+                // consecutive rows, gate/up the gate and up rows of 4 features
+                const bool il16 = !MX || sh;
+                const int ra = phase ? 8 * lane : il16 ? 32 * (lane >> 2) + 4 * (lane & 3) : 4 * lane;
+                const int rb = phase ? ra + 4 : il16 ? ra + 16 : 128 + ra;
+                const bool in = rb < rows;
                 const int lead = few_start(U, G, f.c0) < f.u0 ? 1 : 0;
-                const float* src0 = slots(phase) + (2 * (int64_t)f.c0 + lead) * part_stride + row;
-                const float* src = slots(phase) + 2 * (int64_t)f.c0 * part_stride + row;
+                const float* src = slots(phase) + 2 * (int64_t)f.c0 * part_stride;
+                constexpr int TU = 4;                 // tokens in flight per warp
 #pragma unroll 1
-                for (int t0 = ta + half; t0 < tb; t0 += 8) {
-                    float v0[4], v1[4];
+                for (int t0 = ta + (et >> 5); t0 < tb; t0 += 8 * TU) {
+                    float va[TU][4], vb[TU][4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int t = t0 + 2 * u;
-                        v0[u] = t < tb ? __ldcg(src0 + t * 256) : 0.f;
-                        v1[u] = t < tb && two ? __ldcg(src0 + t * 256 + 128) : 0.f;
-                    }
-#pragma unroll 4
-                    for (int c = 1; c < n; ++c) {
-                        const float* sc = src + 2 * (int64_t)c * part_stride;
+                    for (int u = 0; u < TU; ++u)
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int t = t0 + 2 * u;
-                            if (t < tb) {
-                                v0[u] += __ldcg(sc + t * 256);
-                                if (two) v1[u] += __ldcg(sc + t * 256 + 128);
+                        for (int r = 0; r < 4; ++r) va[u][r] = vb[u][r] = 0.f;
+#pragma unroll 2
+                    for (int c = 0; c < n; ++c) {
+                        const float* sc = src + (2 * (int64_t)c + (c == 0 ? lead : 0)) * part_stride;
+                        float4 x[TU], y[TU];
+#pragma unroll
+                        for (int u = 0; u < TU; ++u) {
+                            const int t = t0 + 8 * u;
+                            x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (t < tb && in) {
+                                x[u] = __ldcg(reinterpret_cast<const float4*>(sc + t * 256 + ra));
+                                y[u] = __ldcg(reinterpret_cast<const float4*>(sc + t * 256 + rb));
                             }
+                        }
+#pragma unroll
+                        for (int u = 0; u < TU; ++u) {
+                            va[u][0] += x[u].x; va[u][1] += x[u].y; va[u][2] += x[u].z; va[u][3] += x[u].w;
+                            vb[u][0] += y[u].x; vb[u][1] += y[u].y; vb[u][2] += y[u].z; vb[u][3] += y[u].w;
                         }
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int t = t0 + 2 * u;
-                        if (t < tb) {
-                            if (phase) store_out(f.tile, t, v0[u], v1[u]);
-                            else store_h(f.a, f.tile, t, v0[u], v1[u]);
+                    for (int u = 0; u < TU; ++u) {
+                        const int t = t0 + 8 * u;
+                        if (t >= tb) break;
+                        if (phase) {
+                            if (in)
+                                *reinterpret_cast<uint4*>(p.out + (int64_t)t * p.H + f.tile * rows + ra) =
+                                    make_uint4(pack_bf16x2(va[u][0], va[u][1]), pack_bf16x2(va[u][2], va[u][3]),
+                                               pack_bf16x2(vb[u][0], vb[u][1]), pack_bf16x2(vb[u][2], vb[u][3]));
+                            continue;
+                        }
+                        float hv[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) hv[r] = silu_f(va[u][r]) * vb[u][r];
+                        if (il16) {
+                            __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)f.a * T * p.I;
+                            if (in)
+                                *reinterpret_cast<uint2*>(hb + (int64_t)t * (sh ? p.Is : p.I) + f.tile * (rows / 2) + 4 * lane) =
+                                    make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
+                        } else {
+                            float am = fmaxf(fmaxf(fabsf(hv[0]), fabsf(hv[1])), fmaxf(fabsf(hv[2]), fabsf(hv[3])));
+#pragma unroll
+                            for (int d = 4; d >= 1; d >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, d));
+                            const uint32_t code = e8m0_code(am);
+                            const float inv = e8m0_inv_scale(code);
+                            const int64_t r = (int64_t)f.a * T + t;
+                            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + r * p.I + f.tile * 128 + 4 * lane) =
+                                f32x2_to_e4m3x2(hv[0] * inv, hv[1] * inv) | (f32x2_to_e4m3x2(hv[2] * inv, hv[3] * inv) << 16);
+                            if ((lane & 7) == 0)
+                                p.hsf[((int64_t)f.a * (p.I / 128) + f.tile) * 512 + sf_chunk_offset(t, lane >> 3)] =
+                                    (uint8_t)code;
                         }
                     }
                 }
@@ -895,6 +928,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             return true;
         });
         ok = ok && finish(0);
+        float acc[2][NC];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) acc[0][i] = acc[1][i] = 0.f;
         ok = ok && few_jobs_down(w, [&](const FewJob& j) {
             if (et < T) {
                 // this expert's routing weights per token; -1: not selected
