@@ -162,6 +162,9 @@ few_logits_kernel(const FewLogitsParams p) {
     const int cl = warp & 3, th = warp >> 2;             // chain of this CTA's four, token half
     const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.W_r) & 15) == 0;
 
+    // every CTA of the cluster runs before any writes to the first one's shared
+    // memory: arrive here, wait below
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_wait();
     pdl_allow_next();
 
@@ -214,7 +217,7 @@ few_logits_kernel(const FewLogitsParams p) {
             p.xsf[(b >> 2) * 512 + sf_chunk_offset(t, b & 3)] = (uint8_t)code;
         }
     }
-    tc::cluster_sync();   // every CTA of the cluster runs before any writes to the first one's shared memory
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int n = 0; n < total; ++n) {
@@ -281,6 +284,11 @@ few_logits_kernel(const FewLogitsParams p) {
 // Kernel 2
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 352;
+// Units that a CTA gets at least: a shorter range costs more in shared tiles
+// than it saves in streaming (H = 2048, I = 512, 8 MXFP8 experts, 128 tokens: 61
+// us at 1, 57 at 2, 45 at 4, 52 at 8; H = 640, I = 1024, 2 tokens: 33.7, 33.6,
+// 31.4, 34.9; layers that fill every SM do not change).
+constexpr int kFewMinUnits = 4;
 constexpr int kFewEpi = 256;      // epilogue threads
 constexpr int kFewEpiBar = 1;     // their named barrier
 
@@ -542,6 +550,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
     __syncthreads();
 
+    pdl_wait();   // the routing, the MXFP8 rows and the zeroed counters are kernel 1's
     for (int i = threadIdx.x; i < T * k; i += kFewThreads) {
         const int e = p.idx[i];
         s_idx[i] = (uint8_t)e;
@@ -574,8 +583,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     w.kbs2 = p.Is / 64;
     w.U1 = (int64_t)w.A * w.t1 * w.kb1 + (int64_t)w.ts1 * w.kbs1;
     w.U2 = (int64_t)w.t2 * (w.A * w.kb2 + w.kbs2);
-    w.G1 = (int)min((int64_t)gridDim.x, w.U1);
-    w.G2 = (int)min((int64_t)gridDim.x, w.U2);
+    w.G1 = (int)min((int64_t)gridDim.x, max((int64_t)1, w.U1 / kFewMinUnits));
+    w.G2 = (int)min((int64_t)gridDim.x, max((int64_t)1, w.U2 / kFewMinUnits));
 
     if (warp == 0) {
         // ------------------------------------------------------------ weights
@@ -783,9 +792,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             o[row] = __float2bfloat16_rn(v0);
             if (128 + row < p.R2) o[128 + row] = __float2bfloat16_rn(v1);
         };
-        // n token rows of an expert's h tile are written: publish them
+        // n token rows of an expert's h tile are written (their readers are TMA
+        // loads): publish them. The barrier and the release order every
+        // thread's writes before the count.
         auto publish_h = [&](int a, int n) {
-            __threadfence();
             tc::fence_proxy_async_global();
             epi_sync();
             if (et == 0) few_red_release(p.hready + a, n);
@@ -794,10 +804,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         // remember the tile
         auto share = [&](const FewJob& j, int c0, int c1) {
             epi_sync();
-            if (et == 0) {
-                __threadfence();
-                few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
-            }
+            if (et == 0) few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
             const FewShared f{j.a, j.tile, j.gtile, c0, c1, j.u0};
             if (n_pend == 0) pend[0] = f;
             else pend[1] = f;
@@ -817,7 +824,6 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 bool ok = true;
                 if (et == 0) ok = few_wait_counter((phase ? p.cnt2 : p.cnt1) + f.gtile, n, st, tmo);
                 if (!epi_and(ok)) return false;
-                __threadfence();
                 const bool sh = f.a == w.A;
                 const int rows = phase ? p.R2 : sh ? p.Rs1 : p.R1;
                 // a warp per token; this lane's two groups of four rows: down 8
@@ -1031,15 +1037,17 @@ cudaError_t run_ffn(const CUtensorMap* tm, const FewParams& p, int grid, cudaStr
     auto kern = few_ffn_kernel<MX, NT>;
     ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmem);
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], tm[6], tm[7], p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
