@@ -49,27 +49,29 @@ namespace {
 // 1, then the bias), the top-k with its weights, the MXFP8 rows of x, and the
 // zeroed counters of kernel 2.
 //
-// A cluster of 8 CTAs takes 8 tokens and all experts, 32 at a time. CTA r holds
-// the chains r, r + 8, r + 16, r + 24, so two levels of the adding tree stay
-// inside it and one value per (token, expert) goes to the first CTA. Warp w runs
-// chain r + 8 (w % 4) for four of the tokens, one expert a lane. The work is a
-// few hundred KB of W_r per CTA: what counts is to have the loads in flight
-// early, so W_r and x stream through a ring of cp.async stages.
+// A cluster of 8 CTAs takes 8 tokens x 32 experts. CTA r holds the chains r,
+// r + 8, r + 16, r + 24, so two levels of the adding tree stay inside it and one
+// value per (token, expert) goes to the first CTA. Warp w runs chain r + 8 (w %
+// 4) for four of the tokens, one expert a lane. The work is about 100 KB of W_r
+// per CTA: what counts is to have the loads in flight early, so W_r and x stream
+// through a ring of cp.async stages that holds H <= 8192 whole. With more than 32
+// experts the clusters of a token group count themselves in, and the last one
+// takes the top-k from the logits of all.
 // ---------------------------------------------------------------------------
 constexpr int kLgThreads = 256;
 constexpr int kLgTokens = 8;       // tokens per cluster
 constexpr int kLgCluster = 8;
 constexpr int kLgChunks = 4;       // 256-wide h chunks per stage
-constexpr int kLgStages = 5;
 constexpr int kLgWBytes = kLgChunks * 32 * 32 * 4;
 constexpr int kLgXBytes = kLgChunks * kLgTokens * 32 * 2;
 constexpr int kLgStageBytes = kLgWBytes + kLgXBytes;
 // after the ring: the four chains' sums of this CTA, the 8 CTAs' sums (written
 // by all of them in the first one), the logits
-constexpr int kLgPartOffset = kLgStages * kLgStageBytes;
-constexpr int kLgRedOffset = kLgPartOffset + 4 * kLgTokens * 32 * 4;
-constexpr int kLgLogOffset = kLgRedOffset + kLgCluster * kLgTokens * 32 * 4;
-constexpr int kLgSmem = kLgLogOffset + kLgTokens * kMaxE * 4;
+constexpr int kLgPartBytes = 4 * kLgTokens * 32 * 4;
+constexpr int kLgRedBytes = kLgCluster * kLgTokens * 32 * 4;
+constexpr int lg_smem_bytes(int stages) {
+    return stages * kLgStageBytes + kLgPartBytes + kLgRedBytes + kLgTokens * kMaxE * 4;
+}
 
 struct FewLogitsParams {
     const __nv_bfloat16* x;
@@ -80,6 +82,8 @@ struct FewLogitsParams {
     float* w;             // [T, k]
     int32_t* topk_idx;    // the caller's copies, or NULL
     float* topk_w;
+    float* logits;        // [T, E] and
+    int* arrived;         // [token groups] zeroed counts: E > 32 only
     uint8_t* xq;          // MXFP8: [T, H] E4M3, else NULL
     uint8_t* xsf;         // chunk order, one 512-byte chunk per 128 columns
     int* zero;            // status block and counters of kernel 2
@@ -146,19 +150,21 @@ __device__ __forceinline__ void few_topk(const float* lg, const FewLogitsParams&
     }
 }
 
+// Grid: (8 * ceil(E / 32), token groups).
+template <int STAGES>
 __global__ void __cluster_dims__(kLgCluster, 1, 1) __launch_bounds__(kLgThreads)
 few_logits_kernel(const FewLogitsParams p) {
     extern __shared__ __align__(128) unsigned char lg_smem[];
-    float* part = reinterpret_cast<float*>(lg_smem + kLgPartOffset);   // [chain of four][token][expert]
-    float* red = reinterpret_cast<float*>(lg_smem + kLgRedOffset);     // [CTA][token][expert]
-    float* lg = reinterpret_cast<float*>(lg_smem + kLgLogOffset);      // [token][kMaxE]
+    __shared__ int s_last;
+    float* part = reinterpret_cast<float*>(lg_smem + STAGES * kLgStageBytes);   // [chain of four][token][expert]
+    float* red = part + kLgPartBytes / 4;                                       // [CTA][token][expert]
+    float* lg = red + kLgRedBytes / 4;                                          // [token][kMaxE]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)tc::cluster_ctarank();
-    const int t0 = ((int)blockIdx.x / kLgCluster) * kLgTokens;
+    const int e0 = ((int)blockIdx.x / kLgCluster) * 32, t0 = (int)blockIdx.y * kLgTokens;
     const int ntok = min(kLgTokens, p.T - t0);
     const int nchunks = ceil_div(p.H, 256);
-    const int per = ceil_div(nchunks, kLgChunks);        // stages per 32 experts
-    const int total = per * ceil_div(p.E, 32);
+    const int total = ceil_div(nchunks, kLgChunks);      // stages
     const int cl = warp & 3, th = warp >> 2;             // chain of this CTA's four, token half
     const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.W_r) & 15) == 0;
 
@@ -172,8 +178,8 @@ few_logits_kernel(const FewLogitsParams p) {
     auto h_of = [&](int i, int r) { return 256 * i + 8 * (rank + 8 * (r >> 3)) + (r & 7); };
     auto issue = [&](int n) {
         if (n < total) {
-            const int e0 = (n / per) * 32, c0 = (n % per) * kLgChunks;
-            unsigned char* st = lg_smem + (n % kLgStages) * kLgStageBytes;
+            const int c0 = n * kLgChunks;
+            unsigned char* st = lg_smem + (n % STAGES) * kLgStageBytes;
             const uint32_t ws = tc::smem_u32(st), xs = ws + kLgWBytes;
             if (vec) {
 #pragma unroll
@@ -200,12 +206,16 @@ few_logits_kernel(const FewLogitsParams p) {
         }
         cp_async_commit();   // one group per stage, empty past the end
     };
-    for (int n = 0; n < kLgStages - 1; ++n) issue(n);
+    for (int n = 0; n < STAGES - 1; ++n) issue(n);
 
     // while the first copies are in flight: the counters of kernel 2, and x in
     // 8 bits (one block of 32 a thread; the bytes of mok_quantize_rows)
-    for (int i = (int)blockIdx.x * kLgThreads + tid; i < p.zero_words; i += (int)gridDim.x * kLgThreads) p.zero[i] = 0;
-    if (p.xq) {
+    if (e0 == 0) {
+        const int part_of = (int)blockIdx.y * kLgCluster + rank;
+        for (int i = part_of * kLgThreads + tid; i < p.zero_words; i += (int)gridDim.y * kLgCluster * kLgThreads)
+            p.zero[i] = 0;
+    }
+    if (p.xq && e0 == 0) {
         const int nb = p.H / 32;
         for (int j = rank * kLgThreads + tid; j < ntok * nb; j += kLgCluster * kLgThreads) {
             const int t = t0 + j / nb, b = j % nb;
@@ -221,12 +231,12 @@ few_logits_kernel(const FewLogitsParams p) {
 
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int n = 0; n < total; ++n) {
-        cp_async_wait<kLgStages - 2>();
+        cp_async_wait<STAGES - 2>();
         __syncthreads();              // stage n has landed for every thread; stage n - 1 is consumed
-        issue(n + kLgStages - 1);
-        const int c0 = (n % per) * kLgChunks;
-        const float* ws = reinterpret_cast<const float*>(lg_smem + (n % kLgStages) * kLgStageBytes);
-        const unsigned char* xs = lg_smem + (n % kLgStages) * kLgStageBytes + kLgWBytes;
+        issue(n + STAGES - 1);
+        const int c0 = n * kLgChunks;
+        const float* ws = reinterpret_cast<const float*>(lg_smem + (n % STAGES) * kLgStageBytes);
+        const unsigned char* xs = lg_smem + (n % STAGES) * kLgStageBytes + kLgWBytes;
 #pragma unroll
         for (int i = 0; i < kLgChunks; ++i) {
             if (h_of(c0 + i, 8 * cl) < p.H) {
@@ -244,40 +254,46 @@ few_logits_kernel(const FewLogitsParams p) {
                 }
             }
         }
-        if (n % per == per - 1) {
-            // the tree over the 32 chains: distances 16 and 8 here, 4, 2 and 1
-            // over the CTAs
-            const int e0 = (n / per) * 32;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                part[(cl * kLgTokens + 4 * th + u) * 32 + lane] = acc[u];
-                acc[u] = 0.f;
-            }
-            __syncthreads();
-            const int o = warp * 32 + lane;             // token = warp
-            constexpr int P = kLgTokens * 32;
-            const float v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
-            const uint32_t dst = tc::mapa_shared(tc::smem_u32(red + rank * P + o), 0);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
-            tc::cluster_sync();
-            if (rank == 0) {
-                float s[kLgCluster];
-#pragma unroll
-                for (int c = 0; c < kLgCluster; ++c) s[c] = red[c * P + o];
-#pragma unroll
-                for (int d = kLgCluster / 2; d >= 1; d >>= 1)
-#pragma unroll
-                    for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
-                const int e = e0 + lane;
-                if (e < p.E) lg[warp * kMaxE + e] = p.bias ? s[0] + p.bias[e] : s[0];
-            }
-            if (n + 1 < total) tc::cluster_sync();      // red is read before the next 32 experts' sums arrive
-        }
     }
-    if (rank == 0 && warp < ntok) {
+    // the tree over the 32 chains: distances 16 and 8 here, 4, 2 and 1 over the
+    // CTAs, then the bias
+    constexpr int P = kLgTokens * 32;
+    const int o = warp * 32 + lane;                      // token = warp
+#pragma unroll
+    for (int u = 0; u < 4; ++u) part[(cl * kLgTokens + 4 * th + u) * 32 + lane] = acc[u];
+    __syncthreads();
+    const float v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
+    const uint32_t dst = tc::mapa_shared(tc::smem_u32(red + rank * P + o), 0);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+    tc::cluster_sync();
+    if (rank != 0) return;
+    float s[kLgCluster];
+#pragma unroll
+    for (int c = 0; c < kLgCluster; ++c) s[c] = red[c * P + o];
+#pragma unroll
+    for (int d = kLgCluster / 2; d >= 1; d >>= 1)
+#pragma unroll
+        for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
+    const int e = e0 + lane;
+    const float l = e < p.E && p.bias ? s[0] + p.bias[e] : s[0];
+    if (gridDim.x == kLgCluster) {                       // 32 experts at most: these are all logits
+        lg[warp * kMaxE + lane] = l;
         __syncwarp();
-        few_topk(lg + warp * kMaxE, p, t0 + warp);
+    } else {
+        if (e < p.E && warp < ntok) p.logits[(int64_t)(t0 + warp) * p.E + e] = l;
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(p.arrived + blockIdx.y, 1) == (int)(gridDim.x / kLgCluster) - 1;
+            __threadfence();
+        }
+        __syncthreads();
+        if (!s_last) return;
+        if (warp < ntok)
+            for (int i = lane; i < p.E; i += 32) lg[warp * kMaxE + i] = __ldcg(p.logits + (int64_t)(t0 + warp) * p.E + i);
+        __syncwarp();
     }
+    if (warp < ntok) few_topk(lg + warp * kMaxE, p, t0 + warp);
 }
 
 // ---------------------------------------------------------------------------
@@ -551,6 +567,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     __syncthreads();
 
     pdl_wait();   // the routing, the MXFP8 rows and the zeroed counters are kernel 1's
+    pdl_allow_next();
     for (int i = threadIdx.x; i < T * k; i += kFewThreads) {
         const int e = p.idx[i];
         s_idx[i] = (uint8_t)e;
@@ -1003,7 +1020,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 int few_columns(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
 struct FewLayout {
-    size_t counters, idx, w, xq, xsf, h, hsf, hs, part, total;
+    size_t counters, arrived, logits, idx, w, xq, xsf, h, hsf, hs, part, total;
     int n_counters, n1;   // ints: E + 1 ready counts, n1 gate/up tiles, down tiles
 };
 
@@ -1019,6 +1036,8 @@ FewLayout few_layout(const mok_problem* p, int ctas) {
     L.n_counters = p->E + 1 + L.n1 + (int)(H / r2);
     size_t o = kStatusBytes;
     L.counters = o; o += align_up((int64_t)L.n_counters * 4, 256);
+    L.arrived = o; if (p->E > 32) o += align_up(ceil_div(p->T, kLgTokens) * 4, 256);
+    L.logits = o; if (p->E > 32) o += align_up(T * p->E * 4, 256);
     L.idx = o; o += align_up(T * p->k * 4, 256);
     L.w = o; o += align_up(T * p->k * 4, 256);
     L.xq = o; if (mx) o += align_up(T * H, 256);
@@ -1029,6 +1048,13 @@ FewLayout few_layout(const mok_problem* p, int ctas) {
     L.part = o; o += (size_t)2 * ctas * 2 * 256 * T * 4;
     L.total = o;
     return L;
+}
+
+template <int STAGES>
+cudaError_t run_logits(const FewLogitsParams& p, dim3 grid, cudaStream_t s) {
+    auto kern = few_logits_kernel<STAGES>;
+    ensure_smem_attr(reinterpret_cast<const void*>(kern), lg_smem_bytes(STAGES));
+    return launch_after(kern, grid, dim3(kLgThreads), lg_smem_bytes(STAGES), s, p);
 }
 
 template <bool MX, int NT>
@@ -1084,6 +1110,8 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     lp.k = q->k;
     lp.idx = reinterpret_cast<int32_t*>(ws + L.idx);
     lp.w = reinterpret_cast<float*>(ws + L.w);
+    lp.logits = reinterpret_cast<float*>(ws + L.logits);
+    lp.arrived = reinterpret_cast<int*>(ws + L.arrived);
     lp.topk_idx = a.topk_idx;
     lp.topk_w = a.topk_w;
     lp.xq = mx ? reinterpret_cast<uint8_t*>(ws + L.xq) : nullptr;
@@ -1128,9 +1156,12 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
              make_tmap_swizzled(&tm[6], a.sdn, H, Is, 2, 64, p.R2) && make_tmap_swizzled(&tm[7], p.hs, T, Is, 2, 64, NT);
     if (!ok) return cudaErrorInvalidValue;
 
-    ensure_smem_attr(reinterpret_cast<const void*>(few_logits_kernel), kLgSmem);
-    cudaError_t e = launch_after(few_logits_kernel, dim3(kLgCluster * ceil_div(T, kLgTokens)),
-                                 dim3(kLgThreads), kLgSmem, s, lp);
+    cudaError_t e = cudaSuccess;
+    const dim3 grid(kLgCluster * ceil_div(E, 32), ceil_div(T, kLgTokens));
+    if (E > 32) e = cudaMemsetAsync(ws + L.arrived, 0, grid.y * 4, s);
+    // a ring for all of H <= 8192 takes an SM for itself; with more clusters than
+    // fit that way, a shorter one lets two CTAs share an SM
+    if (e == cudaSuccess) e = grid.x * grid.y <= 64 ? run_logits<9>(lp, grid, s) : run_logits<5>(lp, grid, s);
     if (e != cudaSuccess) return e;
     return mx ? run_ffn<true>(tm, p, c.num_sms, s) : run_ffn<false>(tm, p, c.num_sms, s);
 }
