@@ -13,9 +13,9 @@
 //   phase 1   h_e = SwiGLU(W_gu[e] x^T)       units: (expert, row tile, K block)
 //   phase 2   out = sum_e w_e * (W_dn[e] h_e^T)   units: (row tile, expert, K block)
 //
-// Each phase's K blocks form one sequence that is cut into equal contiguous
-// ranges, one per CTA, so every SM streams the same number of weight bytes at
-// any T. A row tile cut between CTAs goes through fp32 partial sums in the
+// Each phase's K blocks form one sequence that is cut into contiguous ranges of
+// about equal length, one per CTA (at tile boundaries where that leaves few CTAs
+// idle). A row tile cut between CTAs goes through fp32 partial sums in the
 // workspace: at the end of the phase each CTA that shares the tile waits for the
 // others' partials and adds up its own part of the token columns, always in CTA
 // order, so no bit depends on timing and the additions are spread over the SMs.
@@ -300,11 +300,12 @@ few_logits_kernel(const FewLogitsParams p) {
 // Kernel 2
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 352;
-// Units that a CTA gets at least: a shorter range costs more in shared tiles
-// than it saves in streaming (H = 2048, I = 512, 8 MXFP8 experts, 128 tokens: 61
+// Units that a part of a tile has at least: a shorter one costs more in shared
+// tiles than it saves in streaming (H = 2048, I = 512, 8 MXFP8 experts, 128 tokens: 61
 // us at 1, 57 at 2, 45 at 4, 52 at 8; H = 640, I = 1024, 2 tokens: 33.7, 33.6,
 // 31.4, 34.9; layers that fill every SM do not change).
 constexpr int kFewMinUnits = 4;
+constexpr int kFewMaxParts = 1 << 20;   // parts of a phase, where tiles are cut at all
 constexpr int kFewEpi = 256;      // epilogue threads
 constexpr int kFewEpiBar = 1;     // their named barrier
 
@@ -350,14 +351,51 @@ struct FewCfg {
     static_assert(kStages >= 3 && kSmem <= kLimit && kTmemNeed <= 512, "few-token kernel budget");
 };
 
-// The layer's work as two sequences of K blocks, and this CTA's part of each.
+// The layer's work as two sequences of K blocks (units), and how they are cut:
+// each row tile into p parts of about equal length, the parts in order over G
+// CTAs (CTA c takes the parts P c / G .. P (c + 1) / G).
 struct FewWork {
     int A;                       // active routed experts
     int t1, kb1, ts1, kbs1;      // gate/up: tiles per expert and K blocks per tile, routed and shared
     int t2, kb2, kbs2;           // down: tiles, K blocks per tile and expert, routed and shared
-    int64_t U1, U2;              // units of the phases
-    int G1, G2;                  // CTAs that share them
+    int p1, ps1, P1, G1;         // gate/up: parts per routed and shared tile, all parts, CTAs
+    int p2, P2, G2;              // down
+    int b1, e1, b2, e2;          // this CTA's units of the phases
+
+    __device__ __forceinline__ int upt2() const { return A * kb2 + kbs2; }
+    // first unit of part x of a phase (x = all parts: the end)
+    __device__ __forceinline__ int unit1(int x) const {
+        const int routed = A * t1 * p1;
+        if (x < routed) return x / p1 * kb1 + kb1 * (x % p1) / p1;
+        const int y = x - routed;
+        return A * t1 * kb1 + (ps1 ? y / ps1 * kbs1 + kbs1 * (y % ps1) / ps1 : 0);
+    }
+    __device__ __forceinline__ int unit2(int x) const { return x / p2 * upt2() + upt2() * (x % p2) / p2; }
+    // (at most kFewMaxParts parts and a few hundred CTAs: products fit 32 bits)
+    __device__ __forceinline__ int start1(int c) const { return unit1(P1 * c / G1); }
+    __device__ __forceinline__ int start2(int c) const { return unit2(P2 * c / G2); }
+    // the CTA that takes part x
+    __device__ __forceinline__ int owner1(int x) const { return ((x + 1) * G1 - 1) / P1; }
+    __device__ __forceinline__ int owner2(int x) const { return ((x + 1) * G2 - 1) / P2; }
 };
+
+// Parts per tile for `tiles` tiles (counted in routed tiles of kb units) on M
+// CTAs: the fewest that keep four fifths of the CTAs busy, else the most even cut.
+// A whole tile needs no partial sums and no wait, and the memory is saturated by
+// fewer CTAs than there are (BF16, H = 7168, 16 tokens: 512 tiles on 128 CTAs
+// 442 us, cut evenly over 152 451; down, 28 tiles on 140 CTAs 445). Parts have at
+// least kFewMinUnits units. All 32 lanes call it; lane i tries i + 1.
+__device__ __forceinline__ int few_parts(int tiles, int kb, int M) {
+    const int n = (int)(threadIdx.x & 31) + 1;
+    int key = 0;
+    if (n == 1 || (n * kFewMinUnits <= kb && tiles <= kFewMaxParts / n)) {
+        const int P = tiles * n, q = ceil_div(P, M);
+        const int busy = (int)(1000.f * (float)P / (float)(q * M));
+        key = (busy >= 800 ? 2000 : busy) * 32 + (32 - n);
+    }
+    const int best = (int)__reduce_max_sync(0xffffffffu, (unsigned)key);
+    return 32 - best % 32;
+}
 
 struct FewJob {
     int phase;       // 0 gate/up, 1 down
@@ -365,7 +403,8 @@ struct FewJob {
     int tile;        // gate/up: row tile of the expert; down: row tile
     int gtile;       // index of the tile's arrival counter
     int kb, n;       // K blocks kb .. kb + n - 1
-    int64_t u0, u1;  // unit range of the whole tile (the partial sums' scope)
+    int u0;          // first unit of the tile
+    int c0, c1;      // the CTAs that share the tile
     bool last;       // this CTA's last job of the tile
 };
 
@@ -374,36 +413,33 @@ struct FewJob {
 struct FewShared {
     int a, tile, gtile;
     int c0, c1;      // the CTAs that share it
-    int64_t u0;
+    int u0;
 };
-
-__device__ __forceinline__ int64_t few_start(int64_t U, int G, int c) { return U * c / G; }
-__device__ __forceinline__ int few_owner(int64_t U, int G, int64_t u) { return (int)(((u + 1) * G - 1) / U); }
 
 // Calls f(job) for this CTA's jobs of a phase in order; false as soon as f
 // returns false.
 template <typename F>
 __device__ __forceinline__ bool few_jobs_up(const FewWork& w, F&& f) {
-    const int c = (int)blockIdx.x;
-    if (c >= w.G1) return true;
-    int64_t u = few_start(w.U1, w.G1, c);
-    const int64_t end = few_start(w.U1, w.G1, c + 1);
-    const int64_t routed = (int64_t)w.A * w.t1 * w.kb1;
+    int u = w.b1;
+    const int end = w.e1;
+    const int routed = w.A * w.t1 * w.kb1;
     FewJob j;
     j.phase = 0;
     j.last = true;
     while (u < end) {
         const bool sh = u >= routed;
-        const int kbt = sh ? w.kbs1 : w.kb1;
-        const int64_t v = sh ? u - routed : u;
-        const int g = (int)(v / kbt);
-        j.kb = (int)(v % kbt);
+        const int kbt = sh ? w.kbs1 : w.kb1, p = sh ? w.ps1 : w.p1;
+        const int v = sh ? u - routed : u;
+        const int g = v / kbt;
+        j.kb = v % kbt;
         j.u0 = u - j.kb;
-        j.u1 = j.u0 + kbt;
-        j.n = (int)(min(end, j.u1) - u);
+        j.n = min(end, j.u0 + kbt) - u;
         j.a = sh ? w.A : g / w.t1;
         j.tile = sh ? g : g % w.t1;
         j.gtile = sh ? w.A * w.t1 + g : g;
+        const int x = (sh ? w.A * w.t1 * w.p1 : 0) + g * p;
+        j.c0 = w.owner1(x);
+        j.c1 = w.owner1(x + p - 1);
         u += j.n;
         if (!f(j)) return false;
     }
@@ -411,25 +447,23 @@ __device__ __forceinline__ bool few_jobs_up(const FewWork& w, F&& f) {
 }
 template <typename F>
 __device__ __forceinline__ bool few_jobs_down(const FewWork& w, F&& f) {
-    const int c = (int)blockIdx.x;
-    if (c >= w.G2) return true;
-    int64_t u = few_start(w.U2, w.G2, c);
-    const int64_t end = few_start(w.U2, w.G2, c + 1);
-    const int upt = w.A * w.kb2 + w.kbs2;
+    int u = w.b2;
+    const int end = w.e2;
+    const int upt = w.upt2();
     FewJob j;
     j.phase = 1;
     while (u < end) {
-        j.tile = (int)(u / upt);
-        j.gtile = j.tile;
-        j.u0 = (int64_t)j.tile * upt;
-        j.u1 = j.u0 + upt;
-        const int r = (int)(u - j.u0);
+        j.tile = j.gtile = u / upt;
+        j.u0 = j.tile * upt;
+        const int r = u - j.u0;
         const bool sh = r >= w.A * w.kb2;
         j.a = sh ? w.A : r / w.kb2;
         j.kb = sh ? r - w.A * w.kb2 : r % w.kb2;
-        j.n = (int)min((int64_t)((sh ? w.kbs2 : w.kb2) - j.kb), end - u);
+        j.n = min((sh ? w.kbs2 : w.kb2) - j.kb, end - u);
         u += j.n;
-        j.last = u == end || u == j.u1;
+        j.last = u == end || u == j.u0 + upt;
+        j.c0 = w.owner2(j.tile * w.p2);
+        j.c1 = w.owner2((j.tile + 1) * w.p2 - 1);
         if (!f(j)) return false;
     }
     return true;
@@ -528,7 +562,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     extern __shared__ __align__(1024) unsigned char few_smem[];
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_hit[kMaxE / 32];
-    __shared__ int s_active;
+    __shared__ int s_cut[11];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(few_smem) + 1023) & ~uintptr_t(1023));
     const uint32_t base = tc::smem_u32(smem);
     const uint32_t bar = base + C::kBarOffset;
@@ -575,22 +609,14 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         atomicOr(&s_hit[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    if (warp == 0) {   // the active experts, ascending
-        int n = 0;
-        for (int q = 0; 32 * q < E; ++q) {
-            const uint32_t m = s_hit[q];
-            if ((m >> lane) & 1u) s_act[n + __popc(m & ((1u << lane) - 1))] = (uint16_t)(32 * q + lane);
-            n += __popc(m);
-        }
-        if (lane == 0) s_active = n;
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = s_tmem;
-
+    // the active experts in ascending order (warp 0), and the cut of the two
+    // phases (warps 1 and 2; a K block of the MXFP8 experts holds twice the
+    // elements of the BF16 shared expert's, so a shared tile counts as kbs1 / kb1
+    // routed ones)
     FewWork w;
-    w.A = s_active;
+    w.A = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxE / 32; ++q) w.A += __popc(s_hit[q]);
     w.t1 = 2 * p.I / p.R1;
     w.kb1 = p.H / C::kBK;
     w.ts1 = p.Is ? 2 * p.Is / p.Rs1 : 0;
@@ -598,10 +624,56 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     w.t2 = p.H / p.R2;
     w.kb2 = p.I / C::kBK;
     w.kbs2 = p.Is / 64;
-    w.U1 = (int64_t)w.A * w.t1 * w.kb1 + (int64_t)w.ts1 * w.kbs1;
-    w.U2 = (int64_t)w.t2 * (w.A * w.kb2 + w.kbs2);
-    w.G1 = (int)min((int64_t)gridDim.x, max((int64_t)1, w.U1 / kFewMinUnits));
-    w.G2 = (int)min((int64_t)gridDim.x, max((int64_t)1, w.U2 / kFewMinUnits));
+    const int M = (int)gridDim.x, me = (int)blockIdx.x;
+    if (warp == 0) {
+        int n = 0;
+        for (int q = 0; 32 * q < E; ++q) {
+            const uint32_t m = s_hit[q];
+            if ((m >> lane) & 1u) s_act[n + __popc(m & ((1u << lane) - 1))] = (uint16_t)(32 * q + lane);
+            n += __popc(m);
+        }
+    } else if (warp == 1) {
+        const int heavy = w.ts1 ? (MX ? 2 : 1) : 0;
+        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M);
+        w.ps1 = w.p1 * heavy;
+        w.P1 = w.A * w.t1 * w.p1 + w.ts1 * w.ps1;
+        w.G1 = ceil_div(w.P1, ceil_div(w.P1, M));
+        // lanes 0 and 1: first unit of this CTA and of the next
+        const int u = me < w.G1 ? w.start1(min(me + (lane & 1), w.G1)) : 0;
+        if (lane < 2) s_cut[4 + lane] = u;
+        if (lane == 0) {
+            s_cut[0] = w.p1;
+            s_cut[1] = w.ps1;
+            s_cut[2] = w.P1;
+            s_cut[3] = w.G1;
+        }
+    } else if (warp == 2) {
+        w.p2 = few_parts(w.t2, w.upt2(), M);
+        w.P2 = w.t2 * w.p2;
+        w.G2 = ceil_div(w.P2, ceil_div(w.P2, M));
+        const int u = me < w.G2 ? w.start2(min(me + (lane & 1), w.G2)) : 0;
+        if (lane < 2) s_cut[9 + lane] = u;
+        if (lane == 0) {
+            s_cut[6] = w.p2;
+            s_cut[7] = w.P2;
+            s_cut[8] = w.G2;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    w.p1 = s_cut[0];
+    w.ps1 = s_cut[1];
+    w.P1 = s_cut[2];
+    w.G1 = s_cut[3];
+    w.b1 = s_cut[4];
+    w.e1 = s_cut[5];
+    w.p2 = s_cut[6];
+    w.P2 = s_cut[7];
+    w.G2 = s_cut[8];
+    w.b2 = s_cut[9];
+    w.e2 = s_cut[10];
 
     if (warp == 0) {
         // ------------------------------------------------------------ weights
@@ -819,10 +891,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         };
         // this CTA's partial of a shared tile is written: count it in and
         // remember the tile
-        auto share = [&](const FewJob& j, int c0, int c1) {
+        auto share = [&](const FewJob& j) {
             epi_sync();
             if (et == 0) few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
-            const FewShared f{j.a, j.tile, j.gtile, c0, c1, j.u0};
+            const FewShared f{j.a, j.tile, j.gtile, j.c0, j.c1, j.u0};
             if (n_pend == 0) pend[0] = f;
             else pend[1] = f;
             ++n_pend;
@@ -830,8 +902,6 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         // end of a phase: of each shared tile, sharer i of n adds up the
         // partials of the tokens T i / n .. T (i + 1) / n in CTA order
         auto finish = [&](int phase) {
-            const int64_t U = phase ? w.U2 : w.U1;
-            const int G = phase ? w.G2 : w.G1;
 #pragma unroll 1
             for (int i = 0; i < n_pend; ++i) {
                 const FewShared f = i == 0 ? pend[0] : pend[1];
@@ -849,7 +919,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 const int ra = phase ? 8 * lane : il16 ? 32 * (lane >> 2) + 4 * (lane & 3) : 4 * lane;
                 const int rb = phase ? ra + 4 : il16 ? ra + 16 : 128 + ra;
                 const bool in = rb < rows;
-                const int lead = few_start(U, G, f.c0) < f.u0 ? 1 : 0;
+                const int lead = (phase ? w.start2(f.c0) : w.start1(f.c0)) < f.u0 ? 1 : 0;
                 const float* src = slots(phase) + 2 * (int64_t)f.c0 * part_stride;
                 constexpr int TU = 4;                 // tokens in flight per warp
 #pragma unroll 1
@@ -919,10 +989,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         };
 
         bool ok = few_jobs_up(w, [&](const FewJob& j) {
-            const int c0 = few_owner(w.U1, w.G1, j.u0), c1 = few_owner(w.U1, w.G1, j.u1 - 1);
-            const bool whole = c0 == c1;
+            const bool whole = j.c0 == j.c1;
             const bool two = (j.a == w.A ? p.Rs1 : p.R1) > 128;
-            float* mine = slot_of(0, c_me, few_start(w.U1, w.G1, c_me) < j.u0);
+            float* mine = slot_of(0, c_me, w.b1 < j.u0);
             if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
             ph ^= 1u;
             tc::fence_after_sync();
@@ -947,7 +1016,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tc::fence_before_sync();
             tc::mbar_arrive(acce);
             if (whole) publish_h(j.a, T);
-            else share(j, c0, c1);
+            else share(j);
             return true;
         });
         ok = ok && finish(0);
@@ -988,10 +1057,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tc::fence_before_sync();
             tc::mbar_arrive(acce);
             if (j.last) {
-                const int c0 = few_owner(w.U2, w.G2, j.u0), c1 = few_owner(w.U2, w.G2, j.u1 - 1);
-                const bool whole = c0 == c1;
+                const bool whole = j.c0 == j.c1;
                 const bool two = p.R2 > 128;
-                float* mine = slot_of(1, c_me, few_start(w.U2, w.G2, c_me) < j.u0);
+                float* mine = slot_of(1, c_me, w.b2 < j.u0);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     const int t = col0 + i;
@@ -1005,7 +1073,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                     }
                     acc[0][i] = acc[1][i] = 0.f;
                 }
-                if (!whole) share(j, c0, c1);
+                if (!whole) share(j);
             }
             return true;
         });
