@@ -1,5 +1,6 @@
 // api.cu - the C ABI declared in include/mok.h.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "common.cuh"
@@ -281,14 +282,23 @@ CkptLayout ckpt_layout(const mok_problem* p) {
     return L;
 }
 
-// Requires an sm_103-class device for the tensor-core kernels.
+// Requires an sm_103-class device for the tensor-core kernels. The answer is
+// kept per device: three driver queries would cost a short call a microsecond.
 bool device_ok() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    static std::atomic<int8_t> known[64];   // 0: not asked, 1: yes, 2: no
+    const bool kept = dev >= 0 && dev < 64;
+    if (kept) {
+        const int8_t k = known[dev].load(std::memory_order_relaxed);
+        if (k) return k == 1;
+    }
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    return major == 10 && minor == 3;
+    const bool ok = major == 10 && minor == 3;
+    if (kept) known[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
+    return ok;
 }
 
 }  // namespace
@@ -795,7 +805,7 @@ mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stre
 
 size_t mok_rmsnorm_bwd_workspace_size(int32_t T, int32_t H) {
     if (!norm_dims_ok(T, H)) return 0;
-    return (size_t)std::max(rmsnorm_bwd_partials(T), 1) * H * 4;
+    return (size_t)std::max(rmsnorm_bwd_partials(T, H), 1) * H * 4;
 }
 
 mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args* a, mok_stream_t stream) {

@@ -62,7 +62,7 @@ inline int down_tile_n(int H, bool mx) {
 }
 
 // norm.cu
-int rmsnorm_bwd_partials(int T);   // partial rows of dgain that the backward's workspace holds
+int rmsnorm_bwd_partials(int T, int H);   // partial rows of dgain that the backward's workspace holds
 cudaError_t launch_rmsnorm(int T, int H, const mok_rmsnorm_args& a, cudaStream_t s);
 cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a, cudaStream_t s);
 cudaError_t launch_dequantize_rows(const void* q, const void* sf, int T, int H, void* x, cudaStream_t s);

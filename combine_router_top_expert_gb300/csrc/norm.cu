@@ -19,17 +19,38 @@ namespace mok {
 namespace {
 
 // Sum over the CTA of one value per thread, the same in every thread and in
-// every run (shuffles, then the warps' sums in order). `red` holds one float
+// every run: shuffles in each warp, then over the warps' sums. `red` holds a float
 // per warp; two alternating buffers let one barrier serve each call.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int nw = (int)blockDim.x >> 5;
-    float s = 0.f;
-    for (int w = 0; w < nw; ++w) s += red[w];
-    return s;
+    v = lane < ((int)blockDim.x >> 5) ? red[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// 8 BF16 values as four pairs.
+__device__ __forceinline__ void unpack_pairs(const uint4& v, float2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+__device__ __forceinline__ uint4 pack_pairs(const float2 (&f)[4]) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// 8 fp32 values as four pairs.
+__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
 }
 
 struct NormParams {
@@ -49,77 +70,79 @@ struct NormParams {
     float* rstd;
 };
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
 // One CTA per row; thread i holds the 8-element vectors i, i + blockDim.x, ...
-// (VPT of them), so the row is read once and stays in registers between the
-// sum of squares and the scaling. Lanes 4j..4j+3 of a vector round hold one
-// 32-element MXFP8 block.
+// (VPT of them), so the row is read once and stays in registers between the sum
+// of squares and the scaling. Lanes 4j..4j+3 of a vector round hold one
+// 32-element MXFP8 block. Several CTAs share an SM and hide each other's waits
+// (T = 4096, H = 7168, MXFP8 output: 37 us; CTAs that loop over rows with the next
+// one prefetched to shared memory took 44).
 template <int VPT>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 4 : 1)
 rmsnorm_kernel(const NormParams p) {
-    __shared__ float red[32];
+    __shared__ __align__(16) float red[32];
     pdl_wait();
     pdl_allow_next();
     const int64_t t = blockIdx.x;
     const int nv = p.H / 8;
-    float f[VPT][8];
-    float ss = 0.f;
+    uint4 x[VPT], r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
+        x[i] = r[i] = make_uint4(0, 0, 0, 0);
         if (v < nv) {
-            unpack8(*reinterpret_cast<const uint4*>(p.x + t * p.ldx + 8 * v), f[i]);
-            if (p.r) {
-                float g[8];
-                unpack8(*reinterpret_cast<const uint4*>(p.r + t * p.ldr + 8 * v), g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] += g[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+            x[i] = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + 8 * v);
+            if (p.r) r[i] = *reinterpret_cast<const uint4*>(p.r + t * p.ldr + 8 * v);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(ss, red) / (float)p.H + p.eps);
+    float2 f[VPT][4], ss2 = both(0.f);   // packed fp32 pairs: half the instructions
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float2 g[4];
+        unpack_pairs(x[i], f[i]);
+        unpack_pairs(r[i], g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[i][j] = __fadd2_rn(f[i][j], g[j]);
+            ss2 = __ffma2_rn(f[i][j], f[i][j], ss2);
+        }
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(ss2.x + ss2.y, red) / (float)p.H + p.eps);
     if (p.rstd && threadIdx.x == 0) p.rstd[t] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = threadIdx.x + i * blockDim.x;
         const bool in = v < nv;
-        const uint4 sb = pack8(f[i]);   // the sum as it is carried on (BF16)
+        const uint4 sb = pack_pairs(f[i]);   // the sum as it is carried on (BF16)
         if (in && p.sum) *reinterpret_cast<uint4*>(p.sum + t * p.H + 8 * v) = sb;
         if (p.sum_q) {
-            float b[8];
-            unpack8(sb, b);
             uint2 o;
-            const uint32_t code = quantize8(b, o);
+            const uint32_t code = quantize8_bf16(sb, o);
             if (in) {
                 *reinterpret_cast<uint2*>(p.sum_q + t * p.H + 8 * v) = o;
                 if ((v & 3) == 0) p.sum_sf[t * (p.H / 32) + v / 4] = (uint8_t)code;
             }
         }
         if (p.y || p.y_q) {
-            float y[8];
-            if (in) {
-                const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.gain + 8 * v));
-                const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.gain + 8 * v) + 1);
-                const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+            float2 g[4] = {};
+            if (in) load8(p.gain + 8 * v, g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = f[i][j] * rstd * g[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = 0.f;
-            }
-            const uint4 yb = pack8(y);
+            for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(__fmul2_rn(f[i][j], both(rstd)), g[j]);
+            const uint4 yb = pack_pairs(g);
             if (in && p.y) *reinterpret_cast<uint4*>(p.y + t * p.H + 8 * v) = yb;
             if (p.y_q) {
                 // quantised from the BF16 values, so the bytes are those of
                 // mok_quantize_rows on y
-                float b[8];
-                unpack8(yb, b);
                 uint2 o;
-                const uint32_t code = quantize8(b, o);
+                const uint32_t code = quantize8_bf16(yb, o);
                 if (in) {
                     *reinterpret_cast<uint2*>(p.y_q + t * p.H + 8 * v) = o;
                     if ((v & 3) == 0) p.y_sf[t * (p.H / 32) + v / 4] = (uint8_t)code;
@@ -146,99 +169,199 @@ struct NormBwdParams {
 // CTA b takes rows b, b + gridDim.x, ...; its threads keep their columns'
 // dgain in registers over all of its rows and write one partial row at the
 // end, which rmsnorm_dgain_kernel adds up in CTA order.
-template <int VPT, bool CK>
-__global__ void __launch_bounds__(1024)
+//
+// A row's block-wide sum stands between its loads and its stores, so the loads
+// of the next rows have to be in flight meanwhile: each thread copies its own
+// vectors of STAGES - 1 rows ahead to shared memory (cp.async; nobody else reads
+// them, so no barrier is needed). Up to H = 8192 what the second half needs stays
+// in registers; longer rows read their buffers twice. Rows too long for two buffers (STAGES = 0) are read from memory each time.
+template <int VPT, bool CK, int STAGES>
+__global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
-    __shared__ float red[2][32];
+    constexpr bool PF = STAGES > 0;
+    extern __shared__ __align__(16) unsigned char bwd_smem[];
+    __shared__ __align__(16) float red[2][32];
+    constexpr int kVecs = 3 * VPT;   // 16-byte slots of a thread per row: dy, dsum, s
     pdl_wait();
     pdl_allow_next();
-    const int nv = p.H / 8;
-    float dg[VPT][8];
+    const int nv = p.H / 8, nt = (int)blockDim.x;
+    // slot i of buffer b: consecutive threads side by side
+    auto slot = [&](int b, int i) { return bwd_smem + ((size_t)(b * kVecs + i) * nt + threadIdx.x) * 16; };
+    auto issue = [&](int64_t t, int b) {
+        if constexpr (PF) {
+            if (t < p.T) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int v = threadIdx.x + i * nt;
+                    if (v < nv) {
+                        cp_async16(slot(b, i), p.dy + t * p.H + 8 * v);
+                        if (p.dsum) cp_async16(slot(b, VPT + i), p.dsum + t * p.H + 8 * v);
+                        if constexpr (CK) cp_async8(slot(b, 2 * VPT + i), p.s_q + t * p.H + 8 * v);
+                        else cp_async16(slot(b, 2 * VPT + i), p.s + t * p.H + 8 * v);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    // 8 elements of the sum and of dy
+    auto fetch = [&](int64_t t, int b, int i, int v, uint32_t code, float2 (&s)[4], float2 (&dy)[4]) {
+        const int64_t at = t * p.H + 8 * v;
+        unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, i)) : *reinterpret_cast<const uint4*>(p.dy + at), dy);
+        if constexpr (CK) {
+            float f[8];
+            dequantize8(PF ? *reinterpret_cast<const uint2*>(slot(b, 2 * VPT + i))
+                           : *reinterpret_cast<const uint2*>(p.s_q + at), code, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = make_float2(f[2 * j], f[2 * j + 1]);
+        } else {
+            unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(p.s + at),
+                    s);
+        }
+    };
+    constexpr bool kKeep = VPT == 1;   // gain, s and u stay in registers over the sum
+    float2 dg[VPT][4], gk[4], sk[4], uk[4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
-    int it = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, ++it) {
-        const float rstd = __ldg(p.rstd + t);
-        float a[VPT][8], xh[VPT][8];
-        float dot = 0.f;
+        for (int j = 0; j < 4; ++j) dg[i][j] = both(0.f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v < nv) {
-                float dy[8];
-                unpack8(__ldg(reinterpret_cast<const uint4*>(p.dy + t * p.H + 8 * v)), dy);
-                if constexpr (CK) {
-                    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.s_q + t * p.H + 8 * v));
-                    dequantize8(q, __ldg(p.s_sf + t * (p.H / 32) + v / 4), xh[i]);
-                } else {
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(p.s + t * p.H + 8 * v)), xh[i]);
+    for (int j = 0; j < 4; ++j) gk[j] = sk[j] = uk[j] = both(0.f);
+    if (kKeep && threadIdx.x < nv) load8(p.gain + 8 * threadIdx.x, gk);
+    // a row's rstd and scale codes, loaded as far ahead as its vectors; the loop
+    // is unrolled over the buffers so that they stay in registers
+    constexpr int R = PF ? STAGES : 1;
+    float rstds[R];
+    uint32_t codes[R][VPT];
+    auto small = [&](int64_t t, float& rstd, uint32_t (&code)[VPT]) {
+        rstd = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) code[i] = 0;
+        if (t < p.T) {
+            rstd = __ldg(p.rstd + t);
+            if constexpr (CK) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int v = threadIdx.x + i * nt;
+                    if (v < nv) code[i] = __ldg(p.s_sf + t * (p.H / 32) + v / 4);
                 }
-                const float4 g0 = __ldg(reinterpret_cast<const float4*>(p.gain + 8 * v));
-                const float4 g1 = __ldg(reinterpret_cast<const float4*>(p.gain + 8 * v) + 1);
-                const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    xh[i][j] *= rstd;
-                    dg[i][j] = fmaf(dy[j], xh[i][j], dg[i][j]);
-                    a[i][j] = dy[j] * g[j];
-                    dot = fmaf(a[i][j], xh[i][j], dot);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[i][j] = xh[i][j] = 0.f;
             }
         }
-        const float mean = block_sum(dot, red[it & 1]) / (float)p.H;
+    };
+#pragma unroll
+    for (int n = 0; n < R - 1; ++n) {
+        issue(blockIdx.x + (int64_t)n * gridDim.x, n);
+        small(blockIdx.x + (int64_t)n * gridDim.x, rstds[n], codes[n]);
+    }
+    auto row = [&](int64_t t, int b, int half, float rstd, const uint32_t (&code)[VPT]) {
+        float2 dot = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
+            const int v = threadIdx.x + i * nt;
             if (v < nv) {
-                float d[8];
+                float2 s[4], dy[4], g[4];
+                fetch(t, b, i, v, code[i], s, dy);
+                if constexpr (!kKeep) load8(p.gain + 8 * v, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = __fmul2_rn(dy[j], kKeep ? gk[j] : g[j]);
+                    dg[i][j] = __ffma2_rn(__fmul2_rn(dy[j], both(rstd)), s[j], dg[i][j]);
+                    dot = __ffma2_rn(u, s[j], dot);
+                    if constexpr (kKeep) {
+                        sk[j] = s[j];
+                        uk[j] = u;
+                    }
+                }
+            }
+        }
+        // dx = dsum + rstd u - c s with c = rstd^3 sum(u s) / H
+        const float c = -rstd * (rstd * (rstd * (block_sum(dot.x + dot.y, red[half]) / (float)p.H)));
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = threadIdx.x + i * nt;
+            if (v < nv) {
+                float2 d[4];
                 if (p.dsum) {
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(p.dsum + t * p.H + 8 * v)), d);
+                    unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, VPT + i))
+                               : *reinterpret_cast<const uint4*>(p.dsum + t * p.H + 8 * v), d);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] = 0.f;
+                    for (int j = 0; j < 4; ++j) d[j] = both(0.f);
+                }
+                float2 s[4], u[4];
+                if constexpr (!kKeep) {
+                    float2 g[4];
+                    fetch(t, b, i, v, code[i], s, u);
+                    load8(p.gain + 8 * v, g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(u[j], g[j]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, a[i][j] - xh[i][j] * mean, d[j]);
-                *reinterpret_cast<uint4*>(p.dx + t * p.H + 8 * v) = pack8(d);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 w = __ffma2_rn(both(rstd), kKeep ? uk[j] : u[j], d[j]);
+                    d[j] = __ffma2_rn(both(c), kKeep ? sk[j] : s[j], w);
+                }
+                *reinterpret_cast<uint4*>(p.dx + t * p.H + 8 * v) = pack_pairs(d);
+            }
+        }
+    };
+    int half = 0;   // which of the two sums' scratch
+    for (int64_t t0 = blockIdx.x; t0 < p.T; t0 += (int64_t)R * gridDim.x) {
+#pragma unroll
+        for (int n = 0; n < R; ++n, half ^= 1) {
+            const int64_t t = t0 + (int64_t)n * gridDim.x, ahead = t + (int64_t)(R - 1) * gridDim.x;
+            if (t < p.T) {
+                // into the buffer of the row before this one (this thread is done with it)
+                constexpr int kBack = R - 1;
+                issue(ahead, (n + kBack) % R);
+                small(ahead, rstds[(n + kBack) % R], codes[(n + kBack) % R]);
+                if constexpr (PF) asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+                row(t, n, half, rstds[n], codes[n]);
             }
         }
     }
+    if constexpr (PF) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
+        const int v = threadIdx.x + i * nt;
         if (v < nv) {
             float* o = p.part + (int64_t)blockIdx.x * p.H + 8 * v;
-            *reinterpret_cast<float4*>(o) = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            *reinterpret_cast<float4*>(o) = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
         }
     }
 }
 
-// dgain[h] = sum over the P partial rows, in a fixed order: 8 warps take the
-// rows w, w + 8, ..., then the warps' sums are added in order. 32 columns a CTA.
-__global__ void __launch_bounds__(256)
+// dgain[h] = sum over the P partial rows, in a fixed order: 32 warps take the
+// rows w, w + 32, ... (eight loads in flight), then the warps' sums are added in
+// order. 32 columns a CTA.
+__global__ void __launch_bounds__(1024)
 rmsnorm_dgain_kernel(const float* __restrict__ part, int P, int H, float* __restrict__ dgain) {
-    __shared__ float red[8][32];
+    __shared__ float red[32][33];
     pdl_wait();
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (h < H)
-        for (int b = warp; b < P; b += 8) s += part[(int64_t)b * H + h];
+    if (h < H) {
+        for (int b0 = warp; b0 < P; b0 += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int b = b0 + 32 * u;
+                v[u] = b < P ? part[(int64_t)b * H + h] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
+    }
     red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && h < H) {
-        float v = 0.f;
+    // warp w: the sum of column w over the 32 warps' sums
+    float v = red[lane][warp];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += red[w][lane];
-        dgain[h] = v;
-    }
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (lane == 0 && blockIdx.x * 32 + warp < H) dgain[blockIdx.x * 32 + warp] = v;
 }
 
 // BF16 rows from MXFP8 rows: 8 elements a thread.
@@ -267,23 +390,45 @@ struct RowShape {
 };
 RowShape row_shape(int H) {
     const int nv = H / 8;
-    const int vpt = nv <= 512 ? 1 : nv <= 1024 ? 2 : nv <= 4096 ? 4 : 8;
+    const int vpt = nv <= 512 ? 1 : nv <= 1024 ? 2 : nv <= 4096 ? 4 : 8;   // at most 512 threads up to H = 16384
     return {std::max(32, (int)align_up(ceil_div(nv, vpt), 32)), vpt};
 }
 
+// The backward's CTA: 1024 threads at most, four prefetched rows of dy, dsum and
+// s while they fit shared memory, else two, else none; about 1024 threads an SM.
+struct BwdShape {
+    int threads, vpt, stages, smem, per_sm;
+};
+BwdShape bwd_shape(int H) {
+    const int nv = H / 8, vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
+    BwdShape b{std::max(32, (int)align_up(ceil_div(nv, vpt), 32)), vpt, 0, 0, 1};
+    const int row = 3 * vpt * b.threads * 16, room = 216 * 1024;
+    b.per_sm = std::max(1, std::min(1024 / b.threads, 8));
+    b.stages = vpt == 1 && 4 * row * b.per_sm <= room ? 4 : vpt == 2 && 2 * row <= room ? 2 : 0;
+    b.smem = b.stages * row;
+    return b;
+}
+
+template <int VPT, bool CK, int STAGES>
+cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
+    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES>;
+    if (b.smem > 40 * 1024) ensure_smem_attr(reinterpret_cast<const void*>(kern), b.smem);
+    return launch_after(kern, dim3(grid), dim3(b.threads), b.smem, s, p);
+}
 template <bool CK>
-cudaError_t run_bwd(const NormBwdParams& p, int grid, RowShape r, cudaStream_t s) {
-    switch (r.vpt) {
-        case 1: return launch_after(rmsnorm_bwd_kernel<1, CK>, dim3(grid), dim3(r.threads), 0, s, p);
-        case 2: return launch_after(rmsnorm_bwd_kernel<2, CK>, dim3(grid), dim3(r.threads), 0, s, p);
-        case 4: return launch_after(rmsnorm_bwd_kernel<4, CK>, dim3(grid), dim3(r.threads), 0, s, p);
-        default: return launch_after(rmsnorm_bwd_kernel<8, CK>, dim3(grid), dim3(r.threads), 0, s, p);
-    }
+cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
+    if (b.stages == 4) return run_bwd<1, CK, 4>(p, grid, b, s);   // H <= 8192: one vector a thread
+    if (b.stages == 2) return run_bwd<2, CK, 2>(p, grid, b, s);
+    return b.vpt == 4 ? run_bwd<4, CK, 0>(p, grid, b, s) : run_bwd<8, CK, 0>(p, grid, b, s);
 }
 
 }  // namespace
 
-int rmsnorm_bwd_partials(int T) { return std::min(T, 2 * sm_count()); }
+int rmsnorm_bwd_partials(int T, int H) {
+    const BwdShape b = bwd_shape(H);
+    // with rows prefetched, a CTA that has two is hardly slower than with one
+    return std::min(b.stages ? ceil_div(T, 2) : T, b.per_sm * sm_count());
+}
 
 cudaError_t launch_rmsnorm(int T, int H, const mok_rmsnorm_args& a, cudaStream_t s) {
     NormParams p{};
@@ -325,11 +470,11 @@ cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a,
     p.dx = static_cast<__nv_bfloat16*>(a.dx);
     p.part = static_cast<float*>(a.workspace);
     p.dgain = a.dgain;
-    const int P = rmsnorm_bwd_partials(T);
-    const RowShape r = row_shape(H);
-    cudaError_t e = a.sum_q ? run_bwd<true>(p, P, r, s) : run_bwd<false>(p, P, r, s);
+    const int P = rmsnorm_bwd_partials(T, H);
+    const BwdShape b = bwd_shape(H);
+    cudaError_t e = a.sum_q ? run_bwd<true>(p, P, b, s) : run_bwd<false>(p, P, b, s);
     if (e != cudaSuccess) return e;
-    return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, 32)), dim3(256), 0, s, (const float*)p.part, P, H,
+    return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, 32)), dim3(1024), 0, s, (const float*)p.part, P, H,
                         p.dgain);
 }
 

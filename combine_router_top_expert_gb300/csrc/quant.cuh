@@ -64,6 +64,31 @@ __device__ __forceinline__ uint32_t quantize8(const float (&f)[8], uint2& o) {
     return code;
 }
 
+// The same from 8 BF16 values: the maximum is taken on packed pairs (it is one of
+// the values, so no rounding is involved).
+__device__ __forceinline__ uint32_t quantize8_bf16(const uint4& v, uint2& o) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    auto bf2 = [](uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); };
+    __nv_bfloat162 m = __hmax2(__hmax2(bf2(w[0] & 0x7fff7fffu), bf2(w[1] & 0x7fff7fffu)),
+                               __hmax2(bf2(w[2] & 0x7fff7fffu), bf2(w[3] & 0x7fff7fffu)));
+    uint32_t b = *reinterpret_cast<uint32_t*>(&m);
+    uint32_t a = max(b << 16, b & 0xffff0000u);   // non-negative fp32 patterns order like whole numbers
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const uint32_t code = e8m0_code(__uint_as_float(a));
+    const float inv = e8m0_inv_scale(code);
+    const float2 inv2 = make_float2(inv, inv);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __fmul2_rn(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), inv2);
+        q[i] = f32x2_to_e4m3x2(f.x, f.y);
+    }
+    o.x = q[0] | (q[1] << 16);
+    o.y = q[2] | (q[3] << 16);
+    return code;
+}
+
 // 8 BF16 values (one 16-byte word) to fp32 and back.
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);

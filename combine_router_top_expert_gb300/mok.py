@@ -116,6 +116,8 @@ _lib = None
 def lib():
     """Load libmok.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -190,8 +192,9 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:   # the raw handle: building a Stream object costs 2.5 us a call
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(rc, what):
@@ -415,19 +418,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dense(T, H, dtype, **tensors):
-    """The given tensors (None allowed) are contiguous CUDA tensors [T, H] of one dtype."""
-    for name, t in tensors.items():
-        if t is not None:
-            assert t.is_cuda and t.dtype == dtype and t.shape == (T, H) and t.is_contiguous(), \
-                f"{name}: contiguous {dtype} CUDA tensor [{T}, {H}] expected"
-
-
-def _f32(n, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            assert t.is_cuda and t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous(), \
-                f"{name}: contiguous float32 CUDA tensor [{n}] expected"
+def _dense(name, t, dtype, *shape):
+    """t (or None) is a contiguous CUDA tensor of this type and shape."""
+    if t is not None:
+        assert t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous(), \
+            f"{name}: contiguous {dtype} CUDA tensor {list(shape)} expected"
 
 
 def _rows(name, t, T, H):
@@ -442,11 +437,14 @@ def rmsnorm(x, gain, residual=None, eps=1e-6, sum=None, y=None, y_q=None, y_sf=N
     """Residual's addition and root-mean-square norm, into the outputs given
     (see mok_rmsnorm). x and residual may be row-strided views."""
     T, H = x.shape
-    _dense(T, H, torch.bfloat16, sum=sum, y=y)
-    _dense(T, H, torch.uint8, y_q=y_q, sum_q=sum_q)
-    _dense(T, H // 32, torch.uint8, y_sf=y_sf, sum_sf=sum_sf)
-    _f32(H, gain=gain)
-    _f32(T, rstd=rstd)
+    _dense("sum", sum, torch.bfloat16, T, H)
+    _dense("y", y, torch.bfloat16, T, H)
+    _dense("y_q", y_q, torch.uint8, T, H)
+    _dense("y_sf", y_sf, torch.uint8, T, H // 32)
+    _dense("sum_q", sum_q, torch.uint8, T, H)
+    _dense("sum_sf", sum_sf, torch.uint8, T, H // 32)
+    _dense("gain", gain, torch.float32, H)
+    _dense("rstd", rstd, torch.float32, T)
     a = RmsNormArgs(x.data_ptr(), _rows("x", x, T, H), _addr(residual),
                     0 if residual is None else _rows("residual", residual, T, H), gain.data_ptr(), eps, _addr(sum),
                     _addr(y), _addr(y_q), _addr(y_sf), _addr(sum_q), _addr(sum_sf), _addr(rstd))
@@ -460,11 +458,15 @@ def rmsnorm_bwd_workspace_size(T, H) -> int:
 def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_sf=None, dsum=None, stream=None):
     """Gradients of rmsnorm from the forward's sum, in BF16 (s) or as MXFP8 rows (s_q, s_sf)."""
     T, H = dy.shape
-    _dense(T, H, torch.bfloat16, dy=dy, dx=dx, s=s, dsum=dsum)
-    _dense(T, H, torch.uint8, s_q=s_q)
-    _dense(T, H // 32, torch.uint8, s_sf=s_sf)
-    _f32(H, gain=gain, dgain=dgain)
-    _f32(T, rstd=rstd)
+    _dense("dy", dy, torch.bfloat16, T, H)
+    _dense("dx", dx, torch.bfloat16, T, H)
+    _dense("s", s, torch.bfloat16, T, H)
+    _dense("dsum", dsum, torch.bfloat16, T, H)
+    _dense("s_q", s_q, torch.uint8, T, H)
+    _dense("s_sf", s_sf, torch.uint8, T, H // 32)
+    _dense("gain", gain, torch.float32, H)
+    _dense("dgain", dgain, torch.float32, H)
+    _dense("rstd", rstd, torch.float32, T)
     a = RmsNormBwdArgs(dy.data_ptr(), _addr(s), _addr(s_q), _addr(s_sf), _addr(dsum), rstd.data_ptr(),
                        gain.data_ptr(), dx.data_ptr(), dgain.data_ptr(), workspace.data_ptr(), workspace.numel())
     _check(lib().mok_rmsnorm_backward(T, H, ctypes.byref(a), _stream(stream)), "mok_rmsnorm_backward")
@@ -473,9 +475,9 @@ def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_s
 def dequantize_rows(x_q, x_sf, x, stream=None):
     """BF16 values of MXFP8 rows (the way back from quantize_rows)."""
     T, H = x.shape
-    _dense(T, H, torch.bfloat16, x=x)
-    _dense(T, H, torch.uint8, x_q=x_q)
-    _dense(T, H // 32, torch.uint8, x_sf=x_sf)
+    _dense("x", x, torch.bfloat16, T, H)
+    _dense("x_q", x_q, torch.uint8, T, H)
+    _dense("x_sf", x_sf, torch.uint8, T, H // 32)
     _check(lib().mok_dequantize_rows(_ptr(x_q), _ptr(x_sf), T, H, _ptr(x), _stream(stream)), "mok_dequantize_rows")
 
 
@@ -488,11 +490,13 @@ def few_workspace_size(p: Problem, cfg: Config | None = None) -> int:
 def moe_few(p: Problem, x, W_r, packed, out, workspace, bias=None, packed_shared=None, topk_idx=None, topk_w=None,
             cfg: Config | None = None, stream=None):
     """The whole layer for p.T <= FEW_MAX_TOKENS tokens (p.T * p.k <= FEW_MAX_PAIRS)."""
-    _dense(p.T, p.H, torch.bfloat16, x=x, out=out)
-    _dense(p.H, p.E, torch.float32, W_r=W_r)
-    _dense(p.T, p.k, torch.int32, topk_idx=topk_idx)
-    _dense(p.T, p.k, torch.float32, topk_w=topk_w)
-    _f32(p.E, bias=bias)
+    T, H, E, k = p.T, p.H, p.E, p.k
+    _dense("x", x, torch.bfloat16, T, H)
+    _dense("out", out, torch.bfloat16, T, H)
+    _dense("W_r", W_r, torch.float32, H, E)
+    _dense("topk_idx", topk_idx, torch.int32, T, k)
+    _dense("topk_w", topk_w, torch.float32, T, k)
+    _dense("bias", bias, torch.float32, E)
     a = FewArgs(x.data_ptr(), W_r.data_ptr(), _addr(bias), packed.data_ptr(), _addr(packed_shared), out.data_ptr(),
                 _addr(topk_idx), _addr(topk_w), workspace.data_ptr(), workspace.numel())
     _check(lib().mok_moe_few(ctypes.byref(p), ctypes.byref(a), ctypes.byref(cfg) if cfg else None, _stream(stream)),
@@ -508,7 +512,7 @@ def checkpoint_size(p: Problem) -> int:
 
 def checkpoint_save(p: Problem, x, routing, saved, ckpt, stream=None):
     """MXFP8 copy of a training forward's context (x, pre-activations, partials)."""
-    _dense(p.T, p.H, torch.bfloat16, x=x)
+    _dense("x", x, torch.bfloat16, p.T, p.H)
     if saved.numel() < saved_size(p):
         raise MokError(ERR_INVALID, "mok_checkpoint_save: saved")
     rs = routing_struct(routing)
@@ -518,7 +522,7 @@ def checkpoint_save(p: Problem, x, routing, saved, ckpt, stream=None):
 
 def checkpoint_load(p: Problem, ckpt, routing, x, saved, stream=None):
     """x and the saved context, restored for moe_backward."""
-    _dense(p.T, p.H, torch.bfloat16, x=x)
+    _dense("x", x, torch.bfloat16, p.T, p.H)
     if saved.numel() < saved_size(p):
         raise MokError(ERR_INVALID, "mok_checkpoint_load: saved")
     rs = routing_struct(routing)
