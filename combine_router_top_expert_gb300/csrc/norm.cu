@@ -70,13 +70,21 @@ struct NormParams {
     float* rstd;
 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
 }
 
 // One CTA per row; thread i holds the 8-element vectors i, i + blockDim.x, ...
@@ -180,43 +188,72 @@ __global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool PF = STAGES > 0;
     extern __shared__ __align__(16) unsigned char bwd_smem[];
-    __shared__ __align__(16) float red[2][32];
-    constexpr int kVecs = 3 * VPT;   // 16-byte slots of a thread per row: dy, dsum, s
+    __shared__ float red[2][32];
+    constexpr int kSlots = 3 * VPT;   // 16-byte slots of a thread per row: dy, dsum, s
     pdl_wait();
     pdl_allow_next();
-    const int nv = p.H / 8, nt = (int)blockDim.x;
+    const int H = p.H, nv = H / 8, nt = (int)blockDim.x, tid = (int)threadIdx.x;
+    const int rows = (p.T - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // this CTA's
+    const int64_t stride = (int64_t)gridDim.x * H;
+    const float inv_h = 1.0f / (float)H;
+    const bool has_dsum = p.dsum != nullptr;
+    // running pointers: the row to load next (dy, dsum, s), its scale codes and
+    // rstd, the row to write (dx)
+    const int64_t at = (int64_t)blockIdx.x * H + 8 * tid;
+    const __nv_bfloat16* dy = p.dy + at;
+    const __nv_bfloat16* dsum = p.dsum + at;
+    const __nv_bfloat16* s16 = p.s + at;
+    const uint8_t* s8 = p.s_q + at;
+    const uint8_t* sf = p.s_sf + at / 32;
+    const float* rstdp = p.rstd + blockIdx.x;
+    __nv_bfloat16* dx = p.dx + at;
     // slot i of buffer b: consecutive threads side by side
-    auto slot = [&](int b, int i) { return bwd_smem + ((size_t)(b * kVecs + i) * nt + threadIdx.x) * 16; };
-    auto issue = [&](int64_t t, int b) {
-        if constexpr (PF) {
-            if (t < p.T) {
+    const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(bwd_smem) + tid * 16;
+    auto slot = [&](int b, int i) { return smem0 + (uint32_t)((b * kSlots + i) * nt) * 16; };
+    auto advance = [&]() {
+        dy += stride;
+        if (has_dsum) dsum += stride;
+        if constexpr (CK) s8 += stride;
+        else s16 += stride;
+    };
+    // PF: start the copies of row n (if there is one) into buffer b
+    auto issue = [&](int n, int b) {
+        if (n < rows) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int v = threadIdx.x + i * nt;
-                    if (v < nv) {
-                        cp_async16(slot(b, i), p.dy + t * p.H + 8 * v);
-                        if (p.dsum) cp_async16(slot(b, VPT + i), p.dsum + t * p.H + 8 * v);
-                        if constexpr (CK) cp_async8(slot(b, 2 * VPT + i), p.s_q + t * p.H + 8 * v);
-                        else cp_async16(slot(b, 2 * VPT + i), p.s + t * p.H + 8 * v);
-                    }
+            for (int i = 0; i < VPT; ++i) {
+                const int o = 8 * i * nt;
+                if (tid + i * nt < nv) {
+                    cp_async16(slot(b, i), dy + o);
+                    if (has_dsum) cp_async16(slot(b, VPT + i), dsum + o);
+                    if constexpr (CK) cp_async8(slot(b, 2 * VPT + i), s8 + o);
+                    else cp_async16(slot(b, 2 * VPT + i), s16 + o);
                 }
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            advance();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto load_codes = [&](uint32_t (&code)[VPT], float& rstd) {
+        rstd = __ldg(rstdp);
+        rstdp += gridDim.x;
+        if constexpr (CK) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (tid + i * nt < nv) code[i] = __ldg(sf + i * nt / 4);
+            sf += stride / 32;
         }
     };
     // 8 elements of the sum and of dy
-    auto fetch = [&](int64_t t, int b, int i, int v, uint32_t code, float2 (&s)[4], float2 (&dy)[4]) {
-        const int64_t at = t * p.H + 8 * v;
-        unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, i)) : *reinterpret_cast<const uint4*>(p.dy + at), dy);
+    auto fetch = [&](int b, int i, uint32_t code, float2 (&s)[4], float2 (&g)[4]) {
+        const int o = 8 * i * nt;
+        unpack_pairs(PF ? ld_shared16(slot(b, i)) : *reinterpret_cast<const uint4*>(dy + o), g);
         if constexpr (CK) {
             float f[8];
-            dequantize8(PF ? *reinterpret_cast<const uint2*>(slot(b, 2 * VPT + i))
-                           : *reinterpret_cast<const uint2*>(p.s_q + at), code, f);
+            dequantize8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(s8 + o), code, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = make_float2(f[2 * j], f[2 * j + 1]);
         } else {
-            unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(p.s + at),
-                    s);
+            unpack_pairs(PF ? ld_shared16(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(s16 + o), s);
         }
     };
     constexpr bool kKeep = VPT == 1;   // gain, s and u stay in registers over the sum
@@ -227,45 +264,35 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
         for (int j = 0; j < 4; ++j) dg[i][j] = both(0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) gk[j] = sk[j] = uk[j] = both(0.f);
-    if (kKeep && threadIdx.x < nv) load8(p.gain + 8 * threadIdx.x, gk);
-    // a row's rstd and scale codes, loaded as far ahead as its vectors; the loop
-    // is unrolled over the buffers so that they stay in registers
-    constexpr int R = PF ? STAGES : 1;
-    float rstds[R];
-    uint32_t codes[R][VPT];
-    auto small = [&](int64_t t, float& rstd, uint32_t (&code)[VPT]) {
-        rstd = 0.f;
+    if (kKeep && tid < nv) load8(p.gain + 8 * tid, gk);
+
+    if constexpr (PF) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) code[i] = 0;
-        if (t < p.T) {
-            rstd = __ldg(p.rstd + t);
-            if constexpr (CK) {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int v = threadIdx.x + i * nt;
-                    if (v < nv) code[i] = __ldg(p.s_sf + t * (p.H / 32) + v / 4);
-                }
-            }
-        }
-    };
-#pragma unroll
-    for (int n = 0; n < R - 1; ++n) {
-        issue(blockIdx.x + (int64_t)n * gridDim.x, n);
-        small(blockIdx.x + (int64_t)n * gridDim.x, rstds[n], codes[n]);
+        for (int n = 0; n < STAGES - 1; ++n) issue(n, n);
     }
-    auto row = [&](int64_t t, int b, int half, float rstd, const uint32_t (&code)[VPT]) {
+    uint32_t code[VPT] = {}, code_next[VPT] = {};
+    float rstd = 0.f, rstd_next = 0.f;
+    if (rows > 0) load_codes(code, rstd);
+    int b = 0;   // buffer of this row
+#pragma unroll 1
+    for (int n = 0; n < rows; ++n) {
+        if (n + 1 < rows) load_codes(code_next, rstd_next);
+        if constexpr (PF) {
+            // into the buffer of the row before this one (this thread is done with it)
+            issue(n + STAGES - 1, b == 0 ? STAGES - 1 : b - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        }
         float2 dot = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * nt;
-            if (v < nv) {
-                float2 s[4], dy[4], g[4];
-                fetch(t, b, i, v, code[i], s, dy);
-                if constexpr (!kKeep) load8(p.gain + 8 * v, g);
+            if (tid + i * nt < nv) {
+                float2 s[4], d[4], g[4];
+                fetch(b, i, code[i], s, d);
+                if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 u = __fmul2_rn(dy[j], kKeep ? gk[j] : g[j]);
-                    dg[i][j] = __ffma2_rn(__fmul2_rn(dy[j], both(rstd)), s[j], dg[i][j]);
+                    const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
+                    dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd)), s[j], dg[i][j]);
                     dot = __ffma2_rn(u, s[j], dot);
                     if constexpr (kKeep) {
                         sk[j] = s[j];
@@ -275,24 +302,18 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
             }
         }
         // dx = dsum + rstd u - c s with c = rstd^3 sum(u s) / H
-        const float c = -rstd * (rstd * (rstd * (block_sum(dot.x + dot.y, red[half]) / (float)p.H)));
+        const float c = -rstd * (rstd * (rstd * (block_sum(dot.x + dot.y, red[n & 1]) * inv_h)));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * nt;
-            if (v < nv) {
-                float2 d[4];
-                if (p.dsum) {
-                    unpack_pairs(PF ? *reinterpret_cast<const uint4*>(slot(b, VPT + i))
-                               : *reinterpret_cast<const uint4*>(p.dsum + t * p.H + 8 * v), d);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d[j] = both(0.f);
-                }
+            if (tid + i * nt < nv) {
+                const int o = 8 * i * nt;
+                float2 d[4] = {};
+                if (has_dsum) unpack_pairs(PF ? ld_shared16(slot(b, VPT + i)) : *reinterpret_cast<const uint4*>(dsum + o), d);
                 float2 s[4], u[4];
                 if constexpr (!kKeep) {
                     float2 g[4];
-                    fetch(t, b, i, v, code[i], s, u);
-                    load8(p.gain + 8 * v, g);
+                    fetch(b, i, code[i], s, u);
+                    load8(p.gain + 8 * (tid + i * nt), g);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(u[j], g[j]);
                 }
@@ -301,31 +322,25 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
                     const float2 w = __ffma2_rn(both(rstd), kKeep ? uk[j] : u[j], d[j]);
                     d[j] = __ffma2_rn(both(c), kKeep ? sk[j] : s[j], w);
                 }
-                *reinterpret_cast<uint4*>(p.dx + t * p.H + 8 * v) = pack_pairs(d);
+                *reinterpret_cast<uint4*>(dx + o) = pack_pairs(d);
             }
         }
-    };
-    int half = 0;   // which of the two sums' scratch
-    for (int64_t t0 = blockIdx.x; t0 < p.T; t0 += (int64_t)R * gridDim.x) {
+        dx += stride;
+        if constexpr (PF) {
+            if (++b == STAGES) b = 0;
+        } else {
+            advance();
+        }
+        rstd = rstd_next;
 #pragma unroll
-        for (int n = 0; n < R; ++n, half ^= 1) {
-            const int64_t t = t0 + (int64_t)n * gridDim.x, ahead = t + (int64_t)(R - 1) * gridDim.x;
-            if (t < p.T) {
-                // into the buffer of the row before this one (this thread is done with it)
-                constexpr int kBack = R - 1;
-                issue(ahead, (n + kBack) % R);
-                small(ahead, rstds[(n + kBack) % R], codes[(n + kBack) % R]);
-                if constexpr (PF) asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
-                row(t, n, half, rstds[n], codes[n]);
-            }
-        }
+        for (int i = 0; i < VPT; ++i) code[i] = code_next[i];
     }
     if constexpr (PF) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * nt;
+        const int v = tid + i * nt;
         if (v < nv) {
-            float* o = p.part + (int64_t)blockIdx.x * p.H + 8 * v;
+            float* o = p.part + (int64_t)blockIdx.x * H + 8 * v;
             *reinterpret_cast<float4*>(o) = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
             *reinterpret_cast<float4*>(o + 4) = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
         }
