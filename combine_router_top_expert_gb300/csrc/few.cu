@@ -34,6 +34,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "gemm.cuh"
 #include "moves.cuh"
@@ -49,28 +50,31 @@ namespace {
 // 1, then the bias), the top-k with its weights, the MXFP8 rows of x, and the
 // zeroed counters of kernel 2.
 //
-// A cluster of 8 CTAs takes 8 tokens x 32 experts. CTA r holds the chains r,
-// r + 8, r + 16, r + 24, so two levels of the adding tree stay inside it and one
-// value per (token, expert) goes to the first CTA. Warp w runs chain r + 8 (w %
-// 4) for four of the tokens, one expert a lane. The work is about 100 KB of W_r
-// per CTA: what counts is to have the loads in flight early, so W_r and x stream
-// through a ring of cp.async stages that holds H <= 8192 whole. With more than 32
-// experts the clusters of a token group count themselves in, and the last one
-// takes the top-k from the logits of all.
+// A cluster of CL (8 or 16) CTAs takes 8 tokens x 32 experts. CTA r holds the
+// chains r, r + CL, ..., so the tree's first levels stay inside it and one value
+// per (token, expert) goes to the first CTA. A warp runs one chain for some of the
+// tokens, one expert a lane. The work is about 100 KB of W_r per CTA (CL = 8): what
+// counts is to have the loads in flight early, so W_r and x stream through a ring
+// of cp.async stages that holds H <= 8192 whole. With more than 32 experts the
+// clusters of a token group count themselves in, and the last one takes the top-k
+// from the logits of all.
 // ---------------------------------------------------------------------------
 constexpr int kLgThreads = 256;
+// Clusters up to which 16 CTAs are taken (H = 7168, 32 experts: 8.2 us against 9.6
+// with one token, 10.1 against 13.5 with 16; 17.5 against 14.8 with 64 tokens, whose
+// 8 wide clusters do not all fit at once).
+constexpr int kLgWideClusters = 4;
 constexpr int kLgTokens = 8;       // tokens per cluster
-constexpr int kLgCluster = 8;
-constexpr int kLgChunks = 4;       // 256-wide h chunks per stage
-constexpr int kLgWBytes = kLgChunks * 32 * 32 * 4;
-constexpr int kLgXBytes = kLgChunks * kLgTokens * 32 * 2;
+constexpr int kLgRows = 128;       // rows of W_r per stage and CTA
+constexpr int kLgWBytes = kLgRows * 32 * 4;
+constexpr int kLgXBytes = kLgTokens * kLgRows * 2;
 constexpr int kLgStageBytes = kLgWBytes + kLgXBytes;
-// after the ring: the four chains' sums of this CTA, the 8 CTAs' sums (written
-// by all of them in the first one), the logits
-constexpr int kLgPartBytes = 4 * kLgTokens * 32 * 4;
-constexpr int kLgRedBytes = kLgCluster * kLgTokens * 32 * 4;
-constexpr int lg_smem_bytes(int stages) {
-    return stages * kLgStageBytes + kLgPartBytes + kLgRedBytes + kLgTokens * kMaxE * 4;
+// after the ring: this CTA's chain sums, the CTAs' sums (written by all of them in
+// the first one), the logits
+__host__ __device__ constexpr int lg_part_bytes(int cl) { return 32 / cl * kLgTokens * 32 * 4; }
+__host__ __device__ constexpr int lg_red_bytes(int cl) { return cl * kLgTokens * 32 * 4; }
+__host__ __device__ constexpr int lg_smem_bytes(int cl, int stages) {
+    return stages * kLgStageBytes + lg_part_bytes(cl) + lg_red_bytes(cl) + kLgTokens * kMaxE * 4;
 }
 
 struct FewLogitsParams {
@@ -150,22 +154,25 @@ __device__ __forceinline__ void few_topk(const float* lg, const FewLogitsParams&
     }
 }
 
-// Grid: (8 * ceil(E / 32), token groups).
-template <int STAGES>
-__global__ void __cluster_dims__(kLgCluster, 1, 1) __launch_bounds__(kLgThreads)
+// Grid: (CL * ceil(E / 32), token groups), clusters of CL along x.
+template <int CL, int STAGES>
+__global__ void __launch_bounds__(kLgThreads)
 few_logits_kernel(const FewLogitsParams p) {
+    constexpr int NCH = 32 / CL;               // chains of a CTA; also tokens of a warp
+    constexpr int kChunkRows = 8 * NCH;        // rows of W_r per 256-wide chunk of h
+    constexpr int kChunks = kLgRows / kChunkRows;
     extern __shared__ __align__(128) unsigned char lg_smem[];
     __shared__ int s_last;
-    float* part = reinterpret_cast<float*>(lg_smem + STAGES * kLgStageBytes);   // [chain of four][token][expert]
-    float* red = part + kLgPartBytes / 4;                                       // [CTA][token][expert]
-    float* lg = red + kLgRedBytes / 4;                                          // [token][kMaxE]
+    float* part = reinterpret_cast<float*>(lg_smem + STAGES * kLgStageBytes);   // [chain][token][expert]
+    float* red = part + lg_part_bytes(CL) / 4;                                  // [CTA][token][expert]
+    float* lg = red + lg_red_bytes(CL) / 4;                                     // [token][kMaxE]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)tc::cluster_ctarank();
-    const int e0 = ((int)blockIdx.x / kLgCluster) * 32, t0 = (int)blockIdx.y * kLgTokens;
+    const int e0 = ((int)blockIdx.x / CL) * 32, t0 = (int)blockIdx.y * kLgTokens;
     const int ntok = min(kLgTokens, p.T - t0);
     const int nchunks = ceil_div(p.H, 256);
-    const int total = ceil_div(nchunks, kLgChunks);      // stages
-    const int cl = warp & 3, th = warp >> 2;             // chain of this CTA's four, token half
+    const int total = ceil_div(nchunks, kChunks);        // stages
+    const int cl = warp % NCH, tw = NCH * (warp / NCH);  // this warp's chain and first token
     const bool vec = (p.E & 3) == 0 && (reinterpret_cast<uintptr_t>(p.W_r) & 15) == 0;
 
     // every CTA of the cluster runs before any writes to the first one's shared
@@ -174,34 +181,33 @@ few_logits_kernel(const FewLogitsParams p) {
     pdl_wait();
     pdl_allow_next();
 
-    // row r (0..31) of a chunk's share: chain rank + 8 (r / 8), h = 256 i + 8 chain + r % 8
-    auto h_of = [&](int i, int r) { return 256 * i + 8 * (rank + 8 * (r >> 3)) + (r & 7); };
+    // row r of a chunk's share: chain rank + CL (r / 8), h = 256 i + 8 chain + r % 8
+    auto h_of = [&](int i, int r) { return 256 * i + 8 * (rank + CL * (r >> 3)) + (r & 7); };
     auto issue = [&](int n) {
         if (n < total) {
-            const int c0 = n * kLgChunks;
-            unsigned char* st = lg_smem + (n % STAGES) * kLgStageBytes;
-            const uint32_t ws = tc::smem_u32(st), xs = ws + kLgWBytes;
+            const int c0 = n * kChunks;
+            const uint32_t ws = tc::smem_u32(lg_smem + (n % STAGES) * kLgStageBytes), xs = ws + kLgWBytes;
             if (vec) {
 #pragma unroll
-                for (int i = 0; i < kLgChunks; ++i) {   // 32 rows x 8 vectors a chunk
-                    const int r = tid >> 3, v = tid & 7;
-                    const int h = h_of(c0 + i, r), e = e0 + 4 * v;
+                for (int q = 0; q < kLgRows * 8 / kLgThreads; ++q) {   // rows x 8 vectors
+                    const int r = (tid >> 3) + q * (kLgThreads / 8), v = tid & 7;
+                    const int h = h_of(c0 + r / kChunkRows, r % kChunkRows), e = e0 + 4 * v;
                     const bool in = h < p.H && e < p.E;
-                    cp_async16(ws + ((i * 32 + r) * 32 + 4 * v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+                    cp_async16(ws + (r * 32 + 4 * v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
                 }
             } else {
-                for (int j = tid; j < kLgChunks * 1024; j += kLgThreads) {
-                    const int i = j >> 10, r = (j >> 5) & 31, v = j & 31;
-                    const int h = h_of(c0 + i, r), e = e0 + v;
+                for (int j = tid; j < kLgRows * 32; j += kLgThreads) {
+                    const int r = j >> 5, v = j & 31;
+                    const int h = h_of(c0 + r / kChunkRows, r % kChunkRows), e = e0 + v;
                     const bool in = h < p.H && e < p.E;
-                    cp_async4(ws + ((i * 32 + r) * 32 + v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+                    cp_async4(ws + (r * 32 + v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
                 }
             }
-            if (tid < kLgChunks * kLgTokens * 4) {      // [chunk][token][chain of four][8 h]
-                const int i = tid / (kLgTokens * 4), t = (tid >> 2) & (kLgTokens - 1), v = tid & 3;
+            if (tid < kLgRows) {      // [chunk][token][chain][8 h]
+                const int i = tid / (kLgTokens * NCH), t = (tid / NCH) % kLgTokens, v = tid % NCH;
                 const int h = h_of(c0 + i, 8 * v);
                 const bool in = h < p.H && t < ntok;
-                cp_async16(xs + ((i * kLgTokens + t) * 32 + 8 * v) * 2, in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
+                cp_async16(xs + tid * 16, in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
             }
         }
         cp_async_commit();   // one group per stage, empty past the end
@@ -211,13 +217,13 @@ few_logits_kernel(const FewLogitsParams p) {
     // while the first copies are in flight: the counters of kernel 2, and x in
     // 8 bits (one block of 32 a thread; the bytes of mok_quantize_rows)
     if (e0 == 0) {
-        const int part_of = (int)blockIdx.y * kLgCluster + rank;
-        for (int i = part_of * kLgThreads + tid; i < p.zero_words; i += (int)gridDim.y * kLgCluster * kLgThreads)
+        const int part_of = (int)blockIdx.y * CL + rank;
+        for (int i = part_of * kLgThreads + tid; i < p.zero_words; i += (int)gridDim.y * CL * kLgThreads)
             p.zero[i] = 0;
     }
     if (p.xq && e0 == 0) {
         const int nb = p.H / 32;
-        for (int j = rank * kLgThreads + tid; j < ntok * nb; j += kLgCluster * kLgThreads) {
+        for (int j = rank * kLgThreads + tid; j < ntok * nb; j += CL * kLgThreads) {
             const int t = t0 + j / nb, b = j % nb;
             uint4 o0, o1;
             const uint32_t code = quantize_block32(p.x + (int64_t)t * p.H + b * 32, o0, o1);
@@ -229,25 +235,25 @@ few_logits_kernel(const FewLogitsParams p) {
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[NCH] = {};
     for (int n = 0; n < total; ++n) {
         cp_async_wait<STAGES - 2>();
         __syncthreads();              // stage n has landed for every thread; stage n - 1 is consumed
         issue(n + STAGES - 1);
-        const int c0 = n * kLgChunks;
+        const int c0 = n * kChunks;
         const float* ws = reinterpret_cast<const float*>(lg_smem + (n % STAGES) * kLgStageBytes);
         const unsigned char* xs = lg_smem + (n % STAGES) * kLgStageBytes + kLgWBytes;
 #pragma unroll
-        for (int i = 0; i < kLgChunks; ++i) {
+        for (int i = 0; i < kChunks; ++i) {
             if (h_of(c0 + i, 8 * cl) < p.H) {
                 float w[8];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) w[m] = ws[(i * 32 + 8 * cl + m) * 32 + lane];
+                for (int m = 0; m < 8; ++m) w[m] = ws[(i * kChunkRows + 8 * cl + m) * 32 + lane];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (4 * th + u < ntok) {
+                for (int u = 0; u < NCH; ++u) {
+                    if (tw + u < ntok) {
                         float f[8];
-                        unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + 4 * th + u) * 32 + 8 * cl) * 2), f);
+                        unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + tw + u) * NCH + cl) * 16), f);
 #pragma unroll
                         for (int m = 0; m < 8; ++m) acc[u] = fmaf(f[m], w[m], acc[u]);
                     }
@@ -255,28 +261,31 @@ few_logits_kernel(const FewLogitsParams p) {
             }
         }
     }
-    // the tree over the 32 chains: distances 16 and 8 here, 4, 2 and 1 over the
-    // CTAs, then the bias
+    // the tree over the 32 chains: distances 16 (and 8 with four chains a CTA)
+    // here, the others over the CTAs, then the bias
     constexpr int P = kLgTokens * 32;
     const int o = warp * 32 + lane;                      // token = warp
 #pragma unroll
-    for (int u = 0; u < 4; ++u) part[(cl * kLgTokens + 4 * th + u) * 32 + lane] = acc[u];
+    for (int u = 0; u < NCH; ++u) part[(cl * kLgTokens + tw + u) * 32 + lane] = acc[u];
     __syncthreads();
-    const float v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
+    float v;
+    if constexpr (NCH == 4) v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
+    else v = part[o] + part[P + o];
+    static_assert(NCH == 4 || NCH == 2, "chains per CTA");
     const uint32_t dst = tc::mapa_shared(tc::smem_u32(red + rank * P + o), 0);
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
     tc::cluster_sync();
     if (rank != 0) return;
-    float s[kLgCluster];
+    float s[CL];
 #pragma unroll
-    for (int c = 0; c < kLgCluster; ++c) s[c] = red[c * P + o];
+    for (int c = 0; c < CL; ++c) s[c] = red[c * P + o];
 #pragma unroll
-    for (int d = kLgCluster / 2; d >= 1; d >>= 1)
+    for (int d = CL / 2; d >= 1; d >>= 1)
 #pragma unroll
         for (int c = 0; c < d; ++c) s[c] = s[c] + s[c + d];
     const int e = e0 + lane;
     const float l = e < p.E && p.bias ? s[0] + p.bias[e] : s[0];
-    if (gridDim.x == kLgCluster) {                       // 32 experts at most: these are all logits
+    if (gridDim.x == CL) {                               // 32 experts at most: these are all logits
         lg[warp * kMaxE + lane] = l;
         __syncwarp();
     } else {
@@ -284,7 +293,7 @@ few_logits_kernel(const FewLogitsParams p) {
         __syncthreads();
         if (tid == 0) {
             __threadfence();
-            s_last = atomicAdd(p.arrived + blockIdx.y, 1) == (int)(gridDim.x / kLgCluster) - 1;
+            s_last = atomicAdd(p.arrived + blockIdx.y, 1) == (int)(gridDim.x / CL) - 1;
             __threadfence();
         }
         __syncthreads();
@@ -1118,11 +1127,57 @@ FewLayout few_layout(const mok_problem* p, int ctas) {
     return L;
 }
 
-template <int STAGES>
-cudaError_t run_logits(const FewLogitsParams& p, dim3 grid, cudaStream_t s) {
-    auto kern = few_logits_kernel<STAGES>;
-    ensure_smem_attr(reinterpret_cast<const void*>(kern), lg_smem_bytes(STAGES));
-    return launch_after(kern, grid, dim3(kLgThreads), lg_smem_bytes(STAGES), s, p);
+template <int CL, int STAGES>
+cudaError_t run_logits(const FewLogitsParams& p, cudaStream_t s) {
+    auto kern = few_logits_kernel<CL, STAGES>;
+    const int smem = lg_smem_bytes(CL, STAGES);
+    ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(CL * ceil_div(p.E, 32), ceil_div(p.T, kLgTokens));
+    cfg.blockDim = dim3(kLgThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Clusters of 16 CTAs are beyond the portable 8: whether this device can hold one
+// (asked once per device).
+bool wide_clusters_ok() {
+    static std::atomic<int8_t> known[64];   // 0: not asked, 1: yes, 2: no
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (const int8_t k = known[dev].load(std::memory_order_relaxed)) return k == 1;
+    auto kern = few_logits_kernel<16, 5>;
+    const int smem = lg_smem_bytes(16, 5);
+    ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    int n = 0;
+    bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    if (ok) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kLgThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        ok = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+    }
+    if (!ok) cudaGetLastError();
+    known[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
+    return ok;
 }
 
 template <bool MX, int NT>
@@ -1225,11 +1280,15 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     if (!ok) return cudaErrorInvalidValue;
 
     cudaError_t e = cudaSuccess;
-    const dim3 grid(kLgCluster * ceil_div(E, 32), ceil_div(T, kLgTokens));
-    if (E > 32) e = cudaMemsetAsync(ws + L.arrived, 0, grid.y * 4, s);
-    // a ring for all of H <= 8192 takes an SM for itself; with more clusters than
-    // fit that way, a shorter one lets two CTAs share an SM
-    if (e == cudaSuccess) e = grid.x * grid.y <= 64 ? run_logits<9>(lp, grid, s) : run_logits<5>(lp, grid, s);
+    const int groups = ceil_div(T, kLgTokens), clusters = groups * ceil_div(E, 32);
+    if (E > 32) e = cudaMemsetAsync(ws + L.arrived, 0, groups * 4, s);
+    // few clusters are spread over 16 CTAs each; up to 64 CTAs of 8-wide clusters
+    // hold all of H <= 8192 in their rings, an SM to each; more keep the ring short
+    // so that two CTAs share an SM
+    if (e == cudaSuccess)
+        e = clusters <= kLgWideClusters && wide_clusters_ok() ? run_logits<16, 5>(lp, s)
+            : clusters <= 8                                   ? run_logits<8, 9>(lp, s)
+                                                              : run_logits<8, 5>(lp, s);
     if (e != cudaSuccess) return e;
     return mx ? run_ffn<true>(tm, p, c.num_sms, s) : run_ffn<false>(tm, p, c.num_sms, s);
 }

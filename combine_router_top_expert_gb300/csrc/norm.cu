@@ -18,6 +18,8 @@ namespace mok {
 
 namespace {
 
+constexpr int kBwdGroups = 8;   // row groups of a CTA of the backward, at most
+
 // Sum over the CTA of one value per thread, the same in every thread and in
 // every run: shuffles in each warp, then over the warps' sums. `red` holds a float
 // per warp; two alternating buffers let one barrier serve each call.
@@ -31,6 +33,30 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
+}
+
+// The same for N values of the threads of one group (nt threads, whole warps;
+// `id` < kBwdGroups names it).
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[32], int id, int nt) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if (nt == 32) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[i][((int)threadIdx.x % nt) >> 5] = v[i];
+    }
+    __syncwarp();
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(nt) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane < (nt >> 5) ? red[i][lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
 }
 
 // 8 BF16 values as four pairs.
@@ -75,6 +101,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
     uint4 v;
@@ -162,6 +191,7 @@ rmsnorm_kernel(const NormParams p) {
 
 struct NormBwdParams {
     int T, H;
+    int group;                 // threads of a row group
     const __nv_bfloat16* dy;
     const __nv_bfloat16* s;    // the sum in BF16, or
     const uint8_t* s_q;        // its MXFP8 rows
@@ -174,175 +204,218 @@ struct NormBwdParams {
     float* dgain;              // [H]
 };
 
-// CTA b takes rows b, b + gridDim.x, ...; its threads keep their columns'
-// dgain in registers over all of its rows and write one partial row at the
-// end, which rmsnorm_dgain_kernel adds up in CTA order.
+// A row belongs to a group of `group` threads (whole warps); a CTA has one or
+// more groups, and all groups of the grid take rows in turn. A thread keeps its
+// columns' dgain in registers over all of its rows; at the end the CTA's groups
+// are added up in shared memory and one partial row goes to rmsnorm_dgain_kernel,
+// which adds those of all CTAs in order.
 //
-// A row's block-wide sum stands between its loads and its stores, so the loads
-// of the next rows have to be in flight meanwhile: each thread copies its own
-// vectors of STAGES - 1 rows ahead to shared memory (cp.async; nobody else reads
-// them, so no barrier is needed). Up to H = 8192 what the second half needs stays
-// in registers; longer rows read their buffers twice. Rows too long for two buffers (STAGES = 0) are read from memory each time.
-template <int VPT, bool CK, int STAGES>
+// A row's group-wide sum stands between its loads and its stores, so the loads of
+// the next rows have to be in flight meanwhile: each thread copies its own vectors
+// of the rows ahead to shared memory (cp.async; nobody else reads them, so no
+// barrier is needed). With one group to an SM nothing else runs while it waits for
+// the sum, so it takes two rows (ROWS) to a barrier. Up to H = 8192 what the second
+// half needs stays in registers; longer rows read their buffers twice. Rows too
+// long for two buffers (STAGES = 0) are read from memory each time.
+template <int VPT, bool CK, int STAGES, int ROWS>
 __global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool PF = STAGES > 0;
+    static_assert(PF ? STAGES % ROWS == 0 && STAGES > ROWS : ROWS == 1, "whole steps of rows in the ring");
     extern __shared__ __align__(16) unsigned char bwd_smem[];
-    __shared__ float red[2][32];
+    __shared__ float red[kBwdGroups][2][ROWS][32];
     constexpr int kSlots = 3 * VPT;   // 16-byte slots of a thread per row: dy, dsum, s
     pdl_wait();
     pdl_allow_next();
-    const int H = p.H, nv = H / 8, nt = (int)blockDim.x, tid = (int)threadIdx.x;
-    const int rows = (p.T - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // this CTA's
-    const int64_t stride = (int64_t)gridDim.x * H;
+    const int H = p.H, nv = H / 8, nt = p.group;
+    const int grp = (int)threadIdx.x / nt, tid = (int)threadIdx.x % nt, groups = (int)blockDim.x / nt;
+    const int first = (int)blockIdx.x * groups + grp, total = (int)gridDim.x * groups;
+    const int rows = first < p.T ? (p.T - first + total - 1) / total : 0;   // this group's
+    const int64_t stride = (int64_t)total * H;
     const float inv_h = 1.0f / (float)H;
     const bool has_dsum = p.dsum != nullptr;
-    // running pointers: the row to load next (dy, dsum, s), its scale codes and
-    // rstd, the row to write (dx)
-    const int64_t at = (int64_t)blockIdx.x * H + 8 * tid;
-    const __nv_bfloat16* dy = p.dy + at;
-    const __nv_bfloat16* dsum = p.dsum + at;
-    const __nv_bfloat16* s16 = p.s + at;
-    const uint8_t* s8 = p.s_q + at;
-    const uint8_t* sf = p.s_sf + at / 32;
-    const float* rstdp = p.rstd + blockIdx.x;
-    __nv_bfloat16* dx = p.dx + at;
+    // running element offsets of this thread's first vector: in the row to load
+    // next and in the row at hand
+    int64_t in = (int64_t)first * H + 8 * tid, out = in;
+    int next = first;   // row whose rstd is loaded next
     // slot i of buffer b: consecutive threads side by side
-    const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(bwd_smem) + tid * 16;
-    auto slot = [&](int b, int i) { return smem0 + (uint32_t)((b * kSlots + i) * nt) * 16; };
-    auto advance = [&]() {
-        dy += stride;
-        if (has_dsum) dsum += stride;
-        if constexpr (CK) s8 += stride;
-        else s16 += stride;
-    };
-    // PF: start the copies of row n (if there is one) into buffer b
+    const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(bwd_smem) + threadIdx.x * 16;
+    auto slot = [&](int b, int i) { return smem0 + (uint32_t)((b * kSlots + i) * (int)blockDim.x) * 16; };
+    // behind the ring, the scale codes of the same rows: a byte for four threads,
+    // copied four at a time by every 16th thread where their address allows
+    unsigned char* codes = bwd_smem + (size_t)STAGES * kSlots * blockDim.x * 16;
+    auto code_slot = [&](int b, int i) { return codes + ((b * VPT + i) * (int)blockDim.x + (int)threadIdx.x) / 4; };
+    const bool ring_codes = PF && CK && (H & 127) == 0 && (reinterpret_cast<uintptr_t>(p.s_sf) & 3) == 0;
+    // PF: start the copies of rows n .. n + ROWS - 1 (those there are) into the
+    // buffers from b on, as one group of copies
     auto issue = [&](int n, int b) {
-        if (n < rows) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int o = 8 * i * nt;
-                if (tid + i * nt < nv) {
-                    cp_async16(slot(b, i), dy + o);
-                    if (has_dsum) cp_async16(slot(b, VPT + i), dsum + o);
-                    if constexpr (CK) cp_async8(slot(b, 2 * VPT + i), s8 + o);
-                    else cp_async16(slot(b, 2 * VPT + i), s16 + o);
+        for (int r = 0; r < ROWS; ++r) {
+            if (n + r < rows) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int o = 8 * i * nt;
+                    if (tid + i * nt < nv) {
+                        cp_async16(slot(b + r, i), p.dy + in + o);
+                        if (has_dsum) cp_async16(slot(b + r, VPT + i), p.dsum + in + o);
+                        if constexpr (CK) {
+                            cp_async8(slot(b + r, 2 * VPT + i), p.s_q + in + o);
+                            if (ring_codes && (tid & 15) == 0)
+                                cp_async4((uint32_t)__cvta_generic_to_shared(code_slot(b + r, i)), p.s_sf + (in + o) / 32);
+                        } else {
+                            cp_async16(slot(b + r, 2 * VPT + i), p.s + in + o);
+                        }
+                    }
                 }
+                in += stride;
             }
-            advance();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto load_codes = [&](uint32_t (&code)[VPT], float& rstd) {
-        rstd = __ldg(rstdp);
-        rstdp += gridDim.x;
-        if constexpr (CK) {
+    auto load_rstd = [&](int n, float (&rstd)[ROWS]) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (tid + i * nt < nv) code[i] = __ldg(sf + i * nt / 4);
-            sf += stride / 32;
+        for (int r = 0; r < ROWS; ++r) {
+            if (n + r < rows) {
+                rstd[r] = __ldg(p.rstd + next);
+                next += total;
+            }
         }
     };
-    // 8 elements of the sum and of dy
-    auto fetch = [&](int b, int i, uint32_t code, float2 (&s)[4], float2 (&g)[4]) {
+    // 8 elements of the sum (`out` is the offset of the row at hand)
+    auto fetch_s = [&](int b, int i, float2 (&s)[4]) {
         const int o = 8 * i * nt;
-        unpack_pairs(PF ? ld_shared16(slot(b, i)) : *reinterpret_cast<const uint4*>(dy + o), g);
         if constexpr (CK) {
             float f[8];
-            dequantize8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(s8 + o), code, f);
+            const uint32_t code = ring_codes ? *code_slot(b, i) : __ldg(p.s_sf + (out + o) / 32);
+            dequantize8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(p.s_q + in + o), code, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = make_float2(f[2 * j], f[2 * j + 1]);
         } else {
-            unpack_pairs(PF ? ld_shared16(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(s16 + o), s);
+            unpack_pairs(PF ? ld_shared16(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(p.s + in + o), s);
         }
     };
-    constexpr bool kKeep = VPT == 1;   // gain, s and u stay in registers over the sum
-    float2 dg[VPT][4], gk[4], sk[4], uk[4];
+    auto fetch_dy = [&](int b, int i, float2 (&d)[4]) {
+        unpack_pairs(PF ? ld_shared16(slot(b, i)) : *reinterpret_cast<const uint4*>(p.dy + in + 8 * i * nt), d);
+    };
+    constexpr bool kKeep = VPT == 1;   // the gain and the rows' s stay in registers over the sum
+    float2 dg[VPT][4], gk[4], sk[ROWS][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dg[i][j] = both(0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) gk[j] = sk[j] = uk[j] = both(0.f);
+    for (int j = 0; j < 4; ++j) {
+        gk[j] = both(0.f);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) sk[r][j] = both(0.f);
+    }
     if (kKeep && tid < nv) load8(p.gain + 8 * tid, gk);
 
+    constexpr int kAhead = PF ? STAGES / ROWS - 1 : 0;   // steps in flight beyond this one
     if constexpr (PF) {
 #pragma unroll
-        for (int n = 0; n < STAGES - 1; ++n) issue(n, n);
+        for (int n = 0; n < kAhead; ++n) issue(n * ROWS, n * ROWS);
     }
-    uint32_t code[VPT] = {}, code_next[VPT] = {};
-    float rstd = 0.f, rstd_next = 0.f;
-    if (rows > 0) load_codes(code, rstd);
-    int b = 0;   // buffer of this row
+    float rstd[ROWS] = {}, rstd_next[ROWS] = {};
+    load_rstd(0, rstd);
+    int b = 0, half = 0;   // buffer of this step's first row; which of the sums' scratch
 #pragma unroll 1
-    for (int n = 0; n < rows; ++n) {
-        if (n + 1 < rows) load_codes(code_next, rstd_next);
+    for (int n = 0; n < rows; n += ROWS, half ^= 1) {
+        load_rstd(n + ROWS, rstd_next);
         if constexpr (PF) {
-            // into the buffer of the row before this one (this thread is done with it)
-            issue(n + STAGES - 1, b == 0 ? STAGES - 1 : b - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+            // into the buffers of the step before this one (this thread is done with them)
+            issue(n + kAhead * ROWS, b == 0 ? STAGES - ROWS : b - ROWS);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            if constexpr (CK) __syncwarp();   // the codes are other lanes' copies
         }
-        float2 dot = both(0.f);
+        float dots[ROWS];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (tid + i * nt < nv) {
-                float2 s[4], d[4], g[4];
-                fetch(b, i, code[i], s, d);
-                if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
+        for (int r = 0; r < ROWS; ++r) {
+            float2 dot = both(0.f);
+            if (n + r < rows) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
-                    dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd)), s[j], dg[i][j]);
-                    dot = __ffma2_rn(u, s[j], dot);
-                    if constexpr (kKeep) {
-                        sk[j] = s[j];
-                        uk[j] = u;
+                for (int i = 0; i < VPT; ++i) {
+                    if (tid + i * nt < nv) {
+                        float2 s[4], d[4], g[4];
+                        fetch_s(b + r, i, s);
+                        fetch_dy(b + r, i, d);
+                        if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
+                            dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd[r])), s[j], dg[i][j]);
+                            dot = __ffma2_rn(u, s[j], dot);
+                            if constexpr (kKeep) sk[r][j] = s[j];
+                        }
                     }
                 }
             }
+            dots[r] = dot.x + dot.y;
         }
-        // dx = dsum + rstd u - c s with c = rstd^3 sum(u s) / H
-        const float c = -rstd * (rstd * (rstd * (block_sum(dot.x + dot.y, red[n & 1]) * inv_h)));
+        group_sum<ROWS>(dots, red[grp][half], grp, nt);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (tid + i * nt < nv) {
-                const int o = 8 * i * nt;
-                float2 d[4] = {};
-                if (has_dsum) unpack_pairs(PF ? ld_shared16(slot(b, VPT + i)) : *reinterpret_cast<const uint4*>(dsum + o), d);
-                float2 s[4], u[4];
-                if constexpr (!kKeep) {
-                    float2 g[4];
-                    fetch(b, i, code[i], s, u);
-                    load8(p.gain + 8 * (tid + i * nt), g);
+        for (int r = 0; r < ROWS; ++r) {
+            if (n + r < rows) {
+                // dx = dsum + rstd u - c s with u = gain dy, c = rstd^3 sum(u s) / H
+                const float c = -rstd[r] * (rstd[r] * (rstd[r] * (dots[r] * inv_h)));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) u[j] = __fmul2_rn(u[j], g[j]);
+                for (int i = 0; i < VPT; ++i) {
+                    if (tid + i * nt < nv) {
+                        const int o = 8 * i * nt;
+                        float2 d[4] = {}, s[4], u[4], g[4];
+                        if (has_dsum)
+                            unpack_pairs(PF ? ld_shared16(slot(b + r, VPT + i)) : *reinterpret_cast<const uint4*>(p.dsum + in + o), d);
+                        fetch_dy(b + r, i, u);
+                        if constexpr (!kKeep) {
+                            fetch_s(b + r, i, s);
+                            load8(p.gain + 8 * (tid + i * nt), g);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 w = __fmul2_rn(u[j], kKeep ? gk[j] : g[j]);
+                            d[j] = __ffma2_rn(both(rstd[r]), w, d[j]);
+                            d[j] = __ffma2_rn(both(c), kKeep ? sk[r][j] : s[j], d[j]);
+                        }
+                        *reinterpret_cast<uint4*>(p.dx + out + o) = pack_pairs(d);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 w = __ffma2_rn(both(rstd), kKeep ? uk[j] : u[j], d[j]);
-                    d[j] = __ffma2_rn(both(c), kKeep ? sk[j] : s[j], w);
-                }
-                *reinterpret_cast<uint4*>(dx + o) = pack_pairs(d);
+                out += stride;
+                if constexpr (!PF) in = out;
             }
         }
-        dx += stride;
         if constexpr (PF) {
-            if (++b == STAGES) b = 0;
-        } else {
-            advance();
+            b += ROWS;
+            if (b == STAGES) b = 0;
         }
-        rstd = rstd_next;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) code[i] = code_next[i];
+        for (int r = 0; r < ROWS; ++r) {
+            rstd[r] = rstd_next[r];
+        }
     }
     if constexpr (PF) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float* part = p.part + (int64_t)blockIdx.x * H;
+    if (groups > 1) {
+        // the groups' sums, added in group order (VPT = 1: H floats fit the ring)
+        __syncthreads();
+        float* sum = reinterpret_cast<float*>(bwd_smem);
+        if (tid < nv) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(sum + grp * H + 8 * tid + 2 * j) = dg[0][j];
+        }
+        __syncthreads();
+        for (int h = threadIdx.x; h < H; h += blockDim.x) {
+            float v = 0.f;
+            for (int g = 0; g < groups; ++g) v += sum[g * H + h];
+            part[h] = v;
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = tid + i * nt;
         if (v < nv) {
-            float* o = p.part + (int64_t)blockIdx.x * H + 8 * v;
-            *reinterpret_cast<float4*>(o) = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
+            *reinterpret_cast<float4*>(part + 8 * v) = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+            *reinterpret_cast<float4*>(part + 8 * v + 4) = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
         }
     }
 }
@@ -409,41 +482,40 @@ RowShape row_shape(int H) {
     return {std::max(32, (int)align_up(ceil_div(nv, vpt), 32)), vpt};
 }
 
-// The backward's CTA: 1024 threads at most, four prefetched rows of dy, dsum and
-// s while they fit shared memory, else two, else none; about 1024 threads an SM.
+// The backward's CTA, one per SM: groups of at most 1024 threads, as many as fit
+// 1024 threads (kBwdGroups at most); four prefetched rows a group while they fit
+// shared memory, else two, else none.
 struct BwdShape {
-    int threads, vpt, stages, smem, per_sm;
+    int group, groups, vpt, stages, smem;
 };
 BwdShape bwd_shape(int H) {
     const int nv = H / 8, vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
-    BwdShape b{std::max(32, (int)align_up(ceil_div(nv, vpt), 32)), vpt, 0, 0, 1};
-    const int row = 3 * vpt * b.threads * 16, room = 216 * 1024;
-    b.per_sm = std::max(1, std::min(1024 / b.threads, 8));
-    b.stages = vpt == 1 && 4 * row * b.per_sm <= room ? 4 : vpt == 2 && 2 * row <= room ? 2 : 0;
-    b.smem = b.stages * row;
+    BwdShape b{std::max(32, (int)align_up(ceil_div(nv, vpt), 32)), 1, vpt, 0, 0};
+    b.groups = std::max(1, std::min(1024 / b.group, kBwdGroups));
+    b.stages = vpt == 1 ? 4 : vpt == 2 ? 2 : 0;
+    b.smem = b.stages * vpt * b.group * b.groups * (3 * 16) + b.stages * vpt * b.group * b.groups / 4;   // 197632 at most
     return b;
 }
 
-template <int VPT, bool CK, int STAGES>
+template <int VPT, bool CK, int STAGES, int ROWS>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
-    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES>;
+    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES, ROWS>;
     if (b.smem > 40 * 1024) ensure_smem_attr(reinterpret_cast<const void*>(kern), b.smem);
-    return launch_after(kern, dim3(grid), dim3(b.threads), b.smem, s, p);
+    return launch_after(kern, dim3(grid), dim3(b.group * b.groups), b.smem, s, p);
 }
 template <bool CK>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
-    if (b.stages == 4) return run_bwd<1, CK, 4>(p, grid, b, s);   // H <= 8192: one vector a thread
-    if (b.stages == 2) return run_bwd<2, CK, 2>(p, grid, b, s);
-    return b.vpt == 4 ? run_bwd<4, CK, 0>(p, grid, b, s) : run_bwd<8, CK, 0>(p, grid, b, s);
+    switch (b.vpt) {
+        case 1: return run_bwd<1, CK, 4, 1>(p, grid, b, s);
+        case 2: return run_bwd<2, CK, 2, 1>(p, grid, b, s);
+        case 4: return run_bwd<4, CK, 0, 1>(p, grid, b, s);
+        default: return run_bwd<8, CK, 0, 1>(p, grid, b, s);
+    }
 }
 
 }  // namespace
 
-int rmsnorm_bwd_partials(int T, int H) {
-    const BwdShape b = bwd_shape(H);
-    // with rows prefetched, a CTA that has two is hardly slower than with one
-    return std::min(b.stages ? ceil_div(T, 2) : T, b.per_sm * sm_count());
-}
+int rmsnorm_bwd_partials(int T, int H) { return std::min(ceil_div(T, bwd_shape(H).groups), sm_count()); }
 
 cudaError_t launch_rmsnorm(int T, int H, const mok_rmsnorm_args& a, cudaStream_t s) {
     NormParams p{};
@@ -487,6 +559,7 @@ cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a,
     p.dgain = a.dgain;
     const int P = rmsnorm_bwd_partials(T, H);
     const BwdShape b = bwd_shape(H);
+    p.group = b.group;
     cudaError_t e = a.sum_q ? run_bwd<true>(p, P, b, s) : run_bwd<false>(p, P, b, s);
     if (e != cudaSuccess) return e;
     return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, 32)), dim3(1024), 0, s, (const float*)p.part, P, H,

@@ -133,7 +133,7 @@ def test_rows_of_zeros_infinities_and_nan_stay_apart():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,H", SHAPES + [(4097, 1024)])
+@pytest.mark.parametrize("T,H", SHAPES + [(4097, 1024), (5, 160), (700, 96), (300, 4128), (170, 12288)])
 @pytest.mark.parametrize("ckpt", [False, True])
 @pytest.mark.parametrize("with_dsum", [False, True])
 def test_backward(T, H, ckpt, with_dsum):
@@ -170,6 +170,29 @@ def test_backward(T, H, ckpt, with_dsum):
     dx2, dg2 = dy, torch.empty_like(dgain)
     mok.rmsnorm_backward(dy, gain, rstd, dx2, dg2, ws, dsum=dsum, **kw)
     assert torch.equal(dx2, dx) and torch.equal(dg2, dgain)
+
+
+@pytest.mark.gpu
+def test_backward_from_scale_codes_at_any_address():
+    T, H = 40, 1024
+    g = _gen(8)
+    s, dy, gain = _bf16(g, (T, H), 3.0), _bf16(g, (T, H)), torch.randn(H, generator=g, device="cuda")
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    raw = torch.empty(T * H // 32 + 8, dtype=torch.uint8, device="cuda")
+    sf = raw[:T * H // 32].view(T, H // 32)
+    mok.rmsnorm(s, gain, sum_q=q, sum_sf=sf)
+    rstd = torch.rand(T, generator=g, device="cuda")
+    ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(T, H))
+    outs = []
+    for off in (0, 1, 2):
+        odd = raw[off:off + T * H // 32].view(T, H // 32)
+        odd.copy_(sf.clone()) if off == 0 else odd.copy_(keep)
+        keep = odd.clone()
+        dx, dg = torch.empty_like(dy), torch.empty(H, device="cuda")
+        mok.rmsnorm_backward(dy, gain, rstd, dx, dg, ws, s_q=q, s_sf=odd)
+        outs.append((dx, dg))
+    for dx, dg in outs[1:]:
+        assert torch.equal(dx, outs[0][0]) and torch.equal(dg, outs[0][1])
 
 
 @pytest.mark.gpu
