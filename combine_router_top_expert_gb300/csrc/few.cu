@@ -353,6 +353,7 @@ struct FewCfg {
     static constexpr int kBarOffset = kSfOffset + kStages * kSf;
     static constexpr int kTabOffset = kBarOffset + 512;
     static constexpr int kSmem = kBarOffset + kFixed;
+    static constexpr int kBusy = NT >= 64 ? 900 : 800;     // CTAs of 1000 that a cut keeps busy (few_parts)
     static constexpr int kAccCols = 2 * NT;
     static constexpr int kTmemNeed = kAccCols + (MX ? 12 * kStages : 0);
     static constexpr int kTmemCols = kTmemNeed <= 32 ? 32 : kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128
@@ -389,18 +390,20 @@ struct FewWork {
 };
 
 // Parts per tile for `tiles` tiles (counted in routed tiles of kb units) on M
-// CTAs: the fewest that keep four fifths of the CTAs busy, else the most even cut.
-// A whole tile needs no partial sums and no wait, and the memory is saturated by
-// fewer CTAs than there are (BF16, H = 7168, 16 tokens: 512 tiles on 128 CTAs
-// 442 us, cut evenly over 152 451; down, 28 tiles on 140 CTAs 445). Parts have at
-// least kFewMinUnits units. All 32 lanes call it; lane i tries i + 1.
-__device__ __forceinline__ int few_parts(int tiles, int kb, int M) {
+// CTAs: the fewest that keep `want` of 1000 CTAs busy, else the most even cut. A
+// whole tile needs no partial sums and no wait, and with little shared memory spent
+// on tokens fewer CTAs than there are saturate the memory; with many tokens the
+// ring is shorter and it takes nearly all. H = 7168, I = 2048, 512 gate/up tiles: 16
+// tokens 433 us on 128 CTAs (whole tiles), 437 on 147 (half tiles); 64 tokens
+// (MXFP8) 289 and 281; 125 tokens 503 and 494. Parts have at least kFewMinUnits
+// units. All 32 lanes call it; lane i tries i + 1.
+__device__ __forceinline__ int few_parts(int tiles, int kb, int M, int want) {
     const int n = (int)(threadIdx.x & 31) + 1;
     int key = 0;
     if (n == 1 || (n * kFewMinUnits <= kb && tiles <= kFewMaxParts / n)) {
         const int P = tiles * n, q = ceil_div(P, M);
         const int busy = (int)(1000.f * (float)P / (float)(q * M));
-        key = (busy >= 800 ? 2000 : busy) * 32 + (32 - n);
+        key = (busy >= want ? 2000 : busy) * 32 + (32 - n);
     }
     const int best = (int)__reduce_max_sync(0xffffffffu, (unsigned)key);
     return 32 - best % 32;
@@ -643,7 +646,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
     } else if (warp == 1) {
         const int heavy = w.ts1 ? (MX ? 2 : 1) : 0;
-        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M);
+        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M, C::kBusy);
         w.ps1 = w.p1 * heavy;
         w.P1 = w.A * w.t1 * w.p1 + w.ts1 * w.ps1;
         w.G1 = ceil_div(w.P1, ceil_div(w.P1, M));
@@ -657,7 +660,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             s_cut[3] = w.G1;
         }
     } else if (warp == 2) {
-        w.p2 = few_parts(w.t2, w.upt2(), M);
+        w.p2 = few_parts(w.t2, w.upt2(), M, C::kBusy);
         w.P2 = w.t2 * w.p2;
         w.G2 = ceil_div(w.P2, ceil_div(w.P2, M));
         const int u = me < w.G2 ? w.start2(min(me + (lane & 1), w.G2)) : 0;
