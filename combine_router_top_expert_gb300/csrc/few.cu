@@ -353,8 +353,12 @@ struct FewCfg {
     static constexpr int kBarOffset = kSfOffset + kStages * kSf;
     static constexpr int kTabOffset = kBarOffset + 512;
     static constexpr int kSmem = kBarOffset + kFixed;
-    static constexpr int kBusy = NT >= 64 ? 900 : 800;     // CTAs of 1000 that a cut keeps busy (few_parts)
-    static constexpr int kAccCols = 2 * NT;
+    // a CTA's time for one unit (few_parts): more tokens leave a shorter ring
+    static constexpr float kUnitUs = NT >= 64 ? 0.68f : MX ? 0.58f : NT == 32 ? 0.55f : 0.5f;
+    // two accumulators where tensor memory holds them (all but MXFP8 with 128
+    // tokens), so that the MMAs of a job run while the one before is read
+    static constexpr int kAccs = 4 * NT + (MX ? 12 * kStages : 0) <= 512 ? 2 : 1;
+    static constexpr int kAccCols = kAccs * 2 * NT;
     static constexpr int kTmemNeed = kAccCols + (MX ? 12 * kStages : 0);
     static constexpr int kTmemCols = kTmemNeed <= 32 ? 32 : kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128
                                    : kTmemNeed <= 256 ? 256 : 512;
@@ -390,23 +394,29 @@ struct FewWork {
 };
 
 // Parts per tile for `tiles` tiles (counted in routed tiles of kb units) on M
-// CTAs: the fewest that keep `want` of 1000 CTAs busy, else the most even cut. A
-// whole tile needs no partial sums and no wait, and with little shared memory spent
-// on tokens fewer CTAs than there are saturate the memory; with many tokens the
-// ring is shorter and it takes nearly all. H = 7168, I = 2048, 512 gate/up tiles: 16
-// tokens 433 us on 128 CTAs (whole tiles), 437 on 147 (half tiles); 64 tokens
-// (MXFP8) 289 and 281; 125 tokens 503 and 494. Parts have at least kFewMinUnits
-// units. All 32 lanes call it; lane i tries i + 1.
-__device__ __forceinline__ int few_parts(int tiles, int kb, int M, int want) {
+// CTAs. A phase takes as long as the memory needs for all of its bytes, or as the
+// busiest CTA needs for its units if that is longer, and a cut tile costs the
+// exchange of its partial sums on top; so tiles stay whole, and SMs idle, wherever
+// the remaining ones keep the memory busy. The three times are measured on this
+// GPU (H = 7168, I = 2048, BF16, 16 tokens: 512 gate/up tiles, whole on 128 CTAs
+// 433 us, in halves on 147 437; MXFP8 with 64 tokens 289 and 281):
+//   kUnitsPerUs   32 KB units that the memory delivers
+//   unit_us       a CTA's time for a unit with all of its ring in flight
+//   kShareUs      write, count, wait and add up of a shared tile, and kPartUs for
+//                 each of its parts
+// Parts have at least kFewMinUnits units. All 32 lanes call it; lane i tries i + 1.
+__device__ __forceinline__ int few_parts(int tiles, int kb, int M, float unit_us) {
+    constexpr float kUnitsPerUs = 207.f, kShareUs = 3.5f, kPartUs = 0.25f;
     const int n = (int)(threadIdx.x & 31) + 1;
-    int key = 0;
+    float us = 1e9f;
     if (n == 1 || (n * kFewMinUnits <= kb && tiles <= kFewMaxParts / n)) {
-        const int P = tiles * n, q = ceil_div(P, M);
-        const int busy = (int)(1000.f * (float)P / (float)(q * M));
-        key = (busy >= want ? 2000 : busy) * 32 + (32 - n);
+        const int q = ceil_div(tiles * n, M);   // parts of the busiest CTA
+        us = fmaxf((float)tiles * (float)kb / kUnitsPerUs, (float)(q * ceil_div(kb, n)) * unit_us);
+        if (n > 1) us += kShareUs + kPartUs * (float)n;
     }
-    const int best = (int)__reduce_max_sync(0xffffffffu, (unsigned)key);
-    return 32 - best % 32;
+    // the least time, the fewest parts among (nearly) equal ones
+    const uint32_t key = (__float_as_uint(us) & ~31u) | (uint32_t)(n - 1);
+    return (int)(__reduce_min_sync(0xffffffffu, key) & 31u) + 1;
 }
 
 struct FewJob {
@@ -581,7 +591,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     auto fullA = [&](int s) { return bar + 8u * s; };
     auto fullB = [&](int s) { return bar + 8u * (S + s); };
     auto empty = [&](int s) { return bar + 8u * (2 * S + s); };
-    const uint32_t accf = bar + 8u * (3 * S), acce = bar + 8u * (3 * S + 1), drain = bar + 8u * (3 * S + 2);
+    auto accf = [&](int a) { return bar + 8u * (3 * S + a); };
+    auto acce = [&](int a) { return bar + 8u * (3 * S + C::kAccs + a); };
+    const uint32_t drain = bar + 8u * (3 * S + 2 * C::kAccs);
     auto a_tile = [&](int s) { return base + s * C::kStage; };
     auto b_tile = [&](int s) { return base + s * C::kStage + C::kBytesA; };
     auto sf_tile = [&](int s) { return base + C::kSfOffset + s * C::kSf; };
@@ -601,8 +613,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             tc::mbar_init(fullB(s), 1);
             tc::mbar_init(empty(s), 1);
         }
-        tc::mbar_init(accf, 1);
-        tc::mbar_init(acce, kFewEpi);
+        for (int a = 0; a < C::kAccs; ++a) {
+            tc::mbar_init(accf(a), 1);
+            tc::mbar_init(acce(a), kFewEpi);
+        }
         tc::mbar_init(drain, 1);
         tc::fence_mbar_init();
     }
@@ -646,7 +660,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
     } else if (warp == 1) {
         const int heavy = w.ts1 ? (MX ? 2 : 1) : 0;
-        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M, C::kBusy);
+        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M, C::kUnitUs);
         w.ps1 = w.p1 * heavy;
         w.P1 = w.A * w.t1 * w.p1 + w.ts1 * w.ps1;
         w.G1 = ceil_div(w.P1, ceil_div(w.P1, M));
@@ -660,7 +674,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             s_cut[3] = w.G1;
         }
     } else if (warp == 2) {
-        w.p2 = few_parts(w.t2, w.upt2(), M, C::kBusy);
+        w.p2 = few_parts(w.t2, w.upt2(), M, C::kUnitUs);
         w.P2 = w.t2 * w.p2;
         w.G2 = ceil_div(w.P2, ceil_div(w.P2, M));
         const int u = me < w.G2 ? w.start2(min(me + (lane & 1), w.G2)) : 0;
@@ -779,6 +793,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0, acc_ph = 0;
+            int ac = 0;   // accumulator of this job
             bool issued = false;
             auto give_up = [&]() {
                 if (issued) {   // the MMAs issued so far end before tensor memory is freed
@@ -791,8 +806,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 const bool sh = j.a == w.A;
                 const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
                 const bool two = rows > 128;   // two 128-row blocks
-                if (!tc::mbar_wait(acce, acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return give_up();
+                if (!tc::mbar_wait(acce(ac), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return give_up();
                 tc::fence_after_sync();
+                const uint32_t d0 = tmem + (uint32_t)(ac * 2 * NT), d1 = d0 + NT;
                 for (int i = 0; i < j.n; ++i) {
                     if (!tc::mbar_wait(fullA(s), ph, st, tmo, kSiteMmaFull)) return give_up();
                     if (!tc::mbar_wait(fullB(s), ph, st, tmo, kSiteMmaFull)) return give_up();
@@ -810,18 +826,18 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         tc::tmem_cp_32x128b_warpx4(sf + 8, sd + 64);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            tc::mma_mxf8(tmem, ad + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk), sf, sf + 8,
+                            tc::mma_mxf8(d0, ad + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk), sf, sf + 8,
                                          kk ? 1u : on);
                             if (two)
-                                tc::mma_mxf8(tmem + NT, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk),
+                                tc::mma_mxf8(d1, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_mxf8(128, NT, kk, kk),
                                              sf + 4, sf + 8, kk ? 1u : on);
                         }
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            tc::mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false), kk ? 1u : on);
+                            tc::mma_bf16(d0, ad + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false), kk ? 1u : on);
                             if (two)
-                                tc::mma_bf16(tmem + NT, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false),
+                                tc::mma_bf16(d1, ad + 1024 + 2 * kk, bd + 2 * kk, tc::idesc_bf16(128, NT, false, false),
                                              kk ? 1u : on);
                         }
                     }
@@ -829,8 +845,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                     tc::mma_commit(empty(s));
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                tc::mma_commit(accf);
-                acc_ph ^= 1u;
+                tc::mma_commit(accf(ac));
+                if (++ac == C::kAccs) { ac = 0; acc_ph ^= 1u; }
                 return true;
             });
         }
@@ -843,7 +859,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         const int et = threadIdx.x - 96;            // 0 .. 255
         const int row = 32 * q + lane;              // row in each 128-row block
         const int col0 = half * NC;                 // first token column of this thread
-        const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
+        const uint32_t tq0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
+        int ac = 0;   // accumulator of this job
         const int c_me = (int)blockIdx.x;
         uint32_t ph = 0;
         int wbuf = 0;
@@ -1004,9 +1021,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             const bool whole = j.c0 == j.c1;
             const bool two = (j.a == w.A ? p.Rs1 : p.R1) > 128;
             float* mine = slot_of(0, c_me, w.b1 < j.u0);
-            if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
-            ph ^= 1u;
+            if (!epi_and(tc::mbar_wait(accf(ac), ph, st, tmo, kSiteEpiAccFull))) return false;
             tc::fence_after_sync();
+            const uint32_t tq = tq0 + (uint32_t)(ac * 2 * NT);
 #pragma unroll 1
             for (int cc = 0; cc < NC && col0 + cc < T; cc += CH) {
                 float v0[CH], v1[CH];
@@ -1026,7 +1043,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 }
             }
             tc::fence_before_sync();
-            tc::mbar_arrive(acce);
+            tc::mbar_arrive(acce(ac));
+            if (++ac == C::kAccs) { ac = 0; ph ^= 1u; }
             if (whole) publish_h(j.a, T);
             else share(j);
             return true;
@@ -1045,9 +1063,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                         if (s_idx[et * k + i] == s_act[j.a]) wt = s_w[et * k + i];
                 s_row[wbuf * 128 + et] = wt;
             }
-            if (!epi_and(tc::mbar_wait(accf, ph, st, tmo, kSiteEpiAccFull))) return false;
-            ph ^= 1u;
+            if (!epi_and(tc::mbar_wait(accf(ac), ph, st, tmo, kSiteEpiAccFull))) return false;
             tc::fence_after_sync();
+            const uint32_t tq = tq0 + (uint32_t)(ac * 2 * NT);
             const float* wr = s_row + wbuf * 128 + col0;
             wbuf ^= 1;
 #pragma unroll
@@ -1067,7 +1085,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 }
             }
             tc::fence_before_sync();
-            tc::mbar_arrive(acce);
+            tc::mbar_arrive(acce(ac));
+            if (++ac == C::kAccs) { ac = 0; ph ^= 1u; }
             if (j.last) {
                 const bool whole = j.c0 == j.c1;
                 const bool two = p.R2 > 128;
