@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gemm.cuh"
 #include "moves.cuh"
@@ -329,8 +330,8 @@ struct FewParams {
     void* h;                      // [active experts * T, I]
     uint8_t* hsf;                 // [active experts][I / 128] chunks of 512 bytes
     __nv_bfloat16* hs;            // [T, Is]
-    float* part;                  // [2 phases][CTAs][2][T][256]
-    int* hready;                  // [E + 1] finished (gate/up tile, token) rows per active expert (the shared one last)
+    float* part;                  // [2 phases][CTAs][2][256][T rounded up to 8]
+    int* hready;                  // [E + 1] finished items of h per active expert (the shared one last)
     int* cnt1;                    // arrivals per gate/up tile
     int* cnt2;                    // arrivals per down tile
     __nv_bfloat16* out;
@@ -355,6 +356,7 @@ struct FewCfg {
     static constexpr int kSmem = kBarOffset + kFixed;
     // a CTA's time for one unit (few_parts): more tokens leave a shorter ring
     static constexpr float kUnitUs = NT >= 64 ? 0.68f : MX ? 0.58f : NT == 32 ? 0.55f : 0.5f;
+    static constexpr float kDrainUs = NT == 128 ? 2.5f : NT == 64 ? 1.3f : NT == 32 ? 0.8f : 0.5f;
     // two accumulators where tensor memory holds them (all but MXFP8 with 128
     // tokens), so that the MMAs of a job run while the one before is read
     static constexpr int kAccs = 4 * NT + (MX ? 12 * kStages : 0) <= 512 ? 2 : 1;
@@ -402,16 +404,19 @@ struct FewWork {
 // 433 us, in halves on 147 437; MXFP8 with 64 tokens 289 and 281):
 //   kUnitsPerUs   32 KB units that the memory delivers
 //   unit_us       a CTA's time for a unit with all of its ring in flight
+//   drain_us      a CTA's time for reading an accumulator, once for each of the
+//                 tile's `segs` experts
 //   kShareUs      write, count, wait and add up of a shared tile, and kPartUs for
 //                 each of its parts
 // Parts have at least kFewMinUnits units. All 32 lanes call it; lane i tries i + 1.
-__device__ __forceinline__ int few_parts(int tiles, int kb, int M, float unit_us) {
+__device__ __forceinline__ int few_parts(int tiles, int kb, int segs, int M, float unit_us, float drain_us) {
     constexpr float kUnitsPerUs = 207.f, kShareUs = 3.5f, kPartUs = 0.25f;
     const int n = (int)(threadIdx.x & 31) + 1;
     float us = 1e9f;
     if (n == 1 || (n * kFewMinUnits <= kb && tiles <= kFewMaxParts / n)) {
         const int q = ceil_div(tiles * n, M);   // parts of the busiest CTA
-        us = fmaxf((float)tiles * (float)kb / kUnitsPerUs, (float)(q * ceil_div(kb, n)) * unit_us);
+        us = fmaxf((float)tiles * (float)kb / kUnitsPerUs,
+                   fmaxf((float)(q * ceil_div(kb, n)) * unit_us, (float)(q * ceil_div(segs, n)) * drain_us));
         if (n > 1) us += kShareUs + kPartUs * (float)n;
     }
     // the least time, the fewest parts among (nearly) equal ones
@@ -660,7 +665,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         }
     } else if (warp == 1) {
         const int heavy = w.ts1 ? (MX ? 2 : 1) : 0;
-        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, M, C::kUnitUs);
+        w.p1 = few_parts(w.A * w.t1 + w.ts1 * heavy, w.kb1, 1, M, C::kUnitUs, C::kDrainUs);
         w.ps1 = w.p1 * heavy;
         w.P1 = w.A * w.t1 * w.p1 + w.ts1 * w.ps1;
         w.G1 = ceil_div(w.P1, ceil_div(w.P1, M));
@@ -674,7 +679,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             s_cut[3] = w.G1;
         }
     } else if (warp == 2) {
-        w.p2 = few_parts(w.t2, w.upt2(), M, C::kUnitUs);
+        w.p2 = few_parts(w.t2, w.upt2(), w.A + (w.kbs2 > 0), M, C::kUnitUs, C::kDrainUs);
         w.P2 = w.t2 * w.p2;
         w.G2 = ceil_div(w.P2, ceil_div(w.P2, M));
         const int u = me < w.G2 ? w.start2(min(me + (lane & 1), w.G2)) : 0;
@@ -764,7 +769,9 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             few_jobs(w, [&](const FewJob& j) {
                 const bool sh = j.a == w.A;
                 if (j.phase && ready != j.a) {
-                    if (!few_wait_counter(p.hready + j.a, (sh ? w.ts1 : w.t1) * T, st, tmo)) return give_up();
+                    // (items of 32 rows, or MXFP8 features, and 8 tokens)
+                    const int items = (sh ? 2 * p.Is : MX ? p.I : 2 * p.I) / 32 * ceil_div(T, 8);
+                    if (!few_wait_counter(p.hready + j.a, items, st, tmo)) return give_up();
                     tc::fence_proxy_async_global();
                     ready = j.a;
                 }
@@ -853,7 +860,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     } else {
         // ------------------------------------------------------------ epilogue
         constexpr int NC = NT / 2;                  // token columns of a thread
-        constexpr int CH = NC == 8 || NC == 64 ? 8 : 16;   // columns at a time (NC = 64: what the registers allow)
+        constexpr int CH = 8;                       // columns at a time
         const int q = warp & 3;                     // TMEM lane quadrant of this warp
         const int half = (warp - 3) >> 2;
         const int et = threadIdx.x - 96;            // 0 .. 255
@@ -869,7 +876,11 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         // in (0) and the one it ends in (1)
         FewShared pend[2];
         int n_pend = 0;
-        const int64_t part_stride = 256 * (int64_t)T;
+        const int tpad = ceil_div(T, 8) * 8;
+        // a partial tile: blocks of 32 rows x 8 tokens (1 KB each, a row's 8 tokens
+        // adjacent), by row group and token chunk
+        const int64_t part_stride = 256 * (int64_t)tpad;
+        auto block = [&](int g, int t0) { return ((g * (tpad / 8) + t0 / 8) * 32 + lane) * 8; };
         auto slots = [&](int phase) { return p.part + (int64_t)phase * gridDim.x * 2 * part_stride; };
         // CTA c's partial of a tile whose first unit is u0: only the first
         // sharer may have started before the tile
@@ -877,19 +888,24 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             return slots(phase) + (2 * (int64_t)c + (began_before ? 1 : 0)) * part_stride;
         };
 
+        // MXFP8 h of one token and 32 features (group g of the tile's 128, one a
+        // lane) from their gate and up values
+        auto store_h_mx = [&](int a, int tile, int g, int t, float gate, float up) {
+            const float hv = silu_f(gate) * up;
+            const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(hv)));
+            const uint32_t code = e8m0_code(__uint_as_float(am));
+            const int64_t r = (int64_t)a * T + t;
+            static_cast<uint8_t*>(p.h)[r * p.I + tile * 128 + 32 * g + lane] =
+                (uint8_t)f32x2_to_e4m3x2(hv * e8m0_inv_scale(code), 0.f);
+            if (lane == 0) p.hsf[((int64_t)a * (p.I / 128) + tile) * 512 + sf_chunk_offset(t, g)] = (uint8_t)code;
+        };
         // SwiGLU of one token column: v0, v1 are this thread's values in the
         // tile's two row blocks (all lanes of the warp call it)
         auto store_h = [&](int a, int tile, int t, float v0, float v1) {
             const bool sh = a == w.A;
             if (MX && !sh) {
                 // gate rows 0..127, up rows 128..255 of the same features
-                const float hv = silu_f(v0) * v1;
-                const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(hv)));
-                const uint32_t code = e8m0_code(__uint_as_float(am));
-                const int64_t r = (int64_t)a * T + t;
-                static_cast<uint8_t*>(p.h)[r * p.I + tile * 128 + row] =
-                    (uint8_t)f32x2_to_e4m3x2(hv * e8m0_inv_scale(code), 0.f);
-                if (lane == 0) p.hsf[((int64_t)a * (p.I / 128) + tile) * 512 + sf_chunk_offset(t, q)] = (uint8_t)code;
+                store_h_mx(a, tile, q, t, v0, v1);
             } else {
                 // lanes 0-15 hold gate rows, 16-31 the up rows of the same 16
                 // features: the lower half forms h of the first row block, the
@@ -910,9 +926,28 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             o[row] = __float2bfloat16_rn(v0);
             if (128 + row < p.R2) o[128 + row] = __float2bfloat16_rn(v1);
         };
-        // n token rows of an expert's h tile are written (their readers are TMA
-        // loads): publish them. The barrier and the release order every
-        // thread's writes before the count.
+        // 8 tokens (from column cc of this thread) of a partial tile: one 32-byte
+        // store for each of this thread's rows
+        auto put_part = [&](float* mine, int cc, bool two, const float (&v0)[CH], const float (&v1)[CH]) {
+            uint32_t u[8];
+            float* dst = mine + block(q, col0 + cc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v0[i]);
+            tc::stg_v8(dst, u);
+            if (two) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v1[i]);
+                tc::stg_v8(dst + 128 * tpad, u);
+            }
+        };
+        // A tile is finished in items of one warp: 8 tokens x 32 weight rows (MXFP8
+        // gate/up: 32 features, i.e. 32 gate and 32 up rows).
+        auto groups_of = [&](int phase, bool sh) {
+            return phase ? p.R2 / 32 : sh ? p.Rs1 / 32 : MX ? 4 : p.R1 / 32;
+        };
+        // n items of an expert's h are written (their readers are TMA loads):
+        // publish them. The barrier and the release order every thread's writes
+        // before the count.
         auto publish_h = [&](int a, int n) {
             tc::fence_proxy_async_global();
             epi_sync();
@@ -928,90 +963,87 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             else pend[1] = f;
             ++n_pend;
         };
-        // end of a phase: of each shared tile, sharer i of n adds up the
-        // partials of the tokens T i / n .. T (i + 1) / n in CTA order
+        // end of a phase: of each shared tile, sharer i of n adds up the partials of
+        // its share of the items, in CTA order
         auto finish = [&](int phase) {
 #pragma unroll 1
             for (int i = 0; i < n_pend; ++i) {
                 const FewShared f = i == 0 ? pend[0] : pend[1];
-                const int n = f.c1 - f.c0 + 1, me = c_me - f.c0;
-                const int ta = T * me / n, tb = T * (me + 1) / n;
-                if (ta == tb) continue;
+                const bool sh = f.a == w.A;
+                const int n = f.c1 - f.c0 + 1, me_ = c_me - f.c0;
+                const int groups = groups_of(phase, sh), items = groups * (tpad / 8);
+                const int from = items * me_ / n, to = items * (me_ + 1) / n;
+                if (from == to) continue;
                 bool ok = true;
                 if (et == 0) ok = few_wait_counter((phase ? p.cnt2 : p.cnt1) + f.gtile, n, st, tmo);
                 if (!epi_and(ok)) return false;
-                const bool sh = f.a == w.A;
-                const int rows = phase ? p.R2 : sh ? p.Rs1 : p.R1;
-                // a warp per token; this lane's two groups of four rows: down 8
-                // consecutive rows, gate/up the gate and up rows of 4 features
-                const bool il16 = !MX || sh;
-                const int ra = phase ? 8 * lane : il16 ? 32 * (lane >> 2) + 4 * (lane & 3) : 4 * lane;
-                const int rb = phase ? ra + 4 : il16 ? ra + 16 : 128 + ra;
-                const bool in = rb < rows;
+                const bool pairs = MX && !phase && !sh;   // gate and up rows 128 apart
                 const int lead = (phase ? w.start2(f.c0) : w.start1(f.c0)) < f.u0 ? 1 : 0;
                 const float* src = slots(phase) + 2 * (int64_t)f.c0 * part_stride;
-                constexpr int TU = 4;                 // tokens in flight per warp
+                constexpr int kWarps = kFewEpi / 32;
+                // NI items of a warp at a time (the second one clamped to the last
+                // item, so that the loads need no branch)
+                auto run = [&](auto tag) {
+                    constexpr int NI = decltype(tag)::value;
 #pragma unroll 1
-                for (int t0 = ta + (et >> 5); t0 < tb; t0 += 8 * TU) {
-                    float va[TU][4], vb[TU][4];
+                    for (int it0 = from + (et >> 5); it0 < to; it0 += NI * kWarps) {
+                        float v[NI][8] = {}, up[NI][8] = {};
+                        const float* at[NI];
 #pragma unroll
-                    for (int u = 0; u < TU; ++u)
+                        for (int u = 0; u < NI; ++u) {
+                            const int it = min(it0 + u * kWarps, to - 1);
+                            at[u] = src + block(it % groups, it / groups * 8);
+                        }
+                        auto add = [&](float (&x)[8], const float* q) {
+                            const float4 lo = __ldcg(reinterpret_cast<const float4*>(q));
+                            const float4 hi = __ldcg(reinterpret_cast<const float4*>(q) + 1);
+                            x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+                            x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
+                        };
+#pragma unroll 4
+                        for (int c = 0; c < n; ++c) {
+                            const int64_t o = (2 * (int64_t)c + (c == 0 ? lead : 0)) * part_stride;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) va[u][r] = vb[u][r] = 0.f;
-#pragma unroll 2
-                    for (int c = 0; c < n; ++c) {
-                        const float* sc = src + (2 * (int64_t)c + (c == 0 ? lead : 0)) * part_stride;
-                        float4 x[TU], y[TU];
-#pragma unroll
-                        for (int u = 0; u < TU; ++u) {
-                            const int t = t0 + 8 * u;
-                            x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (t < tb && in) {
-                                x[u] = __ldcg(reinterpret_cast<const float4*>(sc + t * 256 + ra));
-                                y[u] = __ldcg(reinterpret_cast<const float4*>(sc + t * 256 + rb));
+                            for (int u = 0; u < NI; ++u) {
+                                add(v[u], at[u] + o);
+                                if (pairs) add(up[u], at[u] + o + 128 * tpad);
                             }
                         }
 #pragma unroll
-                        for (int u = 0; u < TU; ++u) {
-                            va[u][0] += x[u].x; va[u][1] += x[u].y; va[u][2] += x[u].z; va[u][3] += x[u].w;
-                            vb[u][0] += y[u].x; vb[u][1] += y[u].y; vb[u][2] += y[u].z; vb[u][3] += y[u].w;
+                        for (int u = 0; u < NI; ++u) {
+                            const int it = it0 + u * kWarps;
+                            if (it >= to) break;
+                            const int g = it % groups, t0 = it / groups * 8;
+                            if (phase) {
+                                __nv_bfloat16* o = p.out + (int64_t)t0 * p.H + f.tile * p.R2 + 32 * g + lane;
+#pragma unroll
+                                for (int t = 0; t < 8; ++t)
+                                    if (t0 + t < T) o[(int64_t)t * p.H] = __float2bfloat16_rn(v[u][t]);
+                            } else if (pairs) {
+#pragma unroll
+                                for (int t = 0; t < 8; ++t)
+                                    if (t0 + t < T) store_h_mx(f.a, f.tile, g, t0 + t, v[u][t], up[u][t]);
+                            } else {
+                                // lanes 0-15 gate, 16-31 up of the same 16 features: the
+                                // lower half forms the first four tokens, the upper half
+                                // the others
+                                const bool lower = lane < 16;
+                                const int ld = sh ? p.Is : p.I, fe = f.tile * (groups * 16) + 16 * g + (lane & 15);
+                                __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)f.a * T * p.I;
+#pragma unroll
+                                for (int t = 0; t < 4; ++t) {
+                                    const float other = __shfl_xor_sync(0xffffffffu, lower ? v[u][4 + t] : v[u][t], 16);
+                                    const float hv = silu_f(lower ? v[u][t] : other) * (lower ? other : v[u][4 + t]);
+                                    const int tt = t0 + t + (lower ? 0 : 4);
+                                    if (tt < T) hb[(int64_t)tt * ld + fe] = __float2bfloat16_rn(hv);
+                                }
+                            }
                         }
                     }
-#pragma unroll
-                    for (int u = 0; u < TU; ++u) {
-                        const int t = t0 + 8 * u;
-                        if (t >= tb) break;
-                        if (phase) {
-                            if (in)
-                                *reinterpret_cast<uint4*>(p.out + (int64_t)t * p.H + f.tile * rows + ra) =
-                                    make_uint4(pack_bf16x2(va[u][0], va[u][1]), pack_bf16x2(va[u][2], va[u][3]),
-                                               pack_bf16x2(vb[u][0], vb[u][1]), pack_bf16x2(vb[u][2], vb[u][3]));
-                            continue;
-                        }
-                        float hv[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) hv[r] = silu_f(va[u][r]) * vb[u][r];
-                        if (il16) {
-                            __nv_bfloat16* hb = sh ? p.hs : static_cast<__nv_bfloat16*>(p.h) + (int64_t)f.a * T * p.I;
-                            if (in)
-                                *reinterpret_cast<uint2*>(hb + (int64_t)t * (sh ? p.Is : p.I) + f.tile * (rows / 2) + 4 * lane) =
-                                    make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
-                        } else {
-                            float am = fmaxf(fmaxf(fabsf(hv[0]), fabsf(hv[1])), fmaxf(fabsf(hv[2]), fabsf(hv[3])));
-#pragma unroll
-                            for (int d = 4; d >= 1; d >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, d));
-                            const uint32_t code = e8m0_code(am);
-                            const float inv = e8m0_inv_scale(code);
-                            const int64_t r = (int64_t)f.a * T + t;
-                            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + r * p.I + f.tile * 128 + 4 * lane) =
-                                f32x2_to_e4m3x2(hv[0] * inv, hv[1] * inv) | (f32x2_to_e4m3x2(hv[2] * inv, hv[3] * inv) << 16);
-                            if ((lane & 7) == 0)
-                                p.hsf[((int64_t)f.a * (p.I / 128) + f.tile) * 512 + sf_chunk_offset(t, lane >> 3)] =
-                                    (uint8_t)code;
-                        }
-                    }
-                }
-                if (!phase) publish_h(f.a, tb - ta);
+                };
+                if (NT >= 64 && to - from > kWarps) run(std::integral_constant<int, 2>{});
+                else run(std::integral_constant<int, 1>{});
+                if (!phase) publish_h(f.a, to - from);
             }
             n_pend = 0;
             return true;
@@ -1029,23 +1061,18 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 float v0[CH], v1[CH];
                 few_tmem_ld<CH>(tq + cc, v0);
                 few_tmem_ld<CH>(tq + NT + cc, v1);
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int t = col0 + cc + i;
-                    if (t < T) {
-                        if (whole) {
-                            store_h(j.a, j.tile, t, v0[i], v1[i]);
-                        } else {
-                            __stcg(mine + t * 256 + row, v0[i]);
-                            if (two) __stcg(mine + t * 256 + 128 + row, v1[i]);
-                        }
-                    }
+                    for (int i = 0; i < CH; ++i)
+                        if (col0 + cc + i < T) store_h(j.a, j.tile, col0 + cc + i, v0[i], v1[i]);
+                } else {
+                    put_part(mine, cc, two, v0, v1);
                 }
             }
             tc::fence_before_sync();
             tc::mbar_arrive(acce(ac));
             if (++ac == C::kAccs) { ac = 0; ph ^= 1u; }
-            if (whole) publish_h(j.a, T);
+            if (whole) publish_h(j.a, groups_of(0, j.a == w.A) * (tpad / 8));
             else share(j);
             return true;
         });
@@ -1092,17 +1119,23 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 const bool two = p.R2 > 128;
                 float* mine = slot_of(1, c_me, w.b2 < j.u0);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const int t = col0 + i;
-                    if (t < T) {
+                for (int cc = 0; cc < NC; cc += CH) {
+                    float v0[CH], v1[CH];
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        v0[i] = acc[0][cc + i];
+                        v1[i] = acc[1][cc + i];
+                        acc[0][cc + i] = acc[1][cc + i] = 0.f;
+                    }
+                    if (col0 + cc < T) {
                         if (whole) {
-                            store_out(j.tile, t, acc[0][i], acc[1][i]);
+#pragma unroll
+                            for (int i = 0; i < CH; ++i)
+                                if (col0 + cc + i < T) store_out(j.tile, col0 + cc + i, v0[i], v1[i]);
                         } else {
-                            __stcg(mine + t * 256 + row, acc[0][i]);
-                            if (two) __stcg(mine + t * 256 + 128 + row, acc[1][i]);
+                            put_part(mine, cc, two, v0, v1);
                         }
                     }
-                    acc[0][i] = acc[1][i] = 0.f;
                 }
                 if (!whole) share(j);
             }
@@ -1144,7 +1177,7 @@ FewLayout few_layout(const mok_problem* p, int ctas) {
     L.h = o; o += align_up(act * T * I * (mx ? 1 : 2), 256);
     L.hsf = o; if (mx) o += act * (I / 128) * 512;
     L.hs = o; o += align_up(T * p->I_shared * 2, 256);
-    L.part = o; o += (size_t)2 * ctas * 2 * 256 * T * 4;
+    L.part = o; o += (size_t)2 * ctas * 2 * 256 * align_up(T, 8) * 4;
     L.total = o;
     return L;
 }
