@@ -483,6 +483,11 @@ def dequantize_rows(x_q, x_sf, x, stream=None):
 
 # --------------------------------------------------------------------------- the layer for a few tokens
 
+def few_tokens_ok(T, k) -> bool:
+    """Whether moe_few takes T tokens with k experts each."""
+    return T <= FEW_MAX_TOKENS and T * k <= FEW_MAX_PAIRS
+
+
 def few_workspace_size(p: Problem, cfg: Config | None = None) -> int:
     return int(lib().mok_few_workspace_size(ctypes.byref(p), ctypes.byref(cfg) if cfg else None))
 
