@@ -193,8 +193,8 @@ def _ptr(t):
 
 def _stream(stream=None):
     if stream is None:   # the raw handle: building a Stream object costs 2.5 us a call
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(rc, what):
@@ -426,10 +426,11 @@ def _dense(name, t, dtype, *shape):
 
 
 def _rows(name, t, T, H):
-    """bf16 rows of any pitch: the elements of a row are adjacent."""
-    assert t.is_cuda and t.dtype == torch.bfloat16 and t.shape == (T, H) and (t.stride(1) == 1 or H == 1), \
+    """Row pitch of bf16 rows whose elements are adjacent."""
+    pitch, step = t.stride()
+    assert t.dtype is torch.bfloat16 and step == 1 and t.shape == (T, H) and t.is_cuda, \
         f"{name}: bf16 CUDA tensor [{T}, {H}] with adjacent row elements expected"
-    return t.stride(0) if T > 1 else max(t.stride(0), H)
+    return pitch if T > 1 else max(pitch, H)
 
 
 def rmsnorm(x, gain, residual=None, eps=1e-6, sum=None, y=None, y_q=None, y_sf=None, sum_q=None, sum_sf=None,
@@ -439,10 +440,12 @@ def rmsnorm(x, gain, residual=None, eps=1e-6, sum=None, y=None, y_q=None, y_sf=N
     T, H = x.shape
     _dense("sum", sum, torch.bfloat16, T, H)
     _dense("y", y, torch.bfloat16, T, H)
-    _dense("y_q", y_q, torch.uint8, T, H)
-    _dense("y_sf", y_sf, torch.uint8, T, H // 32)
-    _dense("sum_q", sum_q, torch.uint8, T, H)
-    _dense("sum_sf", sum_sf, torch.uint8, T, H // 32)
+    if y_q is not None or y_sf is not None:
+        _dense("y_q", y_q, torch.uint8, T, H)
+        _dense("y_sf", y_sf, torch.uint8, T, H // 32)
+    if sum_q is not None or sum_sf is not None:
+        _dense("sum_q", sum_q, torch.uint8, T, H)
+        _dense("sum_sf", sum_sf, torch.uint8, T, H // 32)
     _dense("gain", gain, torch.float32, H)
     _dense("rstd", rstd, torch.float32, T)
     a = RmsNormArgs(x.data_ptr(), _rows("x", x, T, H), _addr(residual),
@@ -462,8 +465,9 @@ def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_s
     _dense("dx", dx, torch.bfloat16, T, H)
     _dense("s", s, torch.bfloat16, T, H)
     _dense("dsum", dsum, torch.bfloat16, T, H)
-    _dense("s_q", s_q, torch.uint8, T, H)
-    _dense("s_sf", s_sf, torch.uint8, T, H // 32)
+    if s_q is not None or s_sf is not None:
+        _dense("s_q", s_q, torch.uint8, T, H)
+        _dense("s_sf", s_sf, torch.uint8, T, H // 32)
     _dense("gain", gain, torch.float32, H)
     _dense("dgain", dgain, torch.float32, H)
     _dense("rstd", rstd, torch.float32, T)
