@@ -23,16 +23,32 @@ namespace {
 
 constexpr int kCkThreads = 256;
 
-// Padded segment offsets (each expert's rows start on a 128-row boundary), by
-// the CTA's first thread; the caller's barrier follows.
+// Padded segment offsets (each expert's rows start on a 128-row boundary) by the
+// CTA's first warp, 8 experts a lane, and the barrier that publishes them.
 __device__ __forceinline__ void ck_offsets(const int32_t* counts, int E, int32_t* poff) {
-    if (threadIdx.x == 0) {
-        int s = 0;
-        for (int e = 0; e < E; ++e) {
-            poff[e] = s;
-            s += ceil_div(counts[e], kTileM) * kTileM;
+    static_assert(kMaxE == 256, "8 experts a lane");
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int n[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = 8 * lane + i;
+            n[i] = e < E ? ceil_div(counts[e], kTileM) * kTileM : 0;
+            sum += n[i];
         }
-        poff[E] = s;
+        int s = sum;   // inclusive over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += o;
+        }
+        s -= sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (8 * lane + i <= E) poff[8 * lane + i] = s;
+            s += n[i];
+        }
+        if (lane == 31 && E == kMaxE) poff[E] = s;
     }
     __syncthreads();
 }
@@ -47,10 +63,10 @@ __device__ __forceinline__ int segment_of(const int32_t* start, int E, int r) {
     return lo;
 }
 
-// Vectors of 8 elements that a lane has in flight: a row is read in rounds of
-// kCkBatch * 32 vectors, every load of a round issued before the first is used.
-// These kernels do nothing but move bytes, and one load at a time left them
-// waiting (T = 4096, H = 7168, I = 2048: save 278 us, restore 370).
+// Vectors of 8 elements that a lane of the save has in flight: a row is read in
+// rounds of kCkBatch * 32 vectors, every load of a round issued before the first is
+// used. The save reads 1.07 GB and writes 0.4 at T = 4096, H = 7168, I = 2048, k = 8:
+// 209 us (the copy rate of this GPU; one load at a time left it waiting, 278 us).
 constexpr int kCkBatch = 4;
 
 // One row of n elements (BF16 or fp32) to MXFP8 by one warp. Every lane runs
@@ -124,36 +140,20 @@ checkpoint_save_kernel(const CheckpointParams p) {
 
 // One MXFP8 row of n elements to BF16 by one warp.
 __device__ __forceinline__ void load_row_bf16(const uint8_t* q, const uint8_t* sf, int n, __nv_bfloat16* dst) {
-    const int lane = threadIdx.x & 31, nv = n / 8;
-    constexpr int U = kCkBatch;
-#pragma unroll 1
-    for (int v0 = lane; v0 < nv; v0 += 32 * U) {
-        uint2 x[U];
-        uint32_t code[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = v0 + 32 * u;
-            if (v < nv) {
-                x[u] = __ldg(reinterpret_cast<const uint2*>(q) + v);
-                code[u] = __ldg(sf + v / 4);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = v0 + 32 * u;
-            if (v < nv) {
-                float f[8];
-                dequantize8(x[u], code[u], f);
-                __stcs(reinterpret_cast<uint4*>(dst) + v, pack8(f));
-            }
-        }
+    const int lane = threadIdx.x & 31;
+    for (int v = lane; v < n / 8; v += 32) {
+        float f[8];
+        dequantize8(__ldg(reinterpret_cast<const uint2*>(q) + v), __ldg(sf + v / 4), f);
+        reinterpret_cast<uint4*>(dst)[v] = pack8(f);
     }
 }
 
 // One warp per row. Row jobs in order: the padded rows (A, G|U and h together;
 // pad rows are zero, as the training forward leaves them), the T*k partials,
-// the T tokens. Rows past the last segment are left alone.
-__global__ void __launch_bounds__(kCkThreads, 4)
+// the T tokens. Rows past the last segment are left alone. Bound by its writes
+// (1.76 GB against 0.6 read: 370 us, 4.7 TB/s written); loads in batches and
+// streaming stores measured slower (391, 386 us).
+__global__ void __launch_bounds__(kCkThreads)
 checkpoint_load_kernel(const CheckpointParams p) {
     __shared__ int32_t poff[kMaxE + 1], off[kMaxE + 1];
     for (int e = threadIdx.x; e <= p.E; e += kCkThreads) off[e] = p.offsets[e];
@@ -180,39 +180,22 @@ checkpoint_load_kernel(const CheckpointParams p) {
             const int64_t r = off[e] + local;
             const int64_t t = __ldg(p.row_src + r) / p.k;
             load_row_bf16(p.x_q + t * p.H, p.x_sf + t * (p.H / 32), p.H, A);
-            const uint8_t *gq = p.gu_q + r * W, *gs = p.gu_sf + r * (W / 32);
-            constexpr int B = 2;
-#pragma unroll 1
-            for (int v0 = lane; v0 < p.I / 8; v0 += 32 * B) {
-                uint2 xg[B], xu[B];
-                uint32_t cg[B], cu[B];
+            for (int v = lane; v < p.I / 8; v += 32) {
+                float g[8], u[8], hv[8];
+                uint32_t w[8];
+                dequantize8(__ldg(reinterpret_cast<const uint2*>(p.gu_q + r * W) + v),
+                            __ldg(p.gu_sf + r * (W / 32) + v / 4), g);
+                dequantize8(__ldg(reinterpret_cast<const uint2*>(p.gu_q + r * W + p.I) + v),
+                            __ldg(p.gu_sf + r * (W / 32) + p.I / 32 + v / 4), u);
 #pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    const int v = v0 + 32 * b;
-                    if (v < p.I / 8) {
-                        xg[b] = __ldg(reinterpret_cast<const uint2*>(gq) + v);
-                        xu[b] = __ldg(reinterpret_cast<const uint2*>(gq + p.I) + v);
-                        cg[b] = __ldg(gs + v / 4);
-                        cu[b] = __ldg(gs + p.I / 32 + v / 4);
-                    }
-                }
+                for (int i = 0; i < 8; ++i) hv[i] = silu_f(g[i]) * u[i];
 #pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    const int v = v0 + 32 * b;
-                    if (v < p.I / 8) {
-                        float g[8], u[8];
-                        dequantize8(xg[b], cg[b], g);
-                        dequantize8(xu[b], cu[b], u);
-                        float4 *go = reinterpret_cast<float4*>(gu + 8 * v), *uo = reinterpret_cast<float4*>(gu + p.I + 8 * v);
-                        __stcs(go, make_float4(g[0], g[1], g[2], g[3]));
-                        __stcs(go + 1, make_float4(g[4], g[5], g[6], g[7]));
-                        __stcs(uo, make_float4(u[0], u[1], u[2], u[3]));
-                        __stcs(uo + 1, make_float4(u[4], u[5], u[6], u[7]));
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(g[i]);
+                tc::stg_v8(gu + 8 * v, w);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) g[i] = silu_f(g[i]) * u[i];
-                        __stcs(reinterpret_cast<uint4*>(h) + v, pack8(g));
-                    }
-                }
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(u[i]);
+                tc::stg_v8(gu + p.I + 8 * v, w);
+                reinterpret_cast<uint4*>(h)[v] = pack8(hv);
             }
         } else if (j < P + R) {
             const int64_t i = j - P;
