@@ -1104,7 +1104,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < CH; ++i) {
                         const float wt = col0 + cc + i < T ? wr[cc + i] : -1.f;
-                        if (wt >= 0.f) {
+                        if (!(wt < 0.f)) {   // (a NaN weight, from a row without numbers, goes through)
                             acc[0][cc + i] = fmaf(wt, v0[i], acc[0][cc + i]);
                             acc[1][cc + i] = fmaf(wt, v1[i], acc[1][cc + i]);
                         }

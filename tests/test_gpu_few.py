@@ -154,8 +154,9 @@ def test_ties_and_signed_zeros_take_the_lowest_expert():
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
 def test_a_token_without_numbers_stays_apart(dtype):
-    """A row of NaN or infinities (its own result is unspecified) leaves the
-    other tokens' results as they are, up to the order of the partial sums."""
+    """A row of NaN or infinities (its own routing is unspecified, its result is no
+    number) leaves the other tokens' results as they are, up to the order of the
+    partial sums."""
     wl = S("nan", T=6, H=512, I=256, E=8, k=2, dtype=dtype)
     inp = synth.make_inputs(wl, seed=6)
     layer = layer_for(inp, dtype_of(wl))
@@ -165,6 +166,7 @@ def test_a_token_without_numbers_stays_apart(dtype):
         y = x.clone()
         y[2] = bad
         out, _, _ = run(wl, inp, layer, y)
+        assert not torch.isfinite(out[2]).any()
         keep = [0, 1, 3, 4, 5]
         assert_close(host_bf16_f64(out)[keep], ref[keep], TOL[dtype_of(wl)], f"{bad}")
 
