@@ -171,6 +171,13 @@ BwdLayout bwd_layout(const mok_problem* p) {
 }
 
 mok_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA; }
+// The same, with the error taken back from the runtime, so that the caller's
+// next CUDA check does not see what the status already told.
+mok_status launch_status(cudaError_t e) {
+    if (e == cudaSuccess) return MOK_OK;
+    cudaGetLastError();
+    return MOK_ERR_CUDA;
+}
 
 constexpr int kDefaultMovers = 8;
 // The grouped GEMMs' producers prefetch the weight box this many K blocks
@@ -780,7 +787,7 @@ mok_status mok_moe_few(const mok_problem* p, const mok_few_args* a, const mok_co
     f.topk_w = a->topk_w;
     f.out = a->out;
     f.workspace = a->workspace;
-    return cuda_status(launch_few(f, make_common(a->workspace, cfg, p->dtype), s));
+    return launch_status(launch_few(f, make_common(a->workspace, cfg, p->dtype), s));
 }
 
 mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream) {
@@ -800,7 +807,7 @@ mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stre
         if (o && ((o == a->x && a->ldx != H) || (o == a->residual && a->ldr != H))) return MOK_ERR_INVALID;
     if (!device_ok()) return MOK_ERR_CUDA;
     if (T == 0) return MOK_OK;
-    return cuda_status(launch_rmsnorm(T, H, *a, (cudaStream_t)stream));
+    return launch_status(launch_rmsnorm(T, H, *a, (cudaStream_t)stream));
 }
 
 size_t mok_rmsnorm_bwd_workspace_size(int32_t T, int32_t H) {
@@ -820,7 +827,7 @@ mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args
     if (!device_ok()) return MOK_ERR_CUDA;
     if (a->ws_bytes < mok_rmsnorm_bwd_workspace_size(T, H)) return MOK_ERR_INVALID;
     if (T == 0) return cuda_status(cudaMemsetAsync(a->dgain, 0, (size_t)H * 4, (cudaStream_t)stream));
-    return cuda_status(launch_rmsnorm_backward(T, H, *a, (cudaStream_t)stream));
+    return launch_status(launch_rmsnorm_backward(T, H, *a, (cudaStream_t)stream));
 }
 
 mok_status mok_dequantize_rows(const void* x_q, const void* x_sf, int32_t T, int32_t H, void* x,
@@ -830,7 +837,7 @@ mok_status mok_dequantize_rows(const void* x_q, const void* x_sf, int32_t T, int
     if (!aligned(x_q, 16) || !aligned(x, 16)) return MOK_ERR_INVALID;
     if (!device_ok()) return MOK_ERR_CUDA;
     if (T == 0) return MOK_OK;
-    return cuda_status(launch_dequantize_rows(x_q, x_sf, T, H, x, (cudaStream_t)stream));
+    return launch_status(launch_dequantize_rows(x_q, x_sf, T, H, x, (cudaStream_t)stream));
 }
 
 size_t mok_checkpoint_size(const mok_problem* p) {
@@ -869,7 +876,7 @@ mok_status mok_checkpoint_save(const mok_problem* p, const void* x, const mok_ro
     if (p->T == 0) return MOK_OK;
     CheckpointParams q = ckpt_params(p, routing, ckpt, const_cast<void*>(saved));
     q.x = static_cast<const __nv_bfloat16*>(x);
-    return cuda_status(launch_checkpoint_save(q, (cudaStream_t)stream));
+    return launch_status(launch_checkpoint_save(q, (cudaStream_t)stream));
 }
 
 mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ckpt_bytes, const mok_routing* routing,
@@ -881,7 +888,7 @@ mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ck
     if (p->T == 0) return MOK_OK;
     CheckpointParams q = ckpt_params(p, routing, const_cast<void*>(ckpt), saved);
     q.x_out = static_cast<__nv_bfloat16*>(x);
-    return cuda_status(launch_checkpoint_load(q, (cudaStream_t)stream));
+    return launch_status(launch_checkpoint_load(q, (cudaStream_t)stream));
 }
 
 mok_status mok_route_test_hook(int32_t withhold_copy, int32_t timeout_ms) {
