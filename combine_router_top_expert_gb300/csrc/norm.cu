@@ -36,28 +36,20 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return v;
 }
 
-// The same for N values of the threads of one group (nt threads, whole warps;
-// `id` < kBwdGroups names it).
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[32], int id, int nt) {
+// The same over the threads of one group (nt threads, whole warps; `id` <
+// kBwdGroups names it).
+__device__ __forceinline__ float group_sum(float v, float* red, int id, int nt) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-    if (nt == 32) return;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[i][((int)threadIdx.x % nt) >> 5] = v[i];
-    }
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (nt == 32) return v;
+    if (lane == 0) red[((int)threadIdx.x % nt) >> 5] = v;
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(nt) : "memory");
+    v = lane < (nt >> 5) ? red[lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane < (nt >> 5) ? red[i][lane] : 0.f;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
 }
 
 // 8 BF16 values as four pairs.
@@ -121,8 +113,9 @@ __device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
 // (VPT of them), so the row is read once and stays in registers between the sum
 // of squares and the scaling. Lanes 4j..4j+3 of a vector round hold one
 // 32-element MXFP8 block. Several CTAs share an SM and hide each other's waits
-// (T = 4096, H = 7168, MXFP8 output: 37 us; CTAs that loop over rows with the next
-// one prefetched to shared memory took 44).
+// (T = 4096, H = 7168, the sum out as BF16, y as MXFP8: 32 us, 93% of the copy
+// rate, so the bytes bound it; CTAs that loop over rows with the next one prefetched
+// to shared memory took 44).
 template <int VPT>
 __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 4 : 1)
 rmsnorm_kernel(const NormParams p) {
@@ -214,31 +207,35 @@ struct NormBwdParams {
 // A row's group-wide sum stands between its loads and its stores, so the loads of
 // the next rows have to be in flight meanwhile: each thread copies its own vectors
 // of the rows ahead to shared memory (cp.async; nobody else reads them, so no
-// barrier is needed). With one group to an SM nothing else runs while it waits for
-// the sum, so it takes two rows (ROWS) to a barrier. Up to H = 8192 what the second
-// half needs stays in registers; longer rows read their buffers twice. Rows too
-// long for two buffers (STAGES = 0) are read from memory each time.
-template <int VPT, bool CK, int STAGES, int ROWS>
+// barrier is needed). Up to H = 8192 what the second half needs stays in
+// registers; longer rows read their buffers twice. Rows too long for two buffers
+// (STAGES = 0) are read from memory each time.
+//
+// T = 4096, H = 7168 with dsum, both kernels: 40 us for a BF16 sum (87% of the
+// copy rate), 43.6 for MXFP8 rows (70%), whose 12% fewer bytes are paid back in the
+// instructions that unpack them: issue slots and the barrier of each row bound it.
+// Two rows to a barrier spilled (61 us); 448 threads with two vectors each, two
+// CTAs an SM, took 50.
+template <int VPT, bool CK, int STAGES>
 __global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool PF = STAGES > 0;
-    static_assert(PF ? STAGES % ROWS == 0 && STAGES > ROWS : ROWS == 1, "whole steps of rows in the ring");
     extern __shared__ __align__(16) unsigned char bwd_smem[];
-    __shared__ float red[kBwdGroups][2][ROWS][32];
+    __shared__ float red[kBwdGroups][2][32];
     constexpr int kSlots = 3 * VPT;   // 16-byte slots of a thread per row: dy, dsum, s
     pdl_wait();
     pdl_allow_next();
     const int H = p.H, nv = H / 8, nt = p.group;
     const int grp = (int)threadIdx.x / nt, tid = (int)threadIdx.x % nt, groups = (int)blockDim.x / nt;
     const int first = (int)blockIdx.x * groups + grp, total = (int)gridDim.x * groups;
-    const int rows = first < p.T ? (p.T - first + total - 1) / total : 0;   // this group's
+    const int rows = first < p.T ? (p.T - 1 - first) / total + 1 : 0;   // this group's
     const int64_t stride = (int64_t)total * H;
     const float inv_h = 1.0f / (float)H;
     const bool has_dsum = p.dsum != nullptr;
     // running element offsets of this thread's first vector: in the row to load
     // next and in the row at hand
     int64_t in = (int64_t)first * H + 8 * tid, out = in;
-    int next = first;   // row whose rstd is loaded next
+    uint32_t next = first;   // row whose rstd is loaded next
     // slot i of buffer b: consecutive threads side by side
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(bwd_smem) + threadIdx.x * 16;
     auto slot = [&](int b, int i) { return smem0 + (uint32_t)((b * kSlots + i) * (int)blockDim.x) * 16; };
@@ -247,40 +244,36 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
     unsigned char* codes = bwd_smem + (size_t)STAGES * kSlots * blockDim.x * 16;
     auto code_slot = [&](int b, int i) { return codes + ((b * VPT + i) * (int)blockDim.x + (int)threadIdx.x) / 4; };
     const bool ring_codes = PF && CK && (H & 127) == 0 && (reinterpret_cast<uintptr_t>(p.s_sf) & 3) == 0;
-    // PF: start the copies of rows n .. n + ROWS - 1 (those there are) into the
-    // buffers from b on, as one group of copies
+    // PF: start the copies of row n (if there is one) into buffer b, as one group
+    // of copies
     auto issue = [&](int n, int b) {
+        if (n < rows) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (n + r < rows) {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int o = 8 * i * nt;
-                    if (tid + i * nt < nv) {
-                        cp_async16(slot(b + r, i), p.dy + in + o);
-                        if (has_dsum) cp_async16(slot(b + r, VPT + i), p.dsum + in + o);
-                        if constexpr (CK) {
-                            cp_async8(slot(b + r, 2 * VPT + i), p.s_q + in + o);
-                            if (ring_codes && (tid & 15) == 0)
-                                cp_async4((uint32_t)__cvta_generic_to_shared(code_slot(b + r, i)), p.s_sf + (in + o) / 32);
-                        } else {
-                            cp_async16(slot(b + r, 2 * VPT + i), p.s + in + o);
-                        }
+            for (int i = 0; i < VPT; ++i) {
+                const int o = 8 * i * nt;
+                if (tid + i * nt < nv) {
+                    cp_async16(slot(b, i), p.dy + in + o);
+                    if (has_dsum) cp_async16(slot(b, VPT + i), p.dsum + in + o);
+                    if constexpr (CK) {
+                        cp_async8(slot(b, 2 * VPT + i), p.s_q + in + o);
+                        if (ring_codes && (tid & 15) == 0)
+                            cp_async4((uint32_t)__cvta_generic_to_shared(code_slot(b, i)), p.s_sf + (in + o) / 32);
+                    } else {
+                        cp_async16(slot(b, 2 * VPT + i), p.s + in + o);
                     }
                 }
-                in += stride;
             }
+            in += stride;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto load_rstd = [&](int n, float (&rstd)[ROWS]) {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (n + r < rows) {
-                rstd[r] = __ldg(p.rstd + next);
-                next += total;
-            }
+    auto load_rstd = [&](int n) {
+        float v = 0.f;
+        if (n < rows) {
+            v = __ldg(p.rstd + next);
+            next += total;
         }
+        return v;
     };
     // 8 elements of the sum (`out` is the offset of the row at hand)
     auto fetch_s = [&](int b, int i, float2 (&s)[4]) {
@@ -298,100 +291,79 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
     auto fetch_dy = [&](int b, int i, float2 (&d)[4]) {
         unpack_pairs(PF ? ld_shared16(slot(b, i)) : *reinterpret_cast<const uint4*>(p.dy + in + 8 * i * nt), d);
     };
-    constexpr bool kKeep = VPT == 1;   // the gain and the rows' s stay in registers over the sum
-    float2 dg[VPT][4], gk[4], sk[ROWS][4];
+    constexpr bool kKeep = VPT == 1;   // the gain and the row's s stay in registers over the sum
+    float2 dg[VPT][4], gk[4], sk[4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dg[i][j] = both(0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        gk[j] = both(0.f);
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) sk[r][j] = both(0.f);
-    }
+    for (int j = 0; j < 4; ++j) gk[j] = sk[j] = both(0.f);
     if (kKeep && tid < nv) load8(p.gain + 8 * tid, gk);
 
-    constexpr int kAhead = PF ? STAGES / ROWS - 1 : 0;   // steps in flight beyond this one
+    constexpr int kAhead = PF ? STAGES - 1 : 0;   // rows in flight beyond this one
     if constexpr (PF) {
 #pragma unroll
-        for (int n = 0; n < kAhead; ++n) issue(n * ROWS, n * ROWS);
+        for (int n = 0; n < kAhead; ++n) issue(n, n);
     }
-    float rstd[ROWS] = {}, rstd_next[ROWS] = {};
-    load_rstd(0, rstd);
-    int b = 0, half = 0;   // buffer of this step's first row; which of the sums' scratch
+    float rstd = load_rstd(0);
+    int b = 0;   // this row's buffer
 #pragma unroll 1
-    for (int n = 0; n < rows; n += ROWS, half ^= 1) {
-        load_rstd(n + ROWS, rstd_next);
+    for (int n = 0; n < rows; ++n) {
+        const float rstd_next = load_rstd(n + 1);
         if constexpr (PF) {
-            // into the buffers of the step before this one (this thread is done with them)
-            issue(n + kAhead * ROWS, b == 0 ? STAGES - ROWS : b - ROWS);
+            // into the buffer of the row before this one (this thread is done with it)
+            issue(n + kAhead, b == 0 ? STAGES - 1 : b - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
             if constexpr (CK) __syncwarp();   // the codes are other lanes' copies
         }
-        float dots[ROWS];
+        float2 dot2 = both(0.f);
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            float2 dot = both(0.f);
-            if (n + r < rows) {
+        for (int i = 0; i < VPT; ++i) {
+            if (tid + i * nt < nv) {
+                float2 s[4], d[4], g[4];
+                fetch_s(b, i, s);
+                fetch_dy(b, i, d);
+                if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    if (tid + i * nt < nv) {
-                        float2 s[4], d[4], g[4];
-                        fetch_s(b + r, i, s);
-                        fetch_dy(b + r, i, d);
-                        if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
-                            dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd[r])), s[j], dg[i][j]);
-                            dot = __ffma2_rn(u, s[j], dot);
-                            if constexpr (kKeep) sk[r][j] = s[j];
-                        }
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
+                    dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd)), s[j], dg[i][j]);
+                    dot2 = __ffma2_rn(u, s[j], dot2);
+                    if constexpr (kKeep) sk[j] = s[j];
                 }
             }
-            dots[r] = dot.x + dot.y;
         }
-        group_sum<ROWS>(dots, red[grp][half], grp, nt);
+        const float dot = group_sum(dot2.x + dot2.y, red[grp][n & 1], grp, nt);
+        // dx = dsum + rstd u - c s with u = gain dy, c = rstd^3 sum(u s) / H
+        const float c = -rstd * (rstd * (rstd * (dot * inv_h)));
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (n + r < rows) {
-                // dx = dsum + rstd u - c s with u = gain dy, c = rstd^3 sum(u s) / H
-                const float c = -rstd[r] * (rstd[r] * (rstd[r] * (dots[r] * inv_h)));
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    if (tid + i * nt < nv) {
-                        const int o = 8 * i * nt;
-                        float2 d[4] = {}, s[4], u[4], g[4];
-                        if (has_dsum)
-                            unpack_pairs(PF ? ld_shared16(slot(b + r, VPT + i)) : *reinterpret_cast<const uint4*>(p.dsum + in + o), d);
-                        fetch_dy(b + r, i, u);
-                        if constexpr (!kKeep) {
-                            fetch_s(b + r, i, s);
-                            load8(p.gain + 8 * (tid + i * nt), g);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 w = __fmul2_rn(u[j], kKeep ? gk[j] : g[j]);
-                            d[j] = __ffma2_rn(both(rstd[r]), w, d[j]);
-                            d[j] = __ffma2_rn(both(c), kKeep ? sk[r][j] : s[j], d[j]);
-                        }
-                        *reinterpret_cast<uint4*>(p.dx + out + o) = pack_pairs(d);
-                    }
+        for (int i = 0; i < VPT; ++i) {
+            if (tid + i * nt < nv) {
+                const int o = 8 * i * nt;
+                float2 d[4] = {}, s[4], u[4], g[4];
+                if (has_dsum)
+                    unpack_pairs(PF ? ld_shared16(slot(b, VPT + i)) : *reinterpret_cast<const uint4*>(p.dsum + in + o), d);
+                fetch_dy(b, i, u);
+                if constexpr (!kKeep) {
+                    fetch_s(b, i, s);
+                    load8(p.gain + 8 * (tid + i * nt), g);
                 }
-                out += stride;
-                if constexpr (!PF) in = out;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 w = __fmul2_rn(u[j], kKeep ? gk[j] : g[j]);
+                    d[j] = __ffma2_rn(both(rstd), w, d[j]);
+                    d[j] = __ffma2_rn(both(c), kKeep ? sk[j] : s[j], d[j]);
+                }
+                *reinterpret_cast<uint4*>(p.dx + out + o) = pack_pairs(d);
             }
         }
-        if constexpr (PF) {
-            b += ROWS;
-            if (b == STAGES) b = 0;
-        }
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            rstd[r] = rstd_next[r];
-        }
+        out += stride;
+        if constexpr (!PF) in = out;
+        if constexpr (PF) b = b + 1 == STAGES ? 0 : b + 1;
+        // the next copies may overwrite codes that other lanes have just read again
+        if constexpr (PF && CK && !kKeep) __syncwarp();
+        rstd = rstd_next;
     }
     if constexpr (PF) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float* part = p.part + (int64_t)blockIdx.x * H;
@@ -503,19 +475,19 @@ BwdShape bwd_shape(int H) {
     return b;
 }
 
-template <int VPT, bool CK, int STAGES, int ROWS>
+template <int VPT, bool CK, int STAGES>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
-    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES, ROWS>;
+    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES>;
     if (b.smem > 40 * 1024) ensure_smem_attr(reinterpret_cast<const void*>(kern), b.smem);
     return launch_after(kern, dim3(grid), dim3(b.group * b.groups), b.smem, s, p);
 }
 template <bool CK>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
     switch (b.vpt) {
-        case 1: return run_bwd<1, CK, 4, 1>(p, grid, b, s);
-        case 2: return run_bwd<2, CK, 2, 1>(p, grid, b, s);
-        case 4: return run_bwd<4, CK, 0, 1>(p, grid, b, s);
-        default: return run_bwd<8, CK, 0, 1>(p, grid, b, s);
+        case 1: return run_bwd<1, CK, 4>(p, grid, b, s);
+        case 2: return run_bwd<2, CK, 2>(p, grid, b, s);
+        case 4: return run_bwd<4, CK, 0>(p, grid, b, s);
+        default: return run_bwd<8, CK, 0>(p, grid, b, s);
     }
 }
 
