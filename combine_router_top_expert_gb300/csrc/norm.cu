@@ -393,36 +393,39 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
     }
 }
 
-// dgain[h] = sum over the P partial rows, in a fixed order: 32 warps take the
-// rows w, w + 32, ... (eight loads in flight), then the warps' sums are added in
-// order. 32 columns a CTA.
-__global__ void __launch_bounds__(1024)
+// dgain[h] = sum over the P partial rows, in a fixed order: 8 warps take the rows
+// w, w + 8, ... (ten loads in flight), then the warps' sums are added in order. 64
+// columns a CTA. The CTAs are small enough (32 registers a thread) to be resident
+// beside the backward's CTA of 896 threads, so that they wait there for its end.
+constexpr int kDgainCols = 64;
+__global__ void __launch_bounds__(256, 8)
 rmsnorm_dgain_kernel(const float* __restrict__ part, int P, int H, float* __restrict__ dgain) {
-    __shared__ float red[32][33];
+    __shared__ float2 red[8][32];
     pdl_wait();
     pdl_allow_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x * 32 + lane;
-    float s = 0.f;
+    const int h = blockIdx.x * kDgainCols + 2 * lane;
+    float2 s = both(0.f);
     if (h < H) {
-        for (int b0 = warp; b0 < P; b0 += 8 * 32) {
-            float v[8];
+        for (int b0 = warp; b0 < P; b0 += 10 * 8) {
+            float2 v[10];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int b = b0 + 32 * u;
-                v[u] = b < P ? part[(int64_t)b * H + h] : 0.f;
+            for (int u = 0; u < 10; ++u) {
+                const int b = b0 + 8 * u;
+                v[u] = b < P ? __ldcg(reinterpret_cast<const float2*>(part + (int64_t)b * H + h)) : both(0.f);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += v[u];
+            for (int u = 0; u < 10; ++u) s = __fadd2_rn(s, v[u]);
         }
     }
     red[warp][lane] = s;
     __syncthreads();
-    // warp w: the sum of column w over the 32 warps' sums
-    float v = red[lane][warp];
+    if (warp == 0 && h < H) {
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0 && blockIdx.x * 32 + warp < H) dgain[blockIdx.x * 32 + warp] = v;
+        for (int w = 1; w < 8; ++w) s = __fadd2_rn(s, red[w][lane]);
+        dgain[h] = s.x;   // (4-byte aligned)
+        dgain[h + 1] = s.y;
+    }
 }
 
 // BF16 rows from MXFP8 rows: 8 elements a thread.
@@ -540,7 +543,7 @@ cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a,
     p.group = b.group;
     cudaError_t e = a.sum_q ? run_bwd<true>(p, P, b, s) : run_bwd<false>(p, P, b, s);
     if (e != cudaSuccess) return e;
-    return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, 32)), dim3(1024), 0, s, (const float*)p.part, P, H,
+    return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, kDgainCols)), dim3(256), 0, s, (const float*)p.part, P, H,
                         p.dgain);
 }
 

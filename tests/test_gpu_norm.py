@@ -196,6 +196,25 @@ def test_backward_from_scale_codes_at_any_address():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(37, 64), (300, 1024)])
+def test_dgain_at_any_float_address(T, H):
+    """dgain needs four-byte alignment only: the same bits one float further on."""
+    g = _gen(21)
+    x, dy = _bf16(g, (T, H)), _bf16(g, (T, H))
+    gain = torch.randn(H, device="cuda", generator=g)
+    rstd = torch.rand(T, device="cuda", generator=g) + 0.5
+    ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(T, H))
+    got = []
+    for shift in (0, 1, 3):
+        dx = torch.empty_like(x)
+        d = torch.full((H + 8,), -1.0, device="cuda")
+        mok.rmsnorm_backward(dy, gain, rstd, dx, d[shift:shift + H], ws, s=x)
+        got.append(d[shift:shift + H].clone())
+        assert (d[:shift] == -1).all() and (d[shift + H:] == -1).all()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.gpu
 def test_gradients_against_differences():
     """Central differences of the 64-bit forward, loss = <dy, y> + <dsum, s>,
     step 1e-5 (error about 1e-9); the BF16 dx adds half a spacing."""
