@@ -211,11 +211,13 @@ struct NormBwdParams {
 // registers; longer rows read their buffers twice. Rows too long for two buffers
 // (STAGES = 0) are read from memory each time.
 //
-// T = 4096, H = 7168 with dsum, both kernels: 40 us for a BF16 sum (87% of the
-// copy rate), 43.6 for MXFP8 rows (70%), whose 12% fewer bytes are paid back in the
-// instructions that unpack them: issue slots and the barrier of each row bound it.
-// Two rows to a barrier spilled (61 us); 448 threads with two vectors each, two
-// CTAs an SM, took 50.
+// T = 4096, H = 7168 with dsum, both kernels: 40.0 us for a BF16 sum (87% of the
+// copy rate; the launches, the first rows' way in and the gain gradient take the
+// rest), 42.5 for MXFP8 rows (72%): their 12% fewer bytes are paid back in the
+// instructions that unpack them between a row's loads and its barrier. Slower were
+// two rows to a barrier (spills, 61 us), 448 threads with two vectors each, two
+// CTAs an SM (50), and the second half of a row behind the first half of the next
+// over mbarriers (55).
 template <int VPT, bool CK, int STAGES>
 __global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
@@ -275,17 +277,21 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
         }
         return v;
     };
-    // 8 elements of the sum (`out` is the offset of the row at hand)
+    // 8 elements of the sum over their common factor, which is returned: a block's
+    // scale goes into the factors of its elements (`out` is the offset of the row at
+    // hand)
     auto fetch_s = [&](int b, int i, float2 (&s)[4]) {
         const int o = 8 * i * nt;
         if constexpr (CK) {
             float f[8];
             const uint32_t code = ring_codes ? *code_slot(b, i) : __ldg(p.s_sf + (out + o) / 32);
-            dequantize8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(p.s_q + in + o), code, f);
+            e4m3_values8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(p.s_q + in + o), f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = make_float2(f[2 * j], f[2 * j + 1]);
+            return e8m0_scale(code);
         } else {
             unpack_pairs(PF ? ld_shared16(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(p.s + in + o), s);
+            return 1.0f;
         }
     };
     auto fetch_dy = [&](int b, int i, float2 (&d)[4]) {
@@ -299,6 +305,7 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
         for (int j = 0; j < 4; ++j) dg[i][j] = both(0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) gk[j] = sk[j] = both(0.f);
+    float fk = 1.f;   // factor of sk
     if (kKeep && tid < nv) load8(p.gain + 8 * tid, gk);
 
     constexpr int kAhead = PF ? STAGES - 1 : 0;   // rows in flight beyond this one
@@ -317,24 +324,26 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
             if constexpr (CK) __syncwarp();   // the codes are other lanes' copies
         }
-        float2 dot2 = both(0.f);
+        float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (tid + i * nt < nv) {
-                float2 s[4], d[4], g[4];
-                fetch_s(b, i, s);
+                float2 s[4], d[4], g[4], dot2 = both(0.f);
+                const float f = fetch_s(b, i, s), rf = CK ? rstd * f : rstd;
                 fetch_dy(b, i, d);
                 if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 u = __fmul2_rn(d[j], kKeep ? gk[j] : g[j]);
-                    dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rstd)), s[j], dg[i][j]);
+                    dg[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rf)), s[j], dg[i][j]);
                     dot2 = __ffma2_rn(u, s[j], dot2);
                     if constexpr (kKeep) sk[j] = s[j];
                 }
+                dot = CK ? fmaf(f, dot2.x + dot2.y, dot) : dot + (dot2.x + dot2.y);
+                if constexpr (CK && kKeep) fk = f;
             }
         }
-        const float dot = group_sum(dot2.x + dot2.y, red[grp][n & 1], grp, nt);
+        dot = group_sum(dot, red[grp][n & 1], grp, nt);
         // dx = dsum + rstd u - c s with u = gain dy, c = rstd^3 sum(u s) / H
         const float c = -rstd * (rstd * (rstd * (dot * inv_h)));
 #pragma unroll
@@ -345,15 +354,17 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
                 if (has_dsum)
                     unpack_pairs(PF ? ld_shared16(slot(b, VPT + i)) : *reinterpret_cast<const uint4*>(p.dsum + in + o), d);
                 fetch_dy(b, i, u);
+                float f = fk;
                 if constexpr (!kKeep) {
-                    fetch_s(b, i, s);
+                    f = fetch_s(b, i, s);
                     load8(p.gain + 8 * (tid + i * nt), g);
                 }
+                const float cf = CK ? c * f : c;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 w = __fmul2_rn(u[j], kKeep ? gk[j] : g[j]);
                     d[j] = __ffma2_rn(both(rstd), w, d[j]);
-                    d[j] = __ffma2_rn(both(c), kKeep ? sk[j] : s[j], d[j]);
+                    d[j] = __ffma2_rn(both(cf), kKeep ? sk[j] : s[j], d[j]);
                 }
                 *reinterpret_cast<uint4*>(p.dx + out + o) = pack_pairs(d);
             }

@@ -106,20 +106,28 @@ __device__ __forceinline__ float e8m0_scale(uint32_t code) {
     return code ? __uint_as_float(code << 23) : __uint_as_float(1u << 22);
 }
 
-// The values that 8 E4M3 bytes and their block's scale code stand for. E4M3
-// converts exactly to FP16 and on to fp32, and the scale is a power of two, so
-// every value is exact (and, with 4 significant bits, a BF16 number).
-__device__ __forceinline__ void dequantize8(const uint2& q, uint32_t code, float (&f)[8]) {
-    const float s = e8m0_scale(code);
+// 8 E4M3 values, without their block's scale. E4M3 converts exactly to FP16 and
+// on to fp32.
+__device__ __forceinline__ void e4m3_values8(const uint2& q, float (&f)[8]) {
     const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)));
         const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3));
         const float2 v = __half22float2(h);
-        f[2 * i] = v.x * s;
-        f[2 * i + 1] = v.y * s;
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
     }
+}
+
+// The values that 8 E4M3 bytes and their block's scale code stand for. The scale is
+// a power of two, so every value is exact (and, with 4 significant bits, a BF16
+// number).
+__device__ __forceinline__ void dequantize8(const uint2& q, uint32_t code, float (&f)[8]) {
+    const float s = e8m0_scale(code);
+    e4m3_values8(q, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= s;
 }
 
 }  // namespace mok
