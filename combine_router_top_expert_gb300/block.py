@@ -9,13 +9,31 @@ them. Decode-sized batches take the few-token kernels, others the layer's
 stages. Training keeps 8-bit checkpoints: the stream as MXFP8 rows for the norm's
 backward, and the layer's context (mok_checkpoint_save) in a quarter of the
 memory, so that one full context serves every block of a model.
+
+The workspaces belong to the block (and the full context to its layer): its calls
+go to one stream at a time. With `stream` given, the new tensors are that stream's
+in the allocator, and the inputs have to be ready on it.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
 from . import mok
 from .layer import MoELayer
+
+
+def _on_stream(f):
+    """Runs a method with its `stream` as the current one, so that what it allocates and drops again is not
+    handed to another stream's work while its kernels still use it."""
+    @functools.wraps(f)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return wrapped
 
 
 class MoEBlock:
@@ -27,29 +45,31 @@ class MoEBlock:
 
     # ------------------------------------------------------------------ serving
 
-    def forward(self, x, residual=None, stream=None):
+    @_on_stream
+    def forward(self, x, residual=None):
         """(out, residual stream), both [T, H] bf16 (new tensors). x and residual may be row-strided."""
         T, H = x.shape
         total, y = (torch.empty((T, H), dtype=torch.bfloat16, device=x.device) for _ in range(2))
-        mok.rmsnorm(x, self.gain, residual=residual, eps=self.eps, sum=total, y=y, stream=stream)
+        mok.rmsnorm(x, self.gain, residual=residual, eps=self.eps, sum=total, y=y)
         out = torch.empty_like(y)
         if mok.few_tokens_ok(T, self.layer.k):
-            self._forward_few(y, out, stream)
+            self._forward_few(y, out)
         else:
-            self.layer.forward(y, stream=stream, out=out)
+            self.layer.forward(y, out=out)
         return out, total
 
-    def _forward_few(self, y, out, stream):
+    def _forward_few(self, y, out):
         T, layer = y.shape[0], self.layer
         p = layer.problem(T)
         if T not in self._few:
             self._few[T] = mok.alloc_bytes(mok.few_workspace_size(p), layer.device)
         mok.moe_few(p, y, layer.W_r, layer.packed, out, self._few[T], bias=layer.bias,
-                    packed_shared=layer.packed_shared, stream=stream)
+                    packed_shared=layer.packed_shared)
 
     # ------------------------------------------------------------------ training
 
-    def train_forward(self, x, residual=None, stream=None):
+    @_on_stream
+    def train_forward(self, x, residual=None):
         """(out, residual stream, ctx): ctx holds what train_backward needs."""
         T, H = x.shape
         layer, dev = self.layer, x.device
@@ -58,34 +78,35 @@ class MoEBlock:
                    sum_q=torch.empty((T, H), dtype=torch.uint8, device=dev),
                    sum_sf=torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
         mok.rmsnorm(x, self.gain, residual=residual, eps=self.eps, sum=total, y=y, sum_q=ctx["sum_q"],
-                    sum_sf=ctx["sum_sf"], rstd=ctx["rstd"], stream=stream)
+                    sum_sf=ctx["sum_sf"], rstd=ctx["rstd"])
         p, b = layer.problem(T), layer.buffers(T, True)
         # the checkpoint refers to this routing until the backward, so it is its own
-        ctx["routing"] = mok.route_layout(y, layer.W_r, layer.k, layer.bias, workspace=b["route_ws"], stream=stream)
+        ctx["routing"] = mok.route_layout(y, layer.W_r, layer.k, layer.bias, workspace=b["route_ws"])
         out = torch.empty_like(y)
         mok.moe_forward(p, y, layer.packed, ctx["routing"], out, b["ws"], saved=b["saved"],
-                        packed_shared=layer.packed_shared, stream=stream)
+                        packed_shared=layer.packed_shared)
         ctx["ckpt"] = mok.alloc_bytes(mok.checkpoint_size(p), dev)
-        mok.checkpoint_save(p, y, ctx["routing"], b["saved"], ctx["ckpt"], stream=stream)
+        mok.checkpoint_save(p, y, ctx["routing"], b["saved"], ctx["ckpt"])
         return out, total, ctx
 
-    def train_backward(self, ctx, dout, dstream=None, stream=None):
+    @_on_stream
+    def train_backward(self, ctx, dout, dstream=None):
         """Gradients of a train_forward: dict with dx (of x and of the residual alike), dgain, and the layer's
         dW_gate, dW_up, dW_down, dW_r. dout, dstream: gradients of out and of the residual stream."""
         T, layer = ctx["T"], self.layer
         p, b, H = layer.problem(T), layer.buffers(T, True), layer.H
         y = torch.empty((T, H), dtype=torch.bfloat16, device=dout.device)
-        mok.checkpoint_load(p, ctx["ckpt"], ctx["routing"], y, b["saved"], stream=stream)
+        mok.checkpoint_load(p, ctx["ckpt"], ctx["routing"], y, b["saved"])
         g = dict(dX=torch.empty_like(y), dW_gate=torch.empty_like(layer.Wg), dW_up=torch.empty_like(layer.Wu),
                  dW_down=torch.empty_like(layer.Wd),
                  dW_r=torch.empty((H, layer.E), dtype=torch.float32, device=dout.device))
         mok.moe_backward(p, y, layer.W_r, layer.Wg, layer.Wu, layer.Wd, layer.packed, dout, ctx["routing"],
-                         b["saved"], g, b["ws"], stream=stream, packed_bwd=layer.packed_bwd)
+                         b["saved"], g, b["ws"], packed_bwd=layer.packed_bwd)
         if T not in self._norm_ws:
             self._norm_ws[T] = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(T, H), dout.device)
         g["dx"] = g.pop("dX")
         g["dgain"] = torch.empty(H, dtype=torch.float32, device=dout.device)
         # dx takes dy's place: the layer's input gradient is read before it is overwritten
         mok.rmsnorm_backward(g["dx"], self.gain, ctx["rstd"], g["dx"], g["dgain"], self._norm_ws[T],
-                             s_q=ctx["sum_q"], s_sf=ctx["sum_sf"], dsum=dstream, stream=stream)
+                             s_q=ctx["sum_q"], s_sf=ctx["sum_sf"], dsum=dstream)
         return g

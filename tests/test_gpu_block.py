@@ -93,6 +93,40 @@ def test_training_step(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [7, 300])
+def test_side_stream_keeps_its_temporaries(T):
+    """What a call on another stream allocates and drops is not reused by the
+    current stream while its kernels wait: memory of the same sizes, taken and
+    filled on the current stream right after the call, changes nothing."""
+    wl = synth.small("block", T=T, H=512, I=256, E=8, k=2)
+    _, block, x, r, _ = _block(wl)
+    want, ctx0 = block.train_forward(x, r)[::2]
+    gwant = block.train_backward(ctx0, want)
+    served = block.forward(x, r)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = block.forward(x, r, stream=side)[0]
+    out, _, ctx = block.train_forward(x, r, stream=side)
+    g = block.train_backward(ctx, want, stream=side)
+    trash = [torch.full((T, 512), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, served) and torch.equal(out, want) and len(trash) == 16
+    for n, v in gwant.items():
+        assert torch.equal(g[n], v), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+def test_no_tokens(dtype):
+    wl = synth.small("block", T=4, H=512, I=256, E=8, k=2, dtype=dtype)
+    _, block, x, r, _ = _block(wl)
+    out, stream = block.forward(x[:0], r[:0])
+    assert out.shape == stream.shape == (0, 512)
+
+
+@pytest.mark.gpu
 def test_example_runs():
     for extra in ([], ["--mxfp8"]):
         r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "moe_block.py"), "--layers", "2", "--tokens",
