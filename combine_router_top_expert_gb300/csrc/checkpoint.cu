@@ -208,10 +208,7 @@ checkpoint_load_kernel(const CheckpointParams p) {
 }
 
 int ck_grid(int64_t jobs) {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return (int)std::max<int64_t>(1, std::min<int64_t>((jobs + 7) / 8, (int64_t)n * 8));
+    return (int)std::max<int64_t>(1, std::min<int64_t>((jobs + 7) / 8, (int64_t)sm_count() * 8));
 }
 
 }  // namespace

@@ -579,13 +579,6 @@ __global__ void dwr_reduce_kernel(const float* __restrict__ part, int H, int E, 
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
-static int sm_count() {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 1;
-}
-
 cudaError_t launch_dispatch(bool mx, const void* x, int T, int H, int E, int k, const int32_t* counts,
                             const int32_t* offsets, const int32_t* row_src, void* A, uint8_t* A_sf,
                             const void* scale_src, const float* wslot, cudaStream_t s, bool zero_pads) {

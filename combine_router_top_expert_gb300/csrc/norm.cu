@@ -9,7 +9,6 @@
 // (dx is the gradient of x and of r alike). All sums are held in fp32; each
 // output is rounded once.
 #include <algorithm>
-#include <atomic>
 
 #include "common.cuh"
 #include "moves.cuh"
@@ -450,18 +449,6 @@ dequantize_rows_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict_
         dequantize8(__ldg(reinterpret_cast<const uint2*>(q) + v), __ldg(sf + v / 4), f);
         reinterpret_cast<uint4*>(x)[v] = pack8(f);
     }
-}
-
-// SMs of the current device (asked once per device).
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    n = known[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 // Threads and vectors per thread of a CTA that holds one row.

@@ -525,8 +525,8 @@ def checkpoint_save(p: Problem, x, routing, saved, ckpt, stream=None):
     if saved.numel() < saved_size(p):
         raise MokError(ERR_INVALID, "mok_checkpoint_save: saved")
     rs = routing_struct(routing)
-    _check(lib().mok_checkpoint_save(ctypes.byref(p), _ptr(x), ctypes.byref(rs), _ptr(saved), _ptr(ckpt),
-                                     ckpt.numel(), _stream(stream)), "mok_checkpoint_save")
+    _check(lib().mok_checkpoint_save(ctypes.byref(p), x.data_ptr(), ctypes.byref(rs), saved.data_ptr(),
+                                     ckpt.data_ptr(), ckpt.numel(), _stream(stream)), "mok_checkpoint_save")
 
 
 def checkpoint_load(p: Problem, ckpt, routing, x, saved, stream=None):
@@ -535,8 +535,8 @@ def checkpoint_load(p: Problem, ckpt, routing, x, saved, stream=None):
     if saved.numel() < saved_size(p):
         raise MokError(ERR_INVALID, "mok_checkpoint_load: saved")
     rs = routing_struct(routing)
-    _check(lib().mok_checkpoint_load(ctypes.byref(p), _ptr(ckpt), ckpt.numel(), ctypes.byref(rs), _ptr(x),
-                                     _ptr(saved), _stream(stream)), "mok_checkpoint_load")
+    _check(lib().mok_checkpoint_load(ctypes.byref(p), ckpt.data_ptr(), ckpt.numel(), ctypes.byref(rs), x.data_ptr(),
+                                     saved.data_ptr(), _stream(stream)), "mok_checkpoint_load")
 
 
 def megakernel_trace(workspace, n_ctas):
