@@ -282,11 +282,10 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
     auto fetch_s = [&](int b, int i, float2 (&s)[4]) {
         const int o = 8 * i * nt;
         if constexpr (CK) {
-            float f[8];
             const uint32_t code = ring_codes ? *code_slot(b, i) : __ldg(p.s_sf + (out + o) / 32);
-            e4m3_values8(PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(p.s_q + in + o), f);
+            const uint2 q = PF ? ld_shared8(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint2*>(p.s_q + in + o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = make_float2(f[2 * j], f[2 * j + 1]);
+            for (int j = 0; j < 4; ++j) s[j] = e4m3_pair(q, j);
             return e8m0_scale(code);
         } else {
             unpack_pairs(PF ? ld_shared16(slot(b, 2 * VPT + i)) : *reinterpret_cast<const uint4*>(p.s + in + o), s);

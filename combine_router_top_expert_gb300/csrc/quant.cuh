@@ -106,18 +106,11 @@ __device__ __forceinline__ float e8m0_scale(uint32_t code) {
     return code ? __uint_as_float(code << 23) : __uint_as_float(1u << 22);
 }
 
-// 8 E4M3 values, without their block's scale. E4M3 converts exactly to FP16 and
-// on to fp32.
-__device__ __forceinline__ void e4m3_values8(const uint2& q, float (&f)[8]) {
-    const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)));
-        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3));
-        const float2 v = __half22float2(h);
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
+// Values 2i and 2i + 1 of 8 E4M3 bytes, without their block's scale. E4M3 converts
+// exactly to FP16 and on to fp32.
+__device__ __forceinline__ float2 e4m3_pair(const uint2& q, int i) {
+    const __nv_fp8x2_storage_t pair = (__nv_fp8x2_storage_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1)));
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3)));
 }
 
 // The values that 8 E4M3 bytes and their block's scale code stand for. The scale is
@@ -125,9 +118,12 @@ __device__ __forceinline__ void e4m3_values8(const uint2& q, float (&f)[8]) {
 // number).
 __device__ __forceinline__ void dequantize8(const uint2& q, uint32_t code, float (&f)[8]) {
     const float s = e8m0_scale(code);
-    e4m3_values8(q, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= s;
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = e4m3_pair(q, i);
+        f[2 * i] = v.x * s;
+        f[2 * i + 1] = v.y * s;
+    }
 }
 
 }  // namespace mok
