@@ -110,16 +110,17 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Top-k of one token by one warp (larger logit first, lower expert on ties,
-// -0 = +0): experts lane, lane + 32, ...; keys order like the logits, 0 is
-// "taken". The weights are the softmax over the selected logits.
-__device__ __forceinline__ void few_topk(const float* lg, const FewLogitsParams& p, int64_t t) {
+// -0 = +0): experts lane, lane + 32, ... (NQ of them, E <= 32 NQ); keys order like the
+// logits, 0 is "taken". The weights are the softmax over the selected logits. `sel`
+// holds the selected experts meanwhile (256 bytes of this warp's).
+template <int NQ>
+__device__ __forceinline__ void few_topk(const float* lg, uint8_t* sel, const FewLogitsParams& p, int64_t t) {
     const int lane = threadIdx.x & 31;
-    const int nq = ceil_div(p.E, 32);
-    uint32_t key[kMaxE / 32];
+    uint32_t key[NQ];
 #pragma unroll
-    for (int q = 0; q < kMaxE / 32; ++q) {
+    for (int q = 0; q < NQ; ++q) {
         key[q] = 0;
-        if (q < nq && lane + 32 * q < p.E) {
+        if (lane + 32 * q < p.E) {
             const uint32_t b = __float_as_uint(lg[lane + 32 * q] + 0.0f);
             key[q] = max(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u), 1u);
         }
@@ -129,28 +130,30 @@ __device__ __forceinline__ void few_topk(const float* lg, const FewLogitsParams&
         uint32_t best = key[0];
         int be = lane;
 #pragma unroll
-        for (int q = 1; q < kMaxE / 32; ++q)
-            if (q < nq && key[q] > best) {
+        for (int q = 1; q < NQ; ++q)
+            if (key[q] > best) {
                 best = key[q];
                 be = lane + 32 * q;
             }
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)be : 0xffffu);
+        int e;
+        if constexpr (NQ == 1) e = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        else e = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)be : 0xffffu);
 #pragma unroll
-        for (int q = 0; q < kMaxE / 32; ++q)
+        for (int q = 0; q < NQ; ++q)
             if (e == lane + 32 * q) key[q] = 0;
         const float l = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
         if (j == 0) l0 = l;
         den += expf(l - l0);   // j ascending; identical in every lane
-        if (lane == 0) {
-            p.idx[t * p.k + j] = e;
-            if (p.topk_idx) p.topk_idx[t * p.k + j] = e;
-        }
+        if (lane == 0) sel[j] = (uint8_t)e;
     }
     __syncwarp();
     for (int j = lane; j < p.k; j += 32) {
-        const float w = expf(lg[p.idx[t * p.k + j]] - l0) / den;
+        const int e = sel[j];
+        const float w = expf(lg[e] - l0) / den;
+        p.idx[t * p.k + j] = e;
         p.w[t * p.k + j] = w;
+        if (p.topk_idx) p.topk_idx[t * p.k + j] = e;
         if (p.topk_w) p.topk_w[t * p.k + j] = w;
     }
 }
@@ -184,17 +187,27 @@ few_logits_kernel(const FewLogitsParams p) {
 
     // row r of a chunk's share: chain rank + CL (r / 8), h = 256 i + 8 chain + r % 8
     auto h_of = [&](int i, int r) { return 256 * i + 8 * (rank + CL * (r >> 3)) + (r & 7); };
+    // this thread's copies of a stage: of W_r the vector v0 of rows r0, r0 + 32, ...
+    // (whole chunks apart), of x 8 h of one token
+    constexpr int kRowStep = kLgThreads / 8, kChunkStep = kRowStep / kChunkRows;
+    static_assert(kRowStep % kChunkRows == 0, "whole chunks apart");
+    const int r0 = tid >> 3, v0 = tid & 7;
+    const int hw = h_of(r0 / kChunkRows, r0 % kChunkRows);
+    const bool e_in = e0 + 4 * v0 < p.E;
+    const float* wp = p.W_r + (int64_t)hw * p.E + e0 + 4 * v0;
+    const int xi = tid / (kLgTokens * NCH), xt = (tid / NCH) % kLgTokens;   // [chunk][token][chain][8 h]
+    const int hx = h_of(xi, 8 * (tid % NCH));
+    const __nv_bfloat16* xp = p.x + (int64_t)(t0 + xt) * p.H + hx;
     auto issue = [&](int n) {
         if (n < total) {
             const int c0 = n * kChunks;
             const uint32_t ws = tc::smem_u32(lg_smem + (n % STAGES) * kLgStageBytes), xs = ws + kLgWBytes;
             if (vec) {
 #pragma unroll
-                for (int q = 0; q < kLgRows * 8 / kLgThreads; ++q) {   // rows x 8 vectors
-                    const int r = (tid >> 3) + q * (kLgThreads / 8), v = tid & 7;
-                    const int h = h_of(c0 + r / kChunkRows, r % kChunkRows), e = e0 + 4 * v;
-                    const bool in = h < p.H && e < p.E;
-                    cp_async16(ws + (r * 32 + 4 * v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
+                for (int q = 0; q < kLgRows / kRowStep; ++q) {
+                    const int h = 256 * (c0 + q * kChunkStep);   // from this thread's first
+                    const bool in = hw + h < p.H && e_in;
+                    cp_async16(ws + (r0 + q * kRowStep) * 128 + v0 * 16, in ? wp + (int64_t)h * p.E : p.W_r, in);
                 }
             } else {
                 for (int j = tid; j < kLgRows * 32; j += kLgThreads) {
@@ -204,11 +217,9 @@ few_logits_kernel(const FewLogitsParams p) {
                     cp_async4(ws + (r * 32 + v) * 4, in ? p.W_r + (int64_t)h * p.E + e : p.W_r, in);
                 }
             }
-            if (tid < kLgRows) {      // [chunk][token][chain][8 h]
-                const int i = tid / (kLgTokens * NCH), t = (tid / NCH) % kLgTokens, v = tid % NCH;
-                const int h = h_of(c0 + i, 8 * v);
-                const bool in = h < p.H && t < ntok;
-                cp_async16(xs + tid * 16, in ? p.x + (int64_t)(t0 + t) * p.H + h : p.x, in);
+            if (tid < kLgRows) {
+                const bool in = hx + 256 * c0 < p.H && xt < ntok;
+                cp_async16(xs + tid * 16, in ? xp + 256 * c0 : p.x, in);
             }
         }
         cp_async_commit();   // one group per stage, empty past the end
@@ -236,28 +247,29 @@ few_logits_kernel(const FewLogitsParams p) {
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-    float acc[NCH] = {};
+    float2 acc2[NCH / 2] = {};
     for (int n = 0; n < total; ++n) {
         cp_async_wait<STAGES - 2>();
         __syncthreads();              // stage n has landed for every thread; stage n - 1 is consumed
         issue(n + STAGES - 1);
-        const int c0 = n * kChunks;
         const float* ws = reinterpret_cast<const float*>(lg_smem + (n % STAGES) * kLgStageBytes);
         const unsigned char* xs = lg_smem + (n % STAGES) * kLgStageBytes + kLgWBytes;
+        if (tw < ntok) {
+            // without branches, so that the loads of all chunks run ahead: what lies
+            // past H or past the last token was filled with zeros and adds nothing
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            if (h_of(c0 + i, 8 * cl) < p.H) {
+            for (int i = 0; i < kChunks; ++i) {
                 float w[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) w[m] = ws[(i * kChunkRows + 8 * cl + m) * 32 + lane];
 #pragma unroll
-                for (int u = 0; u < NCH; ++u) {
-                    if (tw + u < ntok) {
-                        float f[8];
-                        unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + tw + u) * NCH + cl) * 16), f);
+                for (int u = 0; u < NCH; u += 2) {
+                    float f0[8], f1[8];
+                    unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + tw + u) * NCH + cl) * 16), f0);
+                    unpack8(*reinterpret_cast<const uint4*>(xs + ((i * kLgTokens + tw + u + 1) * NCH + cl) * 16), f1);
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) acc[u] = fmaf(f[m], w[m], acc[u]);
-                    }
+                    for (int m = 0; m < 8; ++m)
+                        acc2[u / 2] = __ffma2_rn(make_float2(f0[m], f1[m]), make_float2(w[m], w[m]), acc2[u / 2]);
                 }
             }
         }
@@ -267,7 +279,7 @@ few_logits_kernel(const FewLogitsParams p) {
     constexpr int P = kLgTokens * 32;
     const int o = warp * 32 + lane;                      // token = warp
 #pragma unroll
-    for (int u = 0; u < NCH; ++u) part[(cl * kLgTokens + tw + u) * 32 + lane] = acc[u];
+    for (int u = 0; u < NCH; ++u) part[(cl * kLgTokens + tw + u) * 32 + lane] = (u & 1) ? acc2[u / 2].y : acc2[u / 2].x;
     __syncthreads();
     float v;
     if constexpr (NCH == 4) v = (part[o] + part[2 * P + o]) + (part[P + o] + part[3 * P + o]);
@@ -303,7 +315,10 @@ few_logits_kernel(const FewLogitsParams p) {
             for (int i = lane; i < p.E; i += 32) lg[warp * kMaxE + i] = __ldcg(p.logits + (int64_t)(t0 + warp) * p.E + i);
         __syncwarp();
     }
-    if (warp < ntok) few_topk(lg + warp * kMaxE, p, t0 + warp);
+    if (warp >= ntok) return;
+    uint8_t* sel = reinterpret_cast<uint8_t*>(part) + warp * kMaxE;   // (the sums in it were read above)
+    if (p.E <= 32) few_topk<1>(lg + warp * kMaxE, sel, p, t0 + warp);
+    else few_topk<kMaxE / 32>(lg + warp * kMaxE, sel, p, t0 + warp);
 }
 
 // ---------------------------------------------------------------------------
