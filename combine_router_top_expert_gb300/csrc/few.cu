@@ -61,9 +61,9 @@ namespace {
 // from the logits of all.
 // ---------------------------------------------------------------------------
 constexpr int kLgThreads = 256;
-// Clusters up to which 16 CTAs are taken (H = 7168, 32 experts: 8.2 us against 9.6
-// with one token, 10.1 against 13.5 with 16; 17.5 against 14.8 with 64 tokens, whose
-// 8 wide clusters do not all fit at once).
+// Clusters up to which 16 CTAs are taken (H = 7168, 32 experts, the whole layer with
+// I = 128: 24.4 us against 25.4 with one token, 51.1 against 52.0 with 16; 69.4 against
+// 68.2 with 64 tokens, whose 8 wide clusters do not all fit at once).
 constexpr int kLgWideClusters = 4;
 constexpr int kLgTokens = 8;       // tokens per cluster
 constexpr int kLgRows = 128;       // rows of W_r per stage and CTA
@@ -627,6 +627,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     const int T = p.T, E = p.E, k = p.k;
 
     if (threadIdx.x < kMaxE / 32) s_hit[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        const CUtensorMap* maps[8] = {&tmGU, MX ? &tmXq : &tmX, &tmDN, &tmH, &tmSGU, &tmX, &tmSDN, &tmHs};
+        for (int i = 0; i < (p.Is ? 8 : 4); ++i) tc::prefetch_tmap(maps[i]);
+    }
     if (threadIdx.x == 64) {
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(fullA(s), 1);
@@ -648,11 +652,28 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 
     pdl_wait();   // the routing, the MXFP8 rows and the zeroed counters are kernel 1's
     pdl_allow_next();
-    for (int i = threadIdx.x; i < T * k; i += kFewThreads) {
-        const int e = p.idx[i];
-        s_idx[i] = (uint8_t)e;
-        s_w[i] = p.w[i];
-        atomicOr(&s_hit[e >> 5], 1u << (e & 31));
+    {
+        // all loads first: kFewMaxPairs are 6 rounds of the CTA at most
+        constexpr int R = (kFewMaxPairs + kFewThreads - 1) / kFewThreads;
+        int e[R];
+        float v[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = threadIdx.x + r * kFewThreads;
+            if (i < T * k) {
+                e[r] = p.idx[i];
+                v[r] = p.w[i];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = threadIdx.x + r * kFewThreads;
+            if (i < T * k) {
+                s_idx[i] = (uint8_t)e[r];
+                s_w[i] = v[r];
+                atomicOr(&s_hit[e[r] >> 5], 1u << (e[r] & 31));
+            }
+        }
     }
     __syncthreads();
     // the active experts in ascending order (warp 0), and the cut of the two
@@ -1353,8 +1374,9 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     const int groups = ceil_div(T, kLgTokens), clusters = groups * ceil_div(E, 32);
     if (E > 32) e = cudaMemsetAsync(ws + L.arrived, 0, groups * 4, s);
     // few clusters are spread over 16 CTAs each; up to 64 CTAs of 8-wide clusters
-    // hold all of H <= 8192 in their rings, an SM to each; more keep the ring short
-    // so that two CTAs share an SM
+    // hold all of H <= 8192 in their rings, an SM to each (55.1 us against 56.9 with
+    // the short ring at 32 tokens, sizes as above); more keep the ring short so that two
+    // CTAs share an SM
     if (e == cudaSuccess)
         e = clusters <= kLgWideClusters && wide_clusters_ok() ? run_logits<16, 5>(lp, s)
             : clusters <= 8                                   ? run_logits<8, 9>(lp, s)
