@@ -70,7 +70,7 @@ __device__ __forceinline__ int segment_of(const int32_t* start, int E, int r) {
 // Vectors of 8 elements that a lane of the save has in flight: a row is read in
 // rounds of kCkBatch * 32 vectors, every load of a round issued before the first is
 // used. The save reads 1.07 GB and writes 0.4 at T = 4096, H = 7168, I = 2048, k = 8:
-// 209 us (the copy rate of this GPU; one load at a time left it waiting, 278 us).
+// 208 us (the copy rate of this GPU; one load at a time left it waiting, 278 us).
 constexpr int kCkBatch = 4;
 
 // One row of n elements (BF16 or fp32) to MXFP8 by one warp. Every lane runs
@@ -149,15 +149,15 @@ __device__ __forceinline__ void load_row_bf16(const uint8_t* q, const uint8_t* s
     for (int v = lane; v < n / 8; v += 32) {
         float f[8];
         dequantize8(__ldg(reinterpret_cast<const uint2*>(q) + v), __ldg(sf + v / 4), f);
-        reinterpret_cast<uint4*>(dst)[v] = pack8(f);
+        __stcs(reinterpret_cast<uint4*>(dst) + v, pack8(f));
     }
 }
 
 // One warp per row. Row jobs in order: the padded rows (A, G|U and h together;
 // pad rows are zero, as the training forward leaves them), the T*k partials,
-// the T tokens. Rows past the last segment are left alone. Bound by its writes
-// (1.76 GB against 0.6 read: 370 us, 4.7 TB/s written); loads in batches and
-// streaming stores measured slower (391, 386 us).
+// the T tokens. Rows past the last segment are left alone. Bound by its writes,
+// which no launch reads back at once, so they are streamed (1.76 GB against 0.6 read
+// at the save's sizes: 335 us, 7.0 TB/s both ways; 341 with plain stores).
 __global__ void __launch_bounds__(kCkThreads)
 checkpoint_load_kernel(const CheckpointParams p) {
     __shared__ int32_t poff[kMaxE + 1], off[kMaxE + 1];
@@ -198,11 +198,13 @@ checkpoint_load_kernel(const CheckpointParams p) {
             for (int i = 0; i < 8; ++i) hv[i] = silu_f(g[i]) * u[i];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(g[i]);
-            tc::stg_v8(gu + 8 * v, w);
+            __stcs(reinterpret_cast<uint4*>(gu + 8 * v), make_uint4(w[0], w[1], w[2], w[3]));
+            __stcs(reinterpret_cast<uint4*>(gu + 8 * v) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(u[i]);
-            tc::stg_v8(gu + p.I + 8 * v, w);
-            reinterpret_cast<uint4*>(h)[v] = pack8(hv);
+            __stcs(reinterpret_cast<uint4*>(gu + p.I + 8 * v), make_uint4(w[0], w[1], w[2], w[3]));
+            __stcs(reinterpret_cast<uint4*>(gu + p.I + 8 * v) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+            __stcs(reinterpret_cast<uint4*>(h) + v, pack8(hv));
         }
     } else if (j < P + R) {
         const int64_t i = j - P;

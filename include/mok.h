@@ -448,9 +448,10 @@ typedef struct {
  * y = bf16(s * rstd * gain). Needs H % 8 == 0 (H % 32 == 0 for the MXFP8
  * outputs), 8 <= H <= 65536, pointers 16-byte aligned (rstd 4, y_sf and
  * sum_sf 1). sum or y may be x's or residual's own buffer when that buffer's
- * pitch is H; otherwise outputs overlap no input and no other output. A row
- * that holds a NaN or an infinity gives NaN in y (its MXFP8 bytes are then
- * unspecified). T == 0 is a no-op. */
+ * pitch is H; otherwise outputs overlap no input and no other output. Rows
+ * are independent: one that holds a NaN is NaN in y, one that holds an infinity
+ * has rstd 0 (zeros in y, NaN where the infinities stood); its MXFP8 bytes are
+ * then unspecified. T == 0 is a no-op. */
 mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream);
 
 typedef struct {
