@@ -28,13 +28,14 @@
 // in registers; nothing between h and the output is rounded.
 //
 // Both kernels, H = 7168, I = 2048, E = 32, k = 8 (share of the time that the active
-// experts' weights need at the copy rate; the layer's stages take 191, 519, 526, 531
-// and, MXFP8, 135, 311, 314 us):
-//   BF16    1 token 120 us (87%), 16 tokens 419 (98%), 64 444, 125 477 (87%)
-//   MXFP8   1 token 75 us, 64 tokens 258 (83%), 128 317
-// With few tokens the launches, the router and the first bytes' way in are what is
-// missing (12 us before the first weights land), with many the partial sums of the
-// two phases (25 and 15 us at 125 tokens) and, with 128 MXFP8 tokens, the MMAs.
+// experts' weights need at the copy rate; the layer's stages take 191, 518, 526, 531
+// and, MXFP8, 135, 312, 315 us):
+//   BF16    1 token 120 us (87%), 16 tokens 419 (98%), 64 434, 125 462 (90%)
+//   MXFP8   1 token 75 us, 64 tokens 246 (87%), 128 309
+// What is missing: the launches, the router and the first weights' way in (7 us with
+// one token, 12 with 125), the way from the last gate/up tile to the first down one
+// (4 to 10), the partial sums at the end (6 to 15) and, with 128 MXFP8 tokens, the
+// MMAs.
 //
 // CTA layout (one per SM, cooperative launch: phase 2 waits for other CTAs'
 // phase 1 through per-expert counters):
@@ -964,8 +965,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         uint32_t ph = 0;
         int wbuf = 0;
 
-        // this CTA's two shared tiles of a phase: the one its range starts
-        // in (0) and the one it ends in (1)
+        // this CTA's shared tiles of a phase, at most two: the ones that its range
+        // starts and ends in
         FewShared pend[2];
         int n_pend = 0;
         const int tpad = ceil_div(T, 8) * 8;
