@@ -111,6 +111,24 @@ def test_any_number_of_sms(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [7, 40, 100])
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+def test_cut_tiles_before_whole_ones(T, dtype):
+    """CTAs with cut gate/up tiles at both ends of their range and whole ones between: few SMs, many tiles."""
+    wl = S("cuts", T=T, H=2048, I=512, E=8, k=2, dtype=dtype, shared_I=512)
+    inp = synth.make_inputs(wl, seed=6)
+    layer = layer_for(inp, dtype_of(wl))
+    x = to_dev_bf16(inp.x)
+    _, ref = reference(wl, inp)
+    for n in (5, 6, 7, 10, 20, 24, 28):
+        cfg = mok.make_config(num_sms=n)
+        out, _, _ = run(wl, inp, layer, x, cfg=cfg)
+        assert_close(host_bf16_f64(out), ref, TOL[dtype_of(wl)], f"num_sms={n}")
+        again, _, _ = run(wl, inp, layer, x, cfg=cfg)
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)), n
+
+
+@pytest.mark.gpu
 def test_bitwise_deterministic_and_stream_ordered():
     """Many calls back to back on one workspace and on a side stream give the same bits."""
     for wl in (S("det", T=40, H=1024, I=512, E=16, k=4, zipf_s=1.2),
