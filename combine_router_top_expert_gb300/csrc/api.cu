@@ -787,6 +787,7 @@ mok_status mok_moe_few(const mok_problem* p, const mok_few_args* a, const mok_co
     f.topk_w = a->topk_w;
     f.out = a->out;
     f.workspace = a->workspace;
+    f.withhold = cfg && (cfg->flags & MOK_FLAG_TEST_WITHHOLD_PUBLISH) ? 1 : 0;
     return launch_status(launch_few(f, make_common(a->workspace, cfg, p->dtype), s));
 }
 

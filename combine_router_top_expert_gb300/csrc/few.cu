@@ -373,6 +373,7 @@ struct FewParams {
     __nv_bfloat16* out;
     StatusBlock* status;
     unsigned long long timeout_ns;
+    int withhold;                 // test hook: CTA 0 counts nothing of its gate/up phase in
 };
 
 template <bool MX, int NT>
@@ -814,11 +815,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 const CUtensorMap* tm = j.phase ? (sh ? &tmSDN : &tmDN) : (sh ? &tmSGU : &tmGU);
                 const int bk = sh ? 64 : C::kBK;
                 for (int i = 0; i < j.n; ++i) {
-                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) {
-                        for (int q = 0; q < S; ++q)
-                            if (last_par[q] >= 0) few_drain(fullA(q), (uint32_t)last_par[q], tmo);
-                        return false;
-                    }
+                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) return false;
                     const int kb = j.kb + i;
                     uint32_t bytes = (uint32_t)rows * 128u;
                     if constexpr (MX) {
@@ -845,6 +842,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 }
                 return true;
             });
+            // the CTA may end early because of another warp or CTA, but not before
+            // its copies have landed
+            for (int q = 0; q < S; ++q)
+                if (last_par[q] >= 0) few_drain(fullA(q), (uint32_t)last_par[q], tmo);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ tokens
@@ -854,17 +855,12 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             int last_par[S];
             for (int i = 0; i < S; ++i) last_par[i] = -1;
             int ready = -1;   // the expert whose h is known to be complete
-            auto give_up = [&]() {
-                for (int q = 0; q < S; ++q)
-                    if (last_par[q] >= 0) few_drain(fullB(q), (uint32_t)last_par[q], tmo);
-                return false;
-            };
             few_jobs(w, [&](const FewJob& j) {
                 const bool sh = j.a == w.A;
                 if (j.phase && ready != j.a) {
                     // (items of 32 rows, or MXFP8 features, and 8 tokens)
                     const int items = (sh ? 2 * p.Is : MX ? p.I : 2 * p.I) / 32 * ceil_div(T, 8);
-                    if (!few_wait_counter(p.hready + j.a, items, st, tmo)) return give_up();
+                    if (!few_wait_counter(p.hready + j.a, items, st, tmo)) return false;
                     tc::fence_proxy_async_global();
                     ready = j.a;
                 }
@@ -872,7 +868,7 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 const int row0 = j.phase && !sh ? j.a * T : 0;
                 const int bk = sh ? 64 : C::kBK;
                 for (int i = 0; i < j.n; ++i) {
-                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) return give_up();
+                    if (!tc::mbar_wait(empty(s), ph ^ 1u, st, tmo, kSiteProducerEmpty)) return false;
                     const int kb = j.kb + i;
                     tc::mbar_expect_tx(fullB(s), (uint32_t)C::kBytesB + (MX && !sh ? 512u : 0u));
                     tc::tma_load_2d(b_tile(s), tm, fullB(s), kb * bk, row0);
@@ -887,6 +883,8 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 }
                 return true;
             });
+            for (int q = 0; q < S; ++q)
+                if (last_par[q] >= 0) few_drain(fullB(q), (uint32_t)last_par[q], tmo);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
@@ -895,23 +893,16 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
             uint32_t ph = 0, acc_ph = 0;
             int ac = 0;   // accumulator of this job
             bool issued = false;
-            auto give_up = [&]() {
-                if (issued) {   // the MMAs issued so far end before tensor memory is freed
-                    tc::mma_commit(drain);
-                    few_drain(drain, 0, tmo);
-                }
-                return false;
-            };
             few_jobs(w, [&](const FewJob& j) {
                 const bool sh = j.a == w.A;
                 const int rows = j.phase ? p.R2 : sh ? p.Rs1 : p.R1;
                 const bool two = rows > 128;   // two 128-row blocks
-                if (!tc::mbar_wait(acce(ac), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return give_up();
+                if (!tc::mbar_wait(acce(ac), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) return false;
                 tc::fence_after_sync();
                 const uint32_t d0 = tmem + (uint32_t)(ac * 2 * NT), d1 = d0 + NT;
                 for (int i = 0; i < j.n; ++i) {
-                    if (!tc::mbar_wait(fullA(s), ph, st, tmo, kSiteMmaFull)) return give_up();
-                    if (!tc::mbar_wait(fullB(s), ph, st, tmo, kSiteMmaFull)) return give_up();
+                    if (!tc::mbar_wait(fullA(s), ph, st, tmo, kSiteMmaFull)) return false;
+                    if (!tc::mbar_wait(fullB(s), ph, st, tmo, kSiteMmaFull)) return false;
                     tc::fence_after_sync();
                     // descriptors of the stage; K step kk starts 32 bytes (2
                     // descriptor units) further, row block b 16 KB
@@ -949,6 +940,10 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
                 if (++ac == C::kAccs) { ac = 0; acc_ph ^= 1u; }
                 return true;
             });
+            if (issued) {   // the MMAs issued so far end before tensor memory is freed
+                tc::mma_commit(drain);
+                few_drain(drain, 0, tmo);
+            }
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -1044,13 +1039,14 @@ few_ffn_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         auto publish_h = [&](int a, int n) {
             tc::fence_proxy_async_global();
             epi_sync();
-            if (et == 0) few_red_release(p.hready + a, n);
+            if (et == 0 && !(p.withhold && c_me == 0)) few_red_release(p.hready + a, n);
         };
         // this CTA's partial of a shared tile is written: count it in and
         // remember the tile
         auto share = [&](const FewJob& j) {
             epi_sync();
-            if (et == 0) few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
+            if (et == 0 && !(p.withhold && c_me == 0 && !j.phase))
+                few_red_release((j.phase ? p.cnt2 : p.cnt1) + j.gtile, 1);
             const FewShared f{j.a, j.tile, j.gtile, j.c0, j.c1, j.u0};
             if (n_pend == 0) pend[0] = f;
             else pend[1] = f;
@@ -1413,6 +1409,7 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.status = c.status;
     p.timeout_ns = c.timeout_ns;
+    p.withhold = a.withhold;
 
     CUtensorMap tm[8];
     const int NT = few_columns(T), eb = mx ? 1 : 2, bk = 128 / eb;

@@ -118,6 +118,7 @@ struct FewLaunch {
     float* topk_w;
     void* out;
     void* workspace;            // few_workspace_bytes for c.num_sms CTAs
+    int withhold;               // test hook, MOK_FLAG_TEST_WITHHOLD_PUBLISH
 };
 size_t few_workspace_bytes(const mok_problem* p, int ctas);
 cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s);

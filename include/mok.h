@@ -138,7 +138,8 @@ typedef struct {
 /* Test hook: a mover withholds the publish of the last 8-row chunk of the
  * first minibatch, so the tiles waiting for it give up after timeout_ms and
  * the call reports MOK_ERR_TIMEOUT (exercises the bounded waits; never use
- * in production). */
+ * in production). In mok_moe_few the first CTA counts in none of its gate/up
+ * results, so that whoever waits for them gives up. */
 #define MOK_FLAG_TEST_WITHHOLD_PUBLISH 256
 
 /* ------------------------------------------------------------------------- */
@@ -417,8 +418,10 @@ size_t mok_few_workspace_size(const mok_problem* p, const mok_config* cfg);
  * experts in ascending order. Bitwise the same in every run with one num_sms.
  * The second kernel is one cooperative launch with a CTA on each of
  * cfg->num_sms SMs (0: all); it fails with MOK_ERR_CUDA if they cannot all be
- * resident. Of cfg only num_sms and timeout_ms are read. Device-side waits are
- * bounded: mok_device_status on the workspace reports MOK_ERR_TIMEOUT. */
+ * resident. Of cfg only num_sms, timeout_ms and the flag
+ * MOK_FLAG_TEST_WITHHOLD_PUBLISH are read. Device-side waits are bounded:
+ * mok_device_status on the workspace reports MOK_ERR_TIMEOUT, out is then
+ * unspecified, and the CTAs end only after their own copies and MMAs. */
 mok_status mok_moe_few(const mok_problem* p, const mok_few_args* a, const mok_config* cfg, mok_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
