@@ -1412,19 +1412,19 @@ cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s) 
     p.withhold = a.withhold;
 
     CUtensorMap tm[8];
-    const int NT = few_columns(T), eb = mx ? 1 : 2, bk = 128 / eb;
-    bool ok = make_tmap_swizzled(&tm[0], a.x, T, H, 2, 64, NT) &&
-              make_tmap_swizzled(&tm[2], a.gu, (int64_t)E * 2 * I, H, eb, bk, p.R1) &&
-              make_tmap_swizzled(&tm[3], a.dn, (int64_t)E * H, I, eb, bk, p.R2) &&
-              make_tmap_swizzled(&tm[4], p.h, act * T, I, eb, bk, NT);
+    const int NT = few_columns(T), eb = mx ? 1 : 2;
+    bool ok = make_tmap_swizzled(&tm[0], a.x, T, H, 2, NT) &&
+              make_tmap_swizzled(&tm[2], a.gu, (int64_t)E * 2 * I, H, eb, p.R1) &&
+              make_tmap_swizzled(&tm[3], a.dn, (int64_t)E * H, I, eb, p.R2) &&
+              make_tmap_swizzled(&tm[4], p.h, act * T, I, eb, NT);
     tm[1] = tm[0];
-    if (ok && mx) ok = make_tmap_swizzled(&tm[1], lp.xq, T, H, 1, 128, NT);
+    if (ok && mx) ok = make_tmap_swizzled(&tm[1], lp.xq, T, H, 1, NT);
     tm[5] = tm[2];
     tm[6] = tm[3];
     tm[7] = tm[4];
     if (ok && Is)
-        ok = make_tmap_swizzled(&tm[5], a.sgu, 2 * (int64_t)Is, H, 2, 64, p.Rs1) &&
-             make_tmap_swizzled(&tm[6], a.sdn, H, Is, 2, 64, p.R2) && make_tmap_swizzled(&tm[7], p.hs, T, Is, 2, 64, NT);
+        ok = make_tmap_swizzled(&tm[5], a.sgu, 2 * (int64_t)Is, H, 2, p.Rs1) &&
+             make_tmap_swizzled(&tm[6], a.sdn, H, Is, 2, p.R2) && make_tmap_swizzled(&tm[7], p.hs, T, Is, 2, NT);
     if (!ok) return cudaErrorInvalidValue;
 
     cudaError_t e = cudaSuccess;

@@ -97,11 +97,6 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols
     return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_swizzled(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem_bytes, int box_cols,
-                        int box_rows) {
-    return make_tmap(m, base, rows, cols, elem_bytes, box_cols, box_rows);
-}
-
 namespace {
 
 // Clusters of two CTAs that can be resident at once for kernel `kern` with

@@ -1169,20 +1169,20 @@ mega_kernel(const __grid_constant__ CUtensorMap tmRing, const __grid_constant__ 
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 mega_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         cudaDriverEntryPointQueryResult q;
         void* ptr = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                         &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? ptr : nullptr);
+    }();
     return fn;
 }
 
-// Row-major [rows, cols] tensor, box of 128 bytes x box_rows, 128-byte swizzle.
-bool tmap2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int eb, int box_rows) {
+}  // namespace
+
+bool make_tmap_swizzled(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int eb, int box_rows) {
     auto fn = mega_encode();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -1194,8 +1194,6 @@ bool tmap2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int eb
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
-
-}  // namespace
 
 size_t mega_scratch_bytes(int nbatch, int T, int H, int I, int E, int k, int region_rows, bool mx) {
     (void)T;
@@ -1298,10 +1296,10 @@ cudaError_t launch_mega(const MegaLaunch& L, cudaStream_t s) {
 
     CUtensorMap tR, tGU, tH, tDN;
     const int64_t rrows = 2 * (int64_t)L.region_rows;
-    if (!tmap2d(&tR, ring, rrows, H, (int)eb, 128)) return cudaErrorInvalidValue;
-    if (!tmap2d(&tGU, L.gu, (int64_t)E * 2 * I, H, (int)eb, BN)) return cudaErrorInvalidValue;
-    if (!tmap2d(&tH, hbuf, rrows, I, (int)eb, 128)) return cudaErrorInvalidValue;
-    if (!tmap2d(&tDN, L.dn, (int64_t)E * H, I, (int)eb, BN2)) return cudaErrorInvalidValue;
+    if (!make_tmap_swizzled(&tR, ring, rrows, H, (int)eb, 128)) return cudaErrorInvalidValue;
+    if (!make_tmap_swizzled(&tGU, L.gu, (int64_t)E * 2 * I, H, (int)eb, BN)) return cudaErrorInvalidValue;
+    if (!make_tmap_swizzled(&tH, hbuf, rrows, I, (int)eb, 128)) return cudaErrorInvalidValue;
+    if (!make_tmap_swizzled(&tDN, L.dn, (int64_t)E * H, I, (int)eb, BN2)) return cudaErrorInvalidValue;
 
     // Cooperative launch: refused unless every CTA can be resident at once,
     // which the counter waits between CTAs rely on.

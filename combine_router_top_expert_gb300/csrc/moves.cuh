@@ -10,10 +10,6 @@ namespace mok {
 bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem_bytes, int box_cols,
                     int box_rows);
 
-// The same with a 128-byte swizzle (box_cols * elem_bytes == 128).
-bool make_tmap_swizzled(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem_bytes, int box_cols,
-                        int box_rows);
-
 // route.cu
 size_t route_workspace_bytes(int T, int H, int E, int k);
 cudaError_t launch_route_layout(const void* x, const float* W_r, const float* bias, int T, int H, int E, int k,
@@ -102,6 +98,10 @@ struct GemmCommon {
     int cluster;   // 2: grouped GEMMs run as 2-SM CTA pairs (tcgen05 cta_group::2, B rows split
                    // between the two CTAs, no multicast loads; the BF16 default); 1: single CTAs
 };
+// mega.cu: 2-D row-major [rows, cols] tensor of eb-byte elements, read in boxes of 128
+// bytes x box_rows with a 128-byte swizzle; rows out of range read 0.
+bool make_tmap_swizzled(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int eb, int box_rows);
+
 // few.cu: the whole layer for at most kFewMaxTokens tokens and kFewMaxPairs
 // (token, slot) pairs.
 constexpr int kFewMaxTokens = 128;
