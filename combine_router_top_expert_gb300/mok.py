@@ -418,18 +418,20 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# The checks of tensors raise by themselves: a kernel that is given another tensor reads out of range, also where
+# Python drops assert statements (-O).
+
 def _dense(name, t, dtype, *shape):
     """t (or None) is a contiguous CUDA tensor of this type and shape."""
-    if t is not None:
-        assert t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous(), \
-            f"{name}: contiguous {dtype} CUDA tensor {list(shape)} expected"
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        raise AssertionError(f"{name}: contiguous {dtype} CUDA tensor {list(shape)} expected")
 
 
 def _rows(name, t, T, H):
     """Row pitch of bf16 rows whose elements are adjacent."""
     pitch, step = t.stride()
-    assert t.dtype is torch.bfloat16 and step == 1 and t.shape == (T, H) and t.is_cuda, \
-        f"{name}: bf16 CUDA tensor [{T}, {H}] with adjacent row elements expected"
+    if not (t.dtype is torch.bfloat16 and step == 1 and t.shape == (T, H) and t.is_cuda):
+        raise AssertionError(f"{name}: bf16 CUDA tensor [{T}, {H}] with adjacent row elements expected")
     return pitch if T > 1 else max(pitch, H)
 
 
