@@ -428,11 +428,11 @@ def _dense(name, t, dtype, *shape):
 
 
 def _rows(name, t, T, H):
-    """Row pitch of bf16 rows whose elements are adjacent."""
+    """Row pitch of bf16 rows whose elements are adjacent (of a single row: H, whatever view it is)."""
     pitch, step = t.stride()
     if not (t.dtype is torch.bfloat16 and step == 1 and t.shape == (T, H) and t.is_cuda):
         raise AssertionError(f"{name}: bf16 CUDA tensor [{T}, {H}] with adjacent row elements expected")
-    return pitch if T > 1 else max(pitch, H)
+    return pitch if T > 1 else H
 
 
 def rmsnorm(x, gain, residual=None, eps=1e-6, sum=None, y=None, y_q=None, y_sf=None, sum_q=None, sum_sf=None,
