@@ -40,8 +40,8 @@ class MoEBlock:
     def __init__(self, layer: MoELayer, gain: torch.Tensor, eps: float = 1e-6):
         """gain: [H] fp32 on the layer's device."""
         self.layer, self.gain, self.eps = layer, gain, eps
-        self._few = {}
-        self._norm_ws = {}
+        self._few = {}         # few-token workspaces by the most tokens that they hold
+        self._norm_ws = None
 
     # ------------------------------------------------------------------ serving
 
@@ -60,10 +60,14 @@ class MoEBlock:
 
     def _forward_few(self, y, out):
         T, layer = y.shape[0], self.layer
-        p = layer.problem(T)
-        if T not in self._few:
-            self._few[T] = mok.alloc_bytes(mok.few_workspace_size(p), layer.device)
-        mok.moe_few(p, y, layer.W_r, layer.packed, out, self._few[T], bias=layer.bias,
+        # workspaces for the most tokens, half as many, a quarter and so on (0.8 MB a token at H=7168, I=2048, E=32):
+        # together about twice the largest, and none is given back, so that captured calls stay good
+        most = min(mok.FEW_MAX_TOKENS, mok.FEW_MAX_PAIRS // layer.k)
+        while most > 8 and (most + 1) // 2 >= T:
+            most = (most + 1) // 2
+        if most not in self._few:
+            self._few[most] = mok.alloc_bytes(mok.few_workspace_size(layer.problem(most)), layer.device)
+        mok.moe_few(layer.problem(T), y, layer.W_r, layer.packed, out, self._few[most], bias=layer.bias,
                     packed_shared=layer.packed_shared)
 
     # ------------------------------------------------------------------ training
@@ -102,11 +106,11 @@ class MoEBlock:
                  dW_r=torch.empty((H, layer.E), dtype=torch.float32, device=dout.device))
         mok.moe_backward(p, y, layer.W_r, layer.Wg, layer.Wu, layer.Wd, layer.packed, dout, ctx["routing"],
                          b["saved"], g, b["ws"], packed_bwd=layer.packed_bwd)
-        if T not in self._norm_ws:
-            self._norm_ws[T] = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(T, H), dout.device)
+        if self._norm_ws is None:   # a partial row per SM at most, so one for any T
+            self._norm_ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(1 << 24, H), dout.device)
         g["dx"] = g.pop("dX")
         g["dgain"] = torch.empty(H, dtype=torch.float32, device=dout.device)
         # dx takes dy's place: the layer's input gradient is read before it is overwritten
-        mok.rmsnorm_backward(g["dx"], self.gain, ctx["rstd"], g["dx"], g["dgain"], self._norm_ws[T],
+        mok.rmsnorm_backward(g["dx"], self.gain, ctx["rstd"], g["dx"], g["dgain"], self._norm_ws,
                              s_q=ctx["sum_q"], s_sf=ctx["sum_sf"], dsum=dstream)
         return g
