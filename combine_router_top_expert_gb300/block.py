@@ -42,6 +42,7 @@ class MoEBlock:
         self.layer, self.gain, self.eps = layer, gain, eps
         self._few = {}         # few-token workspaces by the most tokens that they hold
         self._norm_ws = None
+        self._last = ()        # status blocks of the last call
 
     # ------------------------------------------------------------------ serving
 
@@ -56,6 +57,8 @@ class MoEBlock:
             self._forward_few(y, out)
         else:
             self.layer.forward(y, out=out)
+            b = self.layer.buffers(T)
+            self._last = (b["route_ws"], b["ws"])
         return out, total
 
     def _forward_few(self, y, out):
@@ -69,6 +72,17 @@ class MoEBlock:
             self._few[most] = mok.alloc_bytes(mok.few_workspace_size(layer.problem(most)), layer.device)
         mok.moe_few(layer.problem(T), y, layer.W_r, layer.packed, out, self._few[most], bias=layer.bias,
                     packed_shared=layer.packed_shared)
+        self._last = (self._few[most],)
+
+    @_on_stream
+    def status(self, ctx=None):
+        """(code, detail) of the first device-side wait that gave up in this block's last call, or in the calls on a
+        training context so far; (mok.OK, 0) if none did. Waits for the stream's work, as MoELayer.status does."""
+        for t in self._last if ctx is None else ctx["status"]:
+            code, detail = mok.device_status(t)
+            if code != mok.OK:
+                return code, detail
+        return mok.OK, 0
 
     # ------------------------------------------------------------------ training
 
@@ -80,18 +94,26 @@ class MoEBlock:
         total, y = (torch.empty((T, H), dtype=torch.bfloat16, device=dev) for _ in range(2))
         ctx = dict(T=T, rstd=torch.empty(T, dtype=torch.float32, device=dev),
                    sum_q=torch.empty((T, H), dtype=torch.uint8, device=dev),
-                   sum_sf=torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
+                   sum_sf=torch.empty((T, H // 32), dtype=torch.uint8, device=dev),
+                   # of the routing, the forward and the backward: later calls on their workspaces clear these
+                   status=torch.zeros((3, mok.STATUS_BYTES), dtype=torch.uint8, device=dev))
         mok.rmsnorm(x, self.gain, residual=residual, eps=self.eps, sum=total, y=y, sum_q=ctx["sum_q"],
                     sum_sf=ctx["sum_sf"], rstd=ctx["rstd"])
         p, b = layer.problem(T), layer.buffers(T, True)
         # the checkpoint refers to this routing until the backward, so it is its own
         ctx["routing"] = mok.route_layout(y, layer.W_r, layer.k, layer.bias, workspace=b["route_ws"])
+        self._keep_status(ctx, 0, b["route_ws"])
         out = torch.empty_like(y)
         mok.moe_forward(p, y, layer.packed, ctx["routing"], out, b["ws"], saved=b["saved"],
                         packed_shared=layer.packed_shared)
+        self._keep_status(ctx, 1, b["ws"])
         ctx["ckpt"] = mok.alloc_bytes(mok.checkpoint_size(p), dev)
         mok.checkpoint_save(p, y, ctx["routing"], b["saved"], ctx["ckpt"])
         return out, total, ctx
+
+    def _keep_status(self, ctx, i, ws):
+        ctx["status"][i].copy_(ws[:mok.STATUS_BYTES])
+        self._last = ctx["status"]
 
     @_on_stream
     def train_backward(self, ctx, dout, dstream=None):
@@ -106,6 +128,7 @@ class MoEBlock:
                  dW_r=torch.empty((H, layer.E), dtype=torch.float32, device=dout.device))
         mok.moe_backward(p, y, layer.W_r, layer.Wg, layer.Wu, layer.Wd, layer.packed, dout, ctx["routing"],
                          b["saved"], g, b["ws"], packed_bwd=layer.packed_bwd)
+        self._keep_status(ctx, 2, b["ws"])
         if self._norm_ws is None:   # a partial row per SM at most, so one for any T
             self._norm_ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(1 << 24, H), dout.device)
         g["dx"] = g.pop("dX")

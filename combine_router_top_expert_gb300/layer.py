@@ -45,28 +45,35 @@ class MoELayer:
     def problem(self, T) -> mok.Problem:
         return mok.make_problem(T, self.H, self.I, self.E, self.k, self.dtype, self.I_shared)
 
-    def buffers(self, T, training=False, cfg=None):
+    def buffers(self, T, training=False, cfg=None, stream=None):
+        """The buffers of calls with T tokens, made on the stream of the first one, their statuses good."""
         key = (T, training)
         if key not in self._bufs:
-            p = self.problem(T)
-            b = dict(
-                route_ws=mok.alloc_bytes(mok.route_workspace_size(T, self.H, self.E, self.k), self.device),
-                routing=dict(topk_idx=torch.empty((T, self.k), dtype=torch.int32, device=self.device),
-                             topk_w=torch.empty((T, self.k), dtype=torch.float32, device=self.device),
-                             counts=torch.empty(self.E, dtype=torch.int32, device=self.device),
-                             offsets=torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
-                             row_src=torch.empty(max(T * self.k, 1), dtype=torch.int32, device=self.device),
-                             slot_row=torch.empty(max(T * self.k, 1), dtype=torch.int32, device=self.device)),
-                ws=mok.alloc_bytes(mok.workspace_size(p, cfg), self.device),
-                out=torch.empty((max(T, 1), self.H), dtype=torch.bfloat16, device=self.device),
-            )
-            if training:
-                b["saved"] = mok.alloc_bytes(mok.saved_size(p), self.device)
-            self._bufs[key] = b
+            with torch.cuda.stream(stream):
+                self._bufs[key] = self._new_buffers(T, training, cfg)
         return self._bufs[key]
 
+    def _new_buffers(self, T, training, cfg):
+        p = self.problem(T)
+        b = dict(
+            route_ws=mok.alloc_bytes(mok.route_workspace_size(T, self.H, self.E, self.k), self.device),
+            routing=dict(topk_idx=torch.empty((T, self.k), dtype=torch.int32, device=self.device),
+                         topk_w=torch.empty((T, self.k), dtype=torch.float32, device=self.device),
+                         counts=torch.empty(self.E, dtype=torch.int32, device=self.device),
+                         offsets=torch.empty(self.E + 1, dtype=torch.int32, device=self.device),
+                         row_src=torch.empty(max(T * self.k, 1), dtype=torch.int32, device=self.device),
+                         slot_row=torch.empty(max(T * self.k, 1), dtype=torch.int32, device=self.device)),
+            ws=mok.alloc_bytes(mok.workspace_size(p, cfg), self.device),
+            out=torch.empty((max(T, 1), self.H), dtype=torch.bfloat16, device=self.device),
+        )
+        if training:
+            b["saved"] = mok.alloc_bytes(mok.saved_size(p), self.device)
+        for n in ("route_ws", "ws"):
+            b[n][:mok.STATUS_BYTES].zero_()
+        return b
+
     def route(self, x, training=False, stream=None):
-        b = self.buffers(x.shape[0], training)
+        b = self.buffers(x.shape[0], training, stream=stream)
         return mok.route_layout(x, self.W_r, self.k, self.bias, out=b["routing"], workspace=b["route_ws"],
                                 stream=stream)
 
@@ -75,7 +82,7 @@ class MoELayer:
         The stage kernels run unless cfg has FLAG_MEGAKERNEL (inference only);
         training keeps the activations the backward needs."""
         T = x.shape[0]
-        b = self.buffers(T, training, cfg)
+        b = self.buffers(T, training, cfg, stream)
         if route:
             self.route(x, training, stream)
         dst = b["out"] if out is None else out
@@ -86,7 +93,7 @@ class MoELayer:
 
     def backward(self, x, dY, cfg=None, stream=None, grads=None):
         T = x.shape[0]
-        b = self.buffers(T, True)
+        b = self.buffers(T, True, cfg, stream)
         if grads is None:
             grads = dict(dX=torch.empty_like(x), dW_gate=torch.empty_like(self.Wg), dW_up=torch.empty_like(self.Wu),
                          dW_down=torch.empty_like(self.Wd),

@@ -107,6 +107,7 @@ class FewArgs(ctypes.Structure):
 
 
 EP_MAX_RANKS = 8
+STATUS_BYTES = 256     # the status block at the start of a workspace
 FEW_MAX_TOKENS = 128   # MOK_FEW_MAX_TOKENS
 FEW_MAX_PAIRS = 2048   # MOK_FEW_MAX_PAIRS
 _lock = threading.Lock()
