@@ -8,11 +8,13 @@ the residual's addition, then the layer, for serving and for training.
 them. Decode-sized batches take the few-token kernels, others the layer's
 stages. Training keeps 8-bit checkpoints: the stream as MXFP8 rows for the norm's
 backward, and the layer's context (mok_checkpoint_save) in a quarter of the
-memory, so that one full context serves every block of a model.
+memory. The full context is needed inside a call only: blocks that are given the
+same BlockBuffers hold one between them, others use their layer's own.
 
-The workspaces belong to the block (and the full context to its layer): its calls
-go to one stream at a time. With `stream` given, the new tensors are that stream's
-in the allocator, and the inputs have to be ready on it.
+The workspaces belong to the block (and the full context to its layer or its
+BlockBuffers): calls that use them go to one stream at a time. With `stream` given,
+the new tensors are that stream's in the allocator, and the inputs have to be ready
+on it.
 """
 from __future__ import annotations
 
@@ -36,10 +38,28 @@ def _on_stream(f):
     return wrapped
 
 
+class BlockBuffers:
+    """The full training context and the layer's workspaces for the blocks of a model, which train on one stream one
+    after the other. One set for each problem (sizes, experts, type and tokens), so the layers need not be alike."""
+
+    def __init__(self):
+        self._sets = {}
+
+    def training(self, layer: MoELayer, T):
+        p = layer.problem(T)
+        key = bytes(p)
+        if key not in self._sets:
+            self._sets[key] = dict(
+                route_ws=mok.alloc_bytes(mok.route_workspace_size(T, layer.H, layer.E, layer.k), layer.device),
+                ws=mok.alloc_bytes(mok.workspace_size(p), layer.device),
+                saved=mok.alloc_bytes(mok.saved_size(p), layer.device))
+        return self._sets[key]
+
+
 class MoEBlock:
-    def __init__(self, layer: MoELayer, gain: torch.Tensor, eps: float = 1e-6):
-        """gain: [H] fp32 on the layer's device."""
-        self.layer, self.gain, self.eps = layer, gain, eps
+    def __init__(self, layer: MoELayer, gain: torch.Tensor, eps: float = 1e-6, buffers: BlockBuffers | None = None):
+        """gain: [H] fp32 on the layer's device. buffers: shared with other blocks (training)."""
+        self.layer, self.gain, self.eps, self.buffers = layer, gain, eps, buffers
         self._few = {}         # few-token workspaces by the most tokens that they hold
         self._norm_ws = None
         self._last = ()        # status blocks of the last call
@@ -99,7 +119,7 @@ class MoEBlock:
                    status=torch.zeros((3, mok.STATUS_BYTES), dtype=torch.uint8, device=dev))
         mok.rmsnorm(x, self.gain, residual=residual, eps=self.eps, sum=total, y=y, sum_q=ctx["sum_q"],
                     sum_sf=ctx["sum_sf"], rstd=ctx["rstd"])
-        p, b = layer.problem(T), layer.buffers(T, True)
+        p, b = layer.problem(T), self._training_buffers(T)
         # the checkpoint refers to this routing until the backward, so it is its own
         ctx["routing"] = mok.route_layout(y, layer.W_r, layer.k, layer.bias, workspace=b["route_ws"])
         self._keep_status(ctx, 0, b["route_ws"])
@@ -111,6 +131,9 @@ class MoEBlock:
         mok.checkpoint_save(p, y, ctx["routing"], b["saved"], ctx["ckpt"])
         return out, total, ctx
 
+    def _training_buffers(self, T):
+        return self.layer.buffers(T, True) if self.buffers is None else self.buffers.training(self.layer, T)
+
     def _keep_status(self, ctx, i, ws):
         ctx["status"][i].copy_(ws[:mok.STATUS_BYTES])
         self._last = ctx["status"]
@@ -120,7 +143,7 @@ class MoEBlock:
         """Gradients of a train_forward: dict with dx (of x and of the residual alike), dgain, and the layer's
         dW_gate, dW_up, dW_down, dW_r. dout, dstream: gradients of out and of the residual stream."""
         T, layer = ctx["T"], self.layer
-        p, b, H = layer.problem(T), layer.buffers(T, True), layer.H
+        p, b, H = layer.problem(T), self._training_buffers(T), layer.H
         y = torch.empty((T, H), dtype=torch.bfloat16, device=dout.device)
         mok.checkpoint_load(p, ctx["ckpt"], ctx["routing"], y, b["saved"])
         g = dict(dX=torch.empty_like(y), dW_gate=torch.empty_like(layer.Wg), dW_up=torch.empty_like(layer.Wu),

@@ -13,7 +13,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from combine_router_top_expert_gb300 import mok, synth  # noqa: E402
-from combine_router_top_expert_gb300.block import MoEBlock  # noqa: E402
+from combine_router_top_expert_gb300.block import BlockBuffers, MoEBlock  # noqa: E402
 from combine_router_top_expert_gb300.layer import MoELayer  # noqa: E402
 
 
@@ -26,15 +26,12 @@ def main():
     a = ap.parse_args()
     H, I, E, k = 1024, 512, 16, 4
     wl = synth.small("block", T=1, H=H, I=I, E=E, k=k, dtype="mxfp8" if a.mxfp8 else "bf16")
+    shared = BlockBuffers()   # one full training context for every block: the checkpoints hold the rest
     blocks = []
     for n in range(a.layers):
         inp = synth.make_inputs(wl, seed=n, with_x=False)
         layer = MoELayer(inp.W_r, inp.Wg, inp.Wu, inp.Wd, k, dtype=mok.MXFP8 if a.mxfp8 else mok.BF16)
-        blocks.append(MoEBlock(layer, torch.ones(H, device="cuda")))
-    # one full training context serves every block: the checkpoints hold the rest
-    shared = blocks[0].layer._bufs
-    for b in blocks:
-        b.layer._bufs = shared
+        blocks.append(MoEBlock(layer, torch.ones(H, device="cuda"), buffers=shared))
 
     g = torch.Generator(device="cuda").manual_seed(0)
     x = torch.randn((a.tokens, H), generator=g, device="cuda").to(torch.bfloat16)
