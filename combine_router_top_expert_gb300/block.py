@@ -108,9 +108,13 @@ class MoEBlock:
 
     @_on_stream
     def train_forward(self, x, residual=None):
-        """(out, residual stream, ctx): ctx holds what train_backward needs."""
+        """(out, residual stream, ctx): ctx holds what train_backward needs. Refuses layers without a backward: with
+        a shared expert, or made with keep_unpacked=False."""
         T, H = x.shape
         layer, dev = self.layer, x.device
+        if layer.I_shared or layer.Wg is None:
+            raise mok.MokError(mok.ERR_UNSUPPORTED, "MoEBlock.train_forward: " + (
+                "no backward of a shared expert" if layer.I_shared else "the layer keeps no unpacked weights"))
         total, y = (torch.empty((T, H), dtype=torch.bfloat16, device=dev) for _ in range(2))
         ctx = dict(T=T, rstd=torch.empty(T, dtype=torch.float32, device=dev),
                    sum_q=torch.empty((T, H), dtype=torch.uint8, device=dev),
