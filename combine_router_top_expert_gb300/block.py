@@ -59,6 +59,8 @@ class BlockBuffers:
 class MoEBlock:
     def __init__(self, layer: MoELayer, gain: torch.Tensor, eps: float = 1e-6, buffers: BlockBuffers | None = None):
         """gain: [H] fp32 on the layer's device. buffers: shared with other blocks (training)."""
+        if gain.shape != (layer.H,):   # the pre-norm holds x to it
+            raise AssertionError(f"gain: [{layer.H}] expected")
         self.layer, self.gain, self.eps, self.buffers = layer, gain, eps, buffers
         self._few = {}         # few-token workspaces by the most tokens that they hold
         self._norm_ws = None
@@ -145,8 +147,10 @@ class MoEBlock:
     @_on_stream
     def train_backward(self, ctx, dout, dstream=None):
         """Gradients of a train_forward: dict with dx (of x and of the residual alike), dgain, and the layer's
-        dW_gate, dW_up, dW_down, dW_r. dout, dstream: gradients of out and of the residual stream."""
+        dW_gate, dW_up, dW_down, dW_r. dout, dstream: gradients of out and of the residual stream, contiguous."""
         T, layer = ctx["T"], self.layer
+        mok._dense("dout", dout, torch.bfloat16, T, layer.H)
+        mok._dense("dstream", dstream, torch.bfloat16, T, layer.H)
         p, b, H = layer.problem(T), self._training_buffers(T), layer.H
         y = torch.empty((T, H), dtype=torch.bfloat16, device=dout.device)
         mok.checkpoint_load(p, ctx["ckpt"], ctx["routing"], y, b["saved"])
