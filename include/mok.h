@@ -508,7 +508,8 @@ mok_status mok_checkpoint_save(const mok_problem* p, const void* x, const mok_ro
  * (mok_saved_size bytes, 1024-byte aligned) with the values that the
  * checkpoint's bytes stand for, h = bf16(silu(G) * U) formed from the restored
  * G and U, pad rows zero. Bytes of `saved` past the last padded row are left
- * as they are (the backward reads none of them). */
+ * as they are: the MXFP8 backward's quantiser may read them with the rows, but
+ * no result depends on them. */
 mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ckpt_bytes,
                                const mok_routing* routing, void* x, void* saved, mok_stream_t stream);
 
