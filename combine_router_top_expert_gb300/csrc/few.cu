@@ -31,11 +31,14 @@
 // experts' weights need at the copy rate; the layer's stages take 191, 518, 526, 531
 // and, MXFP8, 135, 312, 315 us):
 //   BF16    1 token 120 us (87%), 16 tokens 419 (98%), 64 434, 125 462 (90%)
-//   MXFP8   1 token 75 us, 64 tokens 246 (87%), 128 309
+//   MXFP8   1 token 75 us, 64 tokens 246 (87%), 65 292, 128 306 (70%)
 // What is missing: the launches, the router and the first weights' way in (7 us with
 // one token, 12 with 125), the way from the last gate/up tile to the first down one
-// (4 to 10), the partial sums at the end (6 to 15) and, with 128 MXFP8 tokens, the
-// MMAs.
+// (4 to 10) and the partial sums at the end (6 to 15). From 65 MXFP8 tokens on, the
+// 128-column form: its ring has four stages, its one accumulator lets no MMA run
+// while it is read, and its sums spill (the products alone would take about a
+// third of the time). Middle layers pay the fixed part in full (H = 2048, I = 1024,
+// E = 16, k = 4: 32 BF16 tokens 52 us, the bytes need 30).
 //
 // CTA layout (one per SM, cooperative launch: phase 2 waits for other CTAs'
 // phase 1 through per-expert counters):

@@ -114,7 +114,8 @@ __device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
 // 32-element MXFP8 block. Several CTAs share an SM and hide each other's waits
 // (T = 4096, H = 7168, the sum out as BF16, y as MXFP8: 32 us, 93% of the copy
 // rate, so the bytes bound it; CTAs that loop over rows with the next one prefetched
-// to shared memory took 44).
+// to shared memory took 44). Longer rows, BF16 in and out: T = 2048, H = 16384 42 us
+// (94%), T = 1024, H = 32768 49 (81%), T = 512, H = 65536 (VPT = 8 spills) 64 (62%).
 template <int VPT>
 __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 4 : 1)
 rmsnorm_kernel(const NormParams p) {
@@ -208,7 +209,9 @@ struct NormBwdParams {
 // of the rows ahead to shared memory (cp.async; nobody else reads them, so no
 // barrier is needed). Up to H = 8192 what the second half needs stays in
 // registers; longer rows read their buffers twice. Rows too long for two buffers
-// (STAGES = 0) are read from memory each time.
+// (STAGES = 0) are read from memory each time, and spill. BF16 sums: T = 2048, H = 16384
+// 68 us (two buffers, 58% of the copy rate), T = 1024, H = 32768 75 (none, 53%), T = 512,
+// H = 65536 124 (32%).
 //
 // T = 4096, H = 7168 with dsum, both kernels: 40.0 us for a BF16 sum (87% of the
 // copy rate; the launches, the first rows' way in and the gain gradient take the

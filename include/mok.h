@@ -453,8 +453,9 @@ typedef struct {
  * sum_sf 1). sum or y may be x's or residual's own buffer when that buffer's
  * pitch is H; otherwise outputs overlap no input and no other output. Rows
  * are independent: one that holds a NaN is NaN in y, one that holds an infinity
- * has rstd 0 (zeros in y, NaN where the infinities stood); its MXFP8 bytes are
- * then unspecified. T == 0 is a no-op. */
+ * has rstd 0 (zeros in y, NaN where the infinities stood), as has one whose
+ * squares add up past fp32's range; the MXFP8 bytes of NaN and infinities are
+ * unspecified. T == 0 is a no-op. */
 mok_status mok_rmsnorm(int32_t T, int32_t H, const mok_rmsnorm_args* a, mok_stream_t stream);
 
 typedef struct {
