@@ -178,7 +178,7 @@ def _sum_squares(t):
 
 
 def _loss_plain(l, labels):
-    """(loss, lse, valid, label's column) of logits. The loss is formed from the other tokens' share, so that it keeps
+    """(loss, lse, valid, label's column) of logits; a token without a label has 0 in both. The loss is formed from the other tokens' share, so that it keeps
     its digits where the label takes nearly all of the probability."""
     valid = (labels >= 0) & (labels < l.shape[1])
     col = torch.where(valid, labels, torch.zeros_like(labels))[:, None]
@@ -188,7 +188,8 @@ def _loss_plain(l, labels):
     others = e.scatter(1, col, 0.0).sum(1)
     at = torch.gather(l, 1, col)[:, 0] - m[:, 0]
     loss = torch.where(at < -1, torch.log(others + torch.exp(at)) - at, torch.log1p(others * torch.exp(-at)))
-    return torch.where(valid, loss, torch.zeros_like(loss)), lse, valid, col
+    zero = torch.zeros_like(loss)
+    return torch.where(valid, loss, zero), torch.where(valid, lse, zero), valid, col
 
 
 def _head_plain(s):
@@ -336,6 +337,8 @@ def _exact_head(c, s):
         rest[i, y[r][i]] = -math.inf
         rest = torch.logsumexp(rest, 1)                    # of the other tokens
         loss[r][i] = torch.nn.functional.softplus(rest[i] - at, threshold=100.0)
+        if c["op"] != "bwd":
+            lse[r] *= valid[r].cuda()
         if c["op"] == "score":
             continue
         ref = s["lse"].double()[r] if c["op"] == "bwd" else lse[r]
