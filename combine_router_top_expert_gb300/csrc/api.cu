@@ -269,6 +269,16 @@ bool few_ok(const mok_problem* p) {
 // Rows of the pre-norm: whole 16-byte vectors, a row held by one CTA.
 bool norm_dims_ok(int T, int H) { return T >= 0 && H >= 8 && H % 8 == 0 && H <= 65536; }
 
+bool sort_dims_ok(int T, int E, int k) {
+    return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && (int64_t)T * k < (int64_t)1 << 30;
+}
+bool sort_rows_ok(int T, int H, int k, int elem) {
+    return sort_dims_ok(T, 1, k) && H >= 8 && H % 8 == 0 && H <= 65536 && elem >= 0 && elem <= MOK_ELEM_F32;
+}
+bool head_dims_ok(int T, int H, int V) {
+    return T >= 0 && T <= 1 << 24 && H >= 8 && H % 8 == 0 && H <= 65536 && V >= 1 && V <= 1 << 24;
+}
+
 // The 8-bit checkpoint of the training context: codes and scales of x, G|U
 // and the partials.
 struct CkptLayout {
@@ -890,6 +900,145 @@ mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ck
     CheckpointParams q = ckpt_params(p, routing, const_cast<void*>(ckpt), saved);
     q.x_out = static_cast<__nv_bfloat16*>(x);
     return launch_status(launch_checkpoint_load(q, (cudaStream_t)stream));
+}
+
+size_t mok_sort_workspace_size(int32_t T, int32_t E, int32_t k) {
+    if (!sort_dims_ok(T, E, k)) return 0;
+    return std::max<size_t>(sort_workspace_bytes((int64_t)T * k, E), 16);
+}
+
+mok_status mok_sort_layout(const int32_t* topk_idx, int32_t T, int32_t E, int32_t k, int32_t* counts, int32_t* offsets,
+                           int32_t* row_src, int32_t* slot_row, void* workspace, size_t ws_bytes, mok_stream_t stream) {
+    if (!sort_dims_ok(T, E, k) || !counts || !offsets || !workspace) return MOK_ERR_INVALID;
+    if (T > 0 && (!topk_idx || !row_src || !slot_row)) return MOK_ERR_INVALID;
+    if (!aligned(topk_idx, 4) || !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_src, 4) ||
+        !aligned(slot_row, 4) || !aligned(workspace, 4) || ws_bytes < mok_sort_workspace_size(T, E, k))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    return launch_status(launch_sort_layout(topk_idx, (int64_t)T * k, E, counts, offsets, row_src, slot_row, workspace, s));
+}
+
+mok_status mok_sort_rows(const void* x, int64_t ldx, const int32_t* slot_row, int32_t T, int32_t H, int32_t k,
+                         int32_t elem, void* out, mok_stream_t stream) {
+    if (!sort_rows_ok(T, H, k, elem) || ldx < H || ldx % 8) return MOK_ERR_INVALID;
+    if (T > 0 && (!x || !slot_row || !out)) return MOK_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(slot_row, 4) || !aligned(out, 16)) return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (T == 0) return MOK_OK;
+    return launch_status(launch_sort_rows(elem, x, ldx, slot_row, T, H, k, out, (cudaStream_t)stream));
+}
+
+mok_status mok_unsort_rows(const void* y, const int32_t* slot_row, const float* w, int32_t T, int32_t H, int32_t k,
+                           int32_t elem, void* out, mok_stream_t stream) {
+    if (!sort_rows_ok(T, H, k, elem)) return MOK_ERR_INVALID;
+    if (T > 0 && (!y || !slot_row || !out)) return MOK_ERR_INVALID;
+    if (!aligned(y, 16) || !aligned(slot_row, 4) || !aligned(w, 4) || !aligned(out, 16)) return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (T == 0) return MOK_OK;
+    return launch_status(launch_unsort_rows(elem, y, slot_row, w, T, H, k, out, (cudaStream_t)stream));
+}
+
+mok_status mok_unsort_rows_backward(const void* dout, const void* y, const int32_t* slot_row, const float* w, int32_t T,
+                                    int32_t H, int32_t k, int32_t elem, void* dy, float* dw, mok_stream_t stream) {
+    if (!sort_rows_ok(T, H, k, elem)) return MOK_ERR_INVALID;
+    if (T > 0 && (!dout || !y || !slot_row || !w || !dy || !dw)) return MOK_ERR_INVALID;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(slot_row, 4) || !aligned(w, 4) || !aligned(dy, 16) ||
+        !aligned(dw, 4))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (T == 0) return MOK_OK;
+    return launch_status(launch_unsort_rows_backward(elem, dout, y, slot_row, w, T, H, k, dy, dw, (cudaStream_t)stream));
+}
+
+size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, int32_t piece, const mok_config* cfg) {
+    if (!head_dims_ok(T, H, V) || piece < 0) return 0;
+    return head_workspace_bytes(T, H, V, grad != 0, piece, make_common(nullptr, cfg).num_sms);
+}
+
+// Common checks and launch: `forward` writes loss and lse, `grad` dx and dW.
+static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args* a, bool forward, bool grad,
+                            const mok_config* cfg, mok_stream_t stream) {
+    if (!a || !head_dims_ok(T, H, V) || a->piece < 0 || !a->W || !a->workspace) return MOK_ERR_INVALID;
+    if (a->ldx < H || a->ldx % 8) return MOK_ERR_INVALID;
+    if (T > 0 && (!a->x || !a->labels || (forward && !a->loss) || (!forward && !a->lse))) return MOK_ERR_INVALID;
+    if (grad && !a->dx && !a->dW) return MOK_ERR_INVALID;
+    if (grad && a->accumulate && !a->dW_f32) return MOK_ERR_INVALID;
+    if (grad && a->dW && a->dx && a->dx == a->x) return MOK_ERR_INVALID;
+    if (grad && a->dx && a->dx == a->x && a->ldx != H) return MOK_ERR_INVALID;
+    if (!aligned(a->x, 16) || !aligned(a->W, 16) || !aligned(a->labels, a->labels_i64 ? 8 : 4) || !aligned(a->loss, 4) ||
+        !aligned(a->lse, 4) || !aligned(a->dloss, 4) || !aligned(a->dx, 16) || !aligned(a->dW, 16) ||
+        !aligned(a->workspace, 1024))
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    if (a->ws_bytes < mok_head_workspace_size(T, H, V, grad, a->piece, cfg)) return MOK_ERR_INVALID;
+    HeadLaunch h{};
+    h.T = T; h.H = H; h.V = V;
+    h.x = a->x;
+    h.ldx = a->ldx;
+    h.W = a->W;
+    h.labels = a->labels;
+    h.labels_i64 = a->labels_i64 != 0;
+    h.loss = forward ? a->loss : nullptr;
+    h.lse = a->lse;
+    h.piece = a->piece;
+    h.workspace = a->workspace;
+    if (grad) {
+        h.dloss = a->dloss;
+        h.scale = a->scale;
+        h.dx = a->dx;
+        h.dW = a->dW;
+        h.dW_f32 = a->dW_f32 != 0;
+        h.accumulate = a->accumulate != 0;
+    }
+    return launch_status(launch_head(h, make_common(a->workspace, cfg), (cudaStream_t)stream));
+}
+
+mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                         mok_stream_t stream) {
+    return head_call(T, H, V, a, true, false, cfg, stream);
+}
+
+mok_status mok_head_loss_backward(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                                  mok_stream_t stream) {
+    return head_call(T, H, V, a, false, true, cfg, stream);
+}
+
+mok_status mok_head_loss_train(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                               mok_stream_t stream) {
+    return head_call(T, H, V, a, true, true, cfg, stream);
+}
+
+size_t mok_grad_workspace_size(void) { return grad_workspace_bytes(); }
+
+static bool grad_list_ok(int32_t count, const mok_grad_tensor* list) {
+    if (count < 0 || (count > 0 && !list)) return false;
+    for (int32_t i = 0; i < count; ++i) {
+        const mok_grad_tensor& t = list[i];
+        if (t.n < 0 || t.n >= (int64_t)1 << 38 || t.elem < 0 || t.elem > MOK_ELEM_F32) return false;
+        if (t.n > 0 && !t.g) return false;
+        const size_t b = t.elem == MOK_ELEM_F32 ? 4 : 2;
+        if (!aligned(t.g, b) || !aligned(t.out, b)) return false;
+    }
+    return true;
+}
+
+mok_status mok_grad_norm(int32_t count, const mok_grad_tensor* list, float* norm, void* workspace, size_t ws_bytes,
+                         mok_stream_t stream) {
+    if (!grad_list_ok(count, list) || !norm || !aligned(norm, 4) || !workspace || !aligned(workspace, 16) ||
+        ws_bytes < grad_workspace_bytes())
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    return launch_status(launch_grad_clip(count, list, false, 0.0, norm, workspace, (cudaStream_t)stream));
+}
+
+mok_status mok_grad_clip(int32_t count, const mok_grad_tensor* list, double max_norm, float* norm, void* workspace,
+                         size_t ws_bytes, mok_stream_t stream) {
+    if (!grad_list_ok(count, list) || !(max_norm >= 0.0) || !norm || !aligned(norm, 4) || !workspace ||
+        !aligned(workspace, 16) || ws_bytes < grad_workspace_bytes())
+        return MOK_ERR_INVALID;
+    if (!device_ok()) return MOK_ERR_CUDA;
+    return launch_status(launch_grad_clip(count, list, true, max_norm, norm, workspace, (cudaStream_t)stream));
 }
 
 mok_status mok_route_test_hook(int32_t withhold_copy, int32_t timeout_ms) {

@@ -63,6 +63,23 @@ cudaError_t launch_rmsnorm(int T, int H, const mok_rmsnorm_args& a, cudaStream_t
 cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a, cudaStream_t s);
 cudaError_t launch_dequantize_rows(const void* q, const void* sf, int T, int H, void* x, cudaStream_t s);
 
+// sort.cu: tokens sorted by given experts (n = T * k entries), and back.
+int elem_bytes(int elem);
+size_t sort_workspace_bytes(int64_t n, int E);
+cudaError_t launch_sort_layout(const int32_t* idx, int64_t n, int E, int32_t* counts, int32_t* offsets,
+                               int32_t* row_src, int32_t* slot_row, void* ws, cudaStream_t s);
+cudaError_t launch_sort_rows(int elem, const void* x, int64_t ldx, const int32_t* slot_row, int T, int H, int k,
+                             void* out, cudaStream_t s);
+cudaError_t launch_unsort_rows(int elem, const void* y, const int32_t* slot_row, const float* w, int T, int H, int k,
+                               void* out, cudaStream_t s);
+cudaError_t launch_unsort_rows_backward(int elem, const void* dout, const void* y, const int32_t* slot_row,
+                                        const float* w, int T, int H, int k, void* dy, float* dw, cudaStream_t s);
+
+// grads.cu: the norm of all tensors (scale: and clipping by it).
+size_t grad_workspace_bytes();
+cudaError_t launch_grad_clip(int32_t count, const mok_grad_tensor* list, bool scale, double max_norm, float* norm,
+                             void* ws, cudaStream_t s);
+
 // checkpoint.cu: the training context in 8 bits. Save reads x, gu and partials
 // (and counts, offsets) and writes the MXFP8 rows; load reads those (and
 // row_src) and writes the *_out arrays.
@@ -122,6 +139,28 @@ struct FewLaunch {
 };
 size_t few_workspace_bytes(const mok_problem* p, int ctas);
 cudaError_t launch_few(const FewLaunch& a, const GemmCommon& c, cudaStream_t s);
+
+// head.cu: softmax cross entropy over a vocabulary. loss given: the forward
+// (writes loss and lse); dx or dW given: the gradient (from lse where loss is NULL).
+struct HeadLaunch {
+    int T, H, V;
+    const void* x;
+    int64_t ldx;
+    const void* W;
+    const void* labels;
+    int labels_i64;
+    float* loss;
+    float* lse;
+    const float* dloss;
+    float scale;
+    void* dx;
+    void* dW;
+    int dW_f32, accumulate;
+    int piece;
+    void* workspace;
+};
+size_t head_workspace_bytes(int T, int H, int V, bool grad, int piece, int num_sms);
+cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s);
 
 // Forward gate/up GEMM + SwiGLU. A: [rows, H] (bf16 or E4M3 + tile scales);
 // packed B: [E * 2I, H] (interleaved gate/up per il = BN/2 columns).

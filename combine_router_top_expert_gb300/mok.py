@@ -30,7 +30,10 @@ EXPORTS = ["mok_route_workspace_size", "mok_route_layout", "mok_packed_weights_s
            "mok_ep_dispatch", "mok_ep_push", "mok_packed_weights_bwd_size", "mok_pack_weights_bwd",
            "mok_dispatch_tokens", "mok_rmsnorm", "mok_rmsnorm_bwd_workspace_size", "mok_rmsnorm_backward",
            "mok_dequantize_rows", "mok_checkpoint_size", "mok_checkpoint_save", "mok_checkpoint_load",
-           "mok_few_workspace_size", "mok_moe_few"]
+           "mok_few_workspace_size", "mok_moe_few", "mok_sort_workspace_size", "mok_sort_layout", "mok_sort_rows",
+           "mok_unsort_rows", "mok_unsort_rows_backward", "mok_head_workspace_size", "mok_head_loss",
+           "mok_head_loss_backward", "mok_head_loss_train", "mok_grad_workspace_size", "mok_grad_norm",
+           "mok_grad_clip"]
 
 FLAG_MEGAKERNEL = 1
 FLAG_GEMM_PAIRS = 2
@@ -106,6 +109,18 @@ class FewArgs(ctypes.Structure):
                 ("ws_bytes", ctypes.c_size_t)]
 
 
+class HeadArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("labels", ctypes.c_void_p),
+                ("labels_i64", ctypes.c_int32), ("piece", ctypes.c_int32), ("loss", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dloss", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("dW_f32", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("dx", ctypes.c_void_p),
+                ("dW", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("elem", ctypes.c_int32)]
+
+
 EP_MAX_RANKS = 8
 STATUS_BYTES = 256     # the status block at the start of a workspace
 FEW_MAX_TOKENS = 128   # MOK_FEW_MAX_TOKENS
@@ -174,6 +189,19 @@ def lib():
             L.mok_few_workspace_size.argtypes = [PP, PC]
             L.mok_few_workspace_size.restype = SZ
             L.mok_moe_few.argtypes = [PP, ctypes.POINTER(FewArgs), PC, P]
+            L.mok_sort_workspace_size.argtypes = [I32] * 3
+            L.mok_sort_workspace_size.restype = SZ
+            L.mok_sort_layout.argtypes = [P, I32, I32, I32, P, P, P, P, P, SZ, P]
+            L.mok_sort_rows.argtypes = [P, ctypes.c_int64, P, I32, I32, I32, I32, P, P]
+            L.mok_unsort_rows.argtypes = [P, P, P, I32, I32, I32, I32, P, P]
+            L.mok_unsort_rows_backward.argtypes = [P, P, P, P, I32, I32, I32, I32, P, P, P]
+            L.mok_head_workspace_size.argtypes = [I32] * 5 + [PC]
+            L.mok_head_workspace_size.restype = SZ
+            for name in ("mok_head_loss", "mok_head_loss_backward", "mok_head_loss_train"):
+                getattr(L, name).argtypes = [I32, I32, I32, ctypes.POINTER(HeadArgs), PC, P]
+            L.mok_grad_workspace_size.restype = SZ
+            L.mok_grad_norm.argtypes = [I32, ctypes.POINTER(GradTensor), P, P, SZ, P]
+            L.mok_grad_clip.argtypes = [I32, ctypes.POINTER(GradTensor), ctypes.c_double, P, P, SZ, P]
             L.mok_status_string.argtypes = [I32]
             L.mok_status_string.restype = ctypes.c_char_p
             L.mok_version.restype = ctypes.c_char_p
@@ -182,7 +210,9 @@ def lib():
                          "mok_expert_ffn", "mok_combine", "mok_moe_backward", "mok_device_status", "mok_route_test_hook",
                          "mok_ep_dispatch", "mok_ep_push", "mok_pack_weights_bwd", "mok_dispatch_tokens", "mok_rmsnorm",
                          "mok_rmsnorm_backward", "mok_dequantize_rows", "mok_checkpoint_save", "mok_checkpoint_load",
-                         "mok_moe_few"):
+                         "mok_moe_few", "mok_sort_layout", "mok_sort_rows", "mok_unsort_rows",
+                         "mok_unsort_rows_backward", "mok_head_loss", "mok_head_loss_backward",
+                         "mok_head_loss_train", "mok_grad_norm", "mok_grad_clip"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -540,6 +570,205 @@ def checkpoint_load(p: Problem, ckpt, routing, x, saved, stream=None):
     rs = routing_struct(routing)
     _check(lib().mok_checkpoint_load(ctypes.byref(p), ckpt.data_ptr(), ckpt.numel(), ctypes.byref(rs), x.data_ptr(),
                                      saved.data_ptr(), _stream(stream)), "mok_checkpoint_load")
+
+
+# --------------------------------------------------------------------------- rows sorted by given experts
+
+BF16_ROWS, F16_ROWS, F32_ROWS = range(3)   # mok_elem
+_ELEMS = {torch.bfloat16: BF16_ROWS, torch.float16: F16_ROWS, torch.float32: F32_ROWS}
+
+
+def _elem(name, t):
+    """mok_elem of a tensor on the current device."""
+    if t.dtype not in _ELEMS or not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise AssertionError(f"{name}: bf16, fp16 or fp32 tensor on the current CUDA device expected")
+    return _ELEMS[t.dtype]
+
+
+def sort_workspace_size(T, E, k) -> int:
+    return int(lib().mok_sort_workspace_size(T, E, k))
+
+
+def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
+    """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped). Returns a dict of
+    counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see mok_sort_layout)."""
+    T, k = topk_idx.shape
+    dev = topk_idx.device
+    _dense("topk_idx", topk_idx, torch.int32, T, k)
+    if topk_idx.get_device() != torch._C._cuda_getDevice():
+        raise AssertionError("topk_idx: on the current CUDA device expected")
+    if out is None:
+        out = {n: torch.empty(s, dtype=torch.int32, device=dev)
+               for n, s in (("counts", E), ("offsets", E + 1), ("row_src", T * k), ("slot_row", T * k))}
+    for n, s in (("counts", E), ("offsets", E + 1), ("row_src", T * k), ("slot_row", T * k)):
+        _dense(n, out[n], torch.int32, s)
+    if workspace is None:
+        workspace = alloc_bytes(sort_workspace_size(T, E, k), dev)
+    _check(lib().mok_sort_layout(_ptr(topk_idx), T, E, k, _ptr(out["counts"]), _ptr(out["offsets"]),
+                                 _ptr(out["row_src"]), _ptr(out["slot_row"]), _ptr(workspace), workspace.numel(),
+                                 _stream(stream)), "mok_sort_layout")
+    return out
+
+
+def _slots(layout, T):
+    """(slot_row, k) of a layout of T tokens."""
+    s = layout["slot_row"]
+    n = s.numel()
+    if T <= 0:
+        if n or T:
+            raise AssertionError("slot_row: of these tokens expected")
+        return s, 1
+    if n % T or n == 0:
+        raise AssertionError(f"slot_row: a multiple of {T} entries expected")
+    _dense("slot_row", s, torch.int32, n)
+    return s, n // T
+
+
+def sort_rows(x, layout, out, stream=None):
+    """Rows of x [T, H] at their entries' places in out [T*k, H]; later rows of out are left as they are.
+    unsort_rows without weights is the gradient."""
+    T, H = x.shape
+    elem, (slot, k) = _elem("x", x), _slots(layout, T)
+    pitch, step = x.stride()
+    if step != 1 and T:
+        raise AssertionError("x: adjacent row elements expected")
+    _dense("out", out, x.dtype, T * k, H)
+    _check(lib().mok_sort_rows(_ptr(x), pitch if T > 1 else H, _ptr(slot), T, H, k, elem, _ptr(out), _stream(stream)),
+           "mok_sort_rows")
+    return out
+
+
+def unsort_rows(y, layout, out, w=None, stream=None):
+    """out [T, H] = the sum of each token's rows of y [T*k, H], times w [T, k] (fp32) if given."""
+    T, H = out.shape
+    elem, (slot, k) = _elem("out", out), _slots(layout, T)
+    _dense("out", out, out.dtype, T, H)
+    _dense("y", y, out.dtype, T * k, H)
+    _dense("w", w, torch.float32, T, k)
+    _check(lib().mok_unsort_rows(_ptr(y), _ptr(slot), _ptr(w), T, H, k, elem, _ptr(out), _stream(stream)),
+           "mok_unsort_rows")
+    return out
+
+
+def unsort_rows_backward(dout, y, layout, w, dy, dw, stream=None):
+    """Gradients of unsort_rows: dy [T*k, H] (later rows are left as they are) and dw [T, k]."""
+    T, H = dout.shape
+    elem, (slot, k) = _elem("dout", dout), _slots(layout, T)
+    _dense("dout", dout, dout.dtype, T, H)
+    _dense("y", y, dout.dtype, T * k, H)
+    _dense("dy", dy, dout.dtype, T * k, H)
+    _dense("w", w, torch.float32, T, k)
+    _dense("dw", dw, torch.float32, T, k)
+    _check(lib().mok_unsort_rows_backward(_ptr(dout), _ptr(y), _ptr(slot), _ptr(w), T, H, k, elem, _ptr(dy), _ptr(dw),
+                                          _stream(stream)), "mok_unsort_rows_backward")
+
+
+# --------------------------------------------------------------------------- loss of the vocabulary's head
+
+def head_workspace_size(T, H, V, grad=False, piece=0, cfg: Config | None = None) -> int:
+    return int(lib().mok_head_workspace_size(T, H, V, int(grad), piece, ctypes.byref(cfg) if cfg else None))
+
+
+def _head_args(x, W, labels, workspace, piece, loss=None, lse=None, dloss=None, scale=1.0, dx=None, dW=None,
+               accumulate=False):
+    T, H = x.shape
+    V = W.shape[0]
+    pitch = _rows("x", x, T, H)
+    if x.get_device() != torch._C._cuda_getDevice():
+        raise AssertionError("x: on the current CUDA device expected")
+    _dense("W", W, torch.bfloat16, V, H)
+    if labels.dtype not in (torch.int32, torch.int64):
+        raise AssertionError("labels: int32 or int64 expected")
+    _dense("labels", labels, labels.dtype, T)
+    for n, t in (("loss", loss), ("lse", lse), ("dloss", dloss)):
+        _dense(n, t, torch.float32, T)
+    _dense("dx", dx, torch.bfloat16, T, H)
+    f32 = dW is not None and dW.dtype is torch.float32
+    _dense("dW", dW, torch.float32 if f32 else torch.bfloat16, V, H)
+    return T, H, V, HeadArgs(x.data_ptr(), pitch, W.data_ptr(), labels.data_ptr(), labels.dtype is torch.int64, piece,
+                             _addr(loss), _addr(lse), _addr(dloss), scale, f32, bool(accumulate), _addr(dx), _addr(dW),
+                             workspace.data_ptr(), workspace.numel())
+
+
+def _head_call(name, a, cfg, stream):
+    T, H, V, args = a
+    _check(getattr(lib(), name)(T, H, V, ctypes.byref(args), ctypes.byref(cfg) if cfg else None, _stream(stream)), name)
+
+
+def head_loss(x, W, labels, loss, workspace, lse=None, cfg: Config | None = None, stream=None):
+    """Softmax cross entropy of x [T, H] against the vocabulary's rows W [V, H] (see mok_head_loss). labels: int32 or
+    int64, outside 0..V-1: ignored. x may be a row-strided view."""
+    _head_call("mok_head_loss", _head_args(x, W, labels, workspace, 0, loss, lse), cfg, stream)
+    return loss
+
+
+def head_loss_backward(x, W, labels, lse, dx, dW, workspace, dloss=None, scale=1.0, accumulate=False, piece=0,
+                       cfg: Config | None = None, stream=None):
+    """Gradients dx [T, H] and dW [V, H] (bf16 or fp32; either may be None) from head_loss's lse, for the losses'
+    gradient scale * dloss. accumulate: dW (fp32) is added to."""
+    _head_call("mok_head_loss_backward",
+               _head_args(x, W, labels, workspace, piece, None, lse, dloss, scale, dx, dW, accumulate), cfg, stream)
+
+
+def head_loss_train(x, W, labels, loss, dx, dW, workspace, dloss=None, scale=1.0, lse=None, accumulate=False, piece=0,
+                    cfg: Config | None = None, stream=None):
+    """head_loss and head_loss_backward in one call, for a dloss that does not depend on the loss."""
+    _head_call("mok_head_loss_train",
+               _head_args(x, W, labels, workspace, piece, loss, lse, dloss, scale, dx, dW, accumulate), cfg, stream)
+    return loss
+
+
+# --------------------------------------------------------------------------- gradient norm and clipping
+
+class GradList:
+    """Gradients (and where their clipped values go) in the form the library takes; keeps the tensors."""
+
+    def __init__(self, grads, out=None):
+        self.tensors, self.out = list(grads), None if out is None else list(out)
+        if self.out is not None and len(self.out) != len(self.tensors):
+            raise AssertionError("out: a tensor for each gradient expected")
+        n = len(self.tensors)
+        self.array, self.count = (GradTensor * max(n, 1))(), n
+        spans = []
+        for i, g in enumerate(self.tensors):
+            elem, o = _elem(f"grads[{i}]", g), None if self.out is None else self.out[i]
+            _dense(f"grads[{i}]", g, g.dtype, *g.shape)
+            _dense(f"out[{i}]", o, g.dtype, *g.shape)
+            self.array[i] = GradTensor(g.data_ptr(), _addr(o), g.numel(), elem)
+            for t in (g,) if o is None or o.data_ptr() == g.data_ptr() else (g, o):
+                if t.numel():
+                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+        spans.sort()
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise AssertionError("gradients and outputs that do not overlap expected")
+
+
+def grad_list(grads, out=None) -> GradList:
+    """Made once for gradients that stay where they are; grad_norm and grad_clip take it in place of a list."""
+    return GradList(grads, out)
+
+
+def grad_workspace_size() -> int:
+    return int(lib().mok_grad_workspace_size())
+
+
+def grad_norm(grads, norm, workspace, stream=None):
+    """norm [] (fp32) = 2-norm of all elements of a list of bf16, fp16 and fp32 tensors."""
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    _dense("norm", norm, torch.float32)
+    _check(lib().mok_grad_norm(g.count, g.array, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                               _stream(stream)), "mok_grad_norm")
+    return norm
+
+
+def grad_clip(grads, max_norm, norm, workspace, stream=None):
+    """norm as grad_norm, and all gradients times min(1, max_norm / (norm + 1e-6)): in place, or into a grad_list's
+    outputs."""
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    _dense("norm", norm, torch.float32)
+    _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), norm.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), _stream(stream)), "mok_grad_clip")
+    return norm
 
 
 def megakernel_trace(workspace, n_ctas):

@@ -515,6 +515,132 @@ mok_status mok_checkpoint_load(const mok_problem* p, const void* ckpt, size_t ck
                                const mok_routing* routing, void* x, void* saved, mok_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* Tokens sorted by experts that the caller chose, and back: the layer's layout */
+/* and row moves for a router or experts of the caller's own, with gradients.  */
+/* The pages have no counterpart.                                              */
+/* ------------------------------------------------------------------------- */
+
+typedef enum { MOK_ELEM_BF16 = 0, MOK_ELEM_F16 = 1, MOK_ELEM_F32 = 2 } mok_elem;
+
+/* Workspace bytes of mok_sort_layout (0: invalid sizes). */
+size_t mok_sort_workspace_size(int32_t T, int32_t E, int32_t k);
+
+/* The layout of mok_route_layout for given expert indices topk_idx [T,k]: rows
+ * ordered by (expert, t*k+j). An index outside 0..E-1 drops its entry, and a token
+ * may name an expert more than once. counts [E]; offsets [E+1], offsets[E] =
+ * entries kept; row_src [T*k]: t*k+j of each row, -1 from row offsets[E] on;
+ * slot_row [T*k]: each entry's row, -1 for dropped ones. 1 <= E <= 1024, k >= 1,
+ * T*k < 2^30. workspace 4-byte aligned, any content. */
+mok_status mok_sort_layout(const int32_t* topk_idx, int32_t T, int32_t E, int32_t k, int32_t* counts,
+                           int32_t* offsets, int32_t* row_src, int32_t* slot_row, void* workspace,
+                           size_t ws_bytes, mok_stream_t stream);
+
+/* out[slot_row[t*k+j]] = x[t] for every kept entry: out [T*k,H], its rows from
+ * offsets[E] on left as they are. x [T,H] with row pitch ldx >= H. elem: the type
+ * of both (mok_elem). H and ldx multiples of 8; rows 16-byte aligned; buffers do not
+ * overlap. mok_unsort_rows without weights is its gradient. */
+mok_status mok_sort_rows(const void* x, int64_t ldx, const int32_t* slot_row, int32_t T, int32_t H, int32_t k,
+                         int32_t elem, void* out, mok_stream_t stream);
+
+/* out[t] = sum_j w[t,j] * y[slot_row[t*k+j]] over kept entries, fp32, j ascending,
+ * rounded once. y [T*k,H] and out [T,H] of type elem; w [T,k] f32 or NULL (1).
+ * A token without kept entries gets zeros. Sizes and alignment as mok_sort_rows. */
+mok_status mok_unsort_rows(const void* y, const int32_t* slot_row, const float* w, int32_t T, int32_t H, int32_t k,
+                           int32_t elem, void* out, mok_stream_t stream);
+
+/* Gradient of mok_unsort_rows: dy[slot_row[t*k+j]] = w[t,j] * dout[t] (rows from
+ * offsets[E] on left as they are), dw[t,j] = <dout[t], y[slot_row[t*k+j]]> in fp32
+ * and a fixed order, 0 for dropped entries. dout [T,H], y and dy [T*k,H] of type
+ * elem; w, dw [T,k] f32. */
+mok_status mok_unsort_rows_backward(const void* dout, const void* y, const int32_t* slot_row, const float* w,
+                                    int32_t T, int32_t H, int32_t k, int32_t elem, void* dy, float* dw,
+                                    mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Softmax cross entropy over a large vocabulary, with its gradient, without   */
+/* the logits: what follows a model's last block. No counterpart in the pages. */
+/* ------------------------------------------------------------------------- */
+
+typedef struct {
+    const void* x;         /* [T,H] bf16, row pitch ldx elements */
+    int64_t ldx;           /* >= H, a multiple of 8 */
+    const void* W;         /* [V,H] bf16: the vocabulary's rows */
+    const void* labels;    /* [T] i32 or i64; outside 0..V-1: the token is ignored */
+    int32_t labels_i64;
+    int32_t piece;         /* tokens of which the gradient's [piece, V] bf16 buffer is held at once; 0: at most 4 GB */
+    float* loss;           /* [T] */
+    float* lse;            /* [T]: the log of the summed exponentials; see each call */
+    /* gradient */
+    const float* dloss;    /* [T]: gradient of each token's loss, or NULL (1) */
+    float scale;           /* multiplies dloss */
+    int32_t dW_f32;        /* dW is fp32 (else bf16) */
+    int32_t accumulate;    /* dW += (fp32 only) */
+    void* dx;              /* [T,H] bf16 or NULL */
+    void* dW;              /* [V,H] or NULL */
+    void* workspace;       /* mok_head_workspace_size bytes, 1024-byte aligned, any content; status block first */
+    size_t ws_bytes;
+} mok_head_args;
+
+/* Workspace bytes of the calls below on the current device (grad != 0: of those
+ * with a gradient; 0: invalid sizes). Needs H % 8 == 0, 8 <= H <= 65536,
+ * 1 <= V <= 2^24, 0 <= T <= 2^24, piece >= 0. */
+size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, int32_t piece, const mok_config* cfg);
+
+/* With l = x W^T (fp32 sums of bf16 products): lse[t] = log sum_v exp(l[t,v]),
+ * loss[t] = lse[t] - l[t, labels[t]] (formed from the other tokens' share, so that a
+ * small loss keeps its digits). Ignored tokens get 0 in both, whatever their rows
+ * of x hold. lse may be NULL. Bitwise the same in every run on one device.
+ * x, W, dx, dW 16-byte aligned. Of cfg num_sms and timeout_ms are read. Device-side
+ * waits are bounded: mok_device_status on the workspace reports MOK_ERR_TIMEOUT. */
+mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                         mok_stream_t stream);
+
+/* The gradient from a forward's lse (an input here; loss is not used): with
+ * dl[t,v] = scale * dloss[t] * (exp(l[t,v] - lse[t]) - [v == labels[t]]), rounded to
+ * bf16, dx = dl W and dW = dl^T x in fp32, rounded once. Ignored tokens have zeros in
+ * dx and add nothing to dW. At least one of dx and dW is given; dx may be x's own
+ * buffer when ldx == H only if dW is NULL. Logits are formed again. */
+mok_status mok_head_loss_backward(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                                  mok_stream_t stream);
+
+/* Loss and gradient in one call, for a dloss that does not depend on the loss:
+ * the outputs of the two calls above (lse may be NULL). */
+mok_status mok_head_loss_train(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
+                               mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* The global norm of many gradients, and clipping by it. No counterpart in    */
+/* the pages.                                                                  */
+/* ------------------------------------------------------------------------- */
+
+#define MOK_CLIP_EPS 1e-6
+
+typedef struct {
+    void* g;        /* n elements of type elem (mok_elem), aligned to the element */
+    void* out;      /* where the clipped values go, or NULL: in place */
+    int64_t n;      /* 0 <= n < 2^38 */
+    int32_t elem;
+} mok_grad_tensor;
+
+/* Workspace bytes of the two calls below. */
+size_t mok_grad_workspace_size(void);
+
+/* *norm (f32, device) = sqrt of the sum of the squares of all elements of the
+ * `count` tensors (`list` is a host array, read during the call). Sums are held in
+ * fp64 beyond a few elements, and values whose squares leave fp32's range are summed
+ * in fp64 from the start; bitwise the same in every run on one device. A NaN or an
+ * infinity anywhere reaches the norm. workspace 16-byte aligned, any content. */
+mok_status mok_grad_norm(int32_t count, const mok_grad_tensor* list, float* norm, void* workspace, size_t ws_bytes,
+                         mok_stream_t stream);
+
+/* The norm, and every tensor times min(1, max_norm / (norm + MOK_CLIP_EPS)):
+ * in place (not written when the factor is 1) or into out. max_norm >= 0. A norm of
+ * NaN makes every output NaN; an infinite one makes finite values 0 and
+ * infinities NaN. Tensors and outputs do not overlap one another. */
+mok_status mok_grad_clip(int32_t count, const mok_grad_tensor* list, double max_norm, float* norm, void* workspace,
+                         size_t ws_bytes, mok_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Expert parallelism across ranks ([K-ja] 02: experts spread over GPUs, the  */
 /* expert side pulls the token rows it needs, results are pushed back to the  */
 /* tokens' slots; [RW] "Rebuilding the MoE layer around communication").      */
