@@ -13,8 +13,9 @@
 // pairs (head_gemm_kernel):
 //   logits  x W^T    both operands K-major; the epilogue reduces 128 columns of a row
 //                    to (max, sum of exponentials, label's logit), so that a logit
-//                    lives in tensor memory and registers only, and
-//                    with a gradient writes dl (log-sum known) or the exponentials
+//                    lives in tensor memory and registers only, and with a gradient
+//                    writes dl (log-sum known) or the exponentials, which
+//                    head_dl_kernel turns into dl in their place
 //   dX      dl W     A K-major, B MN-major (the vocabulary is K)
 //   dW      dl^T x   both MN-major (the tokens are K)
 #include <cudaTypedefs.h>
@@ -39,12 +40,22 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBarOffset = kStages * kStageBytes;
 constexpr int kSmemBytes = 1024 + kBarOffset + 256;
 constexpr int kStatCols = 128;          // columns behind one (max, sum)
+// K blocks of a logit that are summed in tensor memory; these sums are then added in
+// registers. The tensor cores cut what they add to an accumulator instead of rounding
+// it, which makes a long sum too small by up to 2^-24 of itself a step: H = 7168 in one
+// sum moved a loss by 4.8e-6 of itself, in sums of 1024 by what the other roundings do.
+constexpr int kLogitBlocks = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+// An exponential e is kept as its root times 2^15, s = 2^15 exp((l - top) / 2): FP16 then has a relative error of
+// 2^-11 in s, 2^-10 in e, down to e = 2^-58 (e itself would lose bits below 2^-29).
+constexpr float kRootShift = 15.f;
+constexpr float kRootScale = 1.f / (1 << 30);   // s * s * kRootScale = e
 
 enum HeadEpi : int {
     kEpiStats = 0,   // (max, sum, label's logit)
-    kEpiDl = 1,      // dl from a known log-sum
-    kEpiOut = 2,     // the product itself: BF16 rows, or fp32 rows, or a partial sum
+    kEpiExp = 1,     // the same, and the exponentials
+    kEpiDl = 2,      // dl from a known log-sum
+    kEpiOut = 3,     // the product itself: BF16 rows, or fp32 rows, or a partial sum
 };
 
 struct HeadGemm {
@@ -62,7 +73,6 @@ struct HeadGemm {
     int stat_tiles;
     float* label_logit;     // [tokens]
     const float* lse;       // [T]
-    const float* loss;      // [T] or NULL: the losses, if they are known, too
     const float* dloss;     // [T] or NULL
     float scale;
     __nv_bfloat16* dl;      // [tokens rounded up to 256, ld]
@@ -103,6 +113,17 @@ __device__ __forceinline__ Tile head_tile(int g, int mt, int nt, int group) {
     t.m = first + g % rows;
     t.n = g / rows;
     return t;
+}
+
+// 32 lanes x 16 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
 template <bool A_MN, bool B_MN, int EPI>
@@ -163,6 +184,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int kbs = (K + kBK - 1) / kBK;
     const int total = mt * nt * p.splits;
     const int gstart = (int)blockIdx.x / 2, gstep = (int)gridDim.x / 2;
+    constexpr int kSumBlocks = EPI == kEpiOut ? 1 << 30 : kLogitBlocks;   // K blocks of an accumulator's sum
     auto k_first = [&](int split) { return (int)((int64_t)kbs * split / p.splits); };
 
     if (warp == 0) {
@@ -215,10 +237,13 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const int split = g / (mt * nt);
                 const int kb0 = k_first(split), kb1 = k_first(split + 1);
                 if (kb0 == kb1) continue;
-                if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
-                tc::fence_after_sync();
-                const uint32_t d = tmem + (uint32_t)(acc * kBN);
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    const bool first = (kb - kb0) % kSumBlocks == 0;
+                    if (first) {
+                        if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
+                        tc::fence_after_sync();
+                    }
+                    const uint32_t d = tmem + (uint32_t)(acc * kBN);
                     if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
                     tc::fence_after_sync();
 #pragma unroll
@@ -227,15 +252,16 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                                  : tc::make_sdesc(a_tile(stage) + kk * 32, 16, 1024, tc::kLayoutSW128);
                         const uint64_t bd = B_MN ? tc::make_sdesc(b_tile(stage) + kk * 2048, 8192, 1024, tc::kLayoutSW128)
                                                  : tc::make_sdesc(b_tile(stage) + kk * 32, 16, 1024, tc::kLayoutSW128);
-                        tc::mma_bf16_2sm(d, ad, bd, tc::idesc_bf16(kBM, kBN, A_MN, B_MN), kb > kb0 || kk > 0 ? 1u : 0u);
+                        tc::mma_bf16_2sm(d, ad, bd, tc::idesc_bf16(kBM, kBN, A_MN, B_MN), !first || kk > 0 ? 1u : 0u);
                     }
                     issued = true;
                     tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
                     if (++stage == kStages) { stage = 0; ph ^= 1u; }
+                    if (kb + 1 == kb1 || (kb + 1 - kb0) % kSumBlocks == 0) {
+                        tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
+                        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+                    }
                 }
-                if (!ok) break;
-                tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
-                if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
             }
             if (!ok && issued) {
                 // every MMA issued so far must finish before tensor memory is freed
@@ -249,21 +275,36 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t acc_ph = 0;
         for (int g = gstart; g < total; g += gstep) {
             const Tile t = head_tile(g, mt, nt, p.group);
-            const bool has_acc = k_first(t.split) < k_first(t.split + 1);
+            const int blocks = k_first(t.split + 1) - k_first(t.split);
             float r[4][32];
             __syncwarp();
-            if (has_acc) {
-                if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) break;
+            bool ok = true;
+            for (int b0 = 0; b0 < blocks; b0 += min(kSumBlocks, blocks - b0)) {
+                if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
+                __syncwarp();
                 tc::fence_after_sync();
                 const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kBN + half * 128);
+                if (EPI == kEpiOut || b0 == 0) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc::tmem_ld_32x32b_x32(tbase + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
-                tc::tmem_ld_wait();
+                    for (int c = 0; c < 4; ++c)
+                        tc::tmem_ld_32x32b_x32(tbase + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t v[16];
+                        tmem_ld_x16(tbase + 16 * c, v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[c / 2][16 * (c % 2) + i] += __uint_as_float(v[i]);
+                    }
+                }
                 tc::fence_before_sync();
                 tc::mbar_arrive_cluster(tc::mapa_shared(acce_bar(acc), 0));
                 if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
-            } else {
+            }
+            if (!ok) break;
+            if (blocks == 0) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -272,7 +313,15 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const int row = t.m * kBM + rank * 128 + q * 32 + lane;
             const int col0 = t.n * kBN + half * 128;
             const int nv = min(128, p.N - col0);          // valid columns; none: <= 0
-            if constexpr (EPI == kEpiStats) {
+            if constexpr (EPI == kEpiStats || EPI == kEpiExp) {
+                if (EPI == kEpiExp && row >= M && nv > 0) {
+                    // rows behind the last live token are zeros: dW's last K block reads them
+                    __nv_bfloat16* o = p.dl + (int64_t)row * p.ld_dl + col0;
+                    const uint32_t z[8] = {};
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (16 * c < nv) tc::stg_v8(o + 16 * c, z);
+                }
                 if (row < M && nv > 0) {
                     const int64_t tok = p.rows && !all ? p.rows[row] : row;
                     int64_t lab = label_at(p.labels, p.labels_i64, tok);
@@ -289,17 +338,40 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) mx = fmaxf(mx, r[c][i]);
-                    const float base = mx == -INFINITY ? 0.f : mx * kLog2e;
+                    const float base = kRootShift - (mx == -INFINITY ? 0.f : mx * (0.5f * kLog2e));
                     // the label's own term stays out of the sum, so that the others' share keeps its
                     // digits where the label takes nearly everything
                     float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (EPI == kEpiStats) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float e = exp2_approx(fmaf(r[c][i], kLog2e, -base));
-                            s[c] += 32 * c + i == lc ? 0.f : e;
+                            for (int i = 0; i < 32; ++i) {
+                                const float e = exp2_approx(fmaf(r[c][i], 0.5f * kLog2e, base));
+                                s[c] = 32 * c + i == lc ? s[c] : fmaf(e, e, s[c]);
+                            }
+                    } else {
+                        // relative to the 128 columns' largest: head_dl_kernel makes dl of them
+                        __nv_bfloat16* o = p.dl + (int64_t)row * p.ld_dl + col0;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            if (16 * c >= nv) break;
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float e[2];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int j = 16 * c + 2 * i + h;
+                                    e[h] = exp2_approx(fmaf(r[j / 32][j % 32], 0.5f * kLog2e, base));
+                                    s[c / 2] = j == lc ? s[c / 2] : fmaf(e[h], e[h], s[c / 2]);
+                                }
+                                const __half2 v = __floats2half2_rn(e[0], e[1]);
+                                w[i] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                            tc::stg_v8(o + 16 * c, w);
                         }
+                    }
                     if (lc >= 0) {
                         float own = 0.f;
 #pragma unroll
@@ -308,18 +380,17 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             for (int i = 0; i < 32; ++i) own = 32 * c + i == lc ? r[c][i] : own;
                         p.label_logit[row] = own;
                     }
-                    p.stats[(int64_t)row * p.stat_tiles + col0 / kStatCols] =
-                        make_float2(mx, (s[0] + s[1]) + (s[2] + s[3]));
+                    const float sum = ((s[0] + s[1]) + (s[2] + s[3])) * kRootScale;
+                    p.stats[(int64_t)row * p.stat_tiles + col0 / kStatCols] = make_float2(mx, sum);
                 }
             } else if constexpr (EPI == kEpiDl) {
                 if (nv > 0) {
                     float coef = 0.f, base = 0.f;
                     int lc = -1;
-                    int64_t tok = 0;
                     // rows behind the last live token are zeros: dW's last K block reads them
                     const bool in = row < M;
                     if (in) {
-                        tok = p.rows && !all ? p.rows[row] : row;
+                        const int64_t tok = p.rows && !all ? p.rows[row] : row;
                         const int64_t lab = label_at(p.labels, p.labels_i64, tok);
                         coef = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
                         base = __ldg(p.lse + tok);
@@ -347,8 +418,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) own = 32 * c + i == lc ? r[c][i] : own;
-                        // p - 1 = exp(-loss) - 1: from the loss it keeps the digits of a small 1 - p
-                        o[lc] = __float2bfloat16_rn(coef * expm1f(p.loss ? -__ldg(p.loss + tok) : own - base));
+                        o[lc] = __float2bfloat16_rn(coef * expm1f(own - base));
                     }
                 }
             } else {
@@ -530,6 +600,45 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const float* 
     if (lse) lse[t] = on ? r.top + logf(r.others + r.own) : 0.f;
 }
 
+// The same with a gradient: then the row's exponentials, in their place, become
+//   dl[v] = c e[v] exp(top of its 128 columns - lse),   dl[label] = -c others / (others + own)
+__global__ void __launch_bounds__(kRowThreads)
+head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const float* __restrict__ label_logit,
+               const int32_t* __restrict__ rows, const int32_t* __restrict__ live, const void* labels, int i64,
+               const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld, int V, float* loss,
+               float* lse) {
+    __shared__ float red[64];
+    pdl_wait();
+    pdl_allow_next();
+    const int i = blockIdx.x;
+    if (i >= *live) return;
+    const int64_t t = rows[i];
+    const float2* st = stats + (int64_t)i * stat_tiles;
+    const RowSum r = join_row(st, stat_tiles, label_logit[i], red);
+    const float sum = r.others + r.own, log_sum = r.top + logf(sum);
+    const float coef = scale * (dloss ? dloss[t] : 1.0f);
+    const int label = (int)label_at(labels, i64, t);
+    __nv_bfloat16* row = dl + i * ld;
+    const float inv = coef / sum * kRootScale;
+    for (int v = 8 * threadIdx.x; v < V; v += 8 * kRowThreads) {
+        const uint4 e = *reinterpret_cast<const uint4*>(row + v);
+        const float f = inv * exp2_approx((st[v / kStatCols].x - r.top) * kLog2e);
+        const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            o[j] = pack_bf16x2(a.x * f * a.x, a.y * f * a.y);
+        }
+        *reinterpret_cast<uint4*>(row + v) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (label >= v && label < v + 8) row[label] = __float2bfloat16_rn(-coef * (r.others / sum));
+    }
+    if (threadIdx.x != 0) return;
+    const float at = label_logit[i] - r.top;
+    loss[t] = r.own > r.others ? log1pf(r.others / r.own) : logf(sum) - at;
+    if (lse) lse[t] = log_sum;
+}
+
 // dx rows from the parts of K, added up in order.
 __global__ void __launch_bounds__(256)
 head_join_kernel(const float* __restrict__ part, int64_t stride, int splits, int nv, const int32_t* __restrict__ rows,
@@ -653,7 +762,7 @@ int dx_splits(int tokens, int H, int V, int pairs) {
 }
 
 struct HeadLayout {
-    size_t rows, live, label, lse, stats, xc, dl, part, acc, total;
+    size_t rows, live, label, stats, xc, dl, part, acc, total;
     int piece, splits;
 };
 
@@ -672,7 +781,6 @@ HeadLayout head_layout(int T, int H, int V, bool grad, bool acc, int want, int n
     L.live = take(4);
     L.rows = take(cap * 4);
     L.label = take(cap * 4);
-    L.lse = take(cap * 4);
     L.stats = take(cap * ceil_div(V, kStatCols) * 8);
     if (grad || T > kPlainRows) L.xc = take(cap * H * 2);
     if (grad) L.dl = take(cap * pitch_dl(V) * 2);
@@ -713,10 +821,10 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t0 * a.ldx;
         const void* labels = static_cast<const char*>(a.labels) + (int64_t)t0 * label_bytes;
         float* loss = a.loss ? a.loss + t0 : nullptr;
-        float* lse = a.lse ? a.lse + t0 : grad ? reinterpret_cast<float*>(ws + L.lse) : nullptr;
+        float* lse = a.lse ? a.lse + t0 : nullptr;
         __nv_bfloat16* dx = a.dx ? static_cast<__nv_bfloat16*>(a.dx) + (int64_t)t0 * H : nullptr;
         const bool gather = grad || T > kPlainRows;
-        const bool stats_pass = a.loss != nullptr;
+        const bool forward = a.loss != nullptr;
         HeadGemm p{};
         p.status = c.status;
         p.timeout_ns = c.timeout_ns;
@@ -733,8 +841,8 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             const int per = std::max(8, ceil_div(n, 1024));
             e = launch_after(head_prep_kernel, dim3(ceil_div(n, per)), dim3(kPrepThreads), 0, s,
                              reinterpret_cast<const uint4*>(x), a.ldx / 8, labels, a.labels_i64, n, V, nv, per, rows, live,
-                             reinterpret_cast<uint4*>(ws + L.xc), stats_pass ? loss : nullptr,
-                             stats_pass ? lse : nullptr, reinterpret_cast<uint4*>(dx),
+                             reinterpret_cast<uint4*>(ws + L.xc), forward ? loss : nullptr,
+                             forward ? lse : nullptr, reinterpret_cast<uint4*>(dx),
                              t0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr);
             if (!make_tmap_pitch(&txc, ws + L.xc, cap, H, H, 128)) return cudaErrorInvalidValue;
             p.live = live;
@@ -747,23 +855,30 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         p.M = n;
         p.N = V;
         p.K = H;
-        if (stats_pass) {
-            p.stats = stats;
-            p.stat_tiles = stat_tiles;
-            p.label_logit = label;
+        p.stats = stats;
+        p.stat_tiles = stat_tiles;
+        p.label_logit = label;
+        if (!grad) {
             e = run_head_gemm<false, false, kEpiStats>(txc, tw, tx, p, c.num_sms, s);
             if (e == cudaSuccess)
                 e = launch_after(head_loss_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, stat_tiles,
                                  (const float*)label, (const int32_t*)(gather ? rows : nullptr),
                                  (const int32_t*)(gather ? live : nullptr), labels, a.labels_i64, V, loss, lse);
+            continue;
         }
-        if (!grad || e != cudaSuccess) continue;
-        p.lse = lse;
-        p.loss = loss;
-        p.dloss = a.dloss ? a.dloss + t0 : nullptr;
         p.dl = reinterpret_cast<__nv_bfloat16*>(ws + L.dl);
         p.ld_dl = pitch_dl(V);
-        e = run_head_gemm<false, false, kEpiDl>(txc, tw, tx, p, c.num_sms, s);
+        p.lse = lse;
+        p.dloss = a.dloss ? a.dloss + t0 : nullptr;
+        if (forward) {
+            e = run_head_gemm<false, false, kEpiExp>(txc, tw, tx, p, c.num_sms, s);
+            if (e == cudaSuccess)
+                e = launch_after(head_dl_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, stat_tiles,
+                                 (const float*)label, (const int32_t*)rows, (const int32_t*)live, labels, a.labels_i64,
+                                 p.dloss, a.scale, p.dl, p.ld_dl, V, loss, lse);
+        } else {
+            e = run_head_gemm<false, false, kEpiDl>(txc, tw, tx, p, c.num_sms, s);
+        }
         if (e != cudaSuccess) break;
         if (dx) {
             HeadGemm q = p;
