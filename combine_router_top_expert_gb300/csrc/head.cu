@@ -38,8 +38,9 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kOperandBytes = 128 * kBK * 2;          // a CTA's share of A or of B
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBarOffset = kStages * kStageBytes;
-constexpr int kSmemBytes = 1024 + kBarOffset + 256;
-constexpr int kStatCols = 128;          // columns behind one (max, sum)
+constexpr int kPassBytes = 4096;                      // an epilogue warp's staging: 32 rows x 128 bytes
+constexpr int kStageOutOffset = kBarOffset + 1024;
+constexpr int kSmemBytes = 1024 + kStageOutOffset + kEpiWarps * kPassBytes;
 // K blocks of a logit that are summed in tensor memory; these sums are then added in
 // registers. The tensor cores cut what they add to an accumulator instead of rounding
 // it, which makes a long sum too small by up to 2^-24 of itself a step: H = 7168 in one
@@ -51,8 +52,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRootShift = 15.f;
 constexpr float kRootScale = 1.f / (1 << 30);   // s * s * kRootScale = e
 
+enum Early : int { kEarlyNone = 0, kEarlyA = 1, kEarlyB = 2 };
+
 enum HeadEpi : int {
-    kEpiStats = 0,   // (max, sum, label's logit)
+    kEpiStats = 0,   // (max, sum)
     kEpiExp = 1,     // the same, and the exponentials
     kEpiDl = 2,      // dl from a known log-sum
     kEpiOut = 3,     // the product itself: BF16 rows, or fp32 rows, or a partial sum
@@ -63,15 +66,18 @@ struct HeadGemm {
     int tokens;             // tokens of the piece (the live ones' upper bound)
     int M, N, K;            // K or M is the token count where m_live / k_live is set
     int m_live, k_live;
+    int bn;                 // tile columns (a multiple of 32, at most kBN; the MN-major B's are kBN)
     int splits;             // parts of K, each a tile of its own
     int group;              // row tiles that are walked together
+    int early;              // operands whose first blocks may be loaded before the kernel ahead has ended
+    int wait_late;          // the operands were complete before the kernel ahead began: it is waited for at the end
     // logits
     const void* labels;
     int labels_i64;
     const int32_t* rows;    // live token -> token, or NULL
     float2* stats;          // [tokens, stat tiles]
     int stat_tiles;
-    float* label_logit;     // [tokens]
+    const float* label_logit;   // [tokens]
     const float* lse;       // [T]
     const float* dloss;     // [T] or NULL
     float scale;
@@ -83,18 +89,41 @@ struct HeadGemm {
     const float* add;       // fp32 rows that are added to the product, or NULL
     int64_t split_stride;   // elements between the parts' outputs
     const int32_t* out_rows;   // row -> output row, or NULL
+    int zero_dead;          // rows whose label is not below live_below are zeros
+    int live_below;
     StatusBlock* status;
     unsigned long long timeout_ns;
 };
 
 __device__ __forceinline__ float exp2_approx(float v) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));   // volatile: kept in place, or the epilogues spill
     return r;
 }
 
 __device__ __forceinline__ int64_t label_at(const void* labels, int i64, int64_t t) {
     return i64 ? __ldg(static_cast<const long long*>(labels) + t) : (int64_t)__ldg(static_cast<const int32_t*>(labels) + t);
+}
+
+__device__ __forceinline__ bool is_live(const void* labels, int i64, int64_t t, int V) {
+    const int64_t y = label_at(labels, i64, t);
+    return y >= 0 && y < V;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, __nv_bfloat16 v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(v)) : "memory");
+}
+
+// Arrive on an mbarrier of the pair. What is released is tensor memory that was read;
+// a release at cluster scope would also wait for the thread's stores on their way (1 to
+// 2 us a tile).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 struct Tile {
@@ -168,8 +197,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::tmem_alloc_2sm(tc::smem_u32(&s_tmem_base), 512);
         tc::tmem_relinquish_2sm();
     }
-    pdl_wait();
-    pdl_allow_next();
+    // The kernel behind this one may begin once all that this one reads is complete
+    // (a wait_late kernel reads on that ground); early kernels wait in their roles.
+    if (!p.early) {
+        if (!p.wait_late) pdl_wait();
+        pdl_allow_next();
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -180,44 +213,70 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int live = p.live ? *p.live : p.tokens;
     const bool all = live == p.tokens;
     const int M = p.m_live ? live : p.M, K = p.k_live ? live : p.K;
-    const int mt = (M + kBM - 1) / kBM, nt = (p.N + kBN - 1) / kBN;
+    const int mt = (M + kBM - 1) / kBM, nt = (p.N + p.bn - 1) / p.bn;
     const int kbs = (K + kBK - 1) / kBK;
     const int total = mt * nt * p.splits;
     const int gstart = (int)blockIdx.x / 2, gstep = (int)gridDim.x / 2;
     constexpr int kSumBlocks = EPI == kEpiOut ? 1 << 30 : kLogitBlocks;   // K blocks of an accumulator's sum
-    auto k_first = [&](int split) { return (int)((int64_t)kbs * split / p.splits); };
+    auto k_first = [&](int split) { return p.splits == 1 ? kbs * split : kbs * split / p.splits; };   // below 2^25
 
     if (warp == 0) {
         if (lane == 0) {
             const void* mapA = EPI != kEpiOut && all ? (const void*)&tmAll : (const void*)&tmA;
             const void* mapB = A_MN && B_MN && all ? (const void*)&tmAll : (const void*)&tmB;
-            int stage = 0;
+            const uint32_t bytes = kOperandBytes + (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2);
+            // both halves of a pair signal the leader's barrier, which expects both
+            auto load_a = [&](int stage, const Tile& t, int kb) {
+                const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
+                const int m0 = t.m * kBM + rank * 128, k0 = kb * kBK;
+                if constexpr (A_MN) {
+                    tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
+                    tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
+                } else {
+                    tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, k0, m0);
+                }
+            };
+            auto load_b = [&](int stage, const Tile& t, int kb) {
+                const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
+                const int n0 = t.n * p.bn + rank * (p.bn / 2), k0 = kb * kBK;
+                if constexpr (B_MN) {
+                    tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, n0, k0);
+                    tc::tma_load_2d_2sm(b_tile(stage) + 8192, mapB, lead, n0 + 64, k0);
+                } else {
+                    tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, k0, n0);
+                }
+            };
+            int stage = 0, ahead = 0;   // ahead: blocks whose early operands are on their way
             uint32_t ph = 0;
             int last_par[kStages];
             for (int s = 0; s < kStages; ++s) last_par[s] = -1;
             bool ok = true;
+            if (p.early) {
+                for (int g = gstart; g < total && ahead < kStages; g += gstep) {
+                    const Tile t = head_tile(g, mt, nt, p.group);
+                    const int kend = k_first(t.split + 1);
+                    for (int kb = k_first(t.split); kb < kend && ahead < kStages; ++kb, ++ahead) {
+                        if (rank == 0) tc::mbar_expect_tx(full_bar(ahead), 2 * bytes);
+                        if (p.early & kEarlyA) load_a(ahead, t, kb);
+                        if (p.early & kEarlyB) load_b(ahead, t, kb);
+                    }
+                }
+                pdl_wait();
+                pdl_allow_next();
+            }
             for (int g = gstart; g < total && ok; g += gstep) {
                 const Tile t = head_tile(g, mt, nt, p.group);
-                const int m0 = t.m * kBM + rank * 128, n0 = t.n * kBN + rank * 128;
                 const int kend = k_first(t.split + 1);
                 for (int kb = k_first(t.split); kb < kend; ++kb) {
-                    if (!tc::mbar_wait(empty_bar(stage), ph ^ 1u, st, tmo, kSiteProducerEmpty)) { ok = false; break; }
-                    // both halves signal the leader's barrier, which expects both
-                    const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
-                    if (rank == 0) tc::mbar_expect_tx(full_bar(stage), 2 * kStageBytes);
-                    const int k0 = kb * kBK;
-                    if constexpr (A_MN) {
-                        tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
-                        tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
+                    const bool begun = ahead > 0;   // only in the first round of stages, which are free
+                    if (begun) {
+                        --ahead;
                     } else {
-                        tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, k0, m0);
+                        if (!tc::mbar_wait(empty_bar(stage), ph ^ 1u, st, tmo, kSiteProducerEmpty)) { ok = false; break; }
+                        if (rank == 0) tc::mbar_expect_tx(full_bar(stage), 2 * bytes);
                     }
-                    if constexpr (B_MN) {
-                        tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, n0, k0);
-                        tc::tma_load_2d_2sm(b_tile(stage) + 8192, mapB, lead, n0 + 64, k0);
-                    } else {
-                        tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, k0, n0);
-                    }
+                    if (!begun || !(p.early & kEarlyA)) load_a(stage, t, kb);
+                    if (!begun || !(p.early & kEarlyB)) load_b(stage, t, kb);
                     last_par[stage] = (int)ph;
                     if (++stage == kStages) { stage = 0; ph ^= 1u; }
                 }
@@ -230,37 +289,56 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
+            if (p.early) pdl_wait();
+            const uint32_t idesc = tc::idesc_bf16(kBM, p.bn, A_MN, B_MN);
+            // Of a descriptor only the start address changes (16-byte units, in the low word), so an MMA
+            // costs two additions: what this thread does between MMAs is not hidden behind them. Building
+            // each descriptor from its fields and waiting for every stage by itself left the tensor cores
+            // idle a quarter of the time (T = 2560, H = 7168, V = 50001, score: 1090 us, this 954).
+            constexpr uint32_t kLoA = (A_MN ? 512u : 1u) << 16, kLoB = (B_MN ? 512u : 1u) << 16;
+            constexpr uint32_t kHi = 64u | 1u << 14 | tc::kLayoutSW128 << 29;
+            constexpr uint32_t kStepA = A_MN ? 128u : 2u, kStepB = B_MN ? 128u : 2u;
+            auto mma4 = [&](uint32_t d, int sg, uint32_t more) {
+                const uint32_t al = (a_tile(0) >> 4 | kLoA) + (uint32_t)sg * (kStageBytes >> 4);
+                const uint32_t bl = (b_tile(0) >> 4 | kLoB) + (uint32_t)sg * (kStageBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_bf16_2sm(d, (uint64_t)kHi << 32 | (al + kk * kStepA), (uint64_t)kHi << 32 | (bl + kk * kStepB),
+                                     idesc, kk > 0 ? 1u : more);
+            };
             int stage = 0, acc = 0;
             uint32_t ph = 0, acc_ph = 0;
             bool ok = true, issued = false;
             for (int g = gstart; g < total && ok; g += gstep) {
                 const int split = g / (mt * nt);
-                const int kb0 = k_first(split), kb1 = k_first(split + 1);
-                if (kb0 == kb1) continue;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    const bool first = (kb - kb0) % kSumBlocks == 0;
-                    if (first) {
-                        if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
-                        tc::fence_after_sync();
-                    }
+                int left = k_first(split + 1) - k_first(split);
+                while (left > 0 && ok) {
+                    const int n = min(left, kSumBlocks);
+                    left -= n;
+                    if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
                     const uint32_t d = tmem + (uint32_t)(acc * kBN);
-                    if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t ad = A_MN ? tc::make_sdesc(a_tile(stage) + kk * 2048, 8192, 1024, tc::kLayoutSW128)
-                                                 : tc::make_sdesc(a_tile(stage) + kk * 32, 16, 1024, tc::kLayoutSW128);
-                        const uint64_t bd = B_MN ? tc::make_sdesc(b_tile(stage) + kk * 2048, 8192, 1024, tc::kLayoutSW128)
-                                                 : tc::make_sdesc(b_tile(stage) + kk * 32, 16, 1024, tc::kLayoutSW128);
-                        tc::mma_bf16_2sm(d, ad, bd, tc::idesc_bf16(kBM, kBN, A_MN, B_MN), !first || kk > 0 ? 1u : 0u);
+                    uint32_t more = 0;
+                    for (int i = 0; i < n; i += 2) {
+                        const int s1 = stage + 1 == kStages ? 0 : stage + 1;
+                        const uint32_t p1 = stage + 1 == kStages ? ph ^ 1u : ph;
+                        const bool two = i + 1 < n;
+                        if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
+                        if (two && !tc::mbar_wait(full_bar(s1), p1, st, tmo, kSiteMmaFull)) { ok = false; break; }
+                        tc::fence_after_sync();
+                        mma4(d, stage, more);
+                        more = 1;
+                        tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
+                        stage = s1; ph = p1;
+                        if (two) {
+                            mma4(d, stage, 1);
+                            tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
+                            if (++stage == kStages) { stage = 0; ph ^= 1u; }
+                        }
                     }
                     issued = true;
-                    tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
-                    if (++stage == kStages) { stage = 0; ph ^= 1u; }
-                    if (kb + 1 == kb1 || (kb + 1 - kb0) % kSumBlocks == 0) {
-                        tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
-                        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
-                    }
+                    if (!ok) break;
+                    tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
+                    if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
                 }
             }
             if (!ok && issued) {
@@ -270,21 +348,145 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
         }
     } else {
-        const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quadrant, 128-column half of the tile
+        if (p.early) pdl_wait();
+        const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quadrant, half of the tile's columns
+        const int cols = p.bn / 2;
+        // 32 rows x 128 bytes are put down by row (a thread each) and taken up by eighths of a row, so that a
+        // store instruction writes four whole 128-byte lines (a thread writing its own row touches 32 lines with
+        // each)
+        const uint32_t pass = smem_base + kStageOutOffset + (uint32_t)(warp - 2) * kPassBytes;
+        auto put = [&](int eighth, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            tc::st_shared_v4(pass + lane * 128 + ((eighth ^ (lane & 7)) << 4), a, b, c, d);
+        };
+        auto take = [&](int i0, auto& v) {     // rows 4i + lane / 8 from i = i0 on, eighth lane % 8
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(v) / sizeof(uint4)); ++i) {
+                const int row = 4 * (i0 + i) + (lane >> 3);
+                v[i] = ld_shared16(pass + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            }
+        };
         int acc = 0;
         uint32_t acc_ph = 0;
         for (int g = gstart; g < total; g += gstep) {
             const Tile t = head_tile(g, mt, nt, p.group);
             const int blocks = k_first(t.split + 1) - k_first(t.split);
-            float r[4][32];
+            const int row0 = t.m * kBM + rank * 128 + q * 32, row = row0 + lane;
+            const int col0 = t.n * p.bn + half * cols;
+            const int nv = min(cols, p.N - col0);         // valid columns; none: <= 0
+            const bool in = row < M;
+            // what belongs to the row, fetched while the tile is being summed
+            int lab = -1;                                 // its label
+            float mul = 0.f, base = 0.f;
+            int orow = in ? row : -1;                     // its output row
+            bool dead = false;
+            if constexpr (EPI != kEpiOut) {
+                if (in) {
+                    const int64_t tok = p.rows && !all ? p.rows[row] : row;
+                    const int64_t y = label_at(p.labels, p.labels_i64, tok);
+                    if (y >= 0 && y < p.N) lab = (int)y;
+                    if (EPI == kEpiDl && lab >= 0) {
+                        mul = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
+                        base = -kLog2e * __ldg(p.lse + tok);
+                    }
+                }
+            } else {
+                if (in && p.out_rows && !all) orow = p.out_rows[row];
+                dead = p.zero_dead && in && !is_live(p.labels, p.labels_i64, row, p.live_below);
+            }
             __syncwarp();
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * cols);
+            if constexpr (EPI == kEpiOut) {
+                // 64 columns at a time: tensor memory, registers, staging, memory
+                if (blocks > 0) {
+                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) break;
+                    __syncwarp();
+                    tc::fence_after_sync();
+                }
+                const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
+                const int64_t at = t.split * p.split_stride + col0;
+                int o[8];                           // output rows of this lane's eighths
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float r[2][32];
+                    if (blocks > 0) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tc::tmem_ld_32x32b_x32(tbase + 64 * h + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
+                        tc::tmem_ld_wait();
+                        if (h == 1) {
+                            tc::fence_before_sync();
+                            mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
+                            if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[c][i] = 0.f;
+                    }
+                    if (64 * h >= nv) continue;
+                    uint4 v[8];
+                    if (!p.out_f32 && !p.add) {
+#pragma unroll
+                        for (int e8 = 0; e8 < 8; ++e8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = 8 * e8 + 2 * i;
+                                w[i] = dead ? 0u : pack_bf16x2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                            }
+                            put(e8, w[0], w[1], w[2], w[3]);
+                        }
+                        __syncwarp();
+                        take(0, v);
+                        const int cc = 64 * h + 8 * (lane & 7);
+                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + at + cc;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (o[i] >= 0 && cc < nv) *reinterpret_cast<uint4*>(to + (int64_t)o[i] * p.N) = v[i];
+                        __syncwarp();
+                        continue;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {      // 32 fp32 columns, 128 bytes of a row
+                        const int cc = 64 * h + 32 * c + 4 * (lane & 7);
+#pragma unroll
+                        for (int e8 = 0; e8 < 8; ++e8)
+                            put(e8, __float_as_uint(r[c][4 * e8]), __float_as_uint(r[c][4 * e8 + 1]),
+                                __float_as_uint(r[c][4 * e8 + 2]), __float_as_uint(r[c][4 * e8 + 3]));
+                        __syncwarp();
+                        take(0, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (o[i] < 0 || cc >= nv) continue;
+                            const int64_t to = at + (int64_t)o[i] * p.N + cc;
+                            float4 f = make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y),
+                                                   __uint_as_float(v[i].z), __uint_as_float(v[i].w));
+                            if (p.add) {
+                                const float4 g4 = *reinterpret_cast<const float4*>(p.add + to);
+                                f.x += g4.x; f.y += g4.y; f.z += g4.z; f.w += g4.w;
+                            }
+                            if (p.out_f32)
+                                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = f;
+                            else
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) =
+                                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                        }
+                        __syncwarp();
+                    }
+                }
+                continue;
+            } else {
+            float r[4][32];
             bool ok = true;
             for (int b0 = 0; b0 < blocks; b0 += min(kSumBlocks, blocks - b0)) {
                 if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
                 __syncwarp();
                 tc::fence_after_sync();
-                const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kBN + half * 128);
-                if (EPI == kEpiOut || b0 == 0) {
+                const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
+                if (b0 == 0) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         tc::tmem_ld_32x32b_x32(tbase + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
@@ -300,157 +502,96 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                 }
                 tc::fence_before_sync();
-                tc::mbar_arrive_cluster(tc::mapa_shared(acce_bar(acc), 0));
+                mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
                 if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
             }
             if (!ok) break;
-            if (blocks == 0) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[c][i] = 0.f;
-            }
-            const int row = t.m * kBM + rank * 128 + q * 32 + lane;
-            const int col0 = t.n * kBN + half * 128;
-            const int nv = min(128, p.N - col0);          // valid columns; none: <= 0
-            if constexpr (EPI == kEpiStats || EPI == kEpiExp) {
-                if (EPI == kEpiExp && row >= M && nv > 0) {
-                    // rows behind the last live token are zeros: dW's last K block reads them
-                    __nv_bfloat16* o = p.dl + (int64_t)row * p.ld_dl + col0;
-                    const uint32_t z[8] = {};
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (16 * c < nv) tc::stg_v8(o + 16 * c, z);
-                }
-                if (row < M && nv > 0) {
-                    const int64_t tok = p.rows && !all ? p.rows[row] : row;
-                    int64_t lab = label_at(p.labels, p.labels_i64, tok);
-                    if (lab < 0 || lab >= p.N) lab = -1;
-                    const int lc = lab >= col0 && lab < col0 + nv ? (int)(lab - col0) : -1;
+            if (nv <= 0) continue;
+            {
+                const int lc = lab >= col0 && lab < col0 + nv ? lab - col0 : -1;
+                if constexpr (EPI != kEpiDl) {
                     if (nv < 128) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i < nv ? r[c][i] : -INFINITY;
                     }
-                    float mx = -INFINITY;
+                    mul = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, r[c][i]);
-                    const float base = kRootShift - (mx == -INFINITY ? 0.f : mx * (0.5f * kLog2e));
+                        for (int i = 0; i < 32; ++i) mul = fmaxf(mul, r[c][i]);
+                    base = kRootShift - (mul == -INFINITY ? 0.f : mul * (0.5f * kLog2e));
                     // the label's own term stays out of the sum, so that the others' share keeps its
                     // digits where the label takes nearly everything
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (EPI == kEpiStats) {
+                    if (__any_sync(0xffffffffu, lc >= 0)) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float e = exp2_approx(fmaf(r[c][i], 0.5f * kLog2e, base));
-                                s[c] = 32 * c + i == lc ? s[c] : fmaf(e, e, s[c]);
+                            for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i == lc ? -INFINITY : r[c][i];
+                    }
+                }
+                float2 s[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {      // 64 columns, 128 bytes of a row
+                    if (64 * h >= nv) break;
+#pragma unroll
+                    for (int e8 = 0; e8 < 8; ++e8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            constexpr float kFactor = EPI == kEpiDl ? kLog2e : 0.5f * kLog2e;
+                            const int j = 64 * h + 8 * e8 + 2 * i;
+                            float2 v = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                            v = __ffma2_rn(v, make_float2(kFactor, kFactor), make_float2(base, base));
+                            v = make_float2(exp2_approx(v.x), exp2_approx(v.y));
+                            if constexpr (EPI == kEpiDl) {
+                                v = __fmul2_rn(v, make_float2(mul, mul));
+                                w[i] = lab >= 0 ? pack_bf16x2(v.x, v.y) : 0u;
+                            } else {
+                                s[j / 32] = __ffma2_rn(v, v, s[j / 32]);
+                                const __half2 v2 = __float22half2_rn(v);
+                                w[i] = in ? *reinterpret_cast<const uint32_t*>(&v2) : 0u;
                             }
-                    } else {
-                        // relative to the 128 columns' largest: head_dl_kernel makes dl of them
-                        __nv_bfloat16* o = p.dl + (int64_t)row * p.ld_dl + col0;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (16 * c >= nv) break;
-                            uint32_t w[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float e[2];
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int j = 16 * c + 2 * i + h;
-                                    e[h] = exp2_approx(fmaf(r[j / 32][j % 32], 0.5f * kLog2e, base));
-                                    s[c / 2] = j == lc ? s[c / 2] : fmaf(e[h], e[h], s[c / 2]);
-                                }
-                                const __half2 v = __floats2half2_rn(e[0], e[1]);
-                                w[i] = *reinterpret_cast<const uint32_t*>(&v);
-                            }
-                            tc::stg_v8(o + 16 * c, w);
                         }
+                        if (EPI != kEpiStats) put(e8, w[0], w[1], w[2], w[3]);
                     }
-                    if (lc >= 0) {
-                        float own = 0.f;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) own = 32 * c + i == lc ? r[c][i] : own;
-                        p.label_logit[row] = own;
-                    }
-                    const float sum = ((s[0] + s[1]) + (s[2] + s[3])) * kRootScale;
-                    p.stats[(int64_t)row * p.stat_tiles + col0 / kStatCols] = make_float2(mx, sum);
-                }
-            } else if constexpr (EPI == kEpiDl) {
-                if (nv > 0) {
-                    float coef = 0.f, base = 0.f;
-                    int lc = -1;
-                    // rows behind the last live token are zeros: dW's last K block reads them
-                    const bool in = row < M;
-                    if (in) {
-                        const int64_t tok = p.rows && !all ? p.rows[row] : row;
-                        const int64_t lab = label_at(p.labels, p.labels_i64, tok);
-                        coef = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
-                        base = __ldg(p.lse + tok);
-                        lc = lab >= col0 && lab < col0 + nv ? (int)(lab - col0) : -1;
-                    }
-                    __nv_bfloat16* o = p.dl + (int64_t)row * p.ld_dl + col0;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (32 * c >= nv) break;
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float v[2];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                v[h] = in ? coef * exp2_approx((r[c][2 * i + h] - base) * kLog2e) : 0.f;
-                            w[i] = pack_bf16x2(v[0], v[1]);
+                    if constexpr (EPI != kEpiStats) {
+                        if (EPI == kEpiDl && lc >= 64 * h && lc < 64 * h + 64) {
+                            const int j = lc - 64 * h;
+                            const float at = __ldcg(p.label_logit + row) - __ldg(p.lse + (p.rows && !all ? p.rows[row] : row));
+                            st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
+                                        __float2bfloat16_rn(mul * expm1f(at)));
                         }
-                        tc::stg_v8(o + 32 * c, w);
-                        tc::stg_v8(o + 32 * c + 16, w + 8);
-                    }
-                    if (lc >= 0) {
-                        float own = 0.f;
+                        __syncwarp();
+                        // rows behind the last live token, up to the tile's end, are zeros where the live ones are
+                        // counted on the device: dW's last K block reads some of them
+                        const int row_end = p.m_live ? 1 << 30 : M;
+                        const int cc = 64 * h + 8 * (lane & 7);
+                        __nv_bfloat16* o = p.dl + (int64_t)(row0 + (lane >> 3)) * p.ld_dl + col0 + cc;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int i0 = 0; i0 < 8; i0 += 4) {
+                            uint4 v[4];
+                            take(i0, v);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) own = 32 * c + i == lc ? r[c][i] : own;
-                        o[lc] = __float2bfloat16_rn(coef * expm1f(own - base));
+                            for (int i = 0; i < 4; ++i)
+                                if (row0 + 4 * (i0 + i) + (lane >> 3) < row_end && cc < nv)
+                                    *reinterpret_cast<uint4*>(o + 4 * (i0 + i) * p.ld_dl) = v[i];
+                        }
+                        __syncwarp();
                     }
                 }
-            } else {
-                if (row < M && nv > 0) {
-                    const int64_t orow = p.out_rows && !all ? p.out_rows[row] : row;
-                    const int64_t at = t.split * p.split_stride + orow * p.N + col0;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {     // N is a multiple of 8
-                        if (8 * c >= nv) break;
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = r[c / 4][8 * (c % 4) + i];
-                        if (p.add) {
-                            const float4 a = *reinterpret_cast<const float4*>(p.add + at + 8 * c);
-                            const float4 b = *reinterpret_cast<const float4*>(p.add + at + 8 * c + 4);
-                            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-                        }
-                        if (p.out_f32) {
-                            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + 8 * c);
-                            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-                        } else {
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at + 8 * c) =
-                                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                           pack_bf16x2(v[6], v[7]));
-                        }
-                    }
+                if (EPI != kEpiDl && in) {
+                    const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
+                    p.stats[(int64_t)row * p.stat_tiles + col0 / cols] = make_float2(mul, sum * kRootScale);
                 }
+            }
             }
         }
     }
+    if (p.wait_late && threadIdx.x == 0) pdl_wait();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -460,42 +601,87 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
 // ------------------------------------------------------------------ live tokens
 
-constexpr int kPrepThreads = 256;
+constexpr int kRowThreads = 256;
 
-__device__ __forceinline__ bool is_live(const void* labels, int i64, int64_t t, int V) {
-    const int64_t y = label_at(labels, i64, t);
-    return y >= 0 && y < V;
+// Sum over the CTA's threads (whole warps), the same in each; red holds 33 floats.
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < (int)blockDim.x / 32 ? red[lane] : 0.f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
 }
 
-// CTA b takes `per` tokens: live ones get the next place (tokens in order), their
-// rows are copied there unless every token is live, the others' outputs are zeroed.
-// Each CTA counts the live tokens before its own from the labels themselves.
-// Behind the last live row, rows up to the next multiple of kBK are zeroed: dW's
-// last K block reads them. The first CTA clears the status block.
-__global__ void __launch_bounds__(kPrepThreads)
-head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const void* labels, int i64, int T, int V, int nv, int per,
-                 int32_t* __restrict__ rows, int32_t* __restrict__ live, uint4* __restrict__ xc,
-                 float* loss, float* lse, uint4* dx, int32_t* status) {
-    __shared__ int32_t sh[3];
-    __shared__ int32_t place[kPrepThreads];
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float s) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(bf16_hi(u[i]), bf16_hi(v[i]), fmaf(bf16_lo(u[i]), bf16_lo(v[i]), s));
+    return s;
+}
+
+// A label's logit in fp32 by this thread's vectors (id of n): the tensor cores' sums
+// are cut, and the loss of a well-predicted token is a small difference to this one.
+__device__ __forceinline__ float label_dot(const uint4* x, const uint4* w, int nv, int id, int n) {
+    float s = 0.f;
+    for (int v = id; v < nv; v += n) s = dot8(__ldg(x + v), __ldg(w + v), s);
+    return s;
+}
+
+// For up to one row tile of tokens: a CTA per token copies its row, zeros for a token
+// without a label, for dW (whose K the tokens are), and forms the label's logit if
+// asked. The first CTA clears the status block. Without xc: that alone.
+__global__ void __launch_bounds__(kRowThreads)
+head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
+                  int V, int nv, uint4* __restrict__ xc, float* label_logit, int32_t* status) {
+    __shared__ float red[33];
     pdl_wait();
     pdl_allow_next();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int t0 = blockIdx.x * per, t1 = min(t0 + per, T);
+    const int64_t t = blockIdx.x;
+    if (t == 0 && status && threadIdx.x < kStatusBytes / 4) status[threadIdx.x] = 0;
+    if (!xc) return;
+    const bool on = is_live(labels, i64, t, V);
+    for (int v = threadIdx.x; v < nv; v += kRowThreads)
+        xc[t * nv + v] = on ? __ldg(x + t * ldx + v) : make_uint4(0, 0, 0, 0);
+    if (label_logit && on) {
+        const float s = cta_sum(label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, threadIdx.x, kRowThreads), red);
+        if (threadIdx.x == 0) label_logit[t] = s;
+    }
+}
+
+// For more tokens. CTA b takes kPrepTokens of every `span` tokens from b * span on:
+// live ones get the next place (tokens in order), their rows are copied there unless
+// every token is live, the others' outputs are zeroed; the labels' logits are formed if
+// asked, a warp a token. Each CTA counts the live tokens before its own from the labels
+// themselves. Behind the last live row, rows up to the next multiple of kBK are zeroed:
+// dW's last K block reads them. The first CTA clears the status block.
+constexpr int kPrepTokens = 8;
+__global__ void __launch_bounds__(kRowThreads)
+head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
+                 int T, int V, int nv, int span, int32_t* __restrict__ rows, int32_t* __restrict__ live,
+                 uint4* __restrict__ xc, float* __restrict__ label_logit, float* loss, float* lse, uint4* dx,
+                 int32_t* status) {
+    __shared__ int32_t sh[2];
+    __shared__ int32_t place[kPrepTokens];
+    pdl_wait();
+    pdl_allow_next();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int t0 = blockIdx.x * span, t1 = min(t0 + span, T);
     if (tid < 2) sh[tid] = 0;
     if (blockIdx.x == 0 && status && tid < kStatusBytes / 4) status[tid] = 0;
     __syncthreads();
     int before = 0, count = 0;
-    for (int t = tid; t < T; t += kPrepThreads) {
+#pragma unroll 8
+    for (int t = tid; t < T; t += kRowThreads) {
         const int l = is_live(labels, i64, t, V) ? 1 : 0;
         count += l;
         before += t < t0 ? l : 0;
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, d);
-        count += __shfl_xor_sync(0xffffffffu, count, d);
-    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) {
         atomicAdd(&sh[0], before);
         atomicAdd(&sh[1], count);
@@ -505,43 +691,59 @@ head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const void* labels, i
     int next = sh[0];
     if (blockIdx.x == 0 && tid == 0) *live = total;
     const bool all = total == T;
-    for (int c0 = t0; c0 < t1; c0 += 32) {
-        // places of 32 tokens
+    for (int c0 = t0; c0 < t1; c0 += kPrepTokens) {
+        const int n = min(kPrepTokens, t1 - c0);
+        const bool l = lane < n && is_live(labels, i64, c0 + lane, V);
+        const unsigned b = __ballot_sync(0xffffffffu, l);
         __syncthreads();
-        if (tid < 32) {
-            const int t = c0 + lane;
-            const bool l = t < t1 && is_live(labels, i64, t, V);
-            const unsigned b = __ballot_sync(0xffffffffu, l);
-            place[lane] = l ? next + __popc(b & ((1u << lane) - 1)) : -1;
-            if (lane == 0) sh[2] = __popc(b);
-        }
-        __syncthreads();
-        next += sh[2];
-        for (int j = 0; j < 32 && c0 + j < t1; ++j) {
-            const int64_t t = c0 + j;
-            const int to = place[j];
-            if (to >= 0) {
-                if (tid == 0) rows[to] = (int32_t)t;
-                if (!all)
-                    for (int v = tid; v < nv; v += kPrepThreads) xc[(int64_t)to * nv + v] = __ldg(x + t * ldx + v);
+        if (warp == 0 && lane < n) {
+            const int to = l ? next + __popc(b & ((1u << lane) - 1)) : -1;
+            place[lane] = to;
+            if (l) {
+                rows[to] = c0 + lane;
             } else {
-                if (tid == 0 && loss) loss[t] = 0.f;
-                if (tid == 0 && lse) lse[t] = 0.f;
-                if (dx)
-                    for (int v = tid; v < nv; v += kPrepThreads) dx[t * nv + v] = make_uint4(0, 0, 0, 0);
+                if (loss) loss[c0 + lane] = 0.f;
+                if (lse) lse[c0 + lane] = 0.f;
             }
+        }
+        next += __popc(b);
+        __syncthreads();
+        // the rows' vectors in one run, four loads of a thread in flight
+        for (int i0 = tid; i0 < n * nv; i0 += 4 * kRowThreads) {
+            uint4 a[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kRowThreads;
+                if (!all && i < n * nv) a[u] = __ldg(x + (int64_t)(c0 + i / nv) * ldx + i % nv);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kRowThreads;
+                if (i >= n * nv) continue;
+                const int j = i / nv, v = i % nv, to = place[j];
+                if (to < 0) {
+                    if (dx) dx[(int64_t)(c0 + j) * nv + v] = make_uint4(0, 0, 0, 0);
+                } else if (!all) {
+                    xc[(int64_t)to * nv + v] = a[u];
+                }
+            }
+        }
+        if (label_logit && warp < n && place[warp] >= 0) {
+            const int64_t t = c0 + warp;
+            float s = label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, lane, 32);
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane == 0) label_logit[place[warp]] = s;
         }
     }
     if (!all && t1 == T) {
         const int end = (total + kBK - 1) / kBK * kBK;
-        for (int64_t v = (int64_t)total * nv + tid; v < (int64_t)end * nv; v += kPrepThreads)
+        for (int64_t v = (int64_t)total * nv + tid; v < (int64_t)end * nv; v += kRowThreads)
             xc[v] = make_uint4(0, 0, 0, 0);
     }
 }
 
 // ------------------------------------------------------------------ log-sum and loss
-
-constexpr int kRowThreads = 256;
 
 // The sums of a row's stat tiles joined: the largest logit, the other tokens' sum
 // relative to it and the label's term.
@@ -550,8 +752,8 @@ struct RowSum {
 };
 __device__ __forceinline__ RowSum join_row(const float2* stats, int n, float label_logit, float* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) m = fmaxf(m, stats[i].x);
+    float m = label_logit;   // at its place in the order, if the tiles' own is a little lower
+    for (int i = threadIdx.x; i < n; i += kRowThreads) m = fmaxf(m, __ldcg(stats + i).x);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (lane == 0) red[warp] = m;
@@ -562,16 +764,10 @@ __device__ __forceinline__ RowSum join_row(const float2* stats, int n, float lab
     const float base = m == -INFINITY ? 0.f : m;
     float s = 0.f;
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const float2 v = stats[i];
+        const float2 v = __ldcg(stats + i);
         s += v.y * exp2_approx((v.x == -INFINITY ? -INFINITY : v.x - base) * kLog2e);
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) red[32 + warp] = s;
-    __syncthreads();
-    s = lane < kRowThreads / 32 ? red[32 + lane] : 0.f;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    s = cta_sum(s, red + 32);
     RowSum r;
     r.top = base;
     r.others = s;
@@ -579,50 +775,76 @@ __device__ __forceinline__ RowSum join_row(const float2* stats, int n, float lab
     return r;
 }
 
-// A CTA per live token.
+// log(others + own) - log(own), by the form that loses no digits.
+__device__ __forceinline__ float row_loss(const RowSum& r, float label_logit) {
+    return r.own > r.others ? log1pf(r.others / r.own) : logf(r.others + r.own) - (label_logit - r.top);
+}
+
+// A CTA per live token. The label's logit is formed while the logits' kernel still
+// runs: x, W and labels are the caller's and the list of live tokens is the kernel's
+// before that one, all complete before that one began.
 __global__ void __launch_bounds__(kRowThreads)
-head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const float* __restrict__ label_logit,
-                 const int32_t* __restrict__ rows, const int32_t* __restrict__ live, const void* labels, int i64, int V,
-                 float* loss, float* lse) {
-    __shared__ float red[64];
-    pdl_wait();
+head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
+                 const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
+                 const void* labels, int i64, int V, float* loss, float* lse) {
+    __shared__ float red[128];
     pdl_allow_next();
     const int i = blockIdx.x;
-    if (live && i >= *live) return;
+    if (live && i >= *live) {
+        pdl_wait();   // this kernel ends after the one ahead
+        return;
+    }
     const int64_t t = rows ? rows[i] : i;
-    const bool on = rows || is_live(labels, i64, t, V);
-    const RowSum r = join_row(stats + (int64_t)i * stat_tiles, stat_tiles, on ? label_logit[i] : 0.f, red);
+    const bool on = is_live(labels, i64, t, V);
+    float own = 0.f;
+    if (on) own = cta_sum(label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, threadIdx.x, kRowThreads), red + 96);
+    pdl_wait();
+    const RowSum r = join_row(stats + (int64_t)i * stat_tiles, stat_tiles, on ? own : -INFINITY, red);
     if (threadIdx.x != 0) return;
-    // log(others + own) - log(own), by the form that loses no digits
-    const float at = label_logit[i] - r.top;
-    const float l = r.own > r.others ? log1pf(r.others / r.own) : logf(r.others + r.own) - at;
-    if (loss) loss[t] = on ? l : 0.f;
+    loss[t] = on ? row_loss(r, own) : 0.f;
     if (lse) lse[t] = on ? r.top + logf(r.others + r.own) : 0.f;
 }
 
 // The same with a gradient: then the row's exponentials, in their place, become
-//   dl[v] = c e[v] exp(top of its 128 columns - lse),   dl[label] = -c others / (others + own)
+//   dl[v] = c e[v] exp(top of its columns - lse),   dl[label] = -c others / (others + own)
+// and zeros for a token without a label (rows == NULL; else only live tokens are here).
 __global__ void __launch_bounds__(kRowThreads)
-head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const float* __restrict__ label_logit,
-               const int32_t* __restrict__ rows, const int32_t* __restrict__ live, const void* labels, int i64,
-               const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld, int V, float* loss,
-               float* lse) {
-    __shared__ float red[64];
-    pdl_wait();
+head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, const uint4* __restrict__ x, int64_t ldx,
+               const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
+               const void* labels, int i64, const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld,
+               int V, float* loss, float* lse) {
+    __shared__ float red[128];
     pdl_allow_next();
     const int i = blockIdx.x;
-    if (i >= *live) return;
-    const int64_t t = rows[i];
-    const float2* st = stats + (int64_t)i * stat_tiles;
-    const RowSum r = join_row(st, stat_tiles, label_logit[i], red);
-    const float sum = r.others + r.own, log_sum = r.top + logf(sum);
-    const float coef = scale * (dloss ? dloss[t] : 1.0f);
-    const int label = (int)label_at(labels, i64, t);
+    if (live && i >= *live) {
+        pdl_wait();
+        return;
+    }
+    const int64_t t = rows ? rows[i] : i;
+    const bool on = is_live(labels, i64, t, V);
+    const int label = on ? (int)label_at(labels, i64, t) : 0;
+    float own = 0.f;
+    if (on) own = cta_sum(label_dot(x + t * ldx, W + (int64_t)label * nv, nv, threadIdx.x, kRowThreads), red + 96);
+    pdl_wait();
     __nv_bfloat16* row = dl + i * ld;
+    if (!on) {
+        for (int v = 8 * threadIdx.x; v < V; v += 8 * kRowThreads) *reinterpret_cast<uint4*>(row + v) = make_uint4(0, 0, 0, 0);
+        if (threadIdx.x == 0) {
+            loss[t] = 0.f;
+            if (lse) lse[t] = 0.f;
+        }
+        return;
+    }
+    const float2* st = stats + (int64_t)i * stat_tiles;
+    const RowSum r = join_row(st, stat_tiles, own, red);
+    const float sum = r.others + r.own;
+    const float coef = scale * (dloss ? dloss[t] : 1.0f);
     const float inv = coef / sum * kRootScale;
-    for (int v = 8 * threadIdx.x; v < V; v += 8 * kRowThreads) {
-        const uint4 e = *reinterpret_cast<const uint4*>(row + v);
-        const float f = inv * exp2_approx((st[v / kStatCols].x - r.top) * kLog2e);
+    const int tile = stat_cols / 8;
+#pragma unroll 4
+    for (int v = threadIdx.x; 8 * v < V; v += kRowThreads) {
+        const uint4 e = __ldcg(reinterpret_cast<const uint4*>(row + 8 * v));
+        const float f = inv * exp2_approx((__ldcg(st + v / tile).x - r.top) * kLog2e);
         const uint32_t w[4] = {e.x, e.y, e.z, e.w};
         uint32_t o[4];
 #pragma unroll
@@ -630,34 +852,36 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const float* __
             const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
             o[j] = pack_bf16x2(a.x * f * a.x, a.y * f * a.y);
         }
-        *reinterpret_cast<uint4*>(row + v) = make_uint4(o[0], o[1], o[2], o[3]);
-        if (label >= v && label < v + 8) row[label] = __float2bfloat16_rn(-coef * (r.others / sum));
+        *reinterpret_cast<uint4*>(row + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (label >> 3 == v) row[label] = __float2bfloat16_rn(-coef * (r.others / sum));
     }
     if (threadIdx.x != 0) return;
-    const float at = label_logit[i] - r.top;
-    loss[t] = r.own > r.others ? log1pf(r.others / r.own) : logf(sum) - at;
-    if (lse) lse[t] = log_sum;
+    loss[t] = row_loss(r, own);
+    if (lse) lse[t] = r.top + logf(sum);
 }
 
-// dx rows from the parts of K, added up in order.
+// dx rows from the parts of K, added up in order, four columns a thread; without a
+// list of rows, a token without a label gets zeros.
 __global__ void __launch_bounds__(256)
-head_join_kernel(const float* __restrict__ part, int64_t stride, int splits, int nv, const int32_t* __restrict__ rows,
-                 const int32_t* __restrict__ live, __nv_bfloat16* __restrict__ dx) {
+head_join_kernel(const float4* __restrict__ part, int64_t stride, int splits, int nq, const int32_t* __restrict__ rows,
+                 const int32_t* __restrict__ live, const void* labels, int i64, int V, uint2* __restrict__ dx) {
     pdl_wait();
     pdl_allow_next();
     const int64_t i = blockIdx.x;
-    if (i >= *live) return;
-    const int64_t t = rows[i];
-    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nv; v += gridDim.y * blockDim.x) {
-        float a[8] = {};
-        for (int s = 0; s < splits; ++s) {
-            const float4* q = reinterpret_cast<const float4*>(part + s * stride + (i * nv + v) * 8);
-            const float4 b = q[0], c = q[1];
-            a[0] += b.x; a[1] += b.y; a[2] += b.z; a[3] += b.w;
-            a[4] += c.x; a[5] += c.y; a[6] += c.z; a[7] += c.w;
+    if (live && i >= *live) return;
+    const int64_t t = rows ? rows[i] : i;
+    const bool on = rows || is_live(labels, i64, t, V);
+    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nq; v += gridDim.y * blockDim.x) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
+            const float4* q = part + i * nq + v;
+#pragma unroll 8
+            for (int s = 0; s < splits; ++s) {
+                const float4 b = __ldcg(q + s * stride);
+                a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+            }
         }
-        *reinterpret_cast<uint4*>(dx + (t * nv + v) * 8) = make_uint4(
-            pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+        dx[t * nq + v] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
     }
 }
 
@@ -707,10 +931,23 @@ int resident_pairs(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, HeadGemm)
     return std::min(n, num_sms / 2);
 }
 
+// What a product reads.
+struct Operand {
+    const void* base;
+    int64_t rows, cols, ld;
+};
 
+// One product. `all`: the operand that replaces A (logits) or B (dW) when every token is
+// live. Boxes: 64 columns x 64 rows of K where the operand is MN-major, else a CTA's rows.
 template <bool A_MN, bool B_MN, int EPI>
-cudaError_t run_head_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& all, HeadGemm& p, int num_sms,
+cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all, const HeadGemm& p, int num_sms,
                           cudaStream_t s) {
+    const int box_a = A_MN ? kBK : 128, box_b = B_MN ? kBK : p.bn / 2;
+    CUtensorMap ta, tb, tall;
+    if (!make_tmap_pitch(&ta, a.base, a.rows, a.cols, a.ld, box_a) ||
+        !make_tmap_pitch(&tb, b.base, b.rows, b.cols, b.ld, box_b) ||
+        !make_tmap_pitch(&tall, all.base, all.rows, all.cols, all.ld, EPI == kEpiOut ? box_b : box_a))
+        return cudaErrorInvalidValue;
     auto kern = head_gemm_kernel<A_MN, B_MN, EPI>;
     ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
     cudaLaunchConfig_t cfg = {};
@@ -724,21 +961,37 @@ cudaError_t run_head_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
-    const int64_t tiles = (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, kBN) * p.splits;
+    const int64_t tiles = (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, p.bn) * p.splits;
     const int pairs = (int)std::min<int64_t>(tiles, resident_pairs<A_MN, B_MN, EPI>(kern, cfg, num_sms));
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3(2 * pairs);
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a, b, all, p);
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tall, p);
 }
 
 constexpr int kGroup = 16;              // row tiles of the walk's groups
 constexpr int64_t kPieceBytes = (int64_t)4 << 30;
 constexpr int kPieceMax = 65536;
-// Logits without a gradient: up to one row tile, ignored tokens save nothing.
+// Up to one row tile, ignored tokens cost no products: nothing is gathered then.
 constexpr int kPlainRows = kBM;
+
+// Columns of the logits' tiles: the width whose rounds over all pairs load the least
+// (a K block of a tile brings 256 rows of x and bn of W to a pair).
+int logit_columns(int tokens, int V, int pairs) {
+    int best = kBN;
+    int64_t least = 0;
+    for (int bn = kBN; bn >= 128; bn -= 32) {
+        const int64_t tiles = (int64_t)ceil_div(tokens, kBM) * ceil_div(V, bn);
+        const int64_t cost = (tiles + pairs - 1) / std::max(pairs, 1) * (kBM + bn);
+        if (bn == kBN || cost < least) {
+            least = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
 
 int64_t pitch_dl(int V) { return align_up(V, 64); }
 
@@ -766,9 +1019,9 @@ struct HeadLayout {
     int piece, splits;
 };
 
-HeadLayout head_layout(int T, int H, int V, bool grad, bool acc, int want, int num_sms) {
+HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
     HeadLayout L{};
-    size_t o = kStatusBytes;
+    size_t o = 1024;   // the status block
     auto take = [&](int64_t bytes) {
         const size_t at = o;
         o += align_up(bytes, 1024);
@@ -777,15 +1030,14 @@ HeadLayout head_layout(int T, int H, int V, bool grad, bool acc, int want, int n
     L.piece = piece_tokens(T, V, want);
     L.splits = grad ? dx_splits(L.piece, H, V, num_sms / 2) : 1;
     const int64_t cap = align_up(L.piece, kBM);
-    o = align_up(o, 1024);
     L.live = take(4);
     L.rows = take(cap * 4);
     L.label = take(cap * 4);
-    L.stats = take(cap * ceil_div(V, kStatCols) * 8);
+    L.stats = take(L.piece * (int64_t)ceil_div(V, 64) * 8);   // tiles of 64 columns at least
     if (grad || T > kPlainRows) L.xc = take(cap * H * 2);
     if (grad) L.dl = take(cap * pitch_dl(V) * 2);
-    if (L.splits > 1) L.part = take((int64_t)L.splits * cap * H * 4);
-    if (acc && L.piece < T) L.acc = take((int64_t)V * H * 4);
+    if (L.splits > 1) L.part = take((int64_t)L.splits * L.piece * H * 4);
+    if (grad && L.piece < T) L.acc = take((int64_t)V * H * 4);
     L.total = o;
     return L;
 }
@@ -793,19 +1045,19 @@ HeadLayout head_layout(int T, int H, int V, bool grad, bool acc, int want, int n
 }  // namespace
 
 size_t head_workspace_bytes(int T, int H, int V, bool grad, int piece, int num_sms) {
-    return head_layout(T, H, V, grad, grad, piece, num_sms).total;
+    return head_layout(T, H, V, grad, piece, num_sms).total;
 }
 
 cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s) {
     const int T = a.T, H = a.H, V = a.V;
-    const bool grad = a.dx || a.dW;
-    const HeadLayout L = head_layout(T, H, V, grad, grad, a.piece, c.num_sms);
+    const bool grad = a.dx || a.dW, forward = a.loss != nullptr;
+    const HeadLayout L = head_layout(T, H, V, grad, a.piece, c.num_sms);
     char* ws = static_cast<char*>(a.workspace);
-    int32_t* live = reinterpret_cast<int32_t*>(ws + L.live);
-    int32_t* rows = reinterpret_cast<int32_t*>(ws + L.rows);
-    float* label = reinterpret_cast<float*>(ws + L.label);
     float2* stats = reinterpret_cast<float2*>(ws + L.stats);
-    const int stat_tiles = ceil_div(V, kStatCols);
+    float* label = reinterpret_cast<float*>(ws + L.label);
+    uint4* xc = reinterpret_cast<uint4*>(ws + L.xc);
+    __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(ws + L.dl);
+    const uint4* W = static_cast<const uint4*>(a.W);
     const int nv = H / 8;
     cudaError_t e = cudaSuccess;
     if (T == 0) {
@@ -814,113 +1066,125 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             e = cudaMemsetAsync(a.dW, 0, (size_t)V * H * (a.dW_f32 ? 4 : 2), s);
         return e;
     }
-    const int label_bytes = a.labels_i64 ? 8 : 4;
-    for (int t0 = 0; t0 < T && e == cudaSuccess; t0 += L.piece) {
+    for (int t0 = 0; t0 < T; t0 += L.piece) {
         const int n = std::min(L.piece, T - t0);
         const int64_t cap = align_up(n, kBM);
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t0 * a.ldx;
-        const void* labels = static_cast<const char*>(a.labels) + (int64_t)t0 * label_bytes;
-        float* loss = a.loss ? a.loss + t0 : nullptr;
+        const void* labels = static_cast<const char*>(a.labels) + (int64_t)t0 * (a.labels_i64 ? 8 : 4);
+        float* loss = forward ? a.loss + t0 : nullptr;
         float* lse = a.lse ? a.lse + t0 : nullptr;
+        const float* dloss = a.dloss ? a.dloss + t0 : nullptr;
         __nv_bfloat16* dx = a.dx ? static_cast<__nv_bfloat16*>(a.dx) + (int64_t)t0 * H : nullptr;
-        const bool gather = grad || T > kPlainRows;
-        const bool forward = a.loss != nullptr;
+        // one row tile (of a call of that size, not of a piece): tokens as they are; more: the live ones gathered
+        const bool gather = T > kPlainRows;
+        int32_t* live = gather ? reinterpret_cast<int32_t*>(ws + L.live) : nullptr;
+        int32_t* rows = gather ? reinterpret_cast<int32_t*>(ws + L.rows) : nullptr;
+        const uint4* xv = reinterpret_cast<const uint4*>(x);
+        float* logit = forward ? nullptr : label;
+        int32_t* status = t0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr;
+        if (gather) {
+            const int span = kPrepTokens * ceil_div(n, kPrepTokens * 1024);
+            e = launch_after(head_prep_kernel, dim3(ceil_div(n, span)), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
+                             a.labels_i64, n, V, nv, span, rows, live, xc, logit, loss, forward ? lse : nullptr,
+                             reinterpret_cast<uint4*>(dx), status);
+        } else {
+            e = launch_after(head_start_kernel, dim3(grad ? n : 1), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
+                             a.labels_i64, V, nv, grad ? xc : nullptr, logit, status);
+        }
+        if (e != cudaSuccess) return e;
         HeadGemm p{};
         p.status = c.status;
         p.timeout_ns = c.timeout_ns;
+        p.live = live;
+        p.rows = rows;
         p.tokens = n;
         p.group = kGroup;
         p.splits = 1;
         p.labels = labels;
         p.labels_i64 = a.labels_i64;
+        p.label_logit = label;
         p.scale = a.scale;
-        CUtensorMap tx, txc, tw, tdl;
-        if (!make_tmap_pitch(&tx, x, n, H, a.ldx, 128) || !make_tmap_pitch(&tw, a.W, V, H, H, 128)) return cudaErrorInvalidValue;
-        txc = tx;
-        if (gather) {
-            const int per = std::max(8, ceil_div(n, 1024));
-            e = launch_after(head_prep_kernel, dim3(ceil_div(n, per)), dim3(kPrepThreads), 0, s,
-                             reinterpret_cast<const uint4*>(x), a.ldx / 8, labels, a.labels_i64, n, V, nv, per, rows, live,
-                             reinterpret_cast<uint4*>(ws + L.xc), forward ? loss : nullptr,
-                             forward ? lse : nullptr, reinterpret_cast<uint4*>(dx),
-                             t0 == 0 ? reinterpret_cast<int32_t*>(ws) : nullptr);
-            if (!make_tmap_pitch(&txc, ws + L.xc, cap, H, H, 128)) return cudaErrorInvalidValue;
-            p.live = live;
-            p.rows = rows;
-            p.m_live = 1;
-        } else {
-            e = cudaMemsetAsync(ws, 0, kStatusBytes, s);
-        }
-        if (e != cudaSuccess) break;
+        p.lse = lse;
+        p.dloss = dloss;
+        p.stats = stats;
+        p.dl = dl;
+        p.ld_dl = pitch_dl(V);
         p.M = n;
+        p.m_live = gather;
         p.N = V;
         p.K = H;
-        p.stats = stats;
-        p.stat_tiles = stat_tiles;
-        p.label_logit = label;
+        p.bn = logit_columns(n, V, c.num_sms / 2);
+        p.stat_tiles = ceil_div(V, p.bn / 2);
+        p.early = gather ? kEarlyNone : kEarlyA | kEarlyB;
+        const Operand ox{x, n, H, a.ldx}, ow{a.W, V, H, H};
+        const Operand oxc = gather ? Operand{xc, cap, H, H} : ox;
         if (!grad) {
-            e = run_head_gemm<false, false, kEpiStats>(txc, tw, tx, p, c.num_sms, s);
+            e = run_head_gemm<false, false, kEpiStats>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
-                e = launch_after(head_loss_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, stat_tiles,
-                                 (const float*)label, (const int32_t*)(gather ? rows : nullptr),
-                                 (const int32_t*)(gather ? live : nullptr), labels, a.labels_i64, V, loss, lse);
+                e = launch_after(head_loss_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
+                                 xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live, labels, a.labels_i64, V,
+                                 loss, lse);
+            if (e != cudaSuccess) return e;
             continue;
         }
-        p.dl = reinterpret_cast<__nv_bfloat16*>(ws + L.dl);
-        p.ld_dl = pitch_dl(V);
-        p.lse = lse;
-        p.dloss = a.dloss ? a.dloss + t0 : nullptr;
         if (forward) {
-            e = run_head_gemm<false, false, kEpiExp>(txc, tw, tx, p, c.num_sms, s);
+            e = run_head_gemm<false, false, kEpiExp>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
-                e = launch_after(head_dl_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, stat_tiles,
-                                 (const float*)label, (const int32_t*)rows, (const int32_t*)live, labels, a.labels_i64,
-                                 p.dloss, a.scale, p.dl, p.ld_dl, V, loss, lse);
+                e = launch_after(head_dl_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
+                                 p.bn / 2, xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live, labels,
+                                 a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
         } else {
-            e = run_head_gemm<false, false, kEpiDl>(txc, tw, tx, p, c.num_sms, s);
+            e = run_head_gemm<false, false, kEpiDl>(oxc, ow, ox, p, c.num_sms, s);
         }
-        if (e != cudaSuccess) break;
+        if (e != cudaSuccess) return e;
+        p.bn = kBN;
+        p.early = kEarlyNone;
+        const Operand odl{dl, gather ? cap : n, V, p.ld_dl};
+        const int splits = L.splits;
         if (dx) {
             HeadGemm q = p;
-            CUtensorMap twm;
-            if (!make_tmap_pitch(&tdl, p.dl, cap, V, p.ld_dl, 128) || !make_tmap_pitch(&twm, a.W, V, H, H, 64)) return cudaErrorInvalidValue;
-            q.M = n;
             q.N = H;
             q.K = V;
-            q.splits = L.splits;
-            if (L.splits > 1) {
+            q.splits = splits;
+            q.early = gather ? kEarlyNone : kEarlyB;
+            if (splits > 1) {
                 q.out = ws + L.part;
                 q.out_f32 = 1;
-                q.split_stride = cap * H;
+                q.split_stride = (int64_t)n * H;
             } else {
                 q.out = dx;
                 q.out_rows = rows;
+                q.zero_dead = !gather;
+                q.live_below = V;
             }
-            e = run_head_gemm<false, true, kEpiOut>(tdl, twm, tdl, q, c.num_sms, s);
-            if (e == cudaSuccess && L.splits > 1)
-                e = launch_after(head_join_kernel, dim3(n, std::min(ceil_div(nv, 64), 64)), dim3(64), 0, s,
-                                 (const float*)(ws + L.part), cap * H, L.splits, nv, (const int32_t*)rows,
-                                 (const int32_t*)live, dx);
-            if (e != cudaSuccess) break;
+            e = run_head_gemm<false, true, kEpiOut>(odl, ow, ow, q, c.num_sms, s);
+            if (e != cudaSuccess) return e;
         }
         if (a.dW) {
             HeadGemm q = p;
-            CUtensorMap txm, txcm;
-            if (!make_tmap_pitch(&tdl, p.dl, cap, V, p.ld_dl, 64) || !make_tmap_pitch(&txcm, ws + L.xc, cap, H, H, 64) ||
-                !make_tmap_pitch(&txm, x, n, H, a.ldx, 64))
-                return cudaErrorInvalidValue;
+            const Operand clean{xc, n, H, H};
             q.M = V;
             q.N = H;
             q.K = n;
             q.m_live = 0;
-            q.k_live = 1;
+            q.k_live = gather;
+            // dl and x were complete before dX's kernel began
+            q.wait_late = dx != nullptr;
             // over several pieces the sum goes on in fp32 until the last one
             const bool first = t0 == 0, last = t0 + n >= T;
             float* acc = a.dW_f32 ? static_cast<float*>(a.dW) : reinterpret_cast<float*>(ws + L.acc);
             q.out_f32 = a.dW_f32 || !last;
             q.out = q.out_f32 ? (void*)acc : a.dW;
             q.add = first && !(a.dW_f32 && a.accumulate) ? nullptr : acc;
-            e = run_head_gemm<true, true, kEpiOut>(tdl, txcm, txm, q, c.num_sms, s);
+            e = run_head_gemm<true, true, kEpiOut>(odl, gather ? oxc : clean, gather ? ox : clean, q, c.num_sms, s);
+            if (e != cudaSuccess) return e;
+        }
+        if (dx && splits > 1) {
+            const int nq = H / 4, threads = std::min(256, ceil_div(nq, 32) * 32);
+            e = launch_after(head_join_kernel, dim3(n, ceil_div(nq, threads)), dim3(threads), 0, s,
+                             (const float4*)(ws + L.part), (int64_t)n * nq, splits, nq, (const int32_t*)rows,
+                             (const int32_t*)live, labels, a.labels_i64, V, reinterpret_cast<uint2*>(dx));
+            if (e != cudaSuccess) return e;
         }
     }
     return e;
