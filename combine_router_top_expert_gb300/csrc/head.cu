@@ -32,12 +32,11 @@ namespace {
 
 constexpr int kBM = 256, kBN = 256;     // tile of a pair of CTAs
 constexpr int kBK = 64;                 // K elements of a stage (128 bytes)
-constexpr int kStages = 6;
+constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;            // two per TMEM lane quadrant, 128 columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kOperandBytes = 128 * kBK * 2;          // a CTA's share of A or of B
-constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kBarOffset = kStages * kStageBytes;
+constexpr int kBarOffset = 6 * 2 * kOperandBytes;     // the ring: 6 stages, or more that hold few rows of A
 constexpr int kPassBytes = 4096;                      // an epilogue warp's staging: 32 rows x 128 bytes
 constexpr int kStageOutOffset = kBarOffset + 1024;
 constexpr int kSmemBytes = 1024 + kStageOutOffset + kEpiWarps * kPassBytes;
@@ -45,6 +44,7 @@ constexpr int kSmemBytes = 1024 + kStageOutOffset + kEpiWarps * kPassBytes;
 // registers. The tensor cores cut what they add to an accumulator instead of rounding
 // it, which makes a long sum too small by up to 2^-24 of itself a step: H = 7168 in one
 // sum moved a loss by 4.8e-6 of itself, in sums of 1024 by what the other roundings do.
+// (dl from a known log-sum is rounded to BF16: there one sum does.)
 constexpr int kLogitBlocks = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 // An exponential e is kept as its root times 2^15, s = 2^15 exp((l - top) / 2): FP16 then has a relative error of
@@ -69,6 +69,8 @@ struct HeadGemm {
     int bn;                 // tile columns (a multiple of 32, at most kBN; the MN-major B's are kBN)
     int splits;             // parts of K, each a tile of its own
     int group;              // row tiles that are walked together
+    int a_bytes;            // a CTA's share of A in a stage: whole, or the rows there are where one CTA holds them all
+    int stages;
     int early;              // operands whose first blocks may be loaded before the kernel ahead has ended
     int wait_late;          // the operands were complete before the kernel ahead began: it is waited for at the end
     // logits
@@ -166,18 +168,20 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t bar_base = smem_base + kBarOffset;
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
-    auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
-    auto accf_bar = [&](int a) { return bar_base + 8u * (2 * kStages + a); };
-    auto acce_bar = [&](int a) { return bar_base + 8u * (2 * kStages + 2 + a); };
-    const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4);
-    auto a_tile = [&](int s) { return smem_base + s * kStageBytes; };
-    auto b_tile = [&](int s) { return smem_base + s * kStageBytes + kOperandBytes; };
+    auto empty_bar = [&](int s) { return bar_base + 8u * (kMaxStages + s); };
+    auto accf_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + a); };
+    auto acce_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + 2 + a); };
+    const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
+    const uint32_t stage_bytes = p.a_bytes + kOperandBytes;
+    const int stages = p.stages;
+    auto a_tile = [&](int s) { return smem_base + s * stage_bytes; };
+    auto b_tile = [&](int s) { return smem_base + s * stage_bytes + p.a_bytes; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     StatusBlock* st = p.status;
     const uint64_t tmo = p.timeout_ns;
     if (threadIdx.x == 32) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             tc::mbar_init(full_bar(s), 1);
             tc::mbar_init(empty_bar(s), 1);
         }
@@ -217,14 +221,16 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int kbs = (K + kBK - 1) / kBK;
     const int total = mt * nt * p.splits;
     const int gstart = (int)blockIdx.x / 2, gstep = (int)gridDim.x / 2;
-    constexpr int kSumBlocks = EPI == kEpiOut ? 1 << 30 : kLogitBlocks;   // K blocks of an accumulator's sum
+    constexpr int kSumBlocks = EPI == kEpiStats || EPI == kEpiExp ? kLogitBlocks : 1 << 30;   // K blocks of an accumulator's sum
     auto k_first = [&](int split) { return p.splits == 1 ? kbs * split : kbs * split / p.splits; };   // below 2^25
 
     if (warp == 0) {
         if (lane == 0) {
             const void* mapA = EPI != kEpiOut && all ? (const void*)&tmAll : (const void*)&tmA;
             const void* mapB = A_MN && B_MN && all ? (const void*)&tmAll : (const void*)&tmB;
-            const uint32_t bytes = kOperandBytes + (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2);
+            // few rows: the leader alone has some, and the MMAs' other rows are whatever lies there
+            const bool few = p.a_bytes < kOperandBytes;
+            const uint32_t bytes = (few ? 1 : 2) * p.a_bytes + 2 * (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2);
             // both halves of a pair signal the leader's barrier, which expects both
             auto load_a = [&](int stage, const Tile& t, int kb) {
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
@@ -232,7 +238,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if constexpr (A_MN) {
                     tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
                     tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
-                } else {
+                } else if (!few || rank == 0) {
                     tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, k0, m0);
                 }
             };
@@ -248,15 +254,15 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             };
             int stage = 0, ahead = 0;   // ahead: blocks whose early operands are on their way
             uint32_t ph = 0;
-            int last_par[kStages];
-            for (int s = 0; s < kStages; ++s) last_par[s] = -1;
+            int last_par[kMaxStages];
+            for (int s = 0; s < kMaxStages; ++s) last_par[s] = -1;
             bool ok = true;
             if (p.early) {
-                for (int g = gstart; g < total && ahead < kStages; g += gstep) {
+                for (int g = gstart; g < total && ahead < stages; g += gstep) {
                     const Tile t = head_tile(g, mt, nt, p.group);
                     const int kend = k_first(t.split + 1);
-                    for (int kb = k_first(t.split); kb < kend && ahead < kStages; ++kb, ++ahead) {
-                        if (rank == 0) tc::mbar_expect_tx(full_bar(ahead), 2 * bytes);
+                    for (int kb = k_first(t.split); kb < kend && ahead < stages; ++kb, ++ahead) {
+                        if (rank == 0) tc::mbar_expect_tx(full_bar(ahead), bytes);
                         if (p.early & kEarlyA) load_a(ahead, t, kb);
                         if (p.early & kEarlyB) load_b(ahead, t, kb);
                     }
@@ -273,17 +279,17 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         --ahead;
                     } else {
                         if (!tc::mbar_wait(empty_bar(stage), ph ^ 1u, st, tmo, kSiteProducerEmpty)) { ok = false; break; }
-                        if (rank == 0) tc::mbar_expect_tx(full_bar(stage), 2 * bytes);
+                        if (rank == 0) tc::mbar_expect_tx(full_bar(stage), bytes);
                     }
                     if (!begun || !(p.early & kEarlyA)) load_a(stage, t, kb);
                     if (!begun || !(p.early & kEarlyB)) load_b(stage, t, kb);
                     last_par[stage] = (int)ph;
-                    if (++stage == kStages) { stage = 0; ph ^= 1u; }
+                    if (++stage == stages) { stage = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
                 // let every copy already issued land before the CTA exits
-                for (int s = 0; s < kStages; ++s)
+                for (int s = 0; s < stages; ++s)
                     if (last_par[s] >= 0) tc::mbar_wait(full_bar(s), (uint32_t)last_par[s], st, tmo, kSiteDrain);
             }
         }
@@ -299,8 +305,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             constexpr uint32_t kHi = 64u | 1u << 14 | tc::kLayoutSW128 << 29;
             constexpr uint32_t kStepA = A_MN ? 128u : 2u, kStepB = B_MN ? 128u : 2u;
             auto mma4 = [&](uint32_t d, int sg, uint32_t more) {
-                const uint32_t al = (a_tile(0) >> 4 | kLoA) + (uint32_t)sg * (kStageBytes >> 4);
-                const uint32_t bl = (b_tile(0) >> 4 | kLoB) + (uint32_t)sg * (kStageBytes >> 4);
+                const uint32_t al = (a_tile(0) >> 4 | kLoA) + (uint32_t)sg * (stage_bytes >> 4);
+                const uint32_t bl = (b_tile(0) >> 4 | kLoB) + (uint32_t)sg * (stage_bytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16_2sm(d, (uint64_t)kHi << 32 | (al + kk * kStepA), (uint64_t)kHi << 32 | (bl + kk * kStepB),
@@ -319,8 +325,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     const uint32_t d = tmem + (uint32_t)(acc * kBN);
                     uint32_t more = 0;
                     for (int i = 0; i < n; i += 2) {
-                        const int s1 = stage + 1 == kStages ? 0 : stage + 1;
-                        const uint32_t p1 = stage + 1 == kStages ? ph ^ 1u : ph;
+                        const int s1 = stage + 1 == stages ? 0 : stage + 1;
+                        const uint32_t p1 = stage + 1 == stages ? ph ^ 1u : ph;
                         const bool two = i + 1 < n;
                         if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
                         if (two && !tc::mbar_wait(full_bar(s1), p1, st, tmo, kSiteMmaFull)) { ok = false; break; }
@@ -332,7 +338,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         if (two) {
                             mma4(d, stage, 1);
                             tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
-                            if (++stage == kStages) { stage = 0; ph ^= 1u; }
+                            if (++stage == stages) { stage = 0; ph ^= 1u; }
                         }
                     }
                     issued = true;
@@ -377,8 +383,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             // what belongs to the row, fetched while the tile is being summed
             int lab = -1;                                 // its label
             float mul = 0.f, base = 0.f;
+            float label_at_lse = 0.f;                     // its label's logit less its log-sum
             int orow = in ? row : -1;                     // its output row
             bool dead = false;
+            // dl: rows behind the last live token, up to the tile's end, are zeros where the live ones are
+            // counted on the device: dW's last K block reads some of them
+            const int row_end = p.m_live ? 1 << 30 : M;
             if constexpr (EPI != kEpiOut) {
                 if (in) {
                     const int64_t tok = p.rows && !all ? p.rows[row] : row;
@@ -386,7 +396,9 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (y >= 0 && y < p.N) lab = (int)y;
                     if (EPI == kEpiDl && lab >= 0) {
                         mul = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
-                        base = -kLog2e * __ldg(p.lse + tok);
+                        const float lse = __ldg(p.lse + tok);
+                        base = -kLog2e * lse;
+                        label_at_lse = __ldcg(p.label_logit + row) - lse;
                     }
                 }
             } else {
@@ -395,7 +407,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
             __syncwarp();
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * cols);
-            if constexpr (EPI == kEpiOut) {
+            if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
                 // 64 columns at a time: tensor memory, registers, staging, memory
                 if (blocks > 0) {
                     if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) break;
@@ -428,6 +440,35 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                     if (64 * h >= nv) continue;
                     uint4 v[8];
+                    if constexpr (EPI == kEpiDl) {
+#pragma unroll
+                        for (int e8 = 0; e8 < 8; ++e8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = 8 * e8 + 2 * i;
+                                float2 e = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                                e = __ffma2_rn(e, make_float2(kLog2e, kLog2e), make_float2(base, base));
+                                e = __fmul2_rn(make_float2(exp2_approx(e.x), exp2_approx(e.y)), make_float2(mul, mul));
+                                w[i] = lab >= 0 ? pack_bf16x2(e.x, e.y) : 0u;
+                            }
+                            put(e8, w[0], w[1], w[2], w[3]);
+                        }
+                        const int j = lab - col0 - 64 * h;      // the label's column of these 64
+                        if (lab >= 0 && j >= 0 && j < 64)
+                            st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
+                                        __float2bfloat16_rn(mul * expm1f(label_at_lse)));
+                        __syncwarp();
+                        take(0, v);
+                        const int cc = 64 * h + 8 * (lane & 7);
+                        __nv_bfloat16* to = p.dl + (int64_t)(row0 + (lane >> 3)) * p.ld_dl + col0 + cc;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (row0 + 4 * i + (lane >> 3) < row_end && cc < nv)
+                                *reinterpret_cast<uint4*>(to + 4 * i * p.ld_dl) = v[i];
+                        __syncwarp();
+                        continue;
+                    }
                     if (!p.out_f32 && !p.add) {
 #pragma unroll
                         for (int e8 = 0; e8 < 8; ++e8) {
@@ -509,27 +550,25 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (nv <= 0) continue;
             {
                 const int lc = lab >= col0 && lab < col0 + nv ? lab - col0 : -1;
-                if constexpr (EPI != kEpiDl) {
-                    if (nv < 128) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i < nv ? r[c][i] : -INFINITY;
-                    }
-                    mul = -INFINITY;
+                if (nv < 128) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) mul = fmaxf(mul, r[c][i]);
-                    base = kRootShift - (mul == -INFINITY ? 0.f : mul * (0.5f * kLog2e));
-                    // the label's own term stays out of the sum, so that the others' share keeps its
-                    // digits where the label takes nearly everything
-                    if (__any_sync(0xffffffffu, lc >= 0)) {
+                        for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i < nv ? r[c][i] : -INFINITY;
+                }
+                mul = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i == lc ? -INFINITY : r[c][i];
-                    }
+                    for (int i = 0; i < 32; ++i) mul = fmaxf(mul, r[c][i]);
+                base = kRootShift - (mul == -INFINITY ? 0.f : mul * (0.5f * kLog2e));
+                // the label's own term stays out of the sum, so that the others' share keeps its
+                // digits where the label takes nearly everything
+                if (__any_sync(0xffffffffu, lc >= 0)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i == lc ? -INFINITY : r[c][i];
                 }
                 float2 s[4];
 #pragma unroll
@@ -542,33 +581,18 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            constexpr float kFactor = EPI == kEpiDl ? kLog2e : 0.5f * kLog2e;
                             const int j = 64 * h + 8 * e8 + 2 * i;
                             float2 v = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
-                            v = __ffma2_rn(v, make_float2(kFactor, kFactor), make_float2(base, base));
+                            v = __ffma2_rn(v, make_float2(0.5f * kLog2e, 0.5f * kLog2e), make_float2(base, base));
                             v = make_float2(exp2_approx(v.x), exp2_approx(v.y));
-                            if constexpr (EPI == kEpiDl) {
-                                v = __fmul2_rn(v, make_float2(mul, mul));
-                                w[i] = lab >= 0 ? pack_bf16x2(v.x, v.y) : 0u;
-                            } else {
-                                s[j / 32] = __ffma2_rn(v, v, s[j / 32]);
-                                const __half2 v2 = __float22half2_rn(v);
-                                w[i] = in ? *reinterpret_cast<const uint32_t*>(&v2) : 0u;
-                            }
+                            s[j / 32] = __ffma2_rn(v, v, s[j / 32]);
+                            const __half2 v2 = __float22half2_rn(v);
+                            w[i] = in ? *reinterpret_cast<const uint32_t*>(&v2) : 0u;
                         }
                         if (EPI != kEpiStats) put(e8, w[0], w[1], w[2], w[3]);
                     }
                     if constexpr (EPI != kEpiStats) {
-                        if (EPI == kEpiDl && lc >= 64 * h && lc < 64 * h + 64) {
-                            const int j = lc - 64 * h;
-                            const float at = __ldcg(p.label_logit + row) - __ldg(p.lse + (p.rows && !all ? p.rows[row] : row));
-                            st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
-                                        __float2bfloat16_rn(mul * expm1f(at)));
-                        }
                         __syncwarp();
-                        // rows behind the last live token, up to the tile's end, are zeros where the live ones are
-                        // counted on the device: dW's last K block reads some of them
-                        const int row_end = p.m_live ? 1 << 30 : M;
                         const int cc = 64 * h + 8 * (lane & 7);
                         __nv_bfloat16* o = p.dl + (int64_t)(row0 + (lane >> 3)) * p.ld_dl + col0 + cc;
 #pragma unroll
@@ -583,7 +607,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         __syncwarp();
                     }
                 }
-                if (EPI != kEpiDl && in) {
+                if (in) {
                     const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
                     p.stats[(int64_t)row * p.stat_tiles + col0 / cols] = make_float2(mul, sum * kRootScale);
                 }
@@ -652,13 +676,13 @@ head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restr
     }
 }
 
-// For more tokens. CTA b takes kPrepTokens of every `span` tokens from b * span on:
+// For more tokens. CTA b takes `span` tokens from b * span on, kPrepTokens at a time:
 // live ones get the next place (tokens in order), their rows are copied there unless
-// every token is live, the others' outputs are zeroed; the labels' logits are formed if
-// asked, a warp a token. Each CTA counts the live tokens before its own from the labels
-// themselves. Behind the last live row, rows up to the next multiple of kBK are zeroed:
-// dW's last K block reads them. The first CTA clears the status block.
-constexpr int kPrepTokens = 8;
+// every token is live, and their labels' logits are formed; the others' outputs are
+// zeroed. Each CTA counts the live tokens before its own from the labels themselves.
+// Behind the last live row, rows up to the next multiple of kBK are zeroed: dW's last K
+// block reads them. The first CTA clears the status block.
+constexpr int kPrepTokens = 4;
 __global__ void __launch_bounds__(kRowThreads)
 head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
                  int T, int V, int nv, int span, int32_t* __restrict__ rows, int32_t* __restrict__ live,
@@ -666,6 +690,7 @@ head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restri
                  int32_t* status) {
     __shared__ int32_t sh[2];
     __shared__ int32_t place[kPrepTokens];
+    __shared__ float red[kPrepTokens][kRowThreads / 32];
     pdl_wait();
     pdl_allow_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -708,32 +733,45 @@ head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restri
         }
         next += __popc(b);
         __syncthreads();
-        // the rows' vectors in one run, four loads of a thread in flight
-        for (int i0 = tid; i0 < n * nv; i0 += 4 * kRowThreads) {
-            uint4 a[4];
+        int to[kPrepTokens];
+        const uint4 *xr[kPrepTokens], *wr[kPrepTokens];
+        float dot[kPrepTokens];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * kRowThreads;
-                if (!all && i < n * nv) a[u] = __ldg(x + (int64_t)(c0 + i / nv) * ldx + i % nv);
-            }
+        for (int j = 0; j < kPrepTokens; ++j) {
+            to[j] = j < n ? place[j] : -2;
+            xr[j] = x + (int64_t)(c0 + j) * ldx;
+            wr[j] = to[j] >= 0 ? W + label_at(labels, i64, c0 + j) * nv : W;
+            dot[j] = 0.f;
+        }
+        for (int v = tid; v < nv; v += kRowThreads) {
+            uint4 a[kPrepTokens], w[kPrepTokens];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * kRowThreads;
-                if (i >= n * nv) continue;
-                const int j = i / nv, v = i % nv, to = place[j];
-                if (to < 0) {
-                    if (dx) dx[(int64_t)(c0 + j) * nv + v] = make_uint4(0, 0, 0, 0);
-                } else if (!all) {
-                    xc[(int64_t)to * nv + v] = a[u];
+            for (int j = 0; j < kPrepTokens; ++j)
+                if (to[j] >= 0) {
+                    a[j] = __ldg(xr[j] + v);
+                    w[j] = __ldg(wr[j] + v);
+                }
+#pragma unroll
+            for (int j = 0; j < kPrepTokens; ++j) {
+                if (to[j] >= 0) {
+                    dot[j] = dot8(a[j], w[j], dot[j]);
+                    if (!all) xc[(int64_t)to[j] * nv + v] = a[j];
+                } else if (to[j] == -1 && dx) {
+                    dx[(int64_t)(c0 + j) * nv + v] = make_uint4(0, 0, 0, 0);
                 }
             }
         }
-        if (label_logit && warp < n && place[warp] >= 0) {
-            const int64_t t = c0 + warp;
-            float s = label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, lane, 32);
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (lane == 0) label_logit[place[warp]] = s;
+        for (int j = 0; j < kPrepTokens; ++j) {
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+            if (lane == 0) red[j][warp] = dot[j];
+        }
+        __syncthreads();
+        if (tid < n && place[tid] >= 0) {
+            float s = 0.f;
+            for (int i = 0; i < kRowThreads / 32; ++i) s += red[tid][i];
+            label_logit[place[tid]] = s;
         }
     }
     if (!all && t1 == T) {
@@ -780,13 +818,13 @@ __device__ __forceinline__ float row_loss(const RowSum& r, float label_logit) {
     return r.own > r.others ? log1pf(r.others / r.own) : logf(r.others + r.own) - (label_logit - r.top);
 }
 
-// A CTA per live token. The label's logit is formed while the logits' kernel still
-// runs: x, W and labels are the caller's and the list of live tokens is the kernel's
+// A CTA per live token. For one row tile the label's logit is formed here, while the
+// logits' kernel still runs: x, W and labels are the caller's and the list of live tokens is the kernel's
 // before that one, all complete before that one began.
 __global__ void __launch_bounds__(kRowThreads)
 head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
                  const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
-                 const void* labels, int i64, int V, float* loss, float* lse) {
+                 const float* label_logit, const void* labels, int i64, int V, float* loss, float* lse) {
     __shared__ float red[128];
     pdl_allow_next();
     const int i = blockIdx.x;
@@ -797,7 +835,8 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
     const int64_t t = rows ? rows[i] : i;
     const bool on = is_live(labels, i64, t, V);
     float own = 0.f;
-    if (on) own = cta_sum(label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, threadIdx.x, kRowThreads), red + 96);
+    if (live) own = __ldcg(label_logit + i);
+    else if (on) own = cta_sum(label_dot(x + t * ldx, W + label_at(labels, i64, t) * nv, nv, threadIdx.x, kRowThreads), red + 96);
     pdl_wait();
     const RowSum r = join_row(stats + (int64_t)i * stat_tiles, stat_tiles, on ? own : -INFINITY, red);
     if (threadIdx.x != 0) return;
@@ -811,7 +850,7 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 __global__ void __launch_bounds__(kRowThreads)
 head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, const uint4* __restrict__ x, int64_t ldx,
                const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
-               const void* labels, int i64, const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld,
+               const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld,
                int V, float* loss, float* lse) {
     __shared__ float red[128];
     pdl_allow_next();
@@ -824,7 +863,8 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, 
     const bool on = is_live(labels, i64, t, V);
     const int label = on ? (int)label_at(labels, i64, t) : 0;
     float own = 0.f;
-    if (on) own = cta_sum(label_dot(x + t * ldx, W + (int64_t)label * nv, nv, threadIdx.x, kRowThreads), red + 96);
+    if (live) own = __ldcg(label_logit + i);
+    else if (on) own = cta_sum(label_dot(x + t * ldx, W + (int64_t)label * nv, nv, threadIdx.x, kRowThreads), red + 96);
     pdl_wait();
     __nv_bfloat16* row = dl + i * ld;
     if (!on) {
@@ -940,9 +980,14 @@ struct Operand {
 // One product. `all`: the operand that replaces A (logits) or B (dW) when every token is
 // live. Boxes: 64 columns x 64 rows of K where the operand is MN-major, else a CTA's rows.
 template <bool A_MN, bool B_MN, int EPI>
-cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all, const HeadGemm& p, int num_sms,
+cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all, HeadGemm& p, int num_sms,
                           cudaStream_t s) {
-    const int box_a = A_MN ? kBK : 128, box_b = B_MN ? kBK : p.bn / 2;
+    // up to 128 rows (of a count that the host knows): boxes of as many, and a longer ring. 128-row boxes that are
+    // mostly outside the tensor took as long as full ones (T = 1, H = 1024, V = 32768: 25.9 us, this ...)
+    const int rows = !A_MN && !p.m_live && p.M <= 128 ? (int)align_up(p.M, 8) : 128;
+    p.a_bytes = rows * kBK * 2;
+    p.stages = std::min(kMaxStages, kBarOffset / (p.a_bytes + kOperandBytes));
+    const int box_a = A_MN ? kBK : rows, box_b = B_MN ? kBK : p.bn / 2;
     CUtensorMap ta, tb, tall;
     if (!make_tmap_pitch(&ta, a.base, a.rows, a.cols, a.ld, box_a) ||
         !make_tmap_pitch(&tb, b.base, b.rows, b.cols, b.ld, box_b) ||
@@ -1085,7 +1130,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         if (gather) {
             const int span = kPrepTokens * ceil_div(n, kPrepTokens * 1024);
             e = launch_after(head_prep_kernel, dim3(ceil_div(n, span)), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
-                             a.labels_i64, n, V, nv, span, rows, live, xc, logit, loss, forward ? lse : nullptr,
+                             a.labels_i64, n, V, nv, span, rows, live, xc, label, loss, forward ? lse : nullptr,
                              reinterpret_cast<uint4*>(dx), status);
         } else {
             e = launch_after(head_start_kernel, dim3(grad ? n : 1), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
@@ -1122,8 +1167,8 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             e = run_head_gemm<false, false, kEpiStats>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
                 e = launch_after(head_loss_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
-                                 xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live, labels, a.labels_i64, V,
-                                 loss, lse);
+                                 xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live, (const float*)label, labels,
+                                 a.labels_i64, V, loss, lse);
             if (e != cudaSuccess) return e;
             continue;
         }
@@ -1131,8 +1176,8 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             e = run_head_gemm<false, false, kEpiExp>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
                 e = launch_after(head_dl_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
-                                 p.bn / 2, xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live, labels,
-                                 a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
+                                 p.bn / 2, xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live,
+                                 (const float*)label, labels, a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
         } else {
             e = run_head_gemm<false, false, kEpiDl>(oxc, ow, ox, p, c.num_sms, s);
         }
