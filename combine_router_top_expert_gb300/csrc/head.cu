@@ -71,6 +71,7 @@ struct HeadGemm {
     int group;              // row tiles that are walked together
     int a_bytes;            // a CTA's share of A in a stage: whole, or the rows there are where one CTA holds them all
     int stages;
+    int a_groups, b_groups; // MN-major: the operand's map has groups of 64 columns as its last axis
     int early;              // operands whose first blocks may be loaded before the kernel ahead has ended
     int wait_late;          // the operands were complete before the kernel ahead began: it is waited for at the end
     // logits
@@ -157,6 +158,15 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+// A box of a three-dimensional map, as tma_load_2d_2sm.
+__device__ __forceinline__ void tma_load_3d_2sm(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -236,8 +246,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
                 const int m0 = t.m * kBM + rank * 128, k0 = kb * kBK;
                 if constexpr (A_MN) {
-                    tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
-                    tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
+                    if (p.a_groups) {
+                        tma_load_3d_2sm(a_tile(stage), mapA, lead, 0, k0, m0 / 64);
+                    } else {
+                        tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
+                        tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
+                    }
                 } else if (!few || rank == 0) {
                     tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, k0, m0);
                 }
@@ -246,8 +260,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
                 const int n0 = t.n * p.bn + rank * (p.bn / 2), k0 = kb * kBK;
                 if constexpr (B_MN) {
-                    tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, n0, k0);
-                    tc::tma_load_2d_2sm(b_tile(stage) + 8192, mapB, lead, n0 + 64, k0);
+                    if (p.b_groups) {
+                        tma_load_3d_2sm(b_tile(stage), mapB, lead, 0, k0, n0 / 64);
+                    } else {
+                        tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, n0, k0);
+                        tc::tma_load_2d_2sm(b_tile(stage) + 8192, mapB, lead, n0 + 64, k0);
+                    }
                 } else {
                     tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, k0, n0);
                 }
@@ -952,6 +970,21 @@ bool make_tmap_pitch(CUtensorMap* m, const void* base, int64_t rows, int64_t col
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for an MN-major operand whose rows are whole groups of 64 columns: [groups][rows][64], in boxes of two
+// groups x 64 rows, so that one copy brings a CTA's 128 columns of a K block (two copies for each operand were as much
+// as the producer could issue: dW at T = 2560, H = 7168, V = 32768 took 641 us, this ...).
+bool make_tmap_groups(CUtensorMap* m, const void* base, int64_t rows, int64_t groups, int64_t ld) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)groups};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), 128};
+    cuuint32_t box[3] = {64, 64, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Pairs of CTAs of a kernel that can be resident at once, asked once per kernel and
 // device.
 template <bool A_MN, bool B_MN, int EPI>
@@ -987,11 +1020,16 @@ cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all
     const int rows = !A_MN && !p.m_live && p.M <= 128 ? (int)align_up(p.M, 8) : 128;
     p.a_bytes = rows * kBK * 2;
     p.stages = std::min(kMaxStages, kBarOffset / (p.a_bytes + kOperandBytes));
+    p.a_groups = A_MN && a.cols % 64 == 0;
+    p.b_groups = B_MN && b.cols % 64 == 0;
+    auto map = [](CUtensorMap* m, const Operand& o, bool groups, int box_rows) {
+        return groups ? make_tmap_groups(m, o.base, o.rows, o.cols / 64, o.ld)
+                      : make_tmap_pitch(m, o.base, o.rows, o.cols, o.ld, box_rows);
+    };
     const int box_a = A_MN ? kBK : rows, box_b = B_MN ? kBK : p.bn / 2;
     CUtensorMap ta, tb, tall;
-    if (!make_tmap_pitch(&ta, a.base, a.rows, a.cols, a.ld, box_a) ||
-        !make_tmap_pitch(&tb, b.base, b.rows, b.cols, b.ld, box_b) ||
-        !make_tmap_pitch(&tall, all.base, all.rows, all.cols, all.ld, EPI == kEpiOut ? box_b : box_a))
+    if (!map(&ta, a, p.a_groups, box_a) || !map(&tb, b, p.b_groups, box_b) ||
+        !(EPI == kEpiOut ? map(&tall, all, p.b_groups, box_b) : map(&tall, all, false, box_a)))
         return cudaErrorInvalidValue;
     auto kern = head_gemm_kernel<A_MN, B_MN, EPI>;
     ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
@@ -1221,7 +1259,9 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             q.out_f32 = a.dW_f32 || !last;
             q.out = q.out_f32 ? (void*)acc : a.dW;
             q.add = first && !(a.dW_f32 && a.accumulate) ? nullptr : acc;
-            e = run_head_gemm<true, true, kEpiOut>(odl, gather ? oxc : clean, gather ? ox : clean, q, c.num_sms, s);
+            // dl's rows are padded to whole groups; what lies behind V belongs to rows of dW that there are not
+            const Operand odl64{dl, odl.rows, p.ld_dl, p.ld_dl};
+            e = run_head_gemm<true, true, kEpiOut>(odl64, gather ? oxc : clean, gather ? ox : clean, q, c.num_sms, s);
             if (e != cudaSuccess) return e;
         }
         if (dx && splits > 1) {
