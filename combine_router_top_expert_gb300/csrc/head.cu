@@ -69,7 +69,9 @@ struct HeadGemm {
     int bn;                 // tile columns (a multiple of 32, at most kBN; the MN-major B's are kBN)
     int splits;             // parts of K, each a tile of its own
     int group;              // row tiles that are walked together
-    int a_bytes;            // a CTA's share of A in a stage: whole, or the rows there are where one CTA holds them all
+    int a_mn;               // A is MN-major (two products in one launch; else the kernel's own type says it)
+    int a_bytes;            // what a CTA loads of A: its share, or the rows there are where one CTA holds them all
+    int a_room;             // its room in a stage
     int stages;
     int a_groups, b_groups; // MN-major: the operand's map has groups of 64 columns as its last axis
     int early;              // operands whose first blocks may be loaded before the kernel ahead has ended
@@ -84,18 +86,35 @@ struct HeadGemm {
     const float* lse;       // [T]
     const float* dloss;     // [T] or NULL
     float scale;
-    __nv_bfloat16* dl;      // [tokens rounded up to 256, ld]
+    __nv_bfloat16* dl;      // [dl_rows, ld_dl]
     int64_t ld_dl;
+    int64_t dl_rows;
     // products
+    int tma_out;            // rows leave as tmOut's boxes; else (scattered, or added to) by the warps' stores
     void* out;
     int out_f32;
     const float* add;       // fp32 rows that are added to the product, or NULL
-    int64_t split_stride;   // elements between the parts' outputs
     const int32_t* out_rows;   // row -> output row, or NULL
     int zero_dead;          // rows whose label is not below live_below are zeros
     int live_below;
     StatusBlock* status;
     unsigned long long timeout_ns;
+};
+
+// A product with its operands. all: the caller's own rows in place of the gathered ones,
+// taken when every token is live (logits: for A, dW: for B). out: what the epilogue
+// writes, as [parts][rows][columns] in boxes of 32 rows x 128 bytes (p.tma_out).
+struct HeadJob {
+    CUtensorMap a, b, all, out;
+    HeadGemm p;
+};
+// One product, or two that do not depend on each other (dX and dW): the first `lead`
+// pairs take a tile of the first product each and then share the first `lead_tiles` of
+// the second one's, the other pairs share the rest of those.
+template <int N>
+struct HeadJobs {
+    HeadJob job[N];
+    int lead, lead_tiles;
 };
 
 __device__ __forceinline__ float exp2_approx(float v) {
@@ -167,12 +186,16 @@ __device__ __forceinline__ void tma_load_3d_2sm(uint32_t dst, const void* tmap, 
         : "memory");
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+// Sizes of a product with the live tokens in place.
+struct HeadSize {
+    int M, mt, nt, kbs, total;
+    bool all;
+};
+
+template <bool A_MN, bool B_MN, int EPI, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmAll, const HeadGemm p) {
-    // tmAll: the caller's own rows in place of the gathered ones, taken when every
-    // token is live (logits: A, dW: B)
+head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
+    const HeadGemm& p0 = jobs.job[0].p;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ uint32_t s_tmem_base;
     const uint32_t smem_base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -182,14 +205,14 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     auto accf_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + a); };
     auto acce_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + 2 + a); };
     const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
-    const uint32_t stage_bytes = p.a_bytes + kOperandBytes;
-    const int stages = p.stages;
+    const uint32_t a_room = p0.a_room, stage_bytes = a_room + kOperandBytes;
+    const int stages = p0.stages;
     auto a_tile = [&](int s) { return smem_base + s * stage_bytes; };
-    auto b_tile = [&](int s) { return smem_base + s * stage_bytes + p.a_bytes; };
+    auto b_tile = [&](int s) { return smem_base + s * stage_bytes + a_room; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    StatusBlock* st = p.status;
-    const uint64_t tmo = p.timeout_ns;
+    StatusBlock* st = p0.status;
+    const uint64_t tmo = p0.timeout_ns;
     if (threadIdx.x == 32) {
         for (int s = 0; s < stages; ++s) {
             tc::mbar_init(full_bar(s), 1);
@@ -203,9 +226,11 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::fence_mbar_init();
     }
     if (threadIdx.x == 0) {
-        tc::prefetch_tmap(&tmA);
-        tc::prefetch_tmap(&tmB);
-        tc::prefetch_tmap(&tmAll);
+        for (int j = 0; j < N; ++j) {
+            tc::prefetch_tmap(&jobs.job[j].a);
+            tc::prefetch_tmap(&jobs.job[j].b);
+            tc::prefetch_tmap(&jobs.job[j].all);
+        }
     }
     if (warp == 1) {
         tc::tmem_alloc_2sm(tc::smem_u32(&s_tmem_base), 512);
@@ -213,8 +238,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     // The kernel behind this one may begin once all that this one reads is complete
     // (a wait_late kernel reads on that ground); early kernels wait in their roles.
-    if (!p.early) {
-        if (!p.wait_late) pdl_wait();
+    if (!p0.early) {
+        if (!p0.wait_late) pdl_wait();
         pdl_allow_next();
     }
     tc::fence_before_sync();
@@ -224,85 +249,122 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t tmem = s_tmem_base;
     const int rank = (int)tc::cluster_ctarank();
 
-    const int live = p.live ? *p.live : p.tokens;
-    const bool all = live == p.tokens;
-    const int M = p.m_live ? live : p.M, K = p.k_live ? live : p.K;
-    const int mt = (M + kBM - 1) / kBM, nt = (p.N + p.bn - 1) / p.bn;
-    const int kbs = (K + kBK - 1) / kBK;
-    const int total = mt * nt * p.splits;
-    const int gstart = (int)blockIdx.x / 2, gstep = (int)gridDim.x / 2;
+    const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+    auto size_of = [&](const HeadGemm& p) {
+        HeadSize z;
+        const int live = p.live ? *p.live : p.tokens;
+        z.all = live == p.tokens;
+        z.M = p.m_live ? live : p.M;
+        z.mt = (z.M + kBM - 1) / kBM;
+        z.nt = (p.N + p.bn - 1) / p.bn;
+        z.kbs = ((p.k_live ? live : p.K) + kBK - 1) / kBK;
+        z.total = z.mt * z.nt * p.splits;
+        return z;
+    };
+    // this pair's tiles of product j: from g0 to before g1
+    struct Range {
+        int g0, g1, step;
+    };
+    auto range_of = [&](int j, const HeadSize& z) {
+        Range r{pair, z.total, pairs};
+        if (N == 2 && j == 1) {
+            const bool in_lead = pair < jobs.lead;
+            const int64_t tiles = in_lead ? jobs.lead_tiles : z.total - jobs.lead_tiles;
+            const int k = in_lead ? pair : pair - jobs.lead, of = in_lead ? jobs.lead : pairs - jobs.lead;
+            const int base = in_lead ? 0 : jobs.lead_tiles;
+            r = Range{base + (int)(tiles * k / of), base + (int)(tiles * (k + 1) / of), 1};
+        }
+        return r;
+    };
     constexpr int kSumBlocks = EPI == kEpiStats || EPI == kEpiExp ? kLogitBlocks : 1 << 30;   // K blocks of an accumulator's sum
-    auto k_first = [&](int split) { return p.splits == 1 ? kbs * split : kbs * split / p.splits; };   // below 2^25
+    // first K block of a part (products below 2^25)
+    auto k_first = [](const HeadGemm& p, const HeadSize& z, int split) {
+        return p.splits == 1 ? z.kbs * split : z.kbs * split / p.splits;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
-            const void* mapA = EPI != kEpiOut && all ? (const void*)&tmAll : (const void*)&tmA;
-            const void* mapB = A_MN && B_MN && all ? (const void*)&tmAll : (const void*)&tmB;
-            // few rows: the leader alone has some, and the MMAs' other rows are whatever lies there
-            const bool few = p.a_bytes < kOperandBytes;
-            const uint32_t bytes = (few ? 1 : 2) * p.a_bytes + 2 * (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2);
             // both halves of a pair signal the leader's barrier, which expects both
-            auto load_a = [&](int stage, const Tile& t, int kb) {
+            auto load_a = [&](const HeadJob& J, const HeadSize& z, int stage, const Tile& t, int kb) {
+                const HeadGemm& p = J.p;
+                const void* map = EPI != kEpiOut && z.all ? (const void*)&J.all : (const void*)&J.a;
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
                 const int m0 = t.m * kBM + rank * 128, k0 = kb * kBK;
-                if constexpr (A_MN) {
+                if (N == 2 ? p.a_mn != 0 : A_MN) {
                     if (p.a_groups) {
-                        tma_load_3d_2sm(a_tile(stage), mapA, lead, 0, k0, m0 / 64);
+                        tma_load_3d_2sm(a_tile(stage), map, lead, 0, k0, m0 / 64);
                     } else {
-                        tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, m0, k0);
-                        tc::tma_load_2d_2sm(a_tile(stage) + 8192, mapA, lead, m0 + 64, k0);
+                        tc::tma_load_2d_2sm(a_tile(stage), map, lead, m0, k0);
+                        tc::tma_load_2d_2sm(a_tile(stage) + 8192, map, lead, m0 + 64, k0);
                     }
-                } else if (!few || rank == 0) {
-                    tc::tma_load_2d_2sm(a_tile(stage), mapA, lead, k0, m0);
+                } else if (p.a_bytes == kOperandBytes || rank == 0) {
+                    // (few rows: the leader alone has some, and the MMAs' other rows are whatever lies there)
+                    tc::tma_load_2d_2sm(a_tile(stage), map, lead, k0, m0);
                 }
             };
-            auto load_b = [&](int stage, const Tile& t, int kb) {
+            auto load_b = [&](const HeadJob& J, const HeadSize& z, int stage, const Tile& t, int kb) {
+                const HeadGemm& p = J.p;
+                const void* map = (N == 2 ? p.a_mn != 0 : A_MN) && z.all ? (const void*)&J.all : (const void*)&J.b;
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
                 const int n0 = t.n * p.bn + rank * (p.bn / 2), k0 = kb * kBK;
                 if constexpr (B_MN) {
                     if (p.b_groups) {
-                        tma_load_3d_2sm(b_tile(stage), mapB, lead, 0, k0, n0 / 64);
+                        tma_load_3d_2sm(b_tile(stage), map, lead, 0, k0, n0 / 64);
                     } else {
-                        tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, n0, k0);
-                        tc::tma_load_2d_2sm(b_tile(stage) + 8192, mapB, lead, n0 + 64, k0);
+                        tc::tma_load_2d_2sm(b_tile(stage), map, lead, n0, k0);
+                        tc::tma_load_2d_2sm(b_tile(stage) + 8192, map, lead, n0 + 64, k0);
                     }
                 } else {
-                    tc::tma_load_2d_2sm(b_tile(stage), mapB, lead, k0, n0);
+                    tc::tma_load_2d_2sm(b_tile(stage), map, lead, k0, n0);
                 }
+            };
+            auto bytes_of = [](const HeadGemm& p) {
+                return (uint32_t)((p.a_bytes == kOperandBytes ? 2 : 1) * p.a_bytes +
+                                  2 * (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2));
             };
             int stage = 0, ahead = 0;   // ahead: blocks whose early operands are on their way
             uint32_t ph = 0;
             int last_par[kMaxStages];
             for (int s = 0; s < kMaxStages; ++s) last_par[s] = -1;
             bool ok = true;
-            if (p.early) {
-                for (int g = gstart; g < total && ahead < stages; g += gstep) {
-                    const Tile t = head_tile(g, mt, nt, p.group);
-                    const int kend = k_first(t.split + 1);
-                    for (int kb = k_first(t.split); kb < kend && ahead < stages; ++kb, ++ahead) {
-                        if (rank == 0) tc::mbar_expect_tx(full_bar(ahead), bytes);
-                        if (p.early & kEarlyA) load_a(ahead, t, kb);
-                        if (p.early & kEarlyB) load_b(ahead, t, kb);
+            if (p0.early) {
+                const HeadJob& J = jobs.job[0];
+                const HeadSize z = size_of(p0);
+                for (int g = pair; g < z.total && ahead < stages; g += pairs) {
+                    const Tile t = head_tile(g, z.mt, z.nt, p0.group);
+                    const int kend = k_first(p0, z, t.split + 1);
+                    for (int kb = k_first(p0, z, t.split); kb < kend && ahead < stages; ++kb, ++ahead) {
+                        if (rank == 0) tc::mbar_expect_tx(full_bar(ahead), bytes_of(p0));
+                        if (p0.early & kEarlyA) load_a(J, z, ahead, t, kb);
+                        if (p0.early & kEarlyB) load_b(J, z, ahead, t, kb);
                     }
                 }
                 pdl_wait();
                 pdl_allow_next();
             }
-            for (int g = gstart; g < total && ok; g += gstep) {
-                const Tile t = head_tile(g, mt, nt, p.group);
-                const int kend = k_first(t.split + 1);
-                for (int kb = k_first(t.split); kb < kend; ++kb) {
-                    const bool begun = ahead > 0;   // only in the first round of stages, which are free
-                    if (begun) {
-                        --ahead;
-                    } else {
-                        if (!tc::mbar_wait(empty_bar(stage), ph ^ 1u, st, tmo, kSiteProducerEmpty)) { ok = false; break; }
-                        if (rank == 0) tc::mbar_expect_tx(full_bar(stage), bytes);
+#pragma unroll 1
+            for (int j = 0; j < N && ok; ++j) {
+                const HeadJob& J = jobs.job[j];
+                const HeadGemm& p = J.p;
+                const HeadSize z = size_of(p);
+                const Range r = range_of(j, z);
+                const uint32_t bytes = bytes_of(p);
+                for (int g = r.g0; g < r.g1 && ok; g += r.step) {
+                    const Tile t = head_tile(g, z.mt, z.nt, p.group);
+                    const int kend = k_first(p, z, t.split + 1);
+                    for (int kb = k_first(p, z, t.split); kb < kend; ++kb) {
+                        const bool begun = ahead > 0;   // only in the first round of stages, which are free
+                        if (begun) {
+                            --ahead;
+                        } else {
+                            if (!tc::mbar_wait(empty_bar(stage), ph ^ 1u, st, tmo, kSiteProducerEmpty)) { ok = false; break; }
+                            if (rank == 0) tc::mbar_expect_tx(full_bar(stage), bytes);
+                        }
+                        if (!begun || !(p0.early & kEarlyA)) load_a(J, z, stage, t, kb);
+                        if (!begun || !(p0.early & kEarlyB)) load_b(J, z, stage, t, kb);
+                        last_par[stage] = (int)ph;
+                        if (++stage == stages) { stage = 0; ph ^= 1u; }
                     }
-                    if (!begun || !(p.early & kEarlyA)) load_a(stage, t, kb);
-                    if (!begun || !(p.early & kEarlyB)) load_b(stage, t, kb);
-                    last_par[stage] = (int)ph;
-                    if (++stage == stages) { stage = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
@@ -313,56 +375,67 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            if (p.early) pdl_wait();
-            const uint32_t idesc = tc::idesc_bf16(kBM, p.bn, A_MN, B_MN);
+            if (p0.early) pdl_wait();
             // Of a descriptor only the start address changes (16-byte units, in the low word), so an MMA
             // costs two additions: what this thread does between MMAs is not hidden behind them. Building
             // each descriptor from its fields and waiting for every stage by itself left the tensor cores
             // idle a quarter of the time (T = 2560, H = 7168, V = 50001, score: 1090 us, this 954).
-            constexpr uint32_t kLoA = (A_MN ? 512u : 1u) << 16, kLoB = (B_MN ? 512u : 1u) << 16;
             constexpr uint32_t kHi = 64u | 1u << 14 | tc::kLayoutSW128 << 29;
-            constexpr uint32_t kStepA = A_MN ? 128u : 2u, kStepB = B_MN ? 128u : 2u;
+            constexpr uint32_t kLoB = (B_MN ? 512u : 1u) << 16, kStepB = B_MN ? 128u : 2u;
+            uint32_t idesc = 0, step_a = 0, al0 = 0;
+            const uint32_t bl0 = b_tile(0) >> 4 | kLoB;
             auto mma4 = [&](uint32_t d, int sg, uint32_t more) {
-                const uint32_t al = (a_tile(0) >> 4 | kLoA) + (uint32_t)sg * (stage_bytes >> 4);
-                const uint32_t bl = (b_tile(0) >> 4 | kLoB) + (uint32_t)sg * (stage_bytes >> 4);
+                const uint32_t al = al0 + (uint32_t)sg * (stage_bytes >> 4);
+                const uint32_t bl = bl0 + (uint32_t)sg * (stage_bytes >> 4);
+                const uint32_t sa = N == 2 ? step_a : A_MN ? 128u : 2u;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_bf16_2sm(d, (uint64_t)kHi << 32 | (al + kk * kStepA), (uint64_t)kHi << 32 | (bl + kk * kStepB),
+                    tc::mma_bf16_2sm(d, (uint64_t)kHi << 32 | (al + kk * sa), (uint64_t)kHi << 32 | (bl + kk * kStepB),
                                      idesc, kk > 0 ? 1u : more);
             };
             int stage = 0, acc = 0;
             uint32_t ph = 0, acc_ph = 0;
             bool ok = true, issued = false;
-            for (int g = gstart; g < total && ok; g += gstep) {
-                const int split = g / (mt * nt);
-                int left = k_first(split + 1) - k_first(split);
-                while (left > 0 && ok) {
-                    const int n = min(left, kSumBlocks);
-                    left -= n;
-                    if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
-                    const uint32_t d = tmem + (uint32_t)(acc * kBN);
-                    uint32_t more = 0;
-                    for (int i = 0; i < n; i += 2) {
-                        const int s1 = stage + 1 == stages ? 0 : stage + 1;
-                        const uint32_t p1 = stage + 1 == stages ? ph ^ 1u : ph;
-                        const bool two = i + 1 < n;
-                        if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
-                        if (two && !tc::mbar_wait(full_bar(s1), p1, st, tmo, kSiteMmaFull)) { ok = false; break; }
-                        tc::fence_after_sync();
-                        mma4(d, stage, more);
-                        more = 1;
-                        tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
-                        stage = s1; ph = p1;
-                        if (two) {
-                            mma4(d, stage, 1);
+#pragma unroll 1
+            for (int j = 0; j < N && ok; ++j) {
+                const HeadGemm& p = jobs.job[j].p;
+                const HeadSize z = size_of(p);
+                const Range r = range_of(j, z);
+                const bool a_mn = N == 2 ? p.a_mn != 0 : A_MN;
+                idesc = tc::idesc_bf16(kBM, p.bn, a_mn, B_MN);
+                step_a = a_mn ? 128u : 2u;
+                al0 = a_tile(0) >> 4 | (a_mn ? 512u : 1u) << 16;
+                for (int g = r.g0; g < r.g1 && ok; g += r.step) {
+                    const int split = g / (z.mt * z.nt);
+                    int left = k_first(p, z, split + 1) - k_first(p, z, split);
+                    while (left > 0 && ok) {
+                        const int n = min(left, kSumBlocks);
+                        left -= n;
+                        if (!tc::mbar_wait(acce_bar(acc), acc_ph ^ 1u, st, tmo, kSiteMmaAccEmpty)) { ok = false; break; }
+                        const uint32_t d = tmem + (uint32_t)(acc * kBN);
+                        uint32_t more = 0;
+                        for (int i = 0; i < n; i += 2) {
+                            const int s1 = stage + 1 == stages ? 0 : stage + 1;
+                            const uint32_t p1 = stage + 1 == stages ? ph ^ 1u : ph;
+                            const bool two = i + 1 < n;
+                            if (!tc::mbar_wait(full_bar(stage), ph, st, tmo, kSiteMmaFull)) { ok = false; break; }
+                            if (two && !tc::mbar_wait(full_bar(s1), p1, st, tmo, kSiteMmaFull)) { ok = false; break; }
+                            tc::fence_after_sync();
+                            mma4(d, stage, more);
+                            more = 1;
                             tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
-                            if (++stage == stages) { stage = 0; ph ^= 1u; }
+                            stage = s1; ph = p1;
+                            if (two) {
+                                mma4(d, stage, 1);
+                                tc::mma_commit_2sm_multicast(empty_bar(stage), (uint16_t)0x3);
+                                if (++stage == stages) { stage = 0; ph ^= 1u; }
+                            }
                         }
+                        issued = true;
+                        if (!ok) break;
+                        tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
+                        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
                     }
-                    issued = true;
-                    if (!ok) break;
-                    tc::mma_commit_2sm_multicast(accf_bar(acc), (uint16_t)0x3);
-                    if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
                 }
             }
             if (!ok && issued) {
@@ -372,13 +445,24 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
         }
     } else {
-        if (p.early) pdl_wait();
+        if (p0.early) pdl_wait();
         const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quadrant, half of the tile's columns
-        const int cols = p.bn / 2;
-        // 32 rows x 128 bytes are put down by row (a thread each) and taken up by eighths of a row, so that a
-        // store instruction writes four whole 128-byte lines (a thread writing its own row touches 32 lines with
-        // each)
+        // 32 rows x 128 bytes are put down by row (a thread each), in the 128-byte swizzle, and leave as one box;
+        // or they are taken up by eighths of a row, so that a store instruction writes four whole 128-byte lines (a
+        // thread writing its own row touches 32 lines with each).
         const uint32_t pass = smem_base + kStageOutOffset + (uint32_t)(warp - 2) * kPassBytes;
+        auto begin_pass = [&]() {
+            if (lane == 0) tc::bulk_wait_read<0>();   // the box that left from here before
+            __syncwarp();
+        };
+        auto send_pass = [&](const HeadJob& J, int x, int y, int z) {
+            tc::fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                tc::tma_store_3d(&J.out, pass, x, y, z);
+                tc::bulk_commit();
+            }
+        };
         auto put = [&](int eighth, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             tc::st_shared_v4(pass + lane * 128 + ((eighth ^ (lane & 7)) << 4), a, b, c, d);
         };
@@ -391,9 +475,18 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         };
         int acc = 0;
         uint32_t acc_ph = 0;
-        for (int g = gstart; g < total; g += gstep) {
-            const Tile t = head_tile(g, mt, nt, p.group);
-            const int blocks = k_first(t.split + 1) - k_first(t.split);
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < N && ok; ++j) {
+        const HeadJob& J = jobs.job[j];
+        const HeadGemm& p = J.p;
+        const HeadSize z = size_of(p);
+        const Range range = range_of(j, z);
+        const int M = z.M, cols = p.bn / 2;
+        const bool all = z.all;
+        for (int g = range.g0; g < range.g1; g += range.step) {
+            const Tile t = head_tile(g, z.mt, z.nt, p.group);
+            const int blocks = k_first(p, z, t.split + 1) - k_first(p, z, t.split);
             const int row0 = t.m * kBM + rank * 128 + q * 32, row = row0 + lane;
             const int col0 = t.n * p.bn + half * cols;
             const int nv = min(cols, p.N - col0);         // valid columns; none: <= 0
@@ -404,9 +497,8 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             float label_at_lse = 0.f;                     // its label's logit less its log-sum
             int orow = in ? row : -1;                     // its output row
             bool dead = false;
-            // dl: rows behind the last live token, up to the tile's end, are zeros where the live ones are
-            // counted on the device: dW's last K block reads some of them
-            const int row_end = p.m_live ? 1 << 30 : M;
+            // (dl: rows behind the last live token, up to the tile's end, are written as zeros: dW's last K block
+            // reads some of them)
             if constexpr (EPI != kEpiOut) {
                 if (in) {
                     const int64_t tok = p.rows && !all ? p.rows[row] : row;
@@ -428,12 +520,12 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
                 // 64 columns at a time: tensor memory, registers, staging, memory
                 if (blocks > 0) {
-                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) break;
+                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
                     __syncwarp();
                     tc::fence_after_sync();
                 }
                 const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
-                const int64_t at = t.split * p.split_stride + col0;
+                const int64_t at = col0;
                 int o[8];                           // output rows of this lane's eighths
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
@@ -459,6 +551,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (64 * h >= nv) continue;
                     uint4 v[8];
                     if constexpr (EPI == kEpiDl) {
+                        begin_pass();
 #pragma unroll
                         for (int e8 = 0; e8 < 8; ++e8) {
                             uint32_t w[4];
@@ -476,18 +569,11 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         if (lab >= 0 && j >= 0 && j < 64)
                             st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
                                         __float2bfloat16_rn(mul * expm1f(label_at_lse)));
-                        __syncwarp();
-                        take(0, v);
-                        const int cc = 64 * h + 8 * (lane & 7);
-                        __nv_bfloat16* to = p.dl + (int64_t)(row0 + (lane >> 3)) * p.ld_dl + col0 + cc;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (row0 + 4 * i + (lane >> 3) < row_end && cc < nv)
-                                *reinterpret_cast<uint4*>(to + 4 * i * p.ld_dl) = v[i];
-                        __syncwarp();
+                        if (row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
                         continue;
                     }
                     if (!p.out_f32 && !p.add) {
+                        begin_pass();
 #pragma unroll
                         for (int e8 = 0; e8 < 8; ++e8) {
                             uint32_t w[4];
@@ -497,6 +583,10 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                 w[i] = dead ? 0u : pack_bf16x2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
                             }
                             put(e8, w[0], w[1], w[2], w[3]);
+                        }
+                        if (p.tma_out) {
+                            if (row0 < M) send_pass(J, col0 + 64 * h, row0, 0);
+                            continue;
                         }
                         __syncwarp();
                         take(0, v);
@@ -511,10 +601,15 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {      // 32 fp32 columns, 128 bytes of a row
                         const int cc = 64 * h + 32 * c + 4 * (lane & 7);
+                        begin_pass();
 #pragma unroll
                         for (int e8 = 0; e8 < 8; ++e8)
                             put(e8, __float_as_uint(r[c][4 * e8]), __float_as_uint(r[c][4 * e8 + 1]),
                                 __float_as_uint(r[c][4 * e8 + 2]), __float_as_uint(r[c][4 * e8 + 3]));
+                        if (p.tma_out) {
+                            if (row0 < M && 64 * h + 32 * c < nv) send_pass(J, col0 + 64 * h + 32 * c, row0, t.split);
+                            continue;
+                        }
                         __syncwarp();
                         take(0, v);
 #pragma unroll
@@ -539,7 +634,6 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 continue;
             } else {
             float r[4][32];
-            bool ok = true;
             for (int b0 = 0; b0 < blocks; b0 += min(kSumBlocks, blocks - b0)) {
                 if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
                 __syncwarp();
@@ -594,6 +688,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {      // 64 columns, 128 bytes of a row
                     if (64 * h >= nv) break;
+                    if constexpr (EPI != kEpiStats) begin_pass();
 #pragma unroll
                     for (int e8 = 0; e8 < 8; ++e8) {
                         uint32_t w[4];
@@ -609,21 +704,7 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         }
                         if (EPI != kEpiStats) put(e8, w[0], w[1], w[2], w[3]);
                     }
-                    if constexpr (EPI != kEpiStats) {
-                        __syncwarp();
-                        const int cc = 64 * h + 8 * (lane & 7);
-                        __nv_bfloat16* o = p.dl + (int64_t)(row0 + (lane >> 3)) * p.ld_dl + col0 + cc;
-#pragma unroll
-                        for (int i0 = 0; i0 < 8; i0 += 4) {
-                            uint4 v[4];
-                            take(i0, v);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (row0 + 4 * (i0 + i) + (lane >> 3) < row_end && cc < nv)
-                                    *reinterpret_cast<uint4*>(o + 4 * (i0 + i) * p.ld_dl) = v[i];
-                        }
-                        __syncwarp();
-                    }
+                    if (EPI != kEpiStats && row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
                 }
                 if (in) {
                     const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
@@ -632,8 +713,10 @@ head_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
             }
         }
+        }
     }
-    if (p.wait_late && threadIdx.x == 0) pdl_wait();
+    if (EPI != kEpiStats && warp >= 2 && lane == 0) tc::bulk_wait<0>();   // every box has left and arrived
+    if (p0.wait_late && threadIdx.x == 0) pdl_wait();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -865,6 +948,7 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 // The same with a gradient: then the row's exponentials, in their place, become
 //   dl[v] = c e[v] exp(top of its columns - lse),   dl[label] = -c others / (others + own)
 // and zeros for a token without a label (rows == NULL; else only live tokens are here).
+// Few rows are cut along the vocabulary (gridDim.y), each part joining the sums itself.
 __global__ void __launch_bounds__(kRowThreads)
 head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, const uint4* __restrict__ x, int64_t ldx,
                const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
@@ -885,9 +969,11 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, 
     else if (on) own = cta_sum(label_dot(x + t * ldx, W + (int64_t)label * nv, nv, threadIdx.x, kRowThreads), red + 96);
     pdl_wait();
     __nv_bfloat16* row = dl + i * ld;
+    const int vecs = (V + 7) / 8, per = (vecs + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int v0 = (int)blockIdx.y * per, v1 = min(v0 + per, vecs);
     if (!on) {
-        for (int v = 8 * threadIdx.x; v < V; v += 8 * kRowThreads) *reinterpret_cast<uint4*>(row + v) = make_uint4(0, 0, 0, 0);
-        if (threadIdx.x == 0) {
+        for (int v = v0 + threadIdx.x; v < v1; v += kRowThreads) *reinterpret_cast<uint4*>(row + 8 * v) = make_uint4(0, 0, 0, 0);
+        if (threadIdx.x == 0 && blockIdx.y == 0) {
             loss[t] = 0.f;
             if (lse) lse[t] = 0.f;
         }
@@ -900,7 +986,7 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, 
     const float inv = coef / sum * kRootScale;
     const int tile = stat_cols / 8;
 #pragma unroll 4
-    for (int v = threadIdx.x; 8 * v < V; v += kRowThreads) {
+    for (int v = v0 + threadIdx.x; v < v1; v += kRowThreads) {
         const uint4 e = __ldcg(reinterpret_cast<const uint4*>(row + 8 * v));
         const float f = inv * exp2_approx((__ldcg(st + v / tile).x - r.top) * kLog2e);
         const uint32_t w[4] = {e.x, e.y, e.z, e.w};
@@ -913,29 +999,29 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, 
         *reinterpret_cast<uint4*>(row + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
         if (label >> 3 == v) row[label] = __float2bfloat16_rn(-coef * (r.others / sum));
     }
-    if (threadIdx.x != 0) return;
+    if (threadIdx.x != 0 || blockIdx.y != 0) return;
     loss[t] = row_loss(r, own);
     if (lse) lse[t] = r.top + logf(sum);
 }
 
 // dx rows from the parts of K, added up in order, four columns a thread; without a
-// list of rows, a token without a label gets zeros.
-__global__ void __launch_bounds__(256)
-head_join_kernel(const float4* __restrict__ part, int64_t stride, int splits, int nq, const int32_t* __restrict__ rows,
+// list of rows, a token without a label gets zeros. A kernel of dW's own is launched
+// behind this one and needs nothing of it, so it may begin at once.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
+head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, const int32_t* __restrict__ rows,
                  const int32_t* __restrict__ live, const void* labels, int i64, int V, uint2* __restrict__ dx) {
-    pdl_wait();
     pdl_allow_next();
-    const int64_t i = blockIdx.x;
-    if (live && i >= *live) return;
-    const int64_t t = rows ? rows[i] : i;
-    const bool on = rows || is_live(labels, i64, t, V);
-    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nq; v += gridDim.y * blockDim.x) {
+    pdl_wait();
+    const int64_t total = (int64_t)(live ? *live : n) * nq;
+    for (int64_t at = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; at < total; at += (int64_t)gridDim.x * kJoinThreads) {
+        const int i = (int)(at / nq), v = (int)(at % nq);
+        const int64_t t = rows ? rows[i] : i;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            const float4* q = part + i * nq + v;
+        if (rows || is_live(labels, i64, t, V)) {
 #pragma unroll 8
             for (int s = 0; s < splits; ++s) {
-                const float4 b = __ldcg(q + s * stride);
+                const float4 b = __ldcg(part + s * stride + at);
                 a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
             }
         }
@@ -985,10 +1071,23 @@ bool make_tmap_groups(CUtensorMap* m, const void* base, int64_t rows, int64_t gr
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What an epilogue writes: [parts][rows][cols] of 2- or 4-byte elements, row pitch ld, in boxes of 32 rows x 128 bytes.
+bool make_tmap_out(CUtensorMap* m, void* base, int bytes, int64_t parts, int64_t rows, int64_t cols, int64_t ld) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    cuuint64_t strides[2] = {(cuuint64_t)(ld * bytes), (cuuint64_t)(rows * ld * bytes)};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / bytes), 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Pairs of CTAs of a kernel that can be resident at once, asked once per kernel and
 // device.
-template <bool A_MN, bool B_MN, int EPI>
-int resident_pairs(void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, HeadGemm), cudaLaunchConfig_t cfg, int num_sms) {
+template <bool A_MN, bool B_MN, int EPI, int N>
+int resident_pairs(void (*kern)(HeadJobs<N>), cudaLaunchConfig_t cfg, int num_sms) {
     static std::atomic<int> known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -1010,28 +1109,52 @@ struct Operand {
     int64_t rows, cols, ld;
 };
 
-// One product. `all`: the operand that replaces A (logits) or B (dW) when every token is
-// live. Boxes: 64 columns x 64 rows of K where the operand is MN-major, else a CTA's rows.
-template <bool A_MN, bool B_MN, int EPI>
-cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all, HeadGemm& p, int num_sms,
-                          cudaStream_t s) {
+// A product's maps and ring. `all`: the operand that replaces A (logits) or B (dW) when
+// every token is live. Boxes: two groups of 64 columns x 64 rows of K where the operand is
+// MN-major, else a CTA's rows.
+bool make_job(HeadJob& J, bool a_mn, bool b_mn, int epi, const Operand& a, const Operand& b, const Operand& all,
+              const HeadGemm& params) {
+    J.p = params;
+    HeadGemm& p = J.p;
     // up to 128 rows (of a count that the host knows): boxes of as many, and a longer ring. 128-row boxes that are
-    // mostly outside the tensor took as long as full ones (T = 1, H = 1024, V = 32768: 25.9 us, this ...)
-    const int rows = !A_MN && !p.m_live && p.M <= 128 ? (int)align_up(p.M, 8) : 128;
-    p.a_bytes = rows * kBK * 2;
-    p.stages = std::min(kMaxStages, kBarOffset / (p.a_bytes + kOperandBytes));
-    p.a_groups = A_MN && a.cols % 64 == 0;
-    p.b_groups = B_MN && b.cols % 64 == 0;
+    // mostly outside the tensor took as long as full ones (T = 1, H = 1024, V = 32768: 25.9 us, this 19.7)
+    const int rows = !a_mn && !p.m_live && p.M <= 128 ? (int)align_up(p.M, 8) : 128;
+    p.a_mn = a_mn;
+    p.a_bytes = p.a_room = rows * kBK * 2;
+    p.stages = std::min(kMaxStages, kBarOffset / (p.a_room + kOperandBytes));
+    p.a_groups = a_mn && a.cols % 64 == 0;
+    p.b_groups = b_mn && b.cols % 64 == 0;
     auto map = [](CUtensorMap* m, const Operand& o, bool groups, int box_rows) {
         return groups ? make_tmap_groups(m, o.base, o.rows, o.cols / 64, o.ld)
                       : make_tmap_pitch(m, o.base, o.rows, o.cols, o.ld, box_rows);
     };
-    const int box_a = A_MN ? kBK : rows, box_b = B_MN ? kBK : p.bn / 2;
-    CUtensorMap ta, tb, tall;
-    if (!map(&ta, a, p.a_groups, box_a) || !map(&tb, b, p.b_groups, box_b) ||
-        !(EPI == kEpiOut ? map(&tall, all, p.b_groups, box_b) : map(&tall, all, false, box_a)))
-        return cudaErrorInvalidValue;
-    auto kern = head_gemm_kernel<A_MN, B_MN, EPI>;
+    const int box_a = a_mn ? kBK : rows, box_b = b_mn ? kBK : p.bn / 2;
+    if (!map(&J.a, a, p.a_groups, box_a) || !map(&J.b, b, p.b_groups, box_b)) return false;
+    if (epi == kEpiOut ? !map(&J.all, all, p.b_groups, box_b) : !map(&J.all, all, false, box_a)) return false;
+    p.tma_out = epi != kEpiOut || (!p.out_rows && !p.add && !p.zero_dead);
+    J.out = J.a;
+    if (epi == kEpiExp || epi == kEpiDl) return make_tmap_out(&J.out, p.dl, 2, 1, p.dl_rows, p.ld_dl, p.ld_dl);
+    if (epi == kEpiOut && p.tma_out) return make_tmap_out(&J.out, p.out, p.out_f32 ? 4 : 2, p.splits, p.M, p.N, p.N);
+    return true;
+}
+
+int64_t tiles_of(const HeadGemm& p) { return (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, p.bn) * p.splits; }
+
+// Cycles of a tile of dX and of dW, about 700 a K block and 4000 at least for the latter's
+// way out, and of each pair where all share both products.
+double dx_tile_cycles(const HeadGemm& x) { return 700.0 * ceil_div(x.K, kBK) / x.splits; }
+double dw_tile_cycles(const HeadGemm& w) { return std::max(700 * ceil_div(w.K, kBK), 4000); }
+double pair_cycles(const HeadGemm& x, const HeadGemm& w, int pairs) {
+    return (tiles_of(x) * dx_tile_cycles(x) + tiles_of(w) * dw_tile_cycles(w)) / std::max(pairs, 1);
+}
+// Up to here dX and dW go in one launch: a launch less counts for more than what the
+// fixed shares lose (T = 100, H = 512, V = 8191: 30.6 us in one launch, 33.1 in two;
+// T = 700, H = 1000, V = 20000: 119 and 114).
+constexpr double kOneLaunchCycles = 2e4;
+
+template <bool A_MN, bool B_MN, int EPI, int N>
+cudaError_t launch_jobs(HeadJobs<N>& jobs, int num_sms, cudaStream_t s) {
+    auto kern = head_gemm_kernel<A_MN, B_MN, EPI, N>;
     ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -1044,14 +1167,34 @@ cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
-    const int64_t tiles = (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, p.bn) * p.splits;
-    const int pairs = (int)std::min<int64_t>(tiles, resident_pairs<A_MN, B_MN, EPI>(kern, cfg, num_sms));
+    int pairs = resident_pairs<A_MN, B_MN, EPI, N>(kern, cfg, num_sms);
+    if constexpr (N == 1) {
+        pairs = (int)std::min<int64_t>(tiles_of(jobs.job[0].p), pairs);
+    } else {
+        // the pairs with a tile of dX take as many fewer of dW's as that one costs
+        HeadGemm &x = jobs.job[0].p, &w = jobs.job[1].p;
+        x.a_room = w.a_room;
+        x.stages = w.stages;
+        const int64_t tiles = tiles_of(w);
+        jobs.lead = (int)std::min<int64_t>(tiles_of(x), pairs);
+        const double cx = dx_tile_cycles(x), cw = dw_tile_cycles(w), each = pair_cycles(x, w, pairs);
+        jobs.lead_tiles = jobs.lead == pairs ? (int)tiles
+                                             : (int)std::min<double>(tiles, std::max(0.0, (each - cx) / cw * jobs.lead));
+    }
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3(2 * pairs);
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tall, p);
+    return cudaLaunchKernelEx(&cfg, kern, jobs);
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+cudaError_t run_head_gemm(const Operand& a, const Operand& b, const Operand& all, const HeadGemm& p, int num_sms,
+                          cudaStream_t s) {
+    HeadJobs<1> jobs{};
+    if (!make_job(jobs.job[0], A_MN, B_MN, EPI, a, b, all, p)) return cudaErrorInvalidValue;
+    return launch_jobs<A_MN, B_MN, EPI, 1>(jobs, num_sms, s);
 }
 
 constexpr int kGroup = 16;              // row tiles of the walk's groups
@@ -1062,10 +1205,10 @@ constexpr int kPlainRows = kBM;
 
 // Columns of the logits' tiles: the width whose rounds over all pairs load the least
 // (a K block of a tile brings 256 rows of x and bn of W to a pair).
-int logit_columns(int tokens, int V, int pairs) {
+int logit_columns(int tokens, int V, int pairs, bool boxes) {
     int best = kBN;
     int64_t least = 0;
-    for (int bn = kBN; bn >= 128; bn -= 32) {
+    for (int bn = kBN; bn >= 128; bn -= boxes ? 128 : 32) {   // boxes: halves of whole 64-column boxes
         const int64_t tiles = (int64_t)ceil_div(tokens, kBM) * ceil_div(V, bn);
         const int64_t cost = (tiles + pairs - 1) / std::max(pairs, 1) * (kBM + bn);
         if (bn == kBN || cost < least) {
@@ -1089,12 +1232,16 @@ int piece_tokens(int T, int V, int want) {
     return (int)std::min<int64_t>(most, align_up((T + pieces - 1) / pieces, kBM));
 }
 
-// Parts of the vocabulary for dX: where the tiles alone leave most pairs without
-// work, as many as fill them, each of 8 K blocks at least.
+// Parts of the vocabulary for dX where its tiles alone leave most pairs without work: as
+// many as give each pair one, of 8 K blocks at least.
 int dx_splits(int tokens, int H, int V, int pairs) {
-    const int tiles = ceil_div(tokens, kBM) * ceil_div(H, kBN), kbs = ceil_div(V, kBK);
-    if (2 * tiles > pairs) return 1;
-    return std::max(1, std::min(pairs / tiles, kbs / 8));
+    const int tiles = ceil_div(tokens, kBM) * ceil_div(H, kBN);
+    return 2 * tiles > pairs ? 1 : std::max(1, std::min(pairs / tiles, ceil_div(V, kBK) / 8));
+}
+
+// Parts of a row for head_dl_kernel: three CTAs an SM, each with a vector a thread at least.
+int dl_parts(int rows, int V) {
+    return std::max(1, std::min(3 * sm_count() / rows, ceil_div(V, 8 * kRowThreads)));
 }
 
 struct HeadLayout {
@@ -1192,11 +1339,12 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         p.stats = stats;
         p.dl = dl;
         p.ld_dl = pitch_dl(V);
+        p.dl_rows = gather ? cap : n;
         p.M = n;
         p.m_live = gather;
         p.N = V;
         p.K = H;
-        p.bn = logit_columns(n, V, c.num_sms / 2);
+        p.bn = logit_columns(n, V, c.num_sms / 2, grad);
         p.stat_tiles = ceil_div(V, p.bn / 2);
         p.early = gather ? kEarlyNone : kEarlyA | kEarlyB;
         const Operand ox{x, n, H, a.ldx}, ow{a.W, V, H, H};
@@ -1213,7 +1361,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         if (forward) {
             e = run_head_gemm<false, false, kEpiExp>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
-                e = launch_after(head_dl_kernel, dim3(n), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
+                e = launch_after(head_dl_kernel, dim3(n, dl_parts(n, V)), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
                                  p.bn / 2, xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live,
                                  (const float*)label, labels, a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
         } else {
@@ -1222,55 +1370,64 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         if (e != cudaSuccess) return e;
         p.bn = kBN;
         p.early = kEarlyNone;
-        const Operand odl{dl, gather ? cap : n, V, p.ld_dl};
+        const Operand odl{dl, p.dl_rows, V, p.ld_dl};
         const int splits = L.splits;
+        HeadGemm px = p, pw = p;
         if (dx) {
-            HeadGemm q = p;
-            q.N = H;
-            q.K = V;
-            q.splits = splits;
-            q.early = gather ? kEarlyNone : kEarlyB;
+            px.N = H;
+            px.K = V;
+            px.splits = splits;
+            px.early = gather ? kEarlyNone : kEarlyB;
             if (splits > 1) {
-                q.out = ws + L.part;
-                q.out_f32 = 1;
-                q.split_stride = (int64_t)n * H;
+                px.out = ws + L.part;
+                px.out_f32 = 1;
             } else {
-                q.out = dx;
-                q.out_rows = rows;
-                q.zero_dead = !gather;
-                q.live_below = V;
+                px.out = dx;
+                px.out_rows = rows;
+                px.zero_dead = !gather;
+                px.live_below = V;
             }
-            e = run_head_gemm<false, true, kEpiOut>(odl, ow, ow, q, c.num_sms, s);
-            if (e != cudaSuccess) return e;
         }
+        // dl's rows are padded to whole groups; what lies behind V belongs to rows of dW that there are not
+        const Operand odl64{dl, odl.rows, p.ld_dl, p.ld_dl}, clean{xc, n, H, H};
+        const Operand &owx = gather ? oxc : clean, &owall = gather ? ox : clean;
         if (a.dW) {
-            HeadGemm q = p;
-            const Operand clean{xc, n, H, H};
-            q.M = V;
-            q.N = H;
-            q.K = n;
-            q.m_live = 0;
-            q.k_live = gather;
-            // dl and x were complete before dX's kernel began
-            q.wait_late = dx != nullptr;
+            pw.M = V;
+            pw.N = H;
+            pw.K = n;
+            pw.m_live = 0;
+            pw.k_live = gather;
             // over several pieces the sum goes on in fp32 until the last one
             const bool first = t0 == 0, last = t0 + n >= T;
             float* acc = a.dW_f32 ? static_cast<float*>(a.dW) : reinterpret_cast<float*>(ws + L.acc);
-            q.out_f32 = a.dW_f32 || !last;
-            q.out = q.out_f32 ? (void*)acc : a.dW;
-            q.add = first && !(a.dW_f32 && a.accumulate) ? nullptr : acc;
-            // dl's rows are padded to whole groups; what lies behind V belongs to rows of dW that there are not
-            const Operand odl64{dl, odl.rows, p.ld_dl, p.ld_dl};
-            e = run_head_gemm<true, true, kEpiOut>(odl64, gather ? oxc : clean, gather ? ox : clean, q, c.num_sms, s);
-            if (e != cudaSuccess) return e;
+            pw.out_f32 = a.dW_f32 || !last;
+            pw.out = pw.out_f32 ? (void*)acc : a.dW;
+            pw.add = first && !(a.dW_f32 && a.accumulate) ? nullptr : acc;
         }
-        if (dx && splits > 1) {
-            const int nq = H / 4, threads = std::min(256, ceil_div(nq, 32) * 32);
-            e = launch_after(head_join_kernel, dim3(n, ceil_div(nq, threads)), dim3(threads), 0, s,
-                             (const float4*)(ws + L.part), (int64_t)n * nq, splits, nq, (const int32_t*)rows,
-                             (const int32_t*)live, labels, a.labels_i64, V, reinterpret_cast<uint2*>(dx));
-            if (e != cudaSuccess) return e;
+        auto join = [&]() {
+            const int nq = H / 4;
+            const int ctas = (int)std::min<int64_t>(((int64_t)n * nq + kJoinThreads - 1) / kJoinThreads, 3 * sm_count());
+            return launch_after(head_join_kernel, dim3(ctas), dim3(kJoinThreads), 0, s, (const float4*)(ws + L.part),
+                                (int64_t)n * nq, splits, n, nq, (const int32_t*)rows, (const int32_t*)live, labels,
+                                a.labels_i64, V, reinterpret_cast<uint2*>(dx));
+        };
+        if (dx && a.dW && splits > 1 && pair_cycles(px, pw, c.num_sms / 2) < kOneLaunchCycles) {
+            HeadJobs<2> jobs{};
+            if (!make_job(jobs.job[0], false, true, kEpiOut, odl, ow, ow, px) ||
+                !make_job(jobs.job[1], true, true, kEpiOut, odl64, owx, owall, pw))
+                return cudaErrorInvalidValue;
+            e = launch_jobs<false, true, kEpiOut, 2>(jobs, c.num_sms, s);
+            if (e == cudaSuccess) e = join();
+        } else {
+            if (dx) e = run_head_gemm<false, true, kEpiOut>(odl, ow, ow, px, c.num_sms, s);
+            if (e == cudaSuccess && dx && splits > 1) e = join();
+            if (a.dW && e == cudaSuccess) {
+                // dl and x were complete before dX's kernel let the next ones begin
+                pw.wait_late = dx != nullptr;
+                e = run_head_gemm<true, true, kEpiOut>(odl64, owx, owall, pw, c.num_sms, s);
+            }
         }
+        if (e != cudaSuccess) return e;
     }
     return e;
 }
