@@ -141,14 +141,16 @@ __device__ double chunk_squares(const void* base, int64_t n, int64_t c0) {
     return total;
 }
 
-__device__ __forceinline__ double block_sum_f64(double v, double* red) {
+// Sum of a value per thread, in the CTA's first thread (fixed order). FP64 arithmetic is
+// slow here, two lanes a cycle for the whole SM, so one warp does it: by shuffles in every
+// warp this took 1.3 us of a small call.
+__device__ __forceinline__ double cta_sum_f64(double v, double* all) {
+    all[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+    v = 0.0;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    const int lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < kGradThreads / 32 ? red[lane] : 0.0;
+    for (int i = 0; i < kGradThreads / 32; ++i) v += all[threadIdx.x + 32 * i];
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
@@ -157,7 +159,7 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red) {
 // part[b] = (add ? part[b] : 0) + the squares of CTA b's chunks
 __global__ void __launch_bounds__(kGradThreads, 2)
 grad_squares_kernel(const __grid_constant__ GradTable t, double* part, int add) {
-    __shared__ double red[32];
+    __shared__ double all[kGradThreads];
     pdl_wait();
     pdl_allow_next();
     const int chunks = t.first[t.count];
@@ -171,74 +173,105 @@ grad_squares_kernel(const __grid_constant__ GradTable t, double* part, int add) 
         else if (elem == MOK_ELEM_F16) s += chunk_squares<MOK_ELEM_F16>(t.g[i], n, c0);
         else s += chunk_squares<MOK_ELEM_BF16>(t.g[i], n, c0);
     }
-    s = block_sum_f64(s, red);
+    s = cta_sum_f64(s, all);
     if (threadIdx.x == 0) part[blockIdx.x] = (add ? part[blockIdx.x] : 0.0) + s;
 }
 
-// sqrt of the sum of all partial sums, the same in every CTA.
-__device__ double norm_of(const double* part, int parts, double* red) {
+// sqrt of the sum of all partial sums, in the CTA's first warp, the same in every CTA.
+__device__ __forceinline__ double norm_of(const double* part, int parts) {
     double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kGradThreads) s += part[i];
-    return sqrt(block_sum_f64(s, red));
+    for (int i = threadIdx.x; i < parts; i += 32) s += __ldcg(part + i);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return threadIdx.x == 0 ? sqrt(s) : 0.0;
 }
 
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(32)
 grad_norm_kernel(const double* part, int parts, float* norm) {
-    __shared__ double red[32];
     pdl_wait();
     pdl_allow_next();
-    const double v = norm_of(part, parts, red);
+    const double v = norm_of(part, parts);
     if (threadIdx.x == 0) *norm = (float)v;
 }
 
-template <int ELEM>
-__device__ void scale_chunk(const void* src, void* dst, int64_t n, int64_t c0, float c) {
-    constexpr int kPer = ELEM == MOK_ELEM_F32 ? 4 : 8;
-    const int64_t e0 = c0 * (kChunkBytes / (16 / kPer));
-    const int64_t left = min(n - e0, (int64_t)kChunkBytes / (16 / kPer));
-    if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
-        const uint4* v = reinterpret_cast<const uint4*>(src) + e0 / kPer;
-        uint4* o = reinterpret_cast<uint4*>(dst) + e0 / kPer;
-        const int nv = (int)(left / kPer);
-        uint4 a[kGradVecs];
+// A CTA's chunk: where it is, and its vectors on their way (aligned tensors).
+struct Chunk {
+    const void* src;
+    void* dst;
+    int64_t e0;        // first element
+    int left;          // elements
+    int elem;
+    bool vec;
+    uint4 a[kGradVecs];
+};
+
+__device__ __forceinline__ void load_chunk(const GradTable& t, int k, Chunk& c) {
+    const int i = tensor_of(t, k);
+    c.src = t.g[i];
+    c.dst = t.out[i];
+    c.elem = (int)(t.n[i] & 3);
+    const int per = c.elem == MOK_ELEM_F32 ? 4 : 8;
+    c.e0 = (int64_t)(k - t.first[i]) * (kChunkBytes / 16 * per);
+    c.left = (int)min((t.n[i] >> 2) - c.e0, (int64_t)kChunkBytes / 16 * per);
+    c.vec = ((reinterpret_cast<uintptr_t>(c.src) | reinterpret_cast<uintptr_t>(c.dst)) & 15) == 0;
+    if (!c.vec) return;
+    const uint4* v = reinterpret_cast<const uint4*>(c.src) + c.e0 / per;
+    const int nv = c.left / per;
 #pragma unroll
-        for (int i = 0; i < kGradVecs; ++i) {
-            const int j = threadIdx.x + i * kGradThreads;
-            if (j < nv) a[i] = v[j];
-        }
-#pragma unroll
-        for (int i = 0; i < kGradVecs; ++i) {
-            const int j = threadIdx.x + i * kGradThreads;
-            if (j < nv)
-                o[j] = make_uint4(scale_word<ELEM>(a[i].x, c), scale_word<ELEM>(a[i].y, c),
-                                  scale_word<ELEM>(a[i].z, c), scale_word<ELEM>(a[i].w, c));
-        }
-        const int64_t t = (int64_t)nv * kPer + threadIdx.x;
-        if (t < left) put_elem<ELEM>(dst, e0 + t, elem_at<ELEM>(src, e0 + t) * c);
-    } else {
-        for (int64_t i = threadIdx.x; i < left; i += kGradThreads)
-            put_elem<ELEM>(dst, e0 + i, elem_at<ELEM>(src, e0 + i) * c);
+    for (int j = 0; j < kGradVecs; ++j) {
+        const int at = threadIdx.x + j * kGradThreads;
+        if (at < nv) c.a[j] = v[at];
     }
 }
 
+template <int ELEM>
+__device__ __forceinline__ void scale_chunk(const Chunk& c, float f) {
+    constexpr int kPer = ELEM == MOK_ELEM_F32 ? 4 : 8;
+    int from = 0;
+    if (c.vec) {
+        uint4* o = reinterpret_cast<uint4*>(c.dst) + c.e0 / kPer;
+        const int nv = c.left / kPer;
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+            const int at = threadIdx.x + j * kGradThreads;
+            if (at < nv)
+                o[at] = make_uint4(scale_word<ELEM>(c.a[j].x, f), scale_word<ELEM>(c.a[j].y, f),
+                                   scale_word<ELEM>(c.a[j].z, f), scale_word<ELEM>(c.a[j].w, f));
+        }
+        from = nv * kPer;
+    }
+    for (int i = from + threadIdx.x; i < c.left; i += kGradThreads)
+        put_elem<ELEM>(c.dst, c.e0 + i, elem_at<ELEM>(c.src, c.e0 + i) * f);
+}
+
+// The first chunk is loaded while the norm is still being formed: the gradients were
+// complete before the kernel that sums them began. (A small call: ...)
 __global__ void __launch_bounds__(kGradThreads, 2)
 grad_scale_kernel(const __grid_constant__ GradTable t, const double* part, int parts, double max_norm, float* norm) {
-    __shared__ double red[32];
-    pdl_wait();
+    __shared__ float factor;
     pdl_allow_next();
-    const double v = norm_of(part, parts, red);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-    const double ratio = max_norm / (v + MOK_CLIP_EPS);
-    const float c = ratio >= 1.0 ? 1.0f : (float)ratio;   // NaN stays NaN
-    for (int k = t.first[t.count] - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
-        const int i = tensor_of(t, k);
-        if (c == 1.0f && t.out[i] == t.g[i]) continue;
-        const int64_t n = t.n[i] >> 2;
-        const int elem = (int)(t.n[i] & 3);
-        const int64_t c0 = k - t.first[i];
-        if (elem == MOK_ELEM_F32) scale_chunk<MOK_ELEM_F32>(t.g[i], t.out[i], n, c0, c);
-        else if (elem == MOK_ELEM_F16) scale_chunk<MOK_ELEM_F16>(t.g[i], t.out[i], n, c0, c);
-        else scale_chunk<MOK_ELEM_BF16>(t.g[i], t.out[i], n, c0, c);
+    int k = t.first[t.count] - 1 - (int)blockIdx.x;
+    Chunk c;
+    if (k >= 0) load_chunk(t, k, c);
+    pdl_wait();
+    if (threadIdx.x < 32) {
+        const double v = norm_of(part, parts);
+        if (threadIdx.x == 0) {
+            if (blockIdx.x == 0) *norm = (float)v;
+            const double ratio = max_norm / (v + MOK_CLIP_EPS);
+            factor = ratio >= 1.0 ? 1.0f : (float)ratio;   // NaN stays NaN
+        }
+    }
+    __syncthreads();
+    const float f = factor;
+    while (k >= 0) {
+        if (f != 1.0f || c.dst != c.src) {
+            if (c.elem == MOK_ELEM_F32) scale_chunk<MOK_ELEM_F32>(c, f);
+            else if (c.elem == MOK_ELEM_F16) scale_chunk<MOK_ELEM_F16>(c, f);
+            else scale_chunk<MOK_ELEM_BF16>(c, f);
+        }
+        k -= gridDim.x;
+        if (k >= 0) load_chunk(t, k, c);
     }
 }
 
@@ -278,7 +311,7 @@ cudaError_t launch_grad_clip(int32_t count, const mok_grad_tensor* list, bool sc
     } while (e == cudaSuccess && i < count);
     if (!scale) {
         if (e == cudaSuccess)
-            e = launch_after(grad_norm_kernel, dim3(1), dim3(kGradThreads), 0, s, (const double*)part, grid, norm);
+            e = launch_after(grad_norm_kernel, dim3(1), dim3(32), 0, s, (const double*)part, grid, norm);
         return e;
     }
     i = 0;

@@ -593,19 +593,22 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped). Returns a dict of
     counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see mok_sort_layout)."""
     T, k = topk_idx.shape
-    dev = topk_idx.device
     _dense("topk_idx", topk_idx, torch.int32, T, k)
     if topk_idx.get_device() != torch._C._cuda_getDevice():
         raise AssertionError("topk_idx: on the current CUDA device expected")
+    n = T * k
     if out is None:
-        out = {n: torch.empty(s, dtype=torch.int32, device=dev)
-               for n, s in (("counts", E), ("offsets", E + 1), ("row_src", T * k), ("slot_row", T * k))}
-    for n, s in (("counts", E), ("offsets", E + 1), ("row_src", T * k), ("slot_row", T * k)):
-        _dense(n, out[n], torch.int32, s)
+        out = {name: torch.empty(size, dtype=torch.int32, device=topk_idx.device)
+               for name, size in (("counts", E), ("offsets", E + 1), ("row_src", n), ("slot_row", n))}
+    counts, offsets, row_src, slot_row = out["counts"], out["offsets"], out["row_src"], out["slot_row"]
+    _dense("counts", counts, torch.int32, E)
+    _dense("offsets", offsets, torch.int32, E + 1)
+    _dense("row_src", row_src, torch.int32, n)
+    _dense("slot_row", slot_row, torch.int32, n)
     if workspace is None:
-        workspace = alloc_bytes(sort_workspace_size(T, E, k), dev)
-    _check(lib().mok_sort_layout(_ptr(topk_idx), T, E, k, _ptr(out["counts"]), _ptr(out["offsets"]),
-                                 _ptr(out["row_src"]), _ptr(out["slot_row"]), _ptr(workspace), workspace.numel(),
+        workspace = alloc_bytes(sort_workspace_size(T, E, k), topk_idx.device)
+    _check(lib().mok_sort_layout(topk_idx.data_ptr(), T, E, k, counts.data_ptr(), offsets.data_ptr(),
+                                 row_src.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                  _stream(stream)), "mok_sort_layout")
     return out
 
@@ -633,8 +636,8 @@ def sort_rows(x, layout, out, stream=None):
     if step != 1 and T:
         raise AssertionError("x: adjacent row elements expected")
     _dense("out", out, x.dtype, T * k, H)
-    _check(lib().mok_sort_rows(_ptr(x), pitch if T > 1 else H, _ptr(slot), T, H, k, elem, _ptr(out), _stream(stream)),
-           "mok_sort_rows")
+    _check(lib().mok_sort_rows(x.data_ptr(), pitch if T > 1 else H, slot.data_ptr(), T, H, k, elem, out.data_ptr(),
+                               _stream(stream)), "mok_sort_rows")
     return out
 
 
@@ -645,8 +648,8 @@ def unsort_rows(y, layout, out, w=None, stream=None):
     _dense("out", out, out.dtype, T, H)
     _dense("y", y, out.dtype, T * k, H)
     _dense("w", w, torch.float32, T, k)
-    _check(lib().mok_unsort_rows(_ptr(y), _ptr(slot), _ptr(w), T, H, k, elem, _ptr(out), _stream(stream)),
-           "mok_unsort_rows")
+    _check(lib().mok_unsort_rows(y.data_ptr(), slot.data_ptr(), _addr(w), T, H, k, elem, out.data_ptr(),
+                                 _stream(stream)), "mok_unsort_rows")
     return out
 
 
@@ -659,8 +662,8 @@ def unsort_rows_backward(dout, y, layout, w, dy, dw, stream=None):
     _dense("dy", dy, dout.dtype, T * k, H)
     _dense("w", w, torch.float32, T, k)
     _dense("dw", dw, torch.float32, T, k)
-    _check(lib().mok_unsort_rows_backward(_ptr(dout), _ptr(y), _ptr(slot), _ptr(w), T, H, k, elem, _ptr(dy), _ptr(dw),
-                                          _stream(stream)), "mok_unsort_rows_backward")
+    _check(lib().mok_unsort_rows_backward(dout.data_ptr(), y.data_ptr(), slot.data_ptr(), w.data_ptr(), T, H, k, elem,
+                                          dy.data_ptr(), dw.data_ptr(), _stream(stream)), "mok_unsort_rows_backward")
 
 
 # --------------------------------------------------------------------------- loss of the vocabulary's head
