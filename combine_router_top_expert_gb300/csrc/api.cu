@@ -953,7 +953,7 @@ mok_status mok_unsort_rows_backward(const void* dout, const void* y, const int32
 
 size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, int32_t piece, const mok_config* cfg) {
     if (!head_dims_ok(T, H, V) || piece < 0) return 0;
-    return head_workspace_bytes(T, H, V, grad != 0, piece, make_common(nullptr, cfg).num_sms);
+    return head_workspace_bytes(T, H, V, grad != 0, piece, std::max(make_common(nullptr, cfg).num_sms, 2));
 }
 
 // Common checks and launch: `forward` writes loss and lse, `grad` dx and dW.
@@ -983,6 +983,7 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
     h.lse = a->lse;
     h.piece = a->piece;
     h.workspace = a->workspace;
+    h.withhold = cfg && (cfg->flags & MOK_FLAG_TEST_WITHHOLD_PUBLISH) ? 1 : 0;
     if (grad) {
         h.dloss = a->dloss;
         h.scale = a->scale;
@@ -991,7 +992,9 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
         h.dW_f32 = a->dW_f32 != 0;
         h.accumulate = a->accumulate != 0;
     }
-    return launch_status(launch_head(h, make_common(a->workspace, cfg), (cudaStream_t)stream));
+    GemmCommon c = make_common(a->workspace, cfg);
+    c.num_sms = std::max(c.num_sms, 2);   // a pair of CTAs at least
+    return launch_status(launch_head(h, c, (cudaStream_t)stream));
 }
 
 mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,

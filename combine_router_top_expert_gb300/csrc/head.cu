@@ -97,6 +97,7 @@ struct HeadGemm {
     const int32_t* out_rows;   // row -> output row, or NULL
     int zero_dead;          // rows whose label is not below live_below are zeros
     int live_below;
+    int withhold;           // test hook: the first pair's producers stop before the last K block of a tile
     StatusBlock* status;
     unsigned long long timeout_ns;
 };
@@ -139,6 +140,14 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t a, __nv_bfloat16 v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(v)) : "memory");
+}
+
+// After a wait that gave up: a phase that is to complete by what is already under way
+// (copies, MMAs), waited for whatever the abort flag says, for 10 ms at most.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!tc::mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 10000000ull) {
+    }
 }
 
 // Arrive on an mbarrier of the pair. What is released is tensor memory that was read;
@@ -330,7 +339,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
             if (p0.early) {
                 const HeadJob& J = jobs.job[0];
                 const HeadSize z = size_of(p0);
-                for (int g = pair; g < z.total && ahead < stages; g += pairs) {
+                for (int g = pair; g < z.total && ahead < stages && !(p0.withhold && pair == 0); g += pairs) {
                     const Tile t = head_tile(g, z.mt, z.nt, p0.group);
                     const int kend = k_first(p0, z, t.split + 1);
                     for (int kb = k_first(p0, z, t.split); kb < kend && ahead < stages; ++kb, ++ahead) {
@@ -353,6 +362,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                     const Tile t = head_tile(g, z.mt, z.nt, p.group);
                     const int kend = k_first(p, z, t.split + 1);
                     for (int kb = k_first(p, z, t.split); kb < kend; ++kb) {
+                        if (p0.withhold && pair == 0 && kb + 1 == kend) { ok = false; break; }
                         const bool begun = ahead > 0;   // only in the first round of stages, which are free
                         if (begun) {
                             --ahead;
@@ -368,9 +378,14 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 }
             }
             if (!ok) {
-                // let every copy already issued land before the CTA exits
-                for (int s = 0; s < stages; ++s)
-                    if (last_par[s] >= 0) tc::mbar_wait(full_bar(s), (uint32_t)last_par[s], st, tmo, kSiteDrain);
+                // every copy already issued lands before the pair exits: the leader sees it on its barriers, where
+                // both CTAs' bytes arrive; the time covers those of a stage that the other CTA never reached
+                if (rank == 0)
+                    for (int s = 0; s < stages; ++s)
+                        if (last_par[s] >= 0) drain_wait(full_bar(s), (uint32_t)last_par[s]);
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
             }
         }
     } else if (warp == 1) {
@@ -441,7 +456,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
             if (!ok && issued) {
                 // every MMA issued so far must finish before tensor memory is freed
                 tc::mma_commit_2sm(drain_bar);
-                tc::mbar_wait(drain_bar, 0, st, tmo, kSiteDrain);
+                drain_wait(drain_bar, 0);
             }
         }
     } else {
@@ -1325,6 +1340,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         HeadGemm p{};
         p.status = c.status;
         p.timeout_ns = c.timeout_ns;
+        p.withhold = a.withhold;
         p.live = live;
         p.rows = rows;
         p.tokens = n;

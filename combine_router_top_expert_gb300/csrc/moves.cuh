@@ -158,6 +158,7 @@ struct HeadLaunch {
     int dW_f32, accumulate;
     int piece;
     void* workspace;
+    int withhold;
 };
 size_t head_workspace_bytes(int T, int H, int V, bool grad, int piece, int num_sms);
 cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s);

@@ -139,7 +139,8 @@ typedef struct {
  * first minibatch, so the tiles waiting for it give up after timeout_ms and
  * the call reports MOK_ERR_TIMEOUT (exercises the bounded waits; never use
  * in production). In mok_moe_few the first CTA counts in none of its gate/up
- * results, so that whoever waits for them gives up. */
+ * results, so that whoever waits for them gives up; in the mok_head_loss calls the
+ * first pair of CTAs leaves the last block of a tile unloaded. */
 #define MOK_FLAG_TEST_WITHHOLD_PUBLISH 256
 
 /* ------------------------------------------------------------------------- */
@@ -590,8 +591,10 @@ size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, in
  * loss[t] = lse[t] - l[t, labels[t]] (formed from the other tokens' share, so that a
  * small loss keeps its digits). Ignored tokens get 0 in both, whatever their rows
  * of x hold. lse may be NULL. Bitwise the same in every run on one device.
- * x, W, dx, dW 16-byte aligned. Of cfg num_sms and timeout_ms are read. Device-side
- * waits are bounded: mok_device_status on the workspace reports MOK_ERR_TIMEOUT. */
+ * x, W, dx, dW 16-byte aligned. Of cfg num_sms (2 at least are used), timeout_ms and
+ * MOK_FLAG_TEST_WITHHOLD_PUBLISH are read. Device-side waits are bounded:
+ * mok_device_status on the workspace reports MOK_ERR_TIMEOUT, outputs are then
+ * unspecified, and the CTAs end only after their own copies and MMAs. */
 mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
                          mok_stream_t stream);
 

@@ -310,3 +310,53 @@ def test_captured_and_replayed(drop):
         graph.replay()
         want = _train(x, W, y)
         assert torch.equal(loss, want[0]) and torch.equal(dx, want[2]) and torch.equal(dW, want[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("num_sms", [1, 2, 20])
+def test_fewer_sms(T, num_sms):
+    """The loss does not depend on the SMs that may be used, the gradients only in the order of their sums."""
+    H, V = 136, 1000
+    x, W = ref.exact_head(T, H, V, 23)
+    y = _labels(T, V, 23)
+    cfg = mok.make_config(num_sms=num_sms)
+    loss, lse = _score(x, W, y)
+    ws = mok.alloc_bytes(mok.head_workspace_size(T, H, V, True, 0, cfg))
+    got, dx, dW = _nan(T), _nan(T, H, dtype=torch.bfloat16), _nan(V, H, dtype=torch.bfloat16)
+    mok.head_loss_train(x, W, y, got, dx, dW, ws, cfg=cfg)
+    assert mok.device_status(ws) == (mok.OK, 0)
+    _check_loss(got, lse, x, W, y)
+    want_dx, want_dW, mx, mW = ref.head_grad(x, W, y, torch.ones(T, dtype=torch.float64, device="cuda"))
+    _check_grad(dx, want_dx, mx, V)
+    _check_grad(dW, want_dW, mW, T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,V", [(3, 256, 1000), (400, 512, 3000)])
+@pytest.mark.parametrize("call", ["score", "train", "backward"])
+def test_waits_that_run_out(T, H, V, call):
+    """A block that never comes: the call reports it after its limit, every CTA ends, and the next call is right."""
+    x, W = ref.exact_head(T, H, V, 29)
+    y = _labels(T, V, 29)
+    want = _train(x, W, y, "backward" if call == "backward" else "train")
+    ws = _ws(T, H, V, True)
+    loss, lse, dx, dW = _nan(T), want[1].clone(), _nan(T, H, dtype=torch.bfloat16), _nan(V, H, dtype=torch.bfloat16)
+
+    def run(cfg=None):
+        if call == "score":
+            mok.head_loss(x, W, y, loss, ws, cfg=cfg)
+        elif call == "train":
+            mok.head_loss_train(x, W, y, loss, dx, dW, ws, cfg=cfg)
+        else:
+            mok.head_loss_backward(x, W, y, lse, dx, dW, ws, cfg=cfg)
+        return mok.device_status(ws)[0]
+
+    assert run() == mok.OK
+    assert run(mok.make_config(timeout_ms=50, flags=mok.FLAG_TEST_WITHHOLD_PUBLISH)) == mok.ERR_TIMEOUT
+    for _ in range(2):
+        assert run() == mok.OK
+        if call != "backward":
+            assert torch.equal(loss, want[0])
+        if call != "score":
+            assert torch.equal(dx, want[2]) and torch.equal(dW, want[3])
