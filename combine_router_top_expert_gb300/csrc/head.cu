@@ -66,7 +66,6 @@ struct HeadGemm {
     int tokens;             // tokens of the piece (the live ones' upper bound)
     int M, N, K;            // K or M is the token count where m_live / k_live is set
     int m_live, k_live;
-    int bn;                 // tile columns (a multiple of 32, at most kBN; the MN-major B's are kBN)
     int splits;             // parts of K, each a tile of its own
     int group;              // row tiles that are walked together
     int a_mn;               // A is MN-major (two products in one launch; else the kernel's own type says it)
@@ -265,7 +264,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
         z.all = live == p.tokens;
         z.M = p.m_live ? live : p.M;
         z.mt = (z.M + kBM - 1) / kBM;
-        z.nt = (p.N + p.bn - 1) / p.bn;
+        z.nt = (p.N + kBN - 1) / kBN;
         z.kbs = ((p.k_live ? live : p.K) + kBK - 1) / kBK;
         z.total = z.mt * z.nt * p.splits;
         return z;
@@ -315,7 +314,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 const HeadGemm& p = J.p;
                 const void* map = (N == 2 ? p.a_mn != 0 : A_MN) && z.all ? (const void*)&J.all : (const void*)&J.b;
                 const uint32_t lead = tc::mapa_shared(full_bar(stage), 0);
-                const int n0 = t.n * p.bn + rank * (p.bn / 2), k0 = kb * kBK;
+                const int n0 = t.n * kBN + rank * 128, k0 = kb * kBK;
                 if constexpr (B_MN) {
                     if (p.b_groups) {
                         tma_load_3d_2sm(b_tile(stage), map, lead, 0, k0, n0 / 64);
@@ -328,8 +327,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 }
             };
             auto bytes_of = [](const HeadGemm& p) {
-                return (uint32_t)((p.a_bytes == kOperandBytes ? 2 : 1) * p.a_bytes +
-                                  2 * (B_MN ? kOperandBytes : p.bn / 2 * kBK * 2));
+                return (uint32_t)((p.a_bytes == kOperandBytes ? 2 : 1) * p.a_bytes + 2 * kOperandBytes);
             };
             int stage = 0, ahead = 0;   // ahead: blocks whose early operands are on their way
             uint32_t ph = 0;
@@ -417,7 +415,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 const HeadSize z = size_of(p);
                 const Range r = range_of(j, z);
                 const bool a_mn = N == 2 ? p.a_mn != 0 : A_MN;
-                idesc = tc::idesc_bf16(kBM, p.bn, a_mn, B_MN);
+                idesc = tc::idesc_bf16(kBM, kBN, a_mn, B_MN);
                 step_a = a_mn ? 128u : 2u;
                 al0 = a_tile(0) >> 4 | (a_mn ? 512u : 1u) << 16;
                 for (int g = r.g0; g < r.g1 && ok; g += r.step) {
@@ -497,14 +495,14 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
         const HeadGemm& p = J.p;
         const HeadSize z = size_of(p);
         const Range range = range_of(j, z);
-        const int M = z.M, cols = p.bn / 2;
+        const int M = z.M;
         const bool all = z.all;
         for (int g = range.g0; g < range.g1; g += range.step) {
             const Tile t = head_tile(g, z.mt, z.nt, p.group);
             const int blocks = k_first(p, z, t.split + 1) - k_first(p, z, t.split);
             const int row0 = t.m * kBM + rank * 128 + q * 32, row = row0 + lane;
-            const int col0 = t.n * p.bn + half * cols;
-            const int nv = min(cols, p.N - col0);         // valid columns; none: <= 0
+            const int col0 = t.n * kBN + half * 128;
+            const int nv = min(128, p.N - col0);          // valid columns; none: <= 0
             const bool in = row < M;
             // what belongs to the row, fetched while the tile is being summed
             int lab = -1;                                 // its label
@@ -531,7 +529,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 dead = p.zero_dead && in && !is_live(p.labels, p.labels_i64, row, p.live_below);
             }
             __syncwarp();
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * cols);
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
             if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
                 // 64 columns at a time: tensor memory, registers, staging, memory
                 if (blocks > 0) {
@@ -674,7 +672,11 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
             }
             if (!ok) break;
-            if (nv <= 0) continue;
+            if (nv <= 0) {
+                // nothing of the last tile
+                if (in) p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
             {
                 const int lc = lab >= col0 && lab < col0 + nv ? lab - col0 : -1;
                 if (nv < 128) {
@@ -723,7 +725,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 }
                 if (in) {
                     const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
-                    p.stats[(int64_t)row * p.stat_tiles + col0 / cols] = make_float2(mul, sum * kRootScale);
+                    p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(mul, sum * kRootScale);
                 }
             }
             }
@@ -965,7 +967,7 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 // and zeros for a token without a label (rows == NULL; else only live tokens are here).
 // Few rows are cut along the vocabulary (gridDim.y), each part joining the sums itself.
 __global__ void __launch_bounds__(kRowThreads)
-head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, const uint4* __restrict__ x, int64_t ldx,
+head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
                const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
                const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld,
                int V, float* loss, float* lse) {
@@ -999,11 +1001,10 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, int stat_cols, 
     const float sum = r.others + r.own;
     const float coef = scale * (dloss ? dloss[t] : 1.0f);
     const float inv = coef / sum * kRootScale;
-    const int tile = stat_cols / 8;
 #pragma unroll 4
     for (int v = v0 + threadIdx.x; v < v1; v += kRowThreads) {
         const uint4 e = __ldcg(reinterpret_cast<const uint4*>(row + 8 * v));
-        const float f = inv * exp2_approx((__ldcg(st + v / tile).x - r.top) * kLog2e);
+        const float f = inv * exp2_approx((__ldcg(st + v / 16).x - r.top) * kLog2e);
         const uint32_t w[4] = {e.x, e.y, e.z, e.w};
         uint32_t o[4];
 #pragma unroll
@@ -1143,9 +1144,11 @@ bool make_job(HeadJob& J, bool a_mn, bool b_mn, int epi, const Operand& a, const
         return groups ? make_tmap_groups(m, o.base, o.rows, o.cols / 64, o.ld)
                       : make_tmap_pitch(m, o.base, o.rows, o.cols, o.ld, box_rows);
     };
-    const int box_a = a_mn ? kBK : rows, box_b = b_mn ? kBK : p.bn / 2;
+    const int box_a = a_mn ? kBK : rows, box_b = b_mn ? kBK : 128;
     if (!map(&J.a, a, p.a_groups, box_a) || !map(&J.b, b, p.b_groups, box_b)) return false;
-    if (epi == kEpiOut ? !map(&J.all, all, p.b_groups, box_b) : !map(&J.all, all, false, box_a)) return false;
+    const Operand& other = epi == kEpiOut ? b : a;       // what `all` stands in for
+    J.all = epi == kEpiOut ? J.b : J.a;
+    if (all.base != other.base && !map(&J.all, all, epi == kEpiOut && p.b_groups, epi == kEpiOut ? box_b : box_a)) return false;
     p.tma_out = epi != kEpiOut || (!p.out_rows && !p.add && !p.zero_dead);
     J.out = J.a;
     if (epi == kEpiExp || epi == kEpiDl) return make_tmap_out(&J.out, p.dl, 2, 1, p.dl_rows, p.ld_dl, p.ld_dl);
@@ -1153,7 +1156,7 @@ bool make_job(HeadJob& J, bool a_mn, bool b_mn, int epi, const Operand& a, const
     return true;
 }
 
-int64_t tiles_of(const HeadGemm& p) { return (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, p.bn) * p.splits; }
+int64_t tiles_of(const HeadGemm& p) { return (int64_t)ceil_div(p.M, kBM) * ceil_div(p.N, kBN) * p.splits; }
 
 // Cycles of a tile of dX and of dW, about 700 a K block and 4000 at least for the latter's
 // way out, and of each pair where all share both products.
@@ -1218,22 +1221,6 @@ constexpr int kPieceMax = 65536;
 // Up to one row tile, ignored tokens cost no products: nothing is gathered then.
 constexpr int kPlainRows = kBM;
 
-// Columns of the logits' tiles: the width whose rounds over all pairs load the least
-// (a K block of a tile brings 256 rows of x and bn of W to a pair).
-int logit_columns(int tokens, int V, int pairs, bool boxes) {
-    int best = kBN;
-    int64_t least = 0;
-    for (int bn = kBN; bn >= 128; bn -= boxes ? 128 : 32) {   // boxes: halves of whole 64-column boxes
-        const int64_t tiles = (int64_t)ceil_div(tokens, kBM) * ceil_div(V, bn);
-        const int64_t cost = (tiles + pairs - 1) / std::max(pairs, 1) * (kBM + bn);
-        if (bn == kBN || cost < least) {
-            least = cost;
-            best = bn;
-        }
-    }
-    return best;
-}
-
 int64_t pitch_dl(int V) { return align_up(V, 64); }
 
 // Tokens of a piece: `want` where it is given, else as many as keep dl within
@@ -1278,7 +1265,7 @@ HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
     L.live = take(4);
     L.rows = take(cap * 4);
     L.label = take(cap * 4);
-    L.stats = take(L.piece * (int64_t)ceil_div(V, 64) * 8);   // tiles of 64 columns at least
+    L.stats = take(L.piece * (int64_t)(2 * ceil_div(V, kBN)) * 8);
     if (grad || T > kPlainRows) L.xc = take(cap * H * 2);
     if (grad) L.dl = take(cap * pitch_dl(V) * 2);
     if (L.splits > 1) L.part = take((int64_t)L.splits * L.piece * H * 4);
@@ -1360,8 +1347,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         p.m_live = gather;
         p.N = V;
         p.K = H;
-        p.bn = logit_columns(n, V, c.num_sms / 2, grad);
-        p.stat_tiles = ceil_div(V, p.bn / 2);
+        p.stat_tiles = 2 * ceil_div(V, kBN);
         p.early = gather ? kEarlyNone : kEarlyA | kEarlyB;
         const Operand ox{x, n, H, a.ldx}, ow{a.W, V, H, H};
         const Operand oxc = gather ? Operand{xc, cap, H, H} : ox;
@@ -1378,13 +1364,12 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             e = run_head_gemm<false, false, kEpiExp>(oxc, ow, ox, p, c.num_sms, s);
             if (e == cudaSuccess)
                 e = launch_after(head_dl_kernel, dim3(n, dl_parts(n, V)), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
-                                 p.bn / 2, xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live,
+                                 xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live,
                                  (const float*)label, labels, a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
         } else {
             e = run_head_gemm<false, false, kEpiDl>(oxc, ow, ox, p, c.num_sms, s);
         }
         if (e != cudaSuccess) return e;
-        p.bn = kBN;
         p.early = kEarlyNone;
         const Operand odl{dl, p.dl_rows, V, p.ld_dl};
         const int splits = L.splits;
