@@ -529,6 +529,16 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                 dead = p.zero_dead && in && !is_live(p.labels, p.labels_i64, row, p.live_below);
             }
             __syncwarp();
+            // rows of no token (but for those that dW's last K block reads): the sums are let go unread
+            if (row0 >= (p.m_live ? (M + kBK - 1) / kBK * kBK : M)) {
+                for (int b0 = 0; b0 < blocks && ok; b0 += min(kSumBlocks, blocks - b0)) {
+                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
+                    mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
+                    if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+                }
+                if (!ok) break;
+                continue;
+            }
             const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
             if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
                 // 64 columns at a time: tensor memory, registers, staging, memory
