@@ -964,8 +964,11 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
     if (T > 0 && (!a->x || !a->labels || (forward && !a->loss) || (!forward && !a->lse))) return MOK_ERR_INVALID;
     if (grad && !a->dx && !a->dW) return MOK_ERR_INVALID;
     if (grad && a->accumulate && !a->dW_f32) return MOK_ERR_INVALID;
-    if (grad && a->dW && a->dx && a->dx == a->x) return MOK_ERR_INVALID;
-    if (grad && a->dx && a->dx == a->x && a->ldx != H) return MOK_ERR_INVALID;
+    if (grad && a->dx && T > 0) {   // apart from x, or all of it where dW does not need x any more
+        const char *x = static_cast<const char*>(a->x), *dx = static_cast<const char*>(a->dx);
+        const bool apart = dx + (int64_t)T * H * 2 <= x || x + ((int64_t)(T - 1) * a->ldx + H) * 2 <= dx;
+        if (!apart && (a->dW || dx != x || a->ldx != H)) return MOK_ERR_INVALID;
+    }
     if (!aligned(a->x, 16) || !aligned(a->W, 16) || !aligned(a->labels, a->labels_i64 ? 8 : 4) || !aligned(a->loss, 4) ||
         !aligned(a->lse, 4) || !aligned(a->dloss, 4) || !aligned(a->dx, 16) || !aligned(a->dW, 16) ||
         !aligned(a->workspace, 1024))

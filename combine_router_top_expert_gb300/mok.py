@@ -744,6 +744,13 @@ class GradList:
         spans.sort()
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise AssertionError("gradients and outputs that do not overlap expected")
+        self.device = torch._C._cuda_getDevice() if n else None
+
+    def check(self):
+        """The current device is the one that the gradients are on."""
+        if self.count and self.device != torch._C._cuda_getDevice():
+            raise AssertionError("gradients on the current CUDA device expected")
+        return self
 
 
 def grad_list(grads, out=None) -> GradList:
@@ -757,7 +764,7 @@ def grad_workspace_size() -> int:
 
 def grad_norm(grads, norm, workspace, stream=None):
     """norm [] (fp32) = 2-norm of all elements of a list of bf16, fp16 and fp32 tensors."""
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = grads.check() if isinstance(grads, GradList) else GradList(grads)
     _dense("norm", norm, torch.float32)
     _check(lib().mok_grad_norm(g.count, g.array, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                _stream(stream)), "mok_grad_norm")
@@ -767,7 +774,7 @@ def grad_norm(grads, norm, workspace, stream=None):
 def grad_clip(grads, max_norm, norm, workspace, stream=None):
     """norm as grad_norm, and all gradients times min(1, max_norm / (norm + 1e-6)): in place, or into a grad_list's
     outputs."""
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = grads.check() if isinstance(grads, GradList) else GradList(grads)
     _dense("norm", norm, torch.float32)
     _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), norm.data_ptr(), workspace.data_ptr(),
                                workspace.numel(), _stream(stream)), "mok_grad_clip")

@@ -83,6 +83,37 @@ def test_views_at_any_element(dt, shift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt,like", [(B, True), (B, False), (D, True), (D, False)])
+def test_many_long_views(dt, like):
+    """Views of more than a chunk at any element, more of them than one launch lists; outputs that lie the same way
+    and others."""
+    n, count = 9001, 150
+    flat = torch.randn(n * count + 8, generator=ref.gen(5), device="cuda").to(dt)
+    keep = flat.clone()
+    grads = [flat[1 + i * n:1 + (i + 1) * n] for i in range(count)]
+    room = torch.zeros(n * count + 8, dtype=dt, device="cuda")
+    shift = 1 if like else 2
+    out = [room[shift + i * n:shift + (i + 1) * n] for i in range(count)]
+    want, norm = _norm64(grads), torch.empty((), device="cuda")
+    mok.grad_clip(mok.grad_list(grads, out), want / 3, norm, _ws())
+    assert abs(float(norm) - want) <= REL * want
+    exact = keep[1:1 + n * count].double() * (want / 3 / (want + 1e-6))
+    got = room[shift:shift + n * count].double()
+    assert ((got - exact).abs() <= (HALF[dt] + REL + 3 * 2.0 ** -24) * exact.abs() + TINY[dt]).all()
+    assert torch.equal(flat, keep) and not room[:shift].any() and not room[shift + n * count:].any()
+
+
+@pytest.mark.gpu
+def test_a_list_of_another_device_is_refused(monkeypatch):
+    plan = mok.grad_list(_grads(SETS["odd"], 6))
+    norm, ws = torch.zeros((), device="cuda"), _ws()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: mok.grad_norm(plan, norm, ws), lambda: mok.grad_clip(plan, 1.0, norm, ws)):
+        with pytest.raises(AssertionError):
+            call()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("std", [1e-30, 1e-22, 1e18, 1e30])
 @pytest.mark.parametrize("dt", [B, D])
 def test_values_whose_squares_leave_fp32(std, dt):

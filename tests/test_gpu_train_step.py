@@ -60,6 +60,42 @@ def test_head(T, residual):
 
 
 @pytest.mark.gpu
+def test_head_of_no_tokens():
+    head = _head(1001, 256, 2)
+    x, labels = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"), torch.empty(0, dtype=torch.long, device="cuda")
+    loss, lse = head.score(x, labels)
+    assert loss.shape == lse.shape == (0,)
+    loss, grads = head.train(x, labels)
+    assert loss.shape == (0,) and grads["dx"].shape == (0, 256) and not grads["dW"].any() and not grads["dgain"].any()
+    dW = torch.full((1001, 256), 3.0, device="cuda")
+    head.train(x, labels, dW=dW)
+    assert (dW == 3).all() and head.status() == (mok.OK, 0)
+
+
+@pytest.mark.gpu
+def test_heads_graphs_in_turn_with_eager_calls():
+    """Two captured calls of the same workspace, replayed in turn with eager ones of other sizes between them."""
+    H, V = 256, 3001
+    g = ref.gen(12)
+    head = _head(V, H, 3)
+    xs = [_rows(g, T, H) for T in (5, 6, 300)]
+    ys = [torch.randint(0, V, (x.shape[0],), generator=g, device="cuda") for x in xs]
+    want = [head.train(x, y) for x, y in zip(xs, ys)]
+    graphs, outs = [], []
+    for x, y in zip(xs[:2], ys):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(head.train(x, y))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+            again = head.train(xs[2], ys[2])
+        for (loss, grads), (loss0, grads0) in zip(outs + [again], want):
+            assert torch.equal(loss, loss0) and all(torch.equal(grads[n], grads0[n]) for n in grads0)
+
+
+@pytest.mark.gpu
 def test_head_adds_to_a_gradient_and_goes_in_pieces():
     T, H, V = 600, 128, 700
     g = ref.gen(3)

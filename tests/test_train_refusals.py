@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from combine_router_top_expert_gb300 import build, mok
+from combine_router_top_expert_gb300.head import VocabHead
 
 PTR = 1 << 20   # an aligned address that is not read
 
@@ -43,6 +44,8 @@ def test_head_arguments(L, call):
     if call != "mok_head_loss":
         assert f(4, 64, 100, _head(), None, None) == mok.ERR_INVALID          # dx in x's place, and dW
         assert f(4, 64, 100, _head(dW=None, ldx=72), None, None) == mok.ERR_INVALID
+        for at in (PTR + 128, PTR - 128, PTR + 4 * 128 - 16, PTR - 4 * 128 + 16):     # some of x's rows
+            assert f(4, 64, 100, _head(dW=None, dx=at), None, None) == mok.ERR_INVALID
     missing = dict(lse=None) if call == "mok_head_loss_backward" else dict(loss=None)
     assert f(4, 64, 100, _head(**good, **missing), None, None) == mok.ERR_INVALID
 
@@ -89,3 +92,17 @@ def test_host_tensors_are_refused():
                  lambda: mok.grad_norm([f], norm, u8), lambda: mok.grad_clip([f], 1.0, norm, u8)):
         with pytest.raises(AssertionError):
             call()
+
+
+def test_a_head_of_other_types_or_sizes_is_refused():
+    W, gain = torch.zeros((9, 64), dtype=torch.bfloat16), torch.zeros(64)
+    for w, g in ((W.float(), gain), (W, gain[:8]), (W[0], gain), (W, gain[None])):
+        with pytest.raises(AssertionError):
+            VocabHead(w, g)
+    head, x = VocabHead(W, gain), torch.zeros((4, 64), dtype=torch.bfloat16)
+    assert head.status() == (mok.OK, 0)
+    for labels in (torch.zeros(4, dtype=torch.long), torch.zeros(4)):
+        with pytest.raises(AssertionError):
+            head.score(x, labels)
+        with pytest.raises(AssertionError):
+            head.train(x, labels, dW=torch.zeros((9, 64), dtype=torch.float64))
