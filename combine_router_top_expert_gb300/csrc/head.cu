@@ -5,19 +5,23 @@
 //   l[t,v] = <x_t, W_v>      lse_t = log sum_v exp l[t,v]      loss_t = lse_t - l[t,y_t]
 //   dl[t,v] = c_t (exp(l[t,v] - lse_t) - [v == y_t])           c_t = scale * dloss_t
 //   dX = dl W                dW = dl^T x
-// Tokens whose label is outside 0..V-1 count for nothing: the live ones are
-// gathered first (head_prep_kernel), so what their rows hold does not matter and
-// none of the products is spent on them.
+// Tokens whose label is outside 0..V-1 count for nothing, whatever their rows hold. In
+// a call of more than one row tile the live ones are gathered first (head_prep_kernel),
+// and none of the products is spent on the others.
 //
 // Three products, each a persistent tcgen05 kernel over 256 x 256 tiles of 2-SM
 // pairs (head_gemm_kernel):
 //   logits  x W^T    both operands K-major; the epilogue reduces 128 columns of a row
-//                    to (max, sum of exponentials, label's logit), so that a logit
-//                    lives in tensor memory and registers only, and with a gradient
-//                    writes dl (log-sum known) or the exponentials, which
-//                    head_dl_kernel turns into dl in their place
+//                    to (max, sum of exponentials), so that a logit lives in tensor
+//                    memory and registers only, and with a gradient writes dl (log-sum
+//                    known) or the exponentials, which head_dl_kernel turns into dl in
+//                    their place: 6TVH operations for a training call, none repeated
 //   dX      dl W     A K-major, B MN-major (the vocabulary is K)
 //   dW      dl^T x   both MN-major (the tokens are K)
+// Few tokens are bound by the bytes of W (T = 64, H = 7168, V = 131072: 292 us, 6.4
+// TB/s), many by the tensor cores (T = 2560, H = 7168, V = 50001, scoring: 960 to 1090
+// us, 1.9 to 1.7 PFLOP/s as the power limit lets the clock run; T = 4096, V = 131072,
+// training: 13.2 to 14.5 ms, 1.75 to 1.6 PFLOP/s).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
@@ -200,6 +204,17 @@ struct HeadSize {
     bool all;
 };
 
+// Warp 0 loads (one thread: TMA boxes into the ring), warp 1 of the pair's leader issues the
+// MMAs, warps 2 to 9 turn a tile's sums into what the product is for, while the next tile is
+// summed in the other half of tensor memory. 256 x 256 is the largest tile that leaves two
+// halves; a K block of it costs the pair 0.27 us of MMA and brings 64 KB, 18 TB/s over the
+// GPU, about what L2 gives: narrower tiles bring more for the same work and were no faster,
+// and for few rows, where most of the MMA is spent on rows that there are not, HBM is the
+// bound all the same. T = 2560, H = 7168, V = 32768, the kernels by themselves: logits 622 us
+// (86% of the tensor cores' cycles; V = 50001: 92%), with exponentials 637, dX 686, dW 650
+// (76%; MN-major operands: the power limit sets their clock). Kept out because they gained
+// nothing: clusters of four with multicast, five stages with a second staging buffer, each
+// pair's walk of K begun elsewhere.
 template <bool A_MN, bool B_MN, int EPI, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
@@ -491,255 +506,253 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
         bool ok = true;
 #pragma unroll 1
         for (int j = 0; j < N && ok; ++j) {
-        const HeadJob& J = jobs.job[j];
-        const HeadGemm& p = J.p;
-        const HeadSize z = size_of(p);
-        const Range range = range_of(j, z);
-        const int M = z.M;
-        const bool all = z.all;
-        for (int g = range.g0; g < range.g1; g += range.step) {
-            const Tile t = head_tile(g, z.mt, z.nt, p.group);
-            const int blocks = k_first(p, z, t.split + 1) - k_first(p, z, t.split);
-            const int row0 = t.m * kBM + rank * 128 + q * 32, row = row0 + lane;
-            const int col0 = t.n * kBN + half * 128;
-            const int nv = min(128, p.N - col0);          // valid columns; none: <= 0
-            const bool in = row < M;
-            // what belongs to the row, fetched while the tile is being summed
-            int lab = -1;                                 // its label
-            float mul = 0.f, base = 0.f;
-            float label_at_lse = 0.f;                     // its label's logit less its log-sum
-            int orow = in ? row : -1;                     // its output row
-            bool dead = false;
-            // (dl: rows behind the last live token, up to the tile's end, are written as zeros: dW's last K block
-            // reads some of them)
-            if constexpr (EPI != kEpiOut) {
-                if (in) {
-                    const int64_t tok = p.rows && !all ? p.rows[row] : row;
-                    const int64_t y = label_at(p.labels, p.labels_i64, tok);
-                    if (y >= 0 && y < p.N) lab = (int)y;
-                    if (EPI == kEpiDl && lab >= 0) {
-                        mul = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
-                        const float lse = __ldg(p.lse + tok);
-                        base = -kLog2e * lse;
-                        label_at_lse = __ldcg(p.label_logit + row) - lse;
+            const HeadJob& J = jobs.job[j];
+            const HeadGemm& p = J.p;
+            const HeadSize z = size_of(p);
+            const Range range = range_of(j, z);
+            const int M = z.M;
+            const bool all = z.all;
+            for (int g = range.g0; g < range.g1; g += range.step) {
+                const Tile t = head_tile(g, z.mt, z.nt, p.group);
+                const int blocks = k_first(p, z, t.split + 1) - k_first(p, z, t.split);
+                const int row0 = t.m * kBM + rank * 128 + q * 32, row = row0 + lane;
+                const int col0 = t.n * kBN + half * 128;
+                const int nv = min(128, p.N - col0);          // valid columns; none: <= 0
+                const bool in = row < M;
+                // what belongs to the row, fetched while the tile is being summed
+                int lab = -1;                                 // its label
+                float mul = 0.f, base = 0.f;
+                float label_at_lse = 0.f;                     // its label's logit less its log-sum
+                int orow = in ? row : -1;                     // its output row
+                bool dead = false;
+                // (dl: rows behind the last live token, up to the tile's end, are written as zeros: dW's last K block
+                // reads some of them)
+                if constexpr (EPI != kEpiOut) {
+                    if (in) {
+                        const int64_t tok = p.rows && !all ? p.rows[row] : row;
+                        const int64_t y = label_at(p.labels, p.labels_i64, tok);
+                        if (y >= 0 && y < p.N) lab = (int)y;
+                        if (EPI == kEpiDl && lab >= 0) {
+                            mul = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
+                            const float lse = __ldg(p.lse + tok);
+                            base = -kLog2e * lse;
+                            label_at_lse = __ldcg(p.label_logit + row) - lse;
+                        }
                     }
-                }
-            } else {
-                if (in && p.out_rows && !all) orow = p.out_rows[row];
-                dead = p.zero_dead && in && !is_live(p.labels, p.labels_i64, row, p.live_below);
-            }
-            __syncwarp();
-            // rows of no token (but for those that dW's last K block reads): the sums are let go unread
-            if (row0 >= (p.m_live ? (M + kBK - 1) / kBK * kBK : M)) {
-                for (int b0 = 0; b0 < blocks && ok; b0 += min(kSumBlocks, blocks - b0)) {
-                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
-                    mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
-                    if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
-                }
-                if (!ok) break;
-                continue;
-            }
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
-            if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
-                // 64 columns at a time: tensor memory, registers, staging, memory
-                if (blocks > 0) {
-                    if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
-                    __syncwarp();
-                    tc::fence_after_sync();
-                }
-                const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
-                const int64_t at = col0;
-                int o[8];                           // output rows of this lane's eighths
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    float r[2][32];
-                    if (blocks > 0) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tc::tmem_ld_32x32b_x32(tbase + 64 * h + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
-                        tc::tmem_ld_wait();
-                        if (h == 1) {
-                            tc::fence_before_sync();
-                            mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
-                            if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[c][i] = 0.f;
-                    }
-                    if (64 * h >= nv) continue;
-                    uint4 v[8];
-                    if constexpr (EPI == kEpiDl) {
-                        begin_pass();
-#pragma unroll
-                        for (int e8 = 0; e8 < 8; ++e8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int j = 8 * e8 + 2 * i;
-                                float2 e = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
-                                e = __ffma2_rn(e, make_float2(kLog2e, kLog2e), make_float2(base, base));
-                                e = __fmul2_rn(make_float2(exp2_approx(e.x), exp2_approx(e.y)), make_float2(mul, mul));
-                                w[i] = lab >= 0 ? pack_bf16x2(e.x, e.y) : 0u;
-                            }
-                            put(e8, w[0], w[1], w[2], w[3]);
-                        }
-                        const int j = lab - col0 - 64 * h;      // the label's column of these 64
-                        if (lab >= 0 && j >= 0 && j < 64)
-                            st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
-                                        __float2bfloat16_rn(mul * expm1f(label_at_lse)));
-                        if (row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
-                        continue;
-                    }
-                    if (!p.out_f32 && !p.add) {
-                        begin_pass();
-#pragma unroll
-                        for (int e8 = 0; e8 < 8; ++e8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int j = 8 * e8 + 2 * i;
-                                w[i] = dead ? 0u : pack_bf16x2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
-                            }
-                            put(e8, w[0], w[1], w[2], w[3]);
-                        }
-                        if (p.tma_out) {
-                            if (row0 < M) send_pass(J, col0 + 64 * h, row0, 0);
-                            continue;
-                        }
-                        __syncwarp();
-                        take(0, v);
-                        const int cc = 64 * h + 8 * (lane & 7);
-                        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + at + cc;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (o[i] >= 0 && cc < nv) *reinterpret_cast<uint4*>(to + (int64_t)o[i] * p.N) = v[i];
-                        __syncwarp();
-                        continue;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {      // 32 fp32 columns, 128 bytes of a row
-                        const int cc = 64 * h + 32 * c + 4 * (lane & 7);
-                        begin_pass();
-#pragma unroll
-                        for (int e8 = 0; e8 < 8; ++e8)
-                            put(e8, __float_as_uint(r[c][4 * e8]), __float_as_uint(r[c][4 * e8 + 1]),
-                                __float_as_uint(r[c][4 * e8 + 2]), __float_as_uint(r[c][4 * e8 + 3]));
-                        if (p.tma_out) {
-                            if (row0 < M && 64 * h + 32 * c < nv) send_pass(J, col0 + 64 * h + 32 * c, row0, t.split);
-                            continue;
-                        }
-                        __syncwarp();
-                        take(0, v);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (o[i] < 0 || cc >= nv) continue;
-                            const int64_t to = at + (int64_t)o[i] * p.N + cc;
-                            float4 f = make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y),
-                                                   __uint_as_float(v[i].z), __uint_as_float(v[i].w));
-                            if (p.add) {
-                                const float4 g4 = *reinterpret_cast<const float4*>(p.add + to);
-                                f.x += g4.x; f.y += g4.y; f.z += g4.z; f.w += g4.w;
-                            }
-                            if (p.out_f32)
-                                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = f;
-                            else
-                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) =
-                                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
-                        }
-                        __syncwarp();
-                    }
-                }
-                continue;
-            } else {
-            float r[4][32];
-            for (int b0 = 0; b0 < blocks; b0 += min(kSumBlocks, blocks - b0)) {
-                if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
-                __syncwarp();
-                tc::fence_after_sync();
-                const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
-                if (b0 == 0) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::tmem_ld_32x32b_x32(tbase + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
-                    tc::tmem_ld_wait();
                 } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t v[16];
-                        tmem_ld_x16(tbase + 16 * c, v);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[c / 2][16 * (c % 2) + i] += __uint_as_float(v[i]);
+                    if (in && p.out_rows && !all) orow = p.out_rows[row];
+                    dead = p.zero_dead && in && !is_live(p.labels, p.labels_i64, row, p.live_below);
+                }
+                __syncwarp();
+                // rows of no token (but for those that dW's last K block reads): the sums are let go unread
+                if (row0 >= (p.m_live ? (M + kBK - 1) / kBK * kBK : M)) {
+                    for (int b0 = 0; b0 < blocks && ok; b0 += min(kSumBlocks, blocks - b0)) {
+                        if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
+                        mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
+                        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
                     }
+                    if (!ok) break;
+                    continue;
                 }
-                tc::fence_before_sync();
-                mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
-                if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
-            }
-            if (!ok) break;
-            if (nv <= 0) {
-                // nothing of the last tile
-                if (in) p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(-INFINITY, 0.f);
-                continue;
-            }
-            {
-                const int lc = lab >= col0 && lab < col0 + nv ? lab - col0 : -1;
-                if (nv < 128) {
+                const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+                if constexpr (EPI == kEpiOut || EPI == kEpiDl) {
+                    // 64 columns at a time: tensor memory, registers, staging, memory
+                    if (blocks > 0) {
+                        if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
+                        __syncwarp();
+                        tc::fence_after_sync();
+                    }
+                    const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
+                    const int64_t at = col0;
+                    int o[8];                           // output rows of this lane's eighths
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, orow, 4 * i + (lane >> 3));
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float r[2][32];
+                        if (blocks > 0) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i < nv ? r[c][i] : -INFINITY;
-                }
-                mul = -INFINITY;
+                            for (int c = 0; c < 2; ++c)
+                                tc::tmem_ld_32x32b_x32(tbase + 64 * h + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
+                            tc::tmem_ld_wait();
+                            if (h == 1) {
+                                tc::fence_before_sync();
+                                mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
+                                if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+                            }
+                        } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mul = fmaxf(mul, r[c][i]);
-                base = kRootShift - (mul == -INFINITY ? 0.f : mul * (0.5f * kLog2e));
-                // the label's own term stays out of the sum, so that the others' share keeps its
-                // digits where the label takes nearly everything
-                if (__any_sync(0xffffffffu, lc >= 0)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i == lc ? -INFINITY : r[c][i];
-                }
-                float2 s[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s[c] = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {      // 64 columns, 128 bytes of a row
-                    if (64 * h >= nv) break;
-                    if constexpr (EPI != kEpiStats) begin_pass();
-#pragma unroll
-                    for (int e8 = 0; e8 < 8; ++e8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = 64 * h + 8 * e8 + 2 * i;
-                            float2 v = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
-                            v = __ffma2_rn(v, make_float2(0.5f * kLog2e, 0.5f * kLog2e), make_float2(base, base));
-                            v = make_float2(exp2_approx(v.x), exp2_approx(v.y));
-                            s[j / 32] = __ffma2_rn(v, v, s[j / 32]);
-                            const __half2 v2 = __float22half2_rn(v);
-                            w[i] = in ? *reinterpret_cast<const uint32_t*>(&v2) : 0u;
+                                for (int i = 0; i < 32; ++i) r[c][i] = 0.f;
                         }
-                        if (EPI != kEpiStats) put(e8, w[0], w[1], w[2], w[3]);
+                        if (64 * h >= nv) continue;
+                        uint4 v[8];
+                        if constexpr (EPI == kEpiDl) {
+                            begin_pass();
+#pragma unroll
+                            for (int e8 = 0; e8 < 8; ++e8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int j = 8 * e8 + 2 * i;
+                                    float2 e = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                                    e = __ffma2_rn(e, make_float2(kLog2e, kLog2e), make_float2(base, base));
+                                    e = __fmul2_rn(make_float2(exp2_approx(e.x), exp2_approx(e.y)), make_float2(mul, mul));
+                                    w[i] = lab >= 0 ? pack_bf16x2(e.x, e.y) : 0u;
+                                }
+                                put(e8, w[0], w[1], w[2], w[3]);
+                            }
+                            const int j = lab - col0 - 64 * h;      // the label's column of these 64
+                            if (lab >= 0 && j >= 0 && j < 64)
+                                st_shared16(pass + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4) + 2 * (j & 7),
+                                            __float2bfloat16_rn(mul * expm1f(label_at_lse)));
+                            if (row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
+                            continue;
+                        }
+                        if (!p.out_f32 && !p.add) {
+                            begin_pass();
+#pragma unroll
+                            for (int e8 = 0; e8 < 8; ++e8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int j = 8 * e8 + 2 * i;
+                                    w[i] = dead ? 0u : pack_bf16x2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                                }
+                                put(e8, w[0], w[1], w[2], w[3]);
+                            }
+                            if (p.tma_out) {
+                                if (row0 < M) send_pass(J, col0 + 64 * h, row0, 0);
+                                continue;
+                            }
+                            __syncwarp();
+                            take(0, v);
+                            const int cc = 64 * h + 8 * (lane & 7);
+                            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + at + cc;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (o[i] >= 0 && cc < nv) *reinterpret_cast<uint4*>(to + (int64_t)o[i] * p.N) = v[i];
+                            __syncwarp();
+                            continue;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {      // 32 fp32 columns, 128 bytes of a row
+                            const int cc = 64 * h + 32 * c + 4 * (lane & 7);
+                            begin_pass();
+#pragma unroll
+                            for (int e8 = 0; e8 < 8; ++e8)
+                                put(e8, __float_as_uint(r[c][4 * e8]), __float_as_uint(r[c][4 * e8 + 1]),
+                                    __float_as_uint(r[c][4 * e8 + 2]), __float_as_uint(r[c][4 * e8 + 3]));
+                            if (p.tma_out) {
+                                if (row0 < M && 64 * h + 32 * c < nv) send_pass(J, col0 + 64 * h + 32 * c, row0, t.split);
+                                continue;
+                            }
+                            __syncwarp();
+                            take(0, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                if (o[i] < 0 || cc >= nv) continue;
+                                const int64_t to = at + (int64_t)o[i] * p.N + cc;
+                                float4 f = make_float4(__uint_as_float(v[i].x), __uint_as_float(v[i].y),
+                                                       __uint_as_float(v[i].z), __uint_as_float(v[i].w));
+                                if (p.add) {
+                                    const float4 g4 = *reinterpret_cast<const float4*>(p.add + to);
+                                    f.x += g4.x; f.y += g4.y; f.z += g4.z; f.w += g4.w;
+                                }
+                                if (p.out_f32)
+                                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = f;
+                                else
+                                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) =
+                                        make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                            }
+                            __syncwarp();
+                        }
                     }
-                    if (EPI != kEpiStats && row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
-                }
-                if (in) {
-                    const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
-                    p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(mul, sum * kRootScale);
+                    continue;
+                } else {
+                    float r[4][32];
+                    for (int b0 = 0; b0 < blocks; b0 += min(kSumBlocks, blocks - b0)) {
+                        if (!tc::mbar_wait(accf_bar(acc), acc_ph, st, tmo, kSiteEpiAccFull)) { ok = false; break; }
+                        __syncwarp();
+                        tc::fence_after_sync();
+                        const uint32_t tbase = lanes + (uint32_t)(acc * kBN);
+                        if (b0 == 0) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                tc::tmem_ld_32x32b_x32(tbase + 32 * c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
+                            tc::tmem_ld_wait();
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t v[16];
+                                tmem_ld_x16(tbase + 16 * c, v);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) r[c / 2][16 * (c % 2) + i] += __uint_as_float(v[i]);
+                            }
+                        }
+                        tc::fence_before_sync();
+                        mbar_arrive_pair(tc::mapa_shared(acce_bar(acc), 0));
+                        if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+                    }
+                    if (!ok) break;
+                    if (nv <= 0) {
+                        // nothing of the last tile
+                        if (in) p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(-INFINITY, 0.f);
+                        continue;
+                    }
+                    const int lc = lab >= col0 && lab < col0 + nv ? lab - col0 : -1;
+                    if (nv < 128) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i < nv ? r[c][i] : -INFINITY;
+                    }
+                    mul = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mul = fmaxf(mul, r[c][i]);
+                    base = kRootShift - (mul == -INFINITY ? 0.f : mul * (0.5f * kLog2e));
+                    // the label's own term stays out of the sum, so that the others' share keeps its
+                    // digits where the label takes nearly everything
+                    if (__any_sync(0xffffffffu, lc >= 0)) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[c][i] = 32 * c + i == lc ? -INFINITY : r[c][i];
+                    }
+                    float2 s[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {      // 64 columns, 128 bytes of a row
+                        if (64 * h >= nv) break;
+                        if constexpr (EPI != kEpiStats) begin_pass();
+#pragma unroll
+                        for (int e8 = 0; e8 < 8; ++e8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = 64 * h + 8 * e8 + 2 * i;
+                                float2 v = make_float2(r[j / 32][j % 32], r[j / 32][j % 32 + 1]);
+                                v = __ffma2_rn(v, make_float2(0.5f * kLog2e, 0.5f * kLog2e), make_float2(base, base));
+                                v = make_float2(exp2_approx(v.x), exp2_approx(v.y));
+                                s[j / 32] = __ffma2_rn(v, v, s[j / 32]);
+                                const __half2 v2 = __float22half2_rn(v);
+                                w[i] = in ? *reinterpret_cast<const uint32_t*>(&v2) : 0u;
+                            }
+                            if (EPI != kEpiStats) put(e8, w[0], w[1], w[2], w[3]);
+                        }
+                        if (EPI != kEpiStats && row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
+                    }
+                    if (in) {
+                        const float sum = ((s[0].x + s[0].y) + (s[1].x + s[1].y)) + ((s[2].x + s[2].y) + (s[3].x + s[3].y));
+                        p.stats[(int64_t)row * p.stat_tiles + 2 * t.n + half] = make_float2(mul, sum * kRootScale);
+                    }
                 }
             }
-            }
-        }
         }
     }
     if (EPI != kEpiStats && warp >= 2 && lane == 0) tc::bulk_wait<0>();   // every box has left and arrived
@@ -785,7 +798,8 @@ __device__ __forceinline__ float label_dot(const uint4* x, const uint4* w, int n
 
 // For up to one row tile of tokens: a CTA per token copies its row, zeros for a token
 // without a label, for dW (whose K the tokens are), and forms the label's logit if
-// asked. The first CTA clears the status block. Without xc: that alone.
+// asked. The first CTA clears the status block. Without xc: that alone. Bound by its
+// launch: 5 us by itself at T = 8, less than 1 in a chain of launches.
 __global__ void __launch_bounds__(kRowThreads)
 head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
                   int V, int nv, uint4* __restrict__ xc, float* label_logit, int32_t* status) {
@@ -809,7 +823,11 @@ head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restr
 // every token is live, and their labels' logits are formed; the others' outputs are
 // zeroed. Each CTA counts the live tokens before its own from the labels themselves.
 // Behind the last live row, rows up to the next multiple of kBK are zeroed: dW's last K
-// block reads them. The first CTA clears the status block.
+// block reads them. The first CTA clears the status block. Bound by the loads in flight, so
+// four tokens' rows are read side by side: 25 us at T = 2560, H = 7168 (73 MB, 2.9 TB/s from
+// a cold start). Beside the logits' kernel in a kernel of its own, the labels' logits cost
+// as much time as here (scoring T = 1000, H = 4096, V = 20000: 115.8 and 117.1 us; with a
+// gradient, H = 1024: 124.9 and 122.5).
 constexpr int kPrepTokens = 4;
 __global__ void __launch_bounds__(kRowThreads)
 head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
@@ -947,8 +965,9 @@ __device__ __forceinline__ float row_loss(const RowSum& r, float label_logit) {
 }
 
 // A CTA per live token. For one row tile the label's logit is formed here, while the
-// logits' kernel still runs: x, W and labels are the caller's and the list of live tokens is the kernel's
-// before that one, all complete before that one began.
+// logits' kernel still runs: x, W and labels are the caller's and the list of live tokens
+// is the kernel's before that one, all complete before that one began. Bound by the
+// latency of its two passes over the row's V / 128 pairs: 12 us at T = 2560, V = 32768.
 __global__ void __launch_bounds__(kRowThreads)
 head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
                  const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
@@ -976,11 +995,15 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 //   dl[v] = c e[v] exp(top of its columns - lse),   dl[label] = -c others / (others + own)
 // and zeros for a token without a label (rows == NULL; else only live tokens are here).
 // Few rows are cut along the vocabulary (gridDim.y), each part joining the sums itself.
+// One pass over the bytes, read and written: 322 us at T = 4096, V = 131072 (6.7 TB/s),
+// 57 us at T = 2560, V = 32768. Roundings: the exponential is s * s of an FP16 root
+// (2^-10 relative), dl goes to BF16 (2^-8) because it is an operand of both products; the
+// label's dl comes from the exact fp32 sums.
 __global__ void __launch_bounds__(kRowThreads)
 head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
                const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
-               const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, float scale, __nv_bfloat16* dl, int64_t ld,
-               int V, float* loss, float* lse) {
+               const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, float scale,
+               __nv_bfloat16* dl, int64_t ld, int V, float* loss, float* lse) {
     __shared__ float red[128];
     pdl_allow_next();
     const int i = blockIdx.x;
@@ -1032,7 +1055,9 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
 
 // dx rows from the parts of K, added up in order, four columns a thread; without a
 // list of rows, a token without a label gets zeros. A kernel of dW's own is launched
-// behind this one and needs nothing of it, so it may begin at once.
+// behind this one and needs nothing of it, so it may begin at once. Bound by the parts'
+// way through L2: 5 us for 10 MB (T = 300, H = 1024, 8 parts); two to four CTAs an SM took the
+// same time, one 2% more of the whole call.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
 head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, const int32_t* __restrict__ rows,
@@ -1084,7 +1109,7 @@ bool make_tmap_pitch(CUtensorMap* m, const void* base, int64_t rows, int64_t col
 
 // The same for an MN-major operand whose rows are whole groups of 64 columns: [groups][rows][64], in boxes of two
 // groups x 64 rows, so that one copy brings a CTA's 128 columns of a K block (two copies for each operand were as much
-// as the producer could issue: dW at T = 2560, H = 7168, V = 32768 took 641 us, this ...).
+// as the producer could issue: dW at T = 2560, H = 7168, V = 32768 took 641 us, this 626).
 bool make_tmap_groups(CUtensorMap* m, const void* base, int64_t rows, int64_t groups, int64_t ld) {
     auto fn = encode_fn();
     if (!fn) return false;

@@ -7,6 +7,11 @@
 //   unsort          out[t] = sum_j w[t,j] * y[slot_row[t*k+j]]      (w = 1: sort's gradient)
 //   its gradient    dy[r] = w[t,j] * dout[t],   dw[t,j] = <dout[t], y[r]>
 // Sums run in fp32, j ascending; dropped entries add nothing and have dw = 0.
+//
+// The row moves are bound by memory, and a row is touched once by each: T = 4096,
+// H = 7168, k = 8, BF16, sort 79 us (6.7 TB/s), unsort 81 (6.5), its gradient 146 (6.8).
+// Small calls are bound by their launches: T = 7, k = 8, layout, sort and unsort 5.6 us
+// together in a graph.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -28,7 +33,8 @@ int64_t sort_block_entries(int64_t n) {
     return std::max<int64_t>(rounds, 1) * kSortThreads;
 }
 int sort_blocks(int64_t n) { return (int)((n + sort_block_entries(n) - 1) / sort_block_entries(n)); }
-// Up to this many entries one block counts and places them in one launch.
+// Up to this many entries one block counts and places them in one launch (4096 tokens' 32768
+// entries: count 4.6 us, place 7.8, each by itself).
 constexpr int kSortOneBlock = 2048;
 
 // hist[e * blocks + b] = entries of expert e among block b's (whole numbers, so
@@ -51,7 +57,7 @@ sort_count_kernel(const int32_t* __restrict__ idx, int64_t n, int64_t per, int E
 
 // Places block b's entries. `hist` == NULL: a single block, which counts itself.
 // The entries of a round (one a thread) are ranked by their lane among the same
-// expert's in their warp, then by their warp.
+// expert's in their warp, then by their warp: no atomic decides an order.
 __global__ void __launch_bounds__(kSortThreads)
 sort_place_kernel(const int32_t* __restrict__ idx, int64_t n, int64_t per, int E, const int32_t* __restrict__ hist,
                   int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_src,
@@ -206,7 +212,8 @@ struct Elem<MOK_ELEM_F32> {
 };
 
 // Rows move as 16-byte vectors whatever their type: nv of them a row. A thread
-// holds one vector of the token and writes it to the token's places.
+// holds one vector of the token and writes it to the token's places, so x is read once
+// whatever k.
 __global__ void __launch_bounds__(256)
 sort_rows_kernel(const uint4* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slot_row, int k, int nv,
                  uint4* __restrict__ out) {
