@@ -1053,30 +1053,45 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
     if (lse) lse[t] = r.top + logf(sum);
 }
 
-// dx rows from the parts of K, added up in order, four columns a thread; without a
-// list of rows, a token without a label gets zeros. A kernel of dW's own is launched
-// behind this one and needs nothing of it, so it may begin at once. Bound by the parts'
-// way through L2: 5 us for 10 MB (T = 300, H = 1024, 8 parts); two to four CTAs an SM took the
-// same time, one 2% more of the whole call.
+// dx rows from the parts of K, four columns a thread. WAYS = 1: a thread adds up all parts in
+// order. WAYS = 4, where that leaves most threads without work: the warp's four groups of
+// eight lanes add up every fourth part each, then these sums in a fixed order, so that a
+// thread's loads are one or two trips to L2 (T = 100, H = 512, V = 8191, whole calls: 27.7
+// us, 30.3 with one way; T = 14, H = 496, V = 65750: 61.7 and 67.6; but T = 300, H = 2048,
+// V = 32768: 168.6 and 163.5, bound by the bytes). Without a list of rows, a token without
+// a label gets zeros. A kernel of dW's own is launched behind this one and needs nothing
+// of it, so it may begin at once; two to four CTAs an SM took the same time, one 2% more.
 constexpr int kJoinThreads = 256;
+template <int WAYS>
 __global__ void __launch_bounds__(kJoinThreads)
 head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, const int32_t* __restrict__ rows,
                  const int32_t* __restrict__ live, const void* labels, int i64, int V, uint2* __restrict__ dx) {
     pdl_allow_next();
     pdl_wait();
     const int64_t total = (int64_t)(live ? *live : n) * nq;
-    for (int64_t at = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; at < total; at += (int64_t)gridDim.x * kJoinThreads) {
-        const int i = (int)(at / nq), v = (int)(at % nq);
-        const int64_t t = rows ? rows[i] : i;
+    constexpr int kLanes = 32 / WAYS;
+    const int lane = threadIdx.x & 31, way = lane / kLanes;
+    for (int64_t at0 = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x - lane) / WAYS; at0 < total;
+         at0 += (int64_t)gridDim.x * (kJoinThreads / WAYS)) {
+        const int64_t at = at0 + lane % kLanes;
+        const bool in = at < total;
+        const int64_t t = !in ? 0 : rows ? rows[at / nq] : at / nq;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (rows || is_live(labels, i64, t, V)) {
+        if (in && (rows || is_live(labels, i64, t, V))) {
 #pragma unroll 8
-            for (int s = 0; s < splits; ++s) {
+            for (int s = way; s < splits; s += WAYS) {
                 const float4 b = __ldcg(part + s * stride + at);
                 a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
             }
         }
-        dx[t * nq + v] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+#pragma unroll
+        for (int d = kLanes; d < 32; d <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, d);
+            a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, d);
+            a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+        }
+        if (in && way == 0) dx[t * nq + at % nq] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
     }
 }
 
@@ -1441,9 +1456,11 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             pw.add = first && !(a.dW_f32 && a.accumulate) ? nullptr : acc;
         }
         auto join = [&]() {
-            const int nq = H / 4;
-            const int ctas = (int)std::min<int64_t>(((int64_t)n * nq + kJoinThreads - 1) / kJoinThreads, 3 * sm_count());
-            return launch_after(head_join_kernel, dim3(ctas), dim3(kJoinThreads), 0, s, (const float4*)(ws + L.part),
+            const int nq = H / 4, most = 3 * sm_count();
+            const int64_t at_once = (int64_t)most * kJoinThreads, quads = (int64_t)n * nq;
+            const bool four = 4 * quads <= at_once;
+            const int ctas = (int)std::min<int64_t>(((four ? 4 : 1) * quads + kJoinThreads - 1) / kJoinThreads, most);
+            return launch_after(four ? head_join_kernel<4> : head_join_kernel<1>, dim3(ctas), dim3(kJoinThreads), 0, s, (const float4*)(ws + L.part),
                                 (int64_t)n * nq, splits, n, nq, (const int32_t*)rows, (const int32_t*)live, labels,
                                 a.labels_i64, V, reinterpret_cast<uint2*>(dx));
         };
