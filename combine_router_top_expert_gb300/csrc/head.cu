@@ -936,8 +936,10 @@ struct RowSum {
 };
 __device__ __forceinline__ RowSum join_row(const float2* stats, int n, float label_logit, float* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = label_logit;   // at its place in the order, if the tiles' own is a little lower
-    for (int i = threadIdx.x; i < n; i += kRowThreads) m = fmaxf(m, __ldcg(stats + i).x);
+    // a thread's first pair stays in registers between the two passes
+    const float2 v0 = (int)threadIdx.x < n ? __ldcg(stats + threadIdx.x) : make_float2(-INFINITY, 0.f);
+    float m = fmaxf(label_logit, v0.x);   // the label's, at its place in the order, if the tiles' own is a little lower
+    for (int i = threadIdx.x + kRowThreads; i < n; i += kRowThreads) m = fmaxf(m, __ldcg(stats + i).x);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (lane == 0) red[warp] = m;
@@ -946,11 +948,9 @@ __device__ __forceinline__ RowSum join_row(const float2* stats, int n, float lab
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float base = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const float2 v = __ldcg(stats + i);
-        s += v.y * exp2_approx((v.x == -INFINITY ? -INFINITY : v.x - base) * kLog2e);
-    }
+    auto term = [&](const float2& v) { return v.y * exp2_approx((v.x == -INFINITY ? -INFINITY : v.x - base) * kLog2e); };
+    float s = term(v0);
+    for (int i = threadIdx.x + kRowThreads; i < n; i += kRowThreads) s += term(__ldcg(stats + i));
     s = cta_sum(s, red + 32);
     RowSum r;
     r.top = base;
@@ -1030,14 +1030,20 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
         return;
     }
     const float2* st = stats + (int64_t)i * stat_tiles;
+    // a thread's first eight exponentials are on their way while the sums are joined
+    const int first = v0 + threadIdx.x;
+    uint4 e0 = make_uint4(0, 0, 0, 0);
+    float top0 = 0.f;
+    if (first < v1) {
+        e0 = __ldcg(reinterpret_cast<const uint4*>(row + 8 * first));
+        top0 = __ldcg(st + first / 16).x;
+    }
     const RowSum r = join_row(st, stat_tiles, own, red);
     const float sum = r.others + r.own;
     const float coef = scale * (dloss ? dloss[t] : 1.0f);
     const float inv = coef / sum * kRootScale;
-#pragma unroll 4
-    for (int v = v0 + threadIdx.x; v < v1; v += kRowThreads) {
-        const uint4 e = __ldcg(reinterpret_cast<const uint4*>(row + 8 * v));
-        const float f = inv * exp2_approx((__ldcg(st + v / 16).x - r.top) * kLog2e);
+    auto form = [&](int v, const uint4& e, float top) {
+        const float f = inv * exp2_approx((top - r.top) * kLog2e);
         const uint32_t w[4] = {e.x, e.y, e.z, e.w};
         uint32_t o[4];
 #pragma unroll
@@ -1047,7 +1053,11 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
         }
         *reinterpret_cast<uint4*>(row + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
         if (label >> 3 == v) row[label] = __float2bfloat16_rn(-coef * (r.others / sum));
-    }
+    };
+    if (first < v1) form(first, e0, top0);
+#pragma unroll 4
+    for (int v = first + kRowThreads; v < v1; v += kRowThreads)
+        form(v, __ldcg(reinterpret_cast<const uint4*>(row + 8 * v)), __ldcg(st + v / 16).x);
     if (threadIdx.x != 0 || blockIdx.y != 0) return;
     loss[t] = row_loss(r, own);
     if (lse) lse[t] = r.top + logf(sum);
