@@ -18,8 +18,8 @@
 //                    their place: 6TVH operations for a training call, none repeated
 //   dX      dl W     A K-major, B MN-major (the vocabulary is K)
 //   dW      dl^T x   both MN-major (the tokens are K)
-// Few tokens are bound by the bytes of W (T = 64, H = 7168, V = 131072: 292 us, 6.4
-// TB/s), many by the tensor cores (T = 2560, H = 7168, V = 50001, scoring: 960 to 1090
+// Few tokens are bound by the bytes of W (H = 7168, V = 131072, call after call: T = 64
+// 294 us, 6.4 TB/s, T = 1 278 us), many by the tensor cores (T = 2560, H = 7168, V = 50001, scoring: 960 to 1090
 // us, 1.9 to 1.7 PFLOP/s as the power limit lets the clock run; T = 4096, V = 131072,
 // training: 13.2 to 14.5 ms, 1.75 to 1.6 PFLOP/s).
 #include <cudaTypedefs.h>
@@ -228,10 +228,12 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
     auto accf_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + a); };
     auto acce_bar = [&](int a) { return bar_base + 8u * (2 * kMaxStages + 2 + a); };
     const uint32_t drain_bar = bar_base + 8u * (2 * kMaxStages + 4);
-    const uint32_t a_room = p0.a_room, stage_bytes = a_room + kOperandBytes;
+    // the stages' rows of A, then room for the rest of a tile behind the last one, then their rows of B
+    const uint32_t a_room = p0.a_room;
     const int stages = p0.stages;
-    auto a_tile = [&](int s) { return smem_base + s * stage_bytes; };
-    auto b_tile = [&](int s) { return smem_base + s * stage_bytes + a_room; };
+    const uint32_t b_base = smem_base + (stages - 1) * a_room + kOperandBytes;
+    auto a_tile = [&](int s) { return smem_base + s * a_room; };
+    auto b_tile = [&](int s) { return b_base + s * kOperandBytes; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     StatusBlock* st = p0.status;
@@ -254,6 +256,15 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
             tc::prefetch_tmap(&jobs.job[j].b);
             tc::prefetch_tmap(&jobs.job[j].all);
         }
+    }
+    if (a_room < kOperandBytes && warp >= 2) {
+        // Zeros where no row is loaded: a CTA without tokens, and behind the last stage. Products with whatever
+        // lay there were discarded too, but took power: call after call the SM clock fell to 1560 MHz (T = 1, H =
+        // 7168, V = 131072: 312 us; this 2010 MHz, 278).
+        const uint32_t from = tc::cluster_ctarank() == 0 ? stages * a_room : 0;
+        for (uint32_t a = smem_base + from + (threadIdx.x - 64) * 16; a < b_base; a += 32 * kEpiWarps * 16)
+            tc::st_shared_v4(a, 0, 0, 0, 0);
+        tc::fence_proxy_async_shared();
     }
     if (warp == 1) {
         tc::tmem_alloc_2sm(tc::smem_u32(&s_tmem_base), 512);
@@ -321,7 +332,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                         tc::tma_load_2d_2sm(a_tile(stage) + 8192, map, lead, m0 + 64, k0);
                     }
                 } else if (p.a_bytes == kOperandBytes || rank == 0) {
-                    // (few rows: the leader alone has some, and the MMAs' other rows are whatever lies there)
+                    // (few rows: the leader alone has some, and the MMAs' other rows are the next stages' or zeros)
                     tc::tma_load_2d_2sm(a_tile(stage), map, lead, k0, m0);
                 }
             };
@@ -413,8 +424,8 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
             uint32_t idesc = 0, step_a = 0, al0 = 0;
             const uint32_t bl0 = b_tile(0) >> 4 | kLoB;
             auto mma4 = [&](uint32_t d, int sg, uint32_t more) {
-                const uint32_t al = al0 + (uint32_t)sg * (stage_bytes >> 4);
-                const uint32_t bl = bl0 + (uint32_t)sg * (stage_bytes >> 4);
+                const uint32_t al = al0 + (uint32_t)sg * (a_room >> 4);
+                const uint32_t bl = bl0 + (uint32_t)sg * (kOperandBytes >> 4);
                 const uint32_t sa = N == 2 ? step_a : A_MN ? 128u : 2u;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -1197,7 +1208,7 @@ bool make_job(HeadJob& J, bool a_mn, bool b_mn, int epi, const Operand& a, const
     const int rows = !a_mn && !p.m_live && p.M <= 128 ? (int)align_up(p.M, 8) : 128;
     p.a_mn = a_mn;
     p.a_bytes = p.a_room = rows * kBK * 2;
-    p.stages = std::min(kMaxStages, kBarOffset / (p.a_room + kOperandBytes));
+    p.stages = std::min(kMaxStages, (kBarOffset - kOperandBytes + p.a_room) / (p.a_room + kOperandBytes));
     p.a_groups = a_mn && a.cols % 64 == 0;
     p.b_groups = b_mn && b.cols % 64 == 0;
     auto map = [](CUtensorMap* m, const Operand& o, bool groups, int box_rows) {
