@@ -964,10 +964,17 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
     if (T > 0 && (!a->x || !a->labels || (forward && !a->loss) || (!forward && !a->lse))) return MOK_ERR_INVALID;
     if (grad && !a->dx && !a->dW) return MOK_ERR_INVALID;
     if (grad && a->accumulate && !a->dW_f32) return MOK_ERR_INVALID;
-    if (grad && a->dx && T > 0) {   // apart from x, or all of it where dW does not need x any more
-        const char *x = static_cast<const char*>(a->x), *dx = static_cast<const char*>(a->dx);
-        const bool apart = dx + (int64_t)T * H * 2 <= x || x + ((int64_t)(T - 1) * a->ldx + H) * 2 <= dx;
-        if (!apart && (a->dW || dx != x || a->ldx != H)) return MOK_ERR_INVALID;
+    if (grad) {   // dx may be all of x where dW does not need x any more; else gradients lie apart from what is read
+        const int64_t row = (int64_t)H * 2, x_bytes = T > 0 ? ((int64_t)(T - 1) * a->ldx + H) * 2 : 0;
+        const int64_t dw_bytes = (int64_t)V * H * (a->dW_f32 ? 4 : 2);
+        auto apart = [](const void* p, int64_t n, const void* q, int64_t m) {
+            const char *b = static_cast<const char*>(p), *c = static_cast<const char*>(q);
+            return !b || !c || n == 0 || m == 0 || b + n <= c || c + m <= b;
+        };
+        const bool in_place = a->dx == a->x && a->ldx == H && !a->dW;
+        if (!in_place && !apart(a->dx, T * row, a->x, x_bytes)) return MOK_ERR_INVALID;
+        if (!apart(a->dx, T * row, a->W, V * row) || !apart(a->dx, T * row, a->dW, dw_bytes)) return MOK_ERR_INVALID;
+        if (!apart(a->dW, dw_bytes, a->W, V * row) || !apart(a->dW, dw_bytes, a->x, x_bytes)) return MOK_ERR_INVALID;
     }
     if (!aligned(a->x, 16) || !aligned(a->W, 16) || !aligned(a->labels, a->labels_i64 ? 8 : 4) || !aligned(a->loss, 4) ||
         !aligned(a->lse, 4) || !aligned(a->dloss, 4) || !aligned(a->dx, 16) || !aligned(a->dW, 16) ||

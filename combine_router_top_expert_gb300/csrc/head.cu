@@ -19,9 +19,10 @@
 //   dX      dl W     A K-major, B MN-major (the vocabulary is K)
 //   dW      dl^T x   both MN-major (the tokens are K)
 // Few tokens are bound by the bytes of W (H = 7168, V = 131072, call after call: T = 64
-// 294 us, 6.4 TB/s, T = 1 278 us), many by the tensor cores (T = 2560, H = 7168, V = 50001, scoring: 960 to 1090
-// us, 1.9 to 1.7 PFLOP/s as the power limit lets the clock run; T = 4096, V = 131072,
-// training: 13.2 to 14.5 ms, 1.75 to 1.6 PFLOP/s).
+// 294 us, 6.4 TB/s; T = 1 278 us), many by the tensor cores and what the power limit
+// leaves of their clock (T = 2560, H = 7168, V = 50001, scoring: 975 us when the GPU is
+// cool, 1110 call after call, 1.9 and 1.65 PFLOP/s; T = 4096, V = 131072, training: 12.9
+// and 14.5 ms, 1.8 and 1.6 PFLOP/s).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
@@ -214,7 +215,7 @@ struct HeadSize {
 // (86% of the tensor cores' cycles; V = 50001: 92%), with exponentials 637, dX 686, dW 650
 // (76%; MN-major operands: the power limit sets their clock). Kept out because they gained
 // nothing: clusters of four with multicast, five stages with a second staging buffer, each
-// pair's walk of K begun elsewhere.
+// pair's walk of K begun elsewhere, waits that sleep (the clock rose by 5%, the time too).
 template <bool A_MN, bool B_MN, int EPI, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {

@@ -602,8 +602,8 @@ mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a
  * dl[t,v] = scale * dloss[t] * (exp(l[t,v] - lse[t]) - [v == labels[t]]), rounded to
  * bf16, dx = dl W and dW = dl^T x in fp32, rounded once. Ignored tokens have zeros in
  * dx and add nothing to dW. At least one of dx and dW is given; dx may be x's own
- * buffer if ldx == H and dW is NULL, and does not overlap x otherwise. Logits are
- * formed again. */
+ * buffer if ldx == H and dW is NULL; otherwise dx and dW overlap neither x and W nor
+ * each other. Logits are formed again. */
 mok_status mok_head_loss_backward(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
                                   mok_stream_t stream);
 

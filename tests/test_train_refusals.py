@@ -32,8 +32,11 @@ GRAD_BAD = [dict(dx=None, dW=None), dict(accumulate=1), dict(dx=PTR + 8), dict(d
 @pytest.mark.parametrize("call", ["mok_head_loss", "mok_head_loss_backward", "mok_head_loss_train"])
 def test_head_arguments(L, call):
     f = getattr(L, call)
-    # dx in x's place is refused with dW, so those that are good otherwise have another dx
-    good = dict(dx=PTR << 1)
+    # one that is good (but for the workspace's size, so that nothing is launched)
+    good = dict(dx=PTR << 1, W=PTR << 2, dW=PTR << 3)
+    if not torch.cuda.is_available():
+        assert f(4, 64, 100, _head(**good, ws_bytes=0), None, None) == mok.ERR_CUDA
+        assert f(4, 64, 100, _head(**{**good, "dx": PTR, "dW": None}, ws_bytes=0), None, None) == mok.ERR_CUDA
     for bad in HEAD_BAD + ([] if call == "mok_head_loss" else GRAD_BAD):
         assert f(4, 64, 100, _head(**{**good, **bad}), None, None) == mok.ERR_INVALID, bad
     for T, H, V in ((-1, 64, 100), (4, 60, 100), (4, 0, 100), (4, 65544, 100), (4, 64, 0), (4, 64, (1 << 24) + 1),
@@ -42,10 +45,13 @@ def test_head_arguments(L, call):
         assert mok.head_workspace_size(T, H, V, True) == 0
     assert f(4, 64, 100, None, None, None) == mok.ERR_INVALID
     if call != "mok_head_loss":
-        assert f(4, 64, 100, _head(), None, None) == mok.ERR_INVALID          # dx in x's place, and dW
-        assert f(4, 64, 100, _head(dW=None, ldx=72), None, None) == mok.ERR_INVALID
+        overlaps = [dict(dx=PTR), dict(dx=PTR, dW=None, ldx=72)]              # x's place: with dW, of wider rows
         for at in (PTR + 128, PTR - 128, PTR + 4 * 128 - 16, PTR - 4 * 128 + 16):     # some of x's rows
-            assert f(4, 64, 100, _head(dW=None, dx=at), None, None) == mok.ERR_INVALID
+            overlaps += [dict(dx=at, dW=None), dict(dW=at)]
+        overlaps += [dict(dx=PTR << 2), dict(dW=PTR << 2), dict(dW=(PTR << 2) + 99 * 128), dict(dx=(PTR << 3) + 128),
+                     dict(dW=(PTR << 2) - 128 * 128, dW_f32=1)]
+        for kw in overlaps:
+            assert f(4, 64, 100, _head(**{**good, **kw}), None, None) == mok.ERR_INVALID, kw
     missing = dict(lse=None) if call == "mok_head_loss_backward" else dict(loss=None)
     assert f(4, 64, 100, _head(**good, **missing), None, None) == mok.ERR_INVALID
 
