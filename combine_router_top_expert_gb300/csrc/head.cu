@@ -1333,7 +1333,7 @@ HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
     };
     L.piece = piece_tokens(T, V, want);
     L.splits = grad ? dx_splits(L.piece, H, V, num_sms / 2) : 1;
-    const int64_t cap = align_up(L.piece, kBM);
+    const int64_t cap = T > kPlainRows ? align_up(L.piece, kBM) : L.piece;   // gathered rows fill tiles
     L.live = take(4);
     L.rows = take(cap * 4);
     L.label = take(cap * 4);

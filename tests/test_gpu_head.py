@@ -360,3 +360,43 @@ def test_waits_that_run_out(T, H, V, call):
             assert torch.equal(loss, want[0])
         if call != "score":
             assert torch.equal(dx, want[2]) and torch.equal(dW, want[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5, 129, 256, 257, 300])
+@pytest.mark.parametrize("H,V", [(72, 1003), (512, 2500)])
+@pytest.mark.parametrize("call,f32,piece", [("score", False, 0), ("train", False, 0), ("train", True, 128),
+                                            ("backward", False, 100)])
+def test_nothing_else_is_written(T, H, V, call, f32, piece):
+    """Outputs and a workspace of exactly its size lie between bytes that stay as they were, and so do the inputs."""
+    grad = call != "score"
+    kinds = dict(loss=(torch.float32, (T,)), lse=(torch.float32, (T,)), dx=(torch.bfloat16, (T, H)),
+                 dW=(torch.float32 if f32 else torch.bfloat16, (V, H)),
+                 ws=(torch.uint8, (mok.head_workspace_size(T, H, V, grad, piece if grad else 0),)))
+    gap, spans, at = 8192, {}, 8192
+    for name, (dt, shape) in kinds.items():
+        n = torch.empty(shape, dtype=dt, device="meta").nbytes
+        spans[name] = (at, n)
+        at += n + gap
+        at = (at + 1023) // 1024 * 1024
+    room = torch.full((at + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+    room = room[-room.data_ptr() % 1024:]
+    t = {name: room[a:a + n].view(kinds[name][0]).view(kinds[name][1]) for name, (a, n) in spans.items()}
+    g = ref.gen(T + V)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn((V, H), generator=g, device="cuda") * 0.1).to(torch.bfloat16)
+    y = _labels(T, V, T)
+    kept = [v.clone() for v in (x, W, y)]
+    if call == "score":
+        mok.head_loss(x, W, y, t["loss"], t["ws"], lse=t["lse"])
+    elif call == "train":
+        mok.head_loss_train(x, W, y, t["loss"], t["dx"], t["dW"], t["ws"], lse=t["lse"], piece=piece)
+    else:
+        t["lse"].copy_(_score(x, W, y)[1])
+        mok.head_loss_backward(x, W, y, t["lse"], t["dx"], t["dW"], t["ws"], piece=piece)
+    assert mok.device_status(t["ws"]) == (mok.OK, 0)
+    outside = torch.ones(room.numel(), dtype=torch.bool, device="cuda")
+    for a, n in spans.values():
+        outside[a:a + n] = False
+    assert (room[outside] == 0x5A).all()
+    assert all(torch.equal(a, b) for a, b in zip(kept, (x, W, y)))
