@@ -198,3 +198,41 @@ def test_own_experts(drop):
     want.backward(dout.double())
     for a, b in ((out, want.detach()), (dx, xd.grad), (dw, wd.grad)):
         assert float((a.double() - b).abs().max()) <= 1e-4 * float(b.abs().max())
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Training calls, clipping and sorted rows on two streams side by side, each with its own buffers, give the bits
+    that they give one after the other."""
+    H, V, E, k = 512, 5003, 8, 2
+    g = ref.gen(31)
+    sets = []
+    for T in (300, 64):
+        x, labels = _rows(g, T, H), torch.randint(-1, V, (T,), generator=g, device="cuda")
+        idx = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+        sets.append((_head(V, H, T), x, labels, idx, torch.rand((T, k), generator=g, device="cuda")))
+
+    def step(head, x, labels, idx, w, stream=None):
+        T = x.shape[0]
+        loss, grads = head.train(x, labels, stream=stream)
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            norm, ws = torch.empty((), device="cuda"), mok.alloc_bytes(mok.grad_workspace_size())
+            mok.grad_clip(list(grads.values()), 0.01, norm, ws)
+            layout = mok.sort_layout(idx, E)
+            xs, out = torch.zeros((T * k, H), dtype=x.dtype, device="cuda"), torch.empty_like(x)
+            mok.sort_rows(x, layout, xs)
+            mok.unsort_rows(xs, layout, out, w=w)
+        return [loss, norm, xs, out, *grads.values()]
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[] for _ in sets]
+    for _ in range(20):
+        for i, s in enumerate(sets):
+            got[i].append(step(*s, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, s in enumerate(sets):
+        assert s[0].status() == (mok.OK, 0)
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
