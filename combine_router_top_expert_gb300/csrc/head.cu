@@ -3,8 +3,13 @@
 //
 // With x [T,H], W [V,H] and the label y_t of token t:
 //   l[t,v] = <x_t, W_v>      lse_t = log sum_v exp l[t,v]      loss_t = lse_t - l[t,y_t]
-//   dl[t,v] = c_t (exp(l[t,v] - lse_t) - [v == y_t])           c_t = scale * dloss_t
-//   dX = dl W                dW = dl^T x
+//   dl[t,v] = d_t (exp(l[t,v] - lse_t) - [v == y_t])           d_t = dloss_t / top
+//   dX = c dl W              dW = c dl^T x                     c = scale * top
+// with top the largest finite |dloss| (1 without dloss). dl is rounded to BF16, and an
+// unlikely token's entry is nearly -d_t: with the whole coefficient in it all tokens'
+// entries would be off by the same share, up to 2^-8 (scale = 1/4080: gradients 0.37%
+// too short). So the common factor is taken out and multiplies the fp32 sums, and
+// without dloss, or with equal ones, dl is the softmax less the label.
 // Tokens whose label is outside 0..V-1 count for nothing, whatever their rows hold. In
 // a call of more than one row tile the live ones are gathered first (head_prep_kernel),
 // and none of the products is spent on the others.
@@ -89,7 +94,7 @@ struct HeadGemm {
     const float* label_logit;   // [tokens]
     const float* lse;       // [T]
     const float* dloss;     // [T] or NULL
-    float scale;
+    const float* factors;   // {top, c}, written by the call's first kernel
     __nv_bfloat16* dl;      // [dl_rows, ld_dl]
     int64_t ld_dl;
     int64_t dl_rows;
@@ -97,6 +102,7 @@ struct HeadGemm {
     int tma_out;            // rows leave as tmOut's boxes; else (scattered, or added to) by the warps' stores
     void* out;
     int out_f32;
+    int scaled;             // times c (else what c is to multiply is joined first)
     const float* add;       // fp32 rows that are added to the product, or NULL
     const int32_t* out_rows;   // row -> output row, or NULL
     int zero_dead;          // rows whose label is not below live_below are zeros
@@ -524,6 +530,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
             const Range range = range_of(j, z);
             const int M = z.M;
             const bool all = z.all;
+            const float by = EPI == kEpiOut && p.scaled ? __ldcg(p.factors + 1) : 1.0f;
             for (int g = range.g0; g < range.g1; g += range.step) {
                 const Tile t = head_tile(g, z.mt, z.nt, p.group);
                 const int blocks = k_first(p, z, t.split + 1) - k_first(p, z, t.split);
@@ -545,7 +552,7 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                         const int64_t y = label_at(p.labels, p.labels_i64, tok);
                         if (y >= 0 && y < p.N) lab = (int)y;
                         if (EPI == kEpiDl && lab >= 0) {
-                            mul = p.scale * (p.dloss ? __ldg(p.dloss + tok) : 1.0f);
+                            mul = p.dloss ? __ldg(p.dloss + tok) / __ldcg(p.factors) : 1.0f;
                             const float lse = __ldg(p.lse + tok);
                             base = -kLog2e * lse;
                             label_at_lse = __ldcg(p.label_logit + row) - lse;
@@ -622,6 +629,14 @@ head_gemm_kernel(const __grid_constant__ HeadJobs<N> jobs) {
                             if (row0 < p.dl_rows) send_pass(J, col0 + 64 * h, row0, 0);
                             continue;
                         }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 e = __fmul2_rn(make_float2(r[c][i], r[c][i + 1]), make_float2(by, by));
+                                r[c][i] = e.x;
+                                r[c][i + 1] = e.y;
+                            }
                         if (!p.out_f32 && !p.add) {
                             begin_pass();
 #pragma unroll
@@ -808,19 +823,45 @@ __device__ __forceinline__ float label_dot(const uint4* x, const uint4* w, int n
     return s;
 }
 
+// |d| as bits whose order is its own; 0 for NaN and infinity, which stay their token's.
+__device__ __forceinline__ unsigned finite_bits(float d) {
+    const unsigned u = __float_as_uint(d) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
+}
+// {top, c}; without live tokens c is 0, whatever the scale (1 / 0, say): gradients are zeros.
+__device__ __forceinline__ void put_factors(float* factors, unsigned top_bits, bool any, float scale) {
+    const float top = top_bits ? __uint_as_float(top_bits) : 1.0f;
+    factors[0] = top;
+    factors[1] = any ? scale * top : 0.f;
+}
+
 // For up to one row tile of tokens: a CTA per token copies its row, zeros for a token
 // without a label, for dW (whose K the tokens are), and forms the label's logit if
-// asked. The first CTA clears the status block. Without xc: that alone. Bound by its
-// launch: 5 us by itself at T = 8, less than 1 in a chain of launches.
+// asked. The first CTA clears the status block, and one behind the tokens' forms the
+// gradient's factors. Without xc: the status block alone. Bound by its launch: 5 us by
+// itself at T = 8, less than 1 in a chain of launches.
 __global__ void __launch_bounds__(kRowThreads)
 head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
-                  int V, int nv, uint4* __restrict__ xc, float* label_logit, int32_t* status) {
+                  int V, int nv, const float* __restrict__ dloss, float scale, float* factors, uint4* __restrict__ xc,
+                  float* label_logit, int32_t* status) {
     __shared__ float red[33];
+    __shared__ unsigned top;
     pdl_wait();
     pdl_allow_next();
     const int64_t t = blockIdx.x;
     if (t == 0 && status && threadIdx.x < kStatusBytes / 4) status[threadIdx.x] = 0;
     if (!xc) return;
+    if (t == gridDim.x - 1) {   // at most kPlainRows tokens, one a thread
+        if (threadIdx.x == 0) top = 0;
+        const bool in = threadIdx.x < gridDim.x - 1;
+        const float d = in && dloss ? __ldg(dloss + threadIdx.x) : 0.f;
+        const bool l = in && is_live(labels, i64, threadIdx.x, V);
+        const int any = __syncthreads_or(l);
+        if (l) atomicMax(&top, finite_bits(d));
+        __syncthreads();
+        if (threadIdx.x == 0) put_factors(factors, top, any, scale);
+        return;
+    }
     const bool on = is_live(labels, i64, t, V);
     for (int v = threadIdx.x; v < nv; v += kRowThreads)
         xc[t * nv + v] = on ? __ldg(x + t * ldx + v) : make_uint4(0, 0, 0, 0);
@@ -835,7 +876,8 @@ head_start_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restr
 // every token is live, and their labels' logits are formed; the others' outputs are
 // zeroed. Each CTA counts the live tokens before its own from the labels themselves.
 // Behind the last live row, rows up to the next multiple of kBK are zeroed: dW's last K
-// block reads them. The first CTA clears the status block. Bound by the loads in flight, so
+// block reads them. The first CTA clears the status block and, with a gradient, forms its
+// factors. Bound by the loads in flight, so
 // four tokens' rows are read side by side: 25 us at T = 2560, H = 7168 (73 MB, 2.9 TB/s from
 // a cold start). Beside the logits' kernel in a kernel of its own, the labels' logits cost
 // as much time as here (scoring T = 1000, H = 4096, V = 20000: 115.8 and 117.1 us; with a
@@ -845,8 +887,9 @@ __global__ void __launch_bounds__(kRowThreads)
 head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restrict__ W, const void* labels, int i64,
                  int T, int V, int nv, int span, int32_t* __restrict__ rows, int32_t* __restrict__ live,
                  uint4* __restrict__ xc, float* __restrict__ label_logit, float* loss, float* lse, uint4* dx,
-                 int32_t* status) {
+                 const float* __restrict__ dloss, float scale, float* factors, int32_t* status) {
     __shared__ int32_t sh[2];
+    __shared__ unsigned top;
     __shared__ int32_t place[kPrepTokens];
     __shared__ float red[kPrepTokens][kRowThreads / 32];
     pdl_wait();
@@ -854,25 +897,35 @@ head_prep_kernel(const uint4* __restrict__ x, int64_t ldx, const uint4* __restri
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = blockIdx.x * span, t1 = min(t0 + span, T);
     if (tid < 2) sh[tid] = 0;
+    if (tid == 2) top = 0;
     if (blockIdx.x == 0 && status && tid < kStatusBytes / 4) status[tid] = 0;
     __syncthreads();
     int before = 0, count = 0;
+    unsigned bits = 0;
+    const float* weights = blockIdx.x == 0 ? dloss : nullptr;
 #pragma unroll 8
     for (int t = tid; t < T; t += kRowThreads) {
         const int l = is_live(labels, i64, t, V) ? 1 : 0;
         count += l;
         before += t < t0 ? l : 0;
+        const unsigned b = weights ? finite_bits(__ldg(weights + t)) : 0u;
+        bits = l ? max(bits, b) : bits;
     }
+    bits = __reduce_max_sync(0xffffffffu, bits);
     before = __reduce_add_sync(0xffffffffu, before);
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) {
         atomicAdd(&sh[0], before);
         atomicAdd(&sh[1], count);
+        atomicMax(&top, bits);
     }
     __syncthreads();
     const int total = sh[1];
     int next = sh[0];
-    if (blockIdx.x == 0 && tid == 0) *live = total;
+    if (blockIdx.x == 0 && tid == 0) {
+        *live = total;
+        if (factors) put_factors(factors, top, total > 0, scale);
+    }
     const bool all = total == T;
     for (int c0 = t0; c0 < t1; c0 += kPrepTokens) {
         const int n = min(kPrepTokens, t1 - c0);
@@ -1004,7 +1057,7 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 }
 
 // The same with a gradient: then the row's exponentials, in their place, become
-//   dl[v] = c e[v] exp(top of its columns - lse),   dl[label] = -c others / (others + own)
+//   dl[v] = d e[v] exp(top of its columns - lse),   dl[label] = -d others / (others + own)
 // and zeros for a token without a label (rows == NULL; else only live tokens are here).
 // Few rows are cut along the vocabulary (gridDim.y), each part joining the sums itself.
 // One pass over the bytes, read and written: 322 us at T = 4096, V = 131072 (6.7 TB/s),
@@ -1014,7 +1067,7 @@ head_loss_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* 
 __global__ void __launch_bounds__(kRowThreads)
 head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __restrict__ x, int64_t ldx,
                const uint4* __restrict__ W, int nv, const int32_t* __restrict__ rows, const int32_t* __restrict__ live,
-               const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, float scale,
+               const float* label_logit, const void* labels, int i64, const float* __restrict__ dloss, const float* factors,
                __nv_bfloat16* dl, int64_t ld, int V, float* loss, float* lse) {
     __shared__ float red[128];
     pdl_allow_next();
@@ -1029,6 +1082,7 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
     float own = 0.f;
     if (live) own = __ldcg(label_logit + i);
     else if (on) own = cta_sum(label_dot(x + t * ldx, W + (int64_t)label * nv, nv, threadIdx.x, kRowThreads), red + 96);
+    const float coef = dloss ? dloss[t] / __ldcg(factors) : 1.0f;
     pdl_wait();
     __nv_bfloat16* row = dl + i * ld;
     const int vecs = (V + 7) / 8, per = (vecs + (int)gridDim.y - 1) / (int)gridDim.y;
@@ -1052,7 +1106,6 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
     }
     const RowSum r = join_row(st, stat_tiles, own, red);
     const float sum = r.others + r.own;
-    const float coef = scale * (dloss ? dloss[t] : 1.0f);
     const float inv = coef / sum * kRootScale;
     auto form = [&](int v, const uint4& e, float top) {
         const float f = inv * exp2_approx((top - r.top) * kLog2e);
@@ -1081,14 +1134,16 @@ head_dl_kernel(const float2* __restrict__ stats, int stat_tiles, const uint4* __
 // thread's loads are one or two trips to L2 (T = 100, H = 512, V = 8191, whole calls: 27.7
 // us, 30.3 with one way; T = 14, H = 496, V = 65750: 61.7 and 67.6; but T = 300, H = 2048,
 // V = 32768: 168.6 and 163.5, bound by the bytes). Without a list of rows, a token without
-// a label gets zeros. A kernel of dW's own is launched behind this one and needs nothing
+// a label gets zeros. The sums are multiplied by c. A kernel of dW's own is launched behind this one and needs nothing
 // of it, so it may begin at once; two to four CTAs an SM took the same time, one 2% more.
 constexpr int kJoinThreads = 256;
 template <int WAYS>
 __global__ void __launch_bounds__(kJoinThreads)
 head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, const int32_t* __restrict__ rows,
-                 const int32_t* __restrict__ live, const void* labels, int i64, int V, uint2* __restrict__ dx) {
+                 const int32_t* __restrict__ live, const void* labels, int i64, int V, const float* factors,
+                 uint2* __restrict__ dx) {
     pdl_allow_next();
+    const float c = __ldcg(factors + 1);   // complete since before the kernel ahead began, as the labels
     pdl_wait();
     const int64_t total = (int64_t)(live ? *live : n) * nq;
     constexpr int kLanes = 32 / WAYS;
@@ -1098,8 +1153,9 @@ head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, 
         const int64_t at = at0 + lane % kLanes;
         const bool in = at < total;
         const int64_t t = !in ? 0 : rows ? rows[at / nq] : at / nq;
+        const bool on = in && (rows || is_live(labels, i64, t, V));
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in && (rows || is_live(labels, i64, t, V))) {
+        if (on) {
 #pragma unroll 8
             for (int s = way; s < splits; s += WAYS) {
                 const float4 b = __ldcg(part + s * stride + at);
@@ -1113,7 +1169,8 @@ head_join_kernel(const float4* part, int64_t stride, int splits, int n, int nq, 
             a.z += __shfl_xor_sync(0xffffffffu, a.z, d);
             a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
         }
-        if (in && way == 0) dx[t * nq + at % nq] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        if (in && way == 0)
+            dx[t * nq + at % nq] = on ? make_uint2(pack_bf16x2(a.x * c, a.y * c), pack_bf16x2(a.z * c, a.w * c)) : make_uint2(0, 0);
     }
 }
 
@@ -1334,7 +1391,7 @@ HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
     L.piece = piece_tokens(T, V, want);
     L.splits = grad ? dx_splits(L.piece, H, V, num_sms / 2) : 1;
     const int64_t cap = T > kPlainRows ? align_up(L.piece, kBM) : L.piece;   // gathered rows fill tiles
-    L.live = take(4);
+    L.live = take(12);   // and the gradient's two factors
     L.rows = take(cap * 4);
     L.label = take(cap * 4);
     L.stats = take(L.piece * (int64_t)(2 * ceil_div(V, kBN)) * 8);
@@ -1362,6 +1419,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
     uint4* xc = reinterpret_cast<uint4*>(ws + L.xc);
     __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(ws + L.dl);
     const uint4* W = static_cast<const uint4*>(a.W);
+    float* factors = grad ? reinterpret_cast<float*>(ws + L.live) + 1 : nullptr;
     const int nv = H / 8;
     cudaError_t e = cudaSuccess;
     if (T == 0) {
@@ -1390,10 +1448,10 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             const int span = kPrepTokens * ceil_div(n, kPrepTokens * 1024);
             e = launch_after(head_prep_kernel, dim3(ceil_div(n, span)), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
                              a.labels_i64, n, V, nv, span, rows, live, xc, label, loss, forward ? lse : nullptr,
-                             reinterpret_cast<uint4*>(dx), status);
+                             reinterpret_cast<uint4*>(dx), dloss, a.scale, factors, status);
         } else {
-            e = launch_after(head_start_kernel, dim3(grad ? n : 1), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
-                             a.labels_i64, V, nv, grad ? xc : nullptr, logit, status);
+            e = launch_after(head_start_kernel, dim3(grad ? n + 1 : 1), dim3(kRowThreads), 0, s, xv, a.ldx / 8, W, labels,
+                             a.labels_i64, V, nv, dloss, a.scale, factors, grad ? xc : nullptr, logit, status);
         }
         if (e != cudaSuccess) return e;
         HeadGemm p{};
@@ -1408,7 +1466,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
         p.labels = labels;
         p.labels_i64 = a.labels_i64;
         p.label_logit = label;
-        p.scale = a.scale;
+        p.factors = factors;
         p.lse = lse;
         p.dloss = dloss;
         p.stats = stats;
@@ -1437,7 +1495,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             if (e == cudaSuccess)
                 e = launch_after(head_dl_kernel, dim3(n, dl_parts(n, V)), dim3(kRowThreads), 0, s, (const float2*)stats, p.stat_tiles,
                                  xv, a.ldx / 8, W, nv, (const int32_t*)rows, (const int32_t*)live,
-                                 (const float*)label, labels, a.labels_i64, dloss, a.scale, dl, p.ld_dl, V, loss, lse);
+                                 (const float*)label, labels, a.labels_i64, dloss, (const float*)factors, dl, p.ld_dl, V, loss, lse);
         } else {
             e = run_head_gemm<false, false, kEpiDl>(oxc, ow, ox, p, c.num_sms, s);
         }
@@ -1455,6 +1513,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
                 px.out = ws + L.part;
                 px.out_f32 = 1;
             } else {
+                px.scaled = 1;
                 px.out = dx;
                 px.out_rows = rows;
                 px.zero_dead = !gather;
@@ -1470,6 +1529,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             pw.K = n;
             pw.m_live = 0;
             pw.k_live = gather;
+            pw.scaled = 1;
             // over several pieces the sum goes on in fp32 until the last one
             const bool first = t0 == 0, last = t0 + n >= T;
             float* acc = a.dW_f32 ? static_cast<float*>(a.dW) : reinterpret_cast<float*>(ws + L.acc);
@@ -1484,7 +1544,7 @@ cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s
             const int ctas = (int)std::min<int64_t>(((four ? 4 : 1) * quads + kJoinThreads - 1) / kJoinThreads, most);
             return launch_after(four ? head_join_kernel<4> : head_join_kernel<1>, dim3(ctas), dim3(kJoinThreads), 0, s, (const float4*)(ws + L.part),
                                 (int64_t)n * nq, splits, n, nq, (const int32_t*)rows, (const int32_t*)live, labels,
-                                a.labels_i64, V, reinterpret_cast<uint2*>(dx));
+                                a.labels_i64, V, (const float*)factors, reinterpret_cast<uint2*>(dx));
         };
         if (dx && a.dW && splits > 1 && pair_cycles(px, pw, c.num_sms / 2) < kOneLaunchCycles) {
             HeadJobs<2> jobs{};

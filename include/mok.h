@@ -599,9 +599,11 @@ mok_status mok_head_loss(int32_t T, int32_t H, int32_t V, const mok_head_args* a
                          mok_stream_t stream);
 
 /* The gradient from a forward's lse (an input here; loss is not used): with
- * dl[t,v] = scale * dloss[t] * (exp(l[t,v] - lse[t]) - [v == labels[t]]), rounded to
- * bf16, dx = dl W and dW = dl^T x in fp32, rounded once. Ignored tokens have zeros in
- * dx and add nothing to dW. At least one of dx and dW is given; dx may be x's own
+ * dl[t,v] = dloss[t] / top * (exp(l[t,v] - lse[t]) - [v == labels[t]]), rounded to
+ * bf16, dx = scale * top * dl W and dW = scale * top * dl^T x in fp32, rounded once; top
+ * is the largest finite |dloss| of the (piece's) tokens that count, 1 without dloss, so a
+ * factor that all of them share is not rounded. Ignored tokens have zeros in dx and add
+ * nothing to dW, and without others both are zeros whatever the scale. At least one of dx and dW is given; dx may be x's own
  * buffer if ldx == H and dW is NULL; otherwise dx and dW overlap neither x and W nor
  * each other. Logits are formed again. */
 mok_status mok_head_loss_backward(int32_t T, int32_t H, int32_t V, const mok_head_args* a, const mok_config* cfg,
