@@ -7,6 +7,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -228,6 +229,12 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _allocating(stream):
+    """Context for what a call on `stream` allocates, so that it is not handed to another stream's work once the call
+    has dropped it, while its kernels still use it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _check(rc, what):
     if rc != OK:
         raise MokError(rc, what)
@@ -287,20 +294,22 @@ def alloc_bytes(n, device="cuda"):
 
 
 def route_layout(x, W_r, k, bias=None, out=None, workspace=None, stream=None):
-    """Router + top-k + layout. Returns a dict of device tensors."""
+    """Router + top-k + layout. Returns a dict of device tensors (new ones are `stream`'s in the allocator)."""
     _bf16(x)
     T, H = x.shape
     E = W_r.shape[1]
     dev = x.device
-    if out is None:
-        out = dict(topk_idx=torch.empty((T, k), dtype=torch.int32, device=dev),
-                   topk_w=torch.empty((T, k), dtype=torch.float32, device=dev),
-                   counts=torch.empty(E, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                   row_src=torch.empty(T * k, dtype=torch.int32, device=dev),
-                   slot_row=torch.empty(T * k, dtype=torch.int32, device=dev))
-    if workspace is None:
-        workspace = alloc_bytes(route_workspace_size(T, H, E, k), dev)
+    if out is None or workspace is None:
+        with _allocating(stream):
+            if out is None:
+                out = dict(topk_idx=torch.empty((T, k), dtype=torch.int32, device=dev),
+                           topk_w=torch.empty((T, k), dtype=torch.float32, device=dev),
+                           counts=torch.empty(E, dtype=torch.int32, device=dev),
+                           offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                           row_src=torch.empty(T * k, dtype=torch.int32, device=dev),
+                           slot_row=torch.empty(T * k, dtype=torch.int32, device=dev))
+            if workspace is None:
+                workspace = alloc_bytes(route_workspace_size(T, H, E, k), dev)
     rc = lib().mok_route_layout(_ptr(x), _ptr(W_r), _ptr(bias), T, H, E, k, _ptr(out["topk_idx"]),
                                 _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out["offsets"]),
                                 _ptr(out["row_src"]), _ptr(out["slot_row"]), _ptr(workspace),
@@ -591,22 +600,25 @@ def sort_workspace_size(T, E, k) -> int:
 
 def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped). Returns a dict of
-    counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see mok_sort_layout)."""
+    counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see mok_sort_layout); new ones are `stream`'s in the
+    allocator."""
     T, k = topk_idx.shape
     _dense("topk_idx", topk_idx, torch.int32, T, k)
     if topk_idx.get_device() != torch._C._cuda_getDevice():
         raise AssertionError("topk_idx: on the current CUDA device expected")
     n = T * k
-    if out is None:
-        out = {name: torch.empty(size, dtype=torch.int32, device=topk_idx.device)
-               for name, size in (("counts", E), ("offsets", E + 1), ("row_src", n), ("slot_row", n))}
+    if out is None or workspace is None:
+        with _allocating(stream):
+            if out is None:
+                out = {name: torch.empty(size, dtype=torch.int32, device=topk_idx.device)
+                       for name, size in (("counts", E), ("offsets", E + 1), ("row_src", n), ("slot_row", n))}
+            if workspace is None:
+                workspace = alloc_bytes(sort_workspace_size(T, E, k), topk_idx.device)
     counts, offsets, row_src, slot_row = out["counts"], out["offsets"], out["row_src"], out["slot_row"]
     _dense("counts", counts, torch.int32, E)
     _dense("offsets", offsets, torch.int32, E + 1)
     _dense("row_src", row_src, torch.int32, n)
     _dense("slot_row", slot_row, torch.int32, n)
-    if workspace is None:
-        workspace = alloc_bytes(sort_workspace_size(T, E, k), topk_idx.device)
     _check(lib().mok_sort_layout(topk_idx.data_ptr(), T, E, k, counts.data_ptr(), offsets.data_ptr(),
                                  row_src.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                  _stream(stream)), "mok_sort_layout")
