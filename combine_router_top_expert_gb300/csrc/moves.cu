@@ -112,7 +112,8 @@ dispatch_q_kernel(const uint8_t* __restrict__ xq, const uint32_t* __restrict__ x
 // the four scale codes of a 128-wide chunk, held by four neighbouring lanes,
 // leave as one word. Every token row is read once and no quantised copy of x
 // is written and read back. Pad rows are not written. The bytes equal those
-// of quantize_rows + dispatch_q. Two warps per token keep twice the loads in
+// of quantize_rows + dispatch_q. An index outside 0..E-1 has no row and is passed over.
+// Two warps per token keep twice the loads in
 // flight when there are too few tokens to fill the GPU with one each.
 __global__ void __launch_bounds__(256)
 dispatch_tokens_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, int E, int k, int W,
@@ -129,10 +130,11 @@ dispatch_tokens_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, int E,
     for (int64_t u = (int64_t)blockIdx.x * 8 + warp; u < units; u += (int64_t)gridDim.x * 8) {
         const int64_t t = u / W;
         const int bw = (int)(u % W) * 32;   // this warp's first block
-        // padded destination row of slot j (lane j holds it when k <= 32)
+        // padded destination row of slot j, or -1 (lane j holds it when k <= 32)
         auto dest = [&](int j) {
             const int64_t sl = t * k + j;
             const int e = topk_idx[sl];
+            if ((unsigned)e >= (unsigned)E) return -1;
             return poff[e] + slot_row[sl] - offsets[e];
         };
         const int my_pr = (k <= 32 && lane < k) ? dest(lane) : 0;
@@ -170,7 +172,7 @@ dispatch_tokens_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, int E,
             const uint32_t w8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
             for (int j = 0; j < k; ++j) {
                 const int pr = k <= 32 ? __shfl_sync(0xffffffffu, my_pr, j) : dest(j);
-                if (!act) continue;
+                if (!act || pr < 0) continue;
                 tc::stg_v8(A + (int64_t)pr * H + b * 32, w8);
                 if ((lane & 3) == 0)
                     *reinterpret_cast<uint32_t*>(A_sf + ((int64_t)(pr / kTileM) * kc_row + b / 4) * 512 +
@@ -449,7 +451,7 @@ __global__ void router_dlogit_kernel(const float* __restrict__ w, const float* _
 // j ascending in both sums, the expert term first.
 __global__ void __launch_bounds__(128)
 dx_kernel(const __nv_bfloat16* __restrict__ da, const float* __restrict__ dl, const int32_t* __restrict__ idx,
-          const float* __restrict__ WrT, int H, int k, __nv_bfloat16* __restrict__ dX) {
+          const float* __restrict__ WrT, int H, int E, int k, __nv_bfloat16* __restrict__ dX) {
     const int t = blockIdx.x;
     for (int c = threadIdx.x; c < H / 8; c += blockDim.x) {
         float acc[8];
@@ -472,7 +474,9 @@ dx_kernel(const __nv_bfloat16* __restrict__ da, const float* __restrict__ dl, co
         }
         for (int j = 0; j < k; ++j) {
             const float d = dl[(int64_t)t * k + j];
-            const float4* wr = reinterpret_cast<const float4*>(WrT + (int64_t)idx[(int64_t)t * k + j] * H) + 2 * c;
+            const int e = idx[(int64_t)t * k + j];
+            if ((unsigned)e >= (unsigned)E) continue;
+            const float4* wr = reinterpret_cast<const float4*>(WrT + (int64_t)e * H) + 2 * c;
             float4 a = __ldg(wr), b = __ldg(wr + 1);
             acc[0] = fmaf(d, a.x, acc[0]); acc[1] = fmaf(d, a.y, acc[1]);
             acc[2] = fmaf(d, a.z, acc[2]); acc[3] = fmaf(d, a.w, acc[3]);
@@ -492,7 +496,10 @@ __global__ void dl_scatter_kernel(const float* __restrict__ dl, const int32_t* _
     const int t = blockIdx.x * blockDim.x + threadIdx.x;
     if (t >= T) return;
     for (int e = 0; e < E; ++e) dl_full[(int64_t)t * E + e] = 0.f;
-    for (int j = 0; j < k; ++j) dl_full[(int64_t)t * E + idx[(int64_t)t * k + j]] = dl[(int64_t)t * k + j];
+    for (int j = 0; j < k; ++j) {
+        const int e = idx[(int64_t)t * k + j];
+        if ((unsigned)e < (unsigned)E) dl_full[(int64_t)t * E + e] = dl[(int64_t)t * k + j];
+    }
 }
 
 // dW_r partial sums over a token range: part[split][h][e] = sum_{t in split}
@@ -788,7 +795,7 @@ cudaError_t launch_bwd_small(const void* dY, const void* partials, const float* 
         if (e != cudaSuccess) return e;
         router_dlogit_kernel<<<ceil_div(T, 128), 128, 0, s>>>(w, gw, T, k, dl);
     } else {
-        dx_kernel<<<T, 128, 0, s>>>(static_cast<const __nv_bfloat16*>(da), dl, idx, WrT, H, k,
+        dx_kernel<<<T, 128, 0, s>>>(static_cast<const __nv_bfloat16*>(da), dl, idx, WrT, H, E, k,
                                     static_cast<__nv_bfloat16*>(dX));
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -599,9 +599,10 @@ def sort_workspace_size(T, E, k) -> int:
 
 
 def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
-    """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped). Returns a dict of
-    counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see mok_sort_layout); new ones are `stream`'s in the
-    allocator."""
+    """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped), for sort_rows and
+    unsort_rows. With topk_idx and topk_w beside it, it is the layer's routing too where no entry is dropped and no
+    token names an expert twice. Returns a dict of counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see
+    mok_sort_layout); new ones are `stream`'s in the allocator."""
     T, k = topk_idx.shape
     _dense("topk_idx", topk_idx, torch.int32, T, k)
     if topk_idx.get_device() != torch._C._cuda_getDevice():

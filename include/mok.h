@@ -200,7 +200,10 @@ mok_status mok_pack_weights(int32_t E, int32_t H, int32_t I, int32_t dtype,
 /* Forward                                                                     */
 /* ------------------------------------------------------------------------- */
 
-/* Routing produced by mok_route_layout (device pointers). */
+/* Routing as mok_route_layout makes it (device pointers): k distinct experts a
+ * token, every index below E. The layout of mok_sort_layout, with the caller's
+ * indices and weights, serves too if it is of that kind; with an entry dropped the
+ * layer's outputs are unspecified (mok_sort_rows and mok_unsort_rows take those). */
 typedef struct {
     const int32_t* topk_idx;  /* [T,k] */
     const float* topk_w;      /* [T,k] */
@@ -305,8 +308,9 @@ mok_status mok_dispatch_quantized(const mok_problem* p, const void* x_q, const v
  * each token's row is quantised once (the rule of mok_quantize_rows) and its
  * codes and scale words are written to each of its k routed rows (the bytes
  * of mok_dispatch for routed rows); pad rows are left unwritten. Uses
- * topk_idx, slot_row, counts and offsets of the routing. p->dtype must be
- * MOK_MXFP8; x 16-B and A 32-B aligned. */
+ * topk_idx, slot_row, counts and offsets of the routing; an index outside 0..E-1
+ * has no row and is passed over. p->dtype must be MOK_MXFP8; x 16-B and A 32-B
+ * aligned. */
 mok_status mok_dispatch_tokens(const mok_problem* p, const void* x, const mok_routing* r, void* A, void* A_sf,
                                mok_stream_t stream);
 
@@ -526,8 +530,9 @@ typedef enum { MOK_ELEM_BF16 = 0, MOK_ELEM_F16 = 1, MOK_ELEM_F32 = 2 } mok_elem;
 /* Workspace bytes of mok_sort_layout (0: invalid sizes). */
 size_t mok_sort_workspace_size(int32_t T, int32_t E, int32_t k);
 
-/* The layout of mok_route_layout for given expert indices topk_idx [T,k]: rows
- * ordered by (expert, t*k+j). An index outside 0..E-1 drops its entry, and a token
+/* The layout of mok_route_layout for given expert indices topk_idx [T,k], for the
+ * three calls below, and for the layer's own (mok_routing) where E <= 256, no entry is
+ * dropped and no token names an expert twice: rows ordered by (expert, t*k+j). An index outside 0..E-1 drops its entry, and a token
  * may name an expert more than once. counts [E]; offsets [E+1], offsets[E] =
  * entries kept; row_src [T*k]: t*k+j of each row, -1 from row offsets[E] on;
  * slot_row [T*k]: each entry's row, -1 for dropped ones. 1 <= E <= 1024, k >= 1,
