@@ -263,7 +263,8 @@ grad_scale_kernel(const __grid_constant__ GradTable t, const double* part, int p
         if (threadIdx.x == 0) {
             if (blockIdx.x == 0) *norm = (float)v;
             const double ratio = max_norm / (v + MOK_CLIP_EPS);
-            factor = ratio >= 1.0 ? 1.0f : (float)ratio;   // NaN stays NaN
+            // NaN stays NaN; an infinite norm is not above an infinite bound
+            factor = ratio >= 1.0 || (isinf(v) && isinf(max_norm)) ? 1.0f : (float)ratio;
         }
     }
     __syncthreads();

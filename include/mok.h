@@ -645,9 +645,10 @@ mok_status mok_grad_norm(int32_t count, const mok_grad_tensor* list, float* norm
                          mok_stream_t stream);
 
 /* The norm, and every tensor times min(1, max_norm / (norm + MOK_CLIP_EPS)):
- * in place (not written when the factor is 1) or into out. max_norm >= 0. A norm of
- * NaN makes every output NaN; an infinite one makes finite values 0 and
- * infinities NaN. Tensors and outputs do not overlap one another. */
+ * in place (not written when the factor is 1) or into out. max_norm >= 0; an infinite
+ * one never clips (factor 1, but for a norm of NaN). A norm of NaN makes every output
+ * NaN; an infinite one above a finite max_norm makes finite values 0 and infinities
+ * NaN. Tensors and outputs do not overlap one another. */
 mok_status mok_grad_clip(int32_t count, const mok_grad_tensor* list, double max_norm, float* norm, void* workspace,
                          size_t ws_bytes, mok_stream_t stream);
 
