@@ -467,6 +467,19 @@ def _dense(name, t, dtype, *shape):
         raise AssertionError(f"{name}: contiguous {dtype} CUDA tensor {list(shape)} expected")
 
 
+def _here(name, t, device, dtype, *shape):
+    """The same, on this device (the current one)."""
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
+        raise AssertionError(f"{name}: contiguous {dtype} tensor {list(shape)} on CUDA device {device} expected")
+
+
+def _scratch(t, device):
+    """(address, bytes) of a workspace on this device."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise AssertionError(f"workspace: contiguous tensor on CUDA device {device} expected")
+    return t.data_ptr(), t.numel()
+
+
 def _rows(name, t, T, H):
     """Row pitch of bf16 rows whose elements are adjacent (of a single row: H, whatever view it is)."""
     pitch, step = t.stride()
@@ -588,10 +601,10 @@ _ELEMS = {torch.bfloat16: BF16_ROWS, torch.float16: F16_ROWS, torch.float32: F32
 
 
 def _elem(name, t):
-    """mok_elem of a tensor on the current device."""
+    """(mok_elem, device) of a tensor on the current device."""
     if t.dtype not in _ELEMS or not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise AssertionError(f"{name}: bf16, fp16 or fp32 tensor on the current CUDA device expected")
-    return _ELEMS[t.dtype]
+    return _ELEMS[t.dtype], t.get_device()
 
 
 def sort_workspace_size(T, E, k) -> int:
@@ -605,7 +618,8 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     mok_sort_layout); new ones are `stream`'s in the allocator."""
     T, k = topk_idx.shape
     _dense("topk_idx", topk_idx, torch.int32, T, k)
-    if topk_idx.get_device() != torch._C._cuda_getDevice():
+    dev = topk_idx.get_device()
+    if dev != torch._C._cuda_getDevice():
         raise AssertionError("topk_idx: on the current CUDA device expected")
     n = T * k
     if out is None or workspace is None:
@@ -616,18 +630,18 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
             if workspace is None:
                 workspace = alloc_bytes(sort_workspace_size(T, E, k), topk_idx.device)
     counts, offsets, row_src, slot_row = out["counts"], out["offsets"], out["row_src"], out["slot_row"]
-    _dense("counts", counts, torch.int32, E)
-    _dense("offsets", offsets, torch.int32, E + 1)
-    _dense("row_src", row_src, torch.int32, n)
-    _dense("slot_row", slot_row, torch.int32, n)
+    _here("counts", counts, dev, torch.int32, E)
+    _here("offsets", offsets, dev, torch.int32, E + 1)
+    _here("row_src", row_src, dev, torch.int32, n)
+    _here("slot_row", slot_row, dev, torch.int32, n)
     _check(lib().mok_sort_layout(topk_idx.data_ptr(), T, E, k, counts.data_ptr(), offsets.data_ptr(),
-                                 row_src.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                 row_src.data_ptr(), slot_row.data_ptr(), *_scratch(workspace, dev),
                                  _stream(stream)), "mok_sort_layout")
     return out
 
 
-def _slots(layout, T):
-    """(slot_row, k) of a layout of T tokens."""
+def _slots(layout, T, device):
+    """(slot_row, k) of a layout of T tokens on this device."""
     s = layout["slot_row"]
     n = s.numel()
     if T <= 0:
@@ -636,7 +650,7 @@ def _slots(layout, T):
         return s, 1
     if n % T or n == 0:
         raise AssertionError(f"slot_row: a multiple of {T} entries expected")
-    _dense("slot_row", s, torch.int32, n)
+    _here("slot_row", s, device, torch.int32, n)
     return s, n // T
 
 
@@ -644,11 +658,12 @@ def sort_rows(x, layout, out, stream=None):
     """Rows of x [T, H] at their entries' places in out [T*k, H]; later rows of out are left as they are.
     unsort_rows without weights is the gradient."""
     T, H = x.shape
-    elem, (slot, k) = _elem("x", x), _slots(layout, T)
+    elem, dev = _elem("x", x)
+    slot, k = _slots(layout, T, dev)
     pitch, step = x.stride()
     if step != 1 and T:
         raise AssertionError("x: adjacent row elements expected")
-    _dense("out", out, x.dtype, T * k, H)
+    _here("out", out, dev, x.dtype, T * k, H)
     _check(lib().mok_sort_rows(x.data_ptr(), pitch if T > 1 else H, slot.data_ptr(), T, H, k, elem, out.data_ptr(),
                                _stream(stream)), "mok_sort_rows")
     return out
@@ -657,10 +672,11 @@ def sort_rows(x, layout, out, stream=None):
 def unsort_rows(y, layout, out, w=None, stream=None):
     """out [T, H] = the sum of each token's rows of y [T*k, H], times w [T, k] (fp32) if given."""
     T, H = out.shape
-    elem, (slot, k) = _elem("out", out), _slots(layout, T)
-    _dense("out", out, out.dtype, T, H)
-    _dense("y", y, out.dtype, T * k, H)
-    _dense("w", w, torch.float32, T, k)
+    elem, dev = _elem("out", out)
+    slot, k = _slots(layout, T, dev)
+    _here("out", out, dev, out.dtype, T, H)
+    _here("y", y, dev, out.dtype, T * k, H)
+    _here("w", w, dev, torch.float32, T, k)
     _check(lib().mok_unsort_rows(y.data_ptr(), slot.data_ptr(), _addr(w), T, H, k, elem, out.data_ptr(),
                                  _stream(stream)), "mok_unsort_rows")
     return out
@@ -669,12 +685,13 @@ def unsort_rows(y, layout, out, w=None, stream=None):
 def unsort_rows_backward(dout, y, layout, w, dy, dw, stream=None):
     """Gradients of unsort_rows: dy [T*k, H] (later rows are left as they are) and dw [T, k]."""
     T, H = dout.shape
-    elem, (slot, k) = _elem("dout", dout), _slots(layout, T)
-    _dense("dout", dout, dout.dtype, T, H)
-    _dense("y", y, dout.dtype, T * k, H)
-    _dense("dy", dy, dout.dtype, T * k, H)
-    _dense("w", w, torch.float32, T, k)
-    _dense("dw", dw, torch.float32, T, k)
+    elem, dev = _elem("dout", dout)
+    slot, k = _slots(layout, T, dev)
+    _here("dout", dout, dev, dout.dtype, T, H)
+    _here("y", y, dev, dout.dtype, T * k, H)
+    _here("dy", dy, dev, dout.dtype, T * k, H)
+    _here("w", w, dev, torch.float32, T, k)
+    _here("dw", dw, dev, torch.float32, T, k)
     _check(lib().mok_unsort_rows_backward(dout.data_ptr(), y.data_ptr(), slot.data_ptr(), w.data_ptr(), T, H, k, elem,
                                           dy.data_ptr(), dw.data_ptr(), _stream(stream)), "mok_unsort_rows_backward")
 
@@ -690,20 +707,21 @@ def _head_args(x, W, labels, workspace, piece, loss=None, lse=None, dloss=None, 
     T, H = x.shape
     V = W.shape[0]
     pitch = _rows("x", x, T, H)
-    if x.get_device() != torch._C._cuda_getDevice():
+    dev = x.get_device()
+    if dev != torch._C._cuda_getDevice():
         raise AssertionError("x: on the current CUDA device expected")
-    _dense("W", W, torch.bfloat16, V, H)
+    _here("W", W, dev, torch.bfloat16, V, H)
     if labels.dtype not in (torch.int32, torch.int64):
         raise AssertionError("labels: int32 or int64 expected")
-    _dense("labels", labels, labels.dtype, T)
+    _here("labels", labels, dev, labels.dtype, T)
     for n, t in (("loss", loss), ("lse", lse), ("dloss", dloss)):
-        _dense(n, t, torch.float32, T)
-    _dense("dx", dx, torch.bfloat16, T, H)
+        _here(n, t, dev, torch.float32, T)
+    _here("dx", dx, dev, torch.bfloat16, T, H)
     f32 = dW is not None and dW.dtype is torch.float32
-    _dense("dW", dW, torch.float32 if f32 else torch.bfloat16, V, H)
+    _here("dW", dW, dev, torch.float32 if f32 else torch.bfloat16, V, H)
     return T, H, V, HeadArgs(x.data_ptr(), pitch, W.data_ptr(), labels.data_ptr(), labels.dtype is torch.int64, piece,
                              _addr(loss), _addr(lse), _addr(dloss), scale, f32, bool(accumulate), _addr(dx), _addr(dW),
-                             workspace.data_ptr(), workspace.numel())
+                             *_scratch(workspace, dev))
 
 
 def _head_call(name, a, cfg, stream):
@@ -747,9 +765,9 @@ class GradList:
         self.array, self.count = (GradTensor * max(n, 1))(), n
         spans = []
         for i, g in enumerate(self.tensors):
-            elem, o = _elem(f"grads[{i}]", g), None if self.out is None else self.out[i]
-            _dense(f"grads[{i}]", g, g.dtype, *g.shape)
-            _dense(f"out[{i}]", o, g.dtype, *g.shape)
+            (elem, dev), o = _elem(f"grads[{i}]", g), None if self.out is None else self.out[i]
+            _here(f"grads[{i}]", g, dev, g.dtype, *g.shape)
+            _here(f"out[{i}]", o, dev, g.dtype, *g.shape)
             self.array[i] = GradTensor(g.data_ptr(), _addr(o), g.numel(), elem)
             for t in (g,) if o is None or o.data_ptr() == g.data_ptr() else (g, o):
                 if t.numel():
@@ -775,12 +793,18 @@ def grad_workspace_size() -> int:
     return int(lib().mok_grad_workspace_size())
 
 
+def _norm(norm, workspace):
+    """Addresses of the norm and the workspace, on the current device."""
+    _dense("norm", norm, torch.float32)
+    dev = torch._C._cuda_getDevice()
+    _here("norm", norm, dev, torch.float32)
+    return norm.data_ptr(), *_scratch(workspace, dev)
+
+
 def grad_norm(grads, norm, workspace, stream=None):
     """norm [] (fp32) = 2-norm of all elements of a list of bf16, fp16 and fp32 tensors."""
     g = grads.check() if isinstance(grads, GradList) else GradList(grads)
-    _dense("norm", norm, torch.float32)
-    _check(lib().mok_grad_norm(g.count, g.array, norm.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                               _stream(stream)), "mok_grad_norm")
+    _check(lib().mok_grad_norm(g.count, g.array, *_norm(norm, workspace), _stream(stream)), "mok_grad_norm")
     return norm
 
 
@@ -788,9 +812,8 @@ def grad_clip(grads, max_norm, norm, workspace, stream=None):
     """norm as grad_norm, and all gradients times min(1, max_norm / (norm + 1e-6)): in place, or into a grad_list's
     outputs."""
     g = grads.check() if isinstance(grads, GradList) else GradList(grads)
-    _dense("norm", norm, torch.float32)
-    _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), norm.data_ptr(), workspace.data_ptr(),
-                               workspace.numel(), _stream(stream)), "mok_grad_clip")
+    _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), *_norm(norm, workspace), _stream(stream)),
+           "mok_grad_clip")
     return norm
 
 
