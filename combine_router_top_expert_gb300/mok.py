@@ -607,6 +607,11 @@ def _elem(name, t):
     return _ELEMS[t.dtype], t.get_device()
 
 
+class SortLayout(dict):
+    """sort_layout's arrays by name, and the tokens and entries per token that they are of."""
+    tokens = k = None
+
+
 def sort_workspace_size(T, E, k) -> int:
     return int(lib().mok_sort_workspace_size(T, E, k))
 
@@ -614,7 +619,7 @@ def sort_workspace_size(T, E, k) -> int:
 def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     """Layout of rows sorted by given expert indices [T, k] int32 (outside 0..E-1: dropped), for sort_rows and
     unsort_rows. With topk_idx and topk_w beside it, it is the layer's routing too where no entry is dropped and no
-    token names an expert twice. Returns a dict of counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see
+    token names an expert twice. Returns a SortLayout (a dict) of counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see
     mok_sort_layout); new ones are `stream`'s in the allocator."""
     T, k = topk_idx.shape
     _dense("topk_idx", topk_idx, torch.int32, T, k)
@@ -625,8 +630,8 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     if out is None or workspace is None:
         with _allocating(stream):
             if out is None:
-                out = {name: torch.empty(size, dtype=torch.int32, device=topk_idx.device)
-                       for name, size in (("counts", E), ("offsets", E + 1), ("row_src", n), ("slot_row", n))}
+                out = SortLayout((name, torch.empty(size, dtype=torch.int32, device=topk_idx.device))
+                                 for name, size in (("counts", E), ("offsets", E + 1), ("row_src", n), ("slot_row", n)))
             if workspace is None:
                 workspace = alloc_bytes(sort_workspace_size(T, E, k), topk_idx.device)
     counts, offsets, row_src, slot_row = out["counts"], out["offsets"], out["row_src"], out["slot_row"]
@@ -637,6 +642,9 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     _check(lib().mok_sort_layout(topk_idx.data_ptr(), T, E, k, counts.data_ptr(), offsets.data_ptr(),
                                  row_src.data_ptr(), slot_row.data_ptr(), *_scratch(workspace, dev),
                                  _stream(stream)), "mok_sort_layout")
+    if not isinstance(out, SortLayout):
+        out = SortLayout(out)
+    out.tokens, out.k = T, k
     return out
 
 
@@ -644,12 +652,14 @@ def _slots(layout, T, device):
     """(slot_row, k) of a layout of T tokens on this device."""
     s = layout["slot_row"]
     n = s.numel()
+    if isinstance(layout, SortLayout) and layout.tokens != T:
+        raise AssertionError(f"layout: of {T} tokens expected, not of {layout.tokens}")
     if T <= 0:
         if n or T:
             raise AssertionError("slot_row: of these tokens expected")
         return s, 1
-    if n % T or n == 0:
-        raise AssertionError(f"slot_row: a multiple of {T} entries expected")
+    if n % T or n == 0 or ("topk_idx" in layout and layout["topk_idx"].shape[0] != T):
+        raise AssertionError(f"layout: of {T} tokens expected")
     _here("slot_row", s, device, torch.int32, n)
     return s, n // T
 
