@@ -648,8 +648,8 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     return out
 
 
-def _slots(layout, T, device):
-    """(slot_row, k) of a layout of T tokens on this device."""
+def _slots(layout, T, device, w=None):
+    """(slot_row, k) of a layout of T tokens on this device. Of no tokens, k is the layout's or the weights'."""
     s = layout["slot_row"]
     n = s.numel()
     if isinstance(layout, SortLayout) and layout.tokens != T:
@@ -657,7 +657,7 @@ def _slots(layout, T, device):
     if T <= 0:
         if n or T:
             raise AssertionError("slot_row: of these tokens expected")
-        return s, 1
+        return s, getattr(layout, "k", None) or (w.shape[1] if w is not None and w.dim() == 2 else 1)
     if n % T or n == 0 or ("topk_idx" in layout and layout["topk_idx"].shape[0] != T):
         raise AssertionError(f"layout: of {T} tokens expected")
     _here("slot_row", s, device, torch.int32, n)
@@ -683,7 +683,7 @@ def unsort_rows(y, layout, out, w=None, stream=None):
     """out [T, H] = the sum of each token's rows of y [T*k, H], times w [T, k] (fp32) if given."""
     T, H = out.shape
     elem, dev = _elem("out", out)
-    slot, k = _slots(layout, T, dev)
+    slot, k = _slots(layout, T, dev, w)
     _here("out", out, dev, out.dtype, T, H)
     _here("y", y, dev, out.dtype, T * k, H)
     _here("w", w, dev, torch.float32, T, k)
@@ -696,7 +696,7 @@ def unsort_rows_backward(dout, y, layout, w, dy, dw, stream=None):
     """Gradients of unsort_rows: dy [T*k, H] (later rows are left as they are) and dw [T, k]."""
     T, H = dout.shape
     elem, dev = _elem("dout", dout)
-    slot, k = _slots(layout, T, dev)
+    slot, k = _slots(layout, T, dev, w)
     _here("dout", dout, dev, dout.dtype, T, H)
     _here("y", y, dev, dout.dtype, T * k, H)
     _here("dy", dy, dev, dout.dtype, T * k, H)

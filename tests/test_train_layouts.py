@@ -51,3 +51,14 @@ def test_layouts_of_other_tokens_are_refused():
             call(lay)
         with pytest.raises(AssertionError):
             _calls(T, k)[0](lay)
+
+
+def test_a_layout_of_no_tokens():
+    """Whatever the entries per token; the weights [0, k] of an empty batch included."""
+    lay = _layout(0, 4)
+    for call in _calls(0, 4):
+        call(lay), call(dict(lay))
+    with pytest.raises(AssertionError):
+        _calls(0, 3)[2](lay)
+    with pytest.raises(AssertionError):
+        _calls(4, 4)[0](lay)
