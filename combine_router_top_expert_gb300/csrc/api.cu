@@ -953,7 +953,12 @@ mok_status mok_unsort_rows_backward(const void* dout, const void* y, const int32
 
 size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, int32_t piece, const mok_config* cfg) {
     if (!head_dims_ok(T, H, V) || piece < 0) return 0;
-    return head_workspace_bytes(T, H, V, grad != 0, piece, std::max(make_common(nullptr, cfg).num_sms, 2));
+    constexpr int kinds = MOK_HEAD_DX | MOK_HEAD_DW | MOK_HEAD_DW_F32;
+    int bits = grad & kinds ? 0 : grad ? kHeadDx | kHeadDw : 0;   // no kind named: whatever a call may form
+    if (grad & MOK_HEAD_DX) bits |= kHeadDx;
+    if (grad & MOK_HEAD_DW) bits |= kHeadDw;
+    if (grad & MOK_HEAD_DW_F32) bits |= kHeadDwF32;
+    return head_workspace_bytes(T, H, V, bits, piece, std::max(make_common(nullptr, cfg).num_sms, 2));
 }
 
 // Common checks and launch: `forward` writes loss and lse, `grad` dx and dW.
@@ -981,7 +986,10 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
         !aligned(a->workspace, 1024))
         return MOK_ERR_INVALID;
     if (!device_ok()) return MOK_ERR_CUDA;
-    if (a->ws_bytes < mok_head_workspace_size(T, H, V, grad, a->piece, cfg)) return MOK_ERR_INVALID;
+    GemmCommon c = make_common(a->workspace, cfg);
+    c.num_sms = std::max(c.num_sms, 2);   // a pair of CTAs at least
+    if (a->ws_bytes < head_workspace_bytes(T, H, V, grad ? head_grads(a->dx, a->dW, a->dW_f32) : 0, a->piece, c.num_sms))
+        return MOK_ERR_INVALID;
     HeadLaunch h{};
     h.T = T; h.H = H; h.V = V;
     h.x = a->x;
@@ -1002,8 +1010,6 @@ static mok_status head_call(int32_t T, int32_t H, int32_t V, const mok_head_args
         h.dW_f32 = a->dW_f32 != 0;
         h.accumulate = a->accumulate != 0;
     }
-    GemmCommon c = make_common(a->workspace, cfg);
-    c.num_sms = std::max(c.num_sms, 2);   // a pair of CTAs at least
     return launch_status(launch_head(h, c, (cudaStream_t)stream));
 }
 

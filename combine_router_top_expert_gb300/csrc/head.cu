@@ -1380,7 +1380,9 @@ struct HeadLayout {
     int piece, splits;
 };
 
-HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
+// grad: the gradients that a call forms (HeadGrad bits). dX's parts are held with dx alone, and dW's running sum where a
+// BF16 one is formed in several pieces (an fp32 one is its own sum).
+HeadLayout head_layout(int T, int H, int V, int grad, int want, int num_sms) {
     HeadLayout L{};
     size_t o = 1024;   // the status block
     auto take = [&](int64_t bytes) {
@@ -1389,7 +1391,7 @@ HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
         return at;
     };
     L.piece = piece_tokens(T, V, want);
-    L.splits = grad ? dx_splits(L.piece, H, V, num_sms / 2) : 1;
+    L.splits = grad & kHeadDx ? dx_splits(L.piece, H, V, num_sms / 2) : 1;
     const int64_t cap = T > kPlainRows ? align_up(L.piece, kBM) : L.piece;   // gathered rows fill tiles
     L.live = take(12);   // and the gradient's two factors
     L.rows = take(cap * 4);
@@ -1398,21 +1400,21 @@ HeadLayout head_layout(int T, int H, int V, bool grad, int want, int num_sms) {
     if (grad || T > kPlainRows) L.xc = take(cap * H * 2);
     if (grad) L.dl = take(cap * pitch_dl(V) * 2);
     if (L.splits > 1) L.part = take((int64_t)L.splits * L.piece * H * 4);
-    if (grad && L.piece < T) L.acc = take((int64_t)V * H * 4);
+    if (grad & kHeadDw && L.piece < T) L.acc = take((int64_t)V * H * 4);
     L.total = o;
     return L;
 }
 
 }  // namespace
 
-size_t head_workspace_bytes(int T, int H, int V, bool grad, int piece, int num_sms) {
+size_t head_workspace_bytes(int T, int H, int V, int grad, int piece, int num_sms) {
     return head_layout(T, H, V, grad, piece, num_sms).total;
 }
 
 cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s) {
     const int T = a.T, H = a.H, V = a.V;
     const bool grad = a.dx || a.dW, forward = a.loss != nullptr;
-    const HeadLayout L = head_layout(T, H, V, grad, a.piece, c.num_sms);
+    const HeadLayout L = head_layout(T, H, V, head_grads(a.dx, a.dW, a.dW_f32), a.piece, c.num_sms);
     char* ws = static_cast<char*>(a.workspace);
     float2* stats = reinterpret_cast<float2*>(ws + L.stats);
     float* label = reinterpret_cast<float*>(ws + L.label);

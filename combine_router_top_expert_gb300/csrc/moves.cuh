@@ -160,7 +160,11 @@ struct HeadLaunch {
     void* workspace;
     int withhold;
 };
-size_t head_workspace_bytes(int T, int H, int V, bool grad, int piece, int num_sms);
+enum HeadGrad : int { kHeadDx = 1, kHeadDw = 2, kHeadDwF32 = 4 };   // dW in BF16, dW in fp32
+inline int head_grads(const void* dx, const void* dW, int dW_f32) {
+    return (dx ? kHeadDx : 0) | (!dW ? 0 : dW_f32 ? kHeadDwF32 : kHeadDw);
+}
+size_t head_workspace_bytes(int T, int H, int V, int grad, int piece, int num_sms);   // grad: HeadGrad bits
 cudaError_t launch_head(const HeadLaunch& a, const GemmCommon& c, cudaStream_t s);
 
 // Forward gate/up GEMM + SwiGLU. A: [rows, H] (bf16 or E4M3 + tile scales);

@@ -708,7 +708,11 @@ def unsort_rows_backward(dout, y, layout, w, dy, dw, stream=None):
 
 # --------------------------------------------------------------------------- loss of the vocabulary's head
 
+HEAD_DX, HEAD_DW, HEAD_DW_F32 = 2, 4, 8   # MOK_HEAD_*
+
+
 def head_workspace_size(T, H, V, grad=False, piece=0, cfg: Config | None = None) -> int:
+    """grad: False for head_loss, the sum of the HEAD_* gradients that the call forms, or True for any."""
     return int(lib().mok_head_workspace_size(T, H, V, int(grad), piece, ctypes.byref(cfg) if cfg else None))
 
 

@@ -587,8 +587,15 @@ typedef struct {
     size_t ws_bytes;
 } mok_head_args;
 
-/* Workspace bytes of the calls below on the current device (grad != 0: of those
- * with a gradient; 0: invalid sizes). Needs H % 8 == 0, 8 <= H <= 65536,
+/* Gradients that a call forms, for mok_head_workspace_size. */
+#define MOK_HEAD_DX 2
+#define MOK_HEAD_DW 4        /* in bf16 */
+#define MOK_HEAD_DW_F32 8
+
+/* Workspace bytes of the calls below on the current device (0: invalid sizes). grad:
+ * 0 for mok_head_loss, the sum of the MOK_HEAD_* gradients of the others' call, or 1
+ * for any of them. A bf16 dW formed in several pieces takes an fp32 sum of [V,H]
+ * beside, an fp32 one is its own. Needs H % 8 == 0, 8 <= H <= 65536,
  * 1 <= V <= 2^24, 0 <= T <= 2^24, piece >= 0. */
 size_t mok_head_workspace_size(int32_t T, int32_t H, int32_t V, int32_t grad, int32_t piece, const mok_config* cfg);
 
