@@ -25,22 +25,20 @@ class VocabHead:
             raise AssertionError("W: [V, H] bf16 and gain: [H] expected")
         self.W, self.gain, self.eps, self.piece = W, gain, eps, piece
         self.V, self.H = W.shape
-        self._ws = {}          # by (tokens rounded up to a power of two, training)
+        self._ws = None        # of the largest call so far; smaller ones take part of it
         self._all_ws = []      # none is given back, so that captured calls stay good
         self._norm_ws = None
         self._last = None
 
     def _workspace(self, T, grad):
-        piece = self.piece if grad else 0
-        key = (1 << max(T - 1, 0).bit_length(), grad)
-        need = mok.head_workspace_size(T, self.H, self.V, grad, piece)
-        ws = self._ws.get(key)
-        if ws is None or ws.numel() < need:
-            ws = mok.alloc_bytes(max(need, mok.head_workspace_size(key[0], self.H, self.V, grad, piece)), self.W.device)
-            self._ws[key] = ws
-            self._all_ws.append(ws)
-        self._last = ws
-        return ws
+        need = mok.head_workspace_size(T, self.H, self.V, grad, self.piece if grad else 0)
+        if self._ws is None or self._ws.numel() < need:
+            # half as much again as the last one at least, so that all of them are three times the largest at most
+            room = need if self._ws is None else max(need, self._ws.numel() * 3 // 2)
+            self._ws = mok.alloc_bytes(room, self.W.device)
+            self._all_ws.append(self._ws)
+        self._last = self._ws
+        return self._ws
 
     def _normed(self, x, residual, keep_sum):
         T, H = x.shape
@@ -56,7 +54,7 @@ class VocabHead:
         T = x.shape[0]
         y, _, _ = self._normed(x, residual, False)
         loss, lse = (torch.empty(T, dtype=torch.float32, device=x.device) for _ in range(2))
-        mok.head_loss(y, self.W, labels, loss, self._workspace(T, False), lse=lse)
+        mok.head_loss(y, self.W, labels, loss, self._workspace(T, 0), lse=lse)
         return loss, lse
 
     @_on_stream
@@ -73,8 +71,9 @@ class VocabHead:
             raise AssertionError("dW: fp32 expected")
         if not added:
             dW = torch.empty_like(self.W)
-        mok.head_loss_train(y, self.W, labels, loss, dy, dW, self._workspace(T, True), dloss=dloss, scale=scale,
-                            accumulate=added, piece=self.piece)
+        ws = self._workspace(T, mok.HEAD_DX | (mok.HEAD_DW_F32 if added else mok.HEAD_DW))
+        mok.head_loss_train(y, self.W, labels, loss, dy, dW, ws, dloss=dloss, scale=scale, accumulate=added,
+                            piece=self.piece)
         dgain = torch.empty(self.H, dtype=torch.float32, device=x.device)
         if self._norm_ws is None:   # a partial row per SM at most, so one for any T
             self._norm_ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(1 << 24, self.H), x.device)
