@@ -830,6 +830,7 @@ mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args
     if (!a || !norm_dims_ok(T, H) || !a->dgain || !a->workspace) return MOK_ERR_INVALID;
     if ((a->sum_q != nullptr) != (a->sum_sf != nullptr) || (a->sum_q && (a->sum || H % 32)))
         return MOK_ERR_INVALID;
+    if (a->labels && (a->sum_q || a->V < 1 || !aligned(a->labels, a->labels_i64 ? 8 : 4))) return MOK_ERR_INVALID;
     if (T > 0 && (!a->dy || (!a->sum && !a->sum_q) || !a->rstd || !a->gain || !a->dx)) return MOK_ERR_INVALID;
     if (!aligned(a->dy, 16) || !aligned(a->sum, 16) || !aligned(a->sum_q, 16) || !aligned(a->dsum, 16) ||
         !aligned(a->rstd, 4) || !aligned(a->gain, 16) || !aligned(a->dx, 16) || !aligned(a->dgain, 4) ||

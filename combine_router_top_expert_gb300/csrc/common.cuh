@@ -66,6 +66,16 @@ __device__ __forceinline__ bool abort_requested(const StatusBlock* st) {
     return *((volatile const int32_t*)&st->abort) != 0;
 }
 
+// Token t's label (i32 or i64), and whether it is one of the vocabulary's V.
+__device__ __forceinline__ int64_t label_at(const void* labels, int i64, int64_t t) {
+    return i64 ? __ldg(static_cast<const long long*>(labels) + t) : (int64_t)__ldg(static_cast<const int32_t*>(labels) + t);
+}
+
+__device__ __forceinline__ bool is_live(const void* labels, int i64, int64_t t, int V) {
+    const int64_t y = label_at(labels, i64, t);
+    return y >= 0 && y < V;
+}
+
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch. A kernel launched by launch_after (below)
 // may become resident while the kernel before it on the stream is still

@@ -134,15 +134,6 @@ __device__ __forceinline__ float exp2_approx(float v) {
     return r;
 }
 
-__device__ __forceinline__ int64_t label_at(const void* labels, int i64, int64_t t) {
-    return i64 ? __ldg(static_cast<const long long*>(labels) + t) : (int64_t)__ldg(static_cast<const int32_t*>(labels) + t);
-}
-
-__device__ __forceinline__ bool is_live(const void* labels, int i64, int64_t t, int V) {
-    const int64_t y = label_at(labels, i64, t);
-    return y >= 0 && y < V;
-}
-
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");

@@ -196,6 +196,8 @@ struct NormBwdParams {
     __nv_bfloat16* dx;
     float* part;               // [gridDim.x, H]: dgain of each CTA's rows
     float* dgain;              // [H]
+    const void* labels;        // [T] or NULL: rows whose label is outside 0..V-1 count as zeros
+    int labels_i64, V;
 };
 
 // A row belongs to a group of `group` threads (whole warps); a CTA has one or
@@ -212,6 +214,9 @@ struct NormBwdParams {
 // (STAGES = 0) are read from memory each time, and spill. BF16 sums: T = 2048, H = 16384
 // 68 us (two buffers, 58% of the copy rate), T = 1024, H = 32768 75 (none, 53%), T = 512,
 // H = 65536 124 (32%).
+// MASK: a row whose token is ignored is taken as zeros when it comes out of its buffer, so that
+// a NaN in it reaches neither dx nor the gain's gradient; a kernel of its own, as the others have
+// no instruction to spare.
 //
 // T = 4096, H = 7168 with dsum, both kernels: 40.0 us for a BF16 sum (87% of the
 // copy rate; the launches, the first rows' way in and the gain gradient take the
@@ -220,7 +225,7 @@ struct NormBwdParams {
 // two rows to a barrier (spills, 61 us), 448 threads with two vectors each, two
 // CTAs an SM (50), and the second half of a row behind the first half of the next
 // over mbarriers (55).
-template <int VPT, bool CK, int STAGES>
+template <int VPT, bool CK, int STAGES, bool MASK>
 __global__ void __launch_bounds__(1024, 1)
 rmsnorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool PF = STAGES > 0;
@@ -271,10 +276,11 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto load_rstd = [&](int n) {
+    auto load_rstd = [&](int n, bool& dead) {
         float v = 0.f;
         if (n < rows) {
-            v = __ldg(p.rstd + next);
+            if constexpr (MASK) dead = !is_live(p.labels, p.labels_i64, next, p.V);
+            if (!MASK || !dead) v = __ldg(p.rstd + next);
             next += total;
         }
         return v;
@@ -314,11 +320,12 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) issue(n, n);
     }
-    float rstd = load_rstd(0);
+    bool dead = false, dead_next = false;
+    float rstd = load_rstd(0, dead);
     int b = 0;   // this row's buffer
 #pragma unroll 1
     for (int n = 0; n < rows; ++n) {
-        const float rstd_next = load_rstd(n + 1);
+        const float rstd_next = load_rstd(n + 1, dead_next);
         if constexpr (PF) {
             // into the buffer of the row before this one (this thread is done with it)
             issue(n + kAhead, b == 0 ? STAGES - 1 : b - 1);
@@ -332,6 +339,11 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
                 float2 s[4], d[4], g[4], dot2 = both(0.f);
                 const float f = fetch_s(b, i, s), rf = CK ? rstd * f : rstd;
                 fetch_dy(b, i, d);
+                if constexpr (MASK) {
+                    if (dead)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[j] = d[j] = both(0.f);
+                }
                 if constexpr (!kKeep) load8(p.gain + 8 * (tid + i * nt), g);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -360,6 +372,11 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
                     f = fetch_s(b, i, s);
                     load8(p.gain + 8 * (tid + i * nt), g);
                 }
+                if constexpr (MASK) {
+                    if (dead)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[j] = u[j] = both(0.f);
+                }
                 const float cf = CK ? c * f : c;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -376,6 +393,7 @@ rmsnorm_bwd_kernel(const NormBwdParams p) {
         // the next copies may overwrite codes that other lanes have just read again
         if constexpr (PF && CK && !kKeep) __syncwarp();
         rstd = rstd_next;
+        dead = dead_next;
     }
     if constexpr (PF) asm volatile("cp.async.wait_group 0;" ::: "memory");
     float* part = p.part + (int64_t)blockIdx.x * H;
@@ -478,19 +496,19 @@ BwdShape bwd_shape(int H) {
     return b;
 }
 
-template <int VPT, bool CK, int STAGES>
+template <int VPT, bool CK, int STAGES, bool MASK>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
-    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES>;
+    auto kern = rmsnorm_bwd_kernel<VPT, CK, STAGES, MASK>;
     if (b.smem > 40 * 1024) ensure_smem_attr(reinterpret_cast<const void*>(kern), b.smem);
     return launch_after(kern, dim3(grid), dim3(b.group * b.groups), b.smem, s, p);
 }
-template <bool CK>
+template <bool CK, bool MASK>
 cudaError_t run_bwd(const NormBwdParams& p, int grid, const BwdShape& b, cudaStream_t s) {
     switch (b.vpt) {
-        case 1: return run_bwd<1, CK, 4>(p, grid, b, s);
-        case 2: return run_bwd<2, CK, 2>(p, grid, b, s);
-        case 4: return run_bwd<4, CK, 0>(p, grid, b, s);
-        default: return run_bwd<8, CK, 0>(p, grid, b, s);
+        case 1: return run_bwd<1, CK, 4, MASK>(p, grid, b, s);
+        case 2: return run_bwd<2, CK, 2, MASK>(p, grid, b, s);
+        case 4: return run_bwd<4, CK, 0, MASK>(p, grid, b, s);
+        default: return run_bwd<8, CK, 0, MASK>(p, grid, b, s);
     }
 }
 
@@ -541,7 +559,11 @@ cudaError_t launch_rmsnorm_backward(int T, int H, const mok_rmsnorm_bwd_args& a,
     const int P = rmsnorm_bwd_partials(T, H);
     const BwdShape b = bwd_shape(H);
     p.group = b.group;
-    cudaError_t e = a.sum_q ? run_bwd<true>(p, P, b, s) : run_bwd<false>(p, P, b, s);
+    p.labels = a.labels;
+    p.labels_i64 = a.labels_i64 != 0;
+    p.V = a.V;
+    cudaError_t e = a.sum_q ? run_bwd<true, false>(p, P, b, s)
+                  : a.labels ? run_bwd<false, true>(p, P, b, s) : run_bwd<false, false>(p, P, b, s);
     if (e != cudaSuccess) return e;
     return launch_after(rmsnorm_dgain_kernel, dim3(ceil_div(H, kDgainCols)), dim3(256), 0, s, (const float*)p.part, P, H,
                         p.dgain);

@@ -4,7 +4,8 @@
     loss   = cross entropy of rmsnorm(stream) * gain against the vocabulary's rows W
 
 x and residual are the last block's `out` and `stream` (block.py). `score` gives the losses, `train` the losses and all
-gradients in one call; neither holds the logits. Tokens whose label is outside the vocabulary (-100, say) are ignored.
+gradients in one call; neither holds the logits. Tokens whose label is outside the vocabulary (-100, say) are ignored,
+whatever their rows hold.
 
 The workspaces belong to the head: calls that use them go to one stream at a time. With `stream` given, the new
 tensors are that stream's in the allocator, and the inputs have to be ready on it.
@@ -78,7 +79,7 @@ class VocabHead:
         if self._norm_ws is None:   # a partial row per SM at most, so one for any T
             self._norm_ws = mok.alloc_bytes(mok.rmsnorm_bwd_workspace_size(1 << 24, self.H), x.device)
         # dx takes dy's place: the norm's output gradient is read before it is overwritten
-        mok.rmsnorm_backward(dy, self.gain, rstd, dy, dgain, self._norm_ws, s=total)
+        mok.rmsnorm_backward(dy, self.gain, rstd, dy, dgain, self._norm_ws, s=total, labels=labels, V=self.V)
         return loss, dict(dx=dy, dgain=dgain, dW=dW)
 
     @_on_stream

@@ -100,7 +100,8 @@ class RmsNormBwdArgs(ctypes.Structure):
     _fields_ = [("dy", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("sum_q", ctypes.c_void_p),
                 ("sum_sf", ctypes.c_void_p), ("dsum", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
                 ("gain", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dgain", ctypes.c_void_p),
-                ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+                ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t), ("labels", ctypes.c_void_p),
+                ("labels_i64", ctypes.c_int32), ("V", ctypes.c_int32)]
 
 
 class FewArgs(ctypes.Structure):
@@ -513,8 +514,10 @@ def rmsnorm_bwd_workspace_size(T, H) -> int:
     return int(lib().mok_rmsnorm_bwd_workspace_size(T, H))
 
 
-def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_sf=None, dsum=None, stream=None):
-    """Gradients of rmsnorm from the forward's sum, in BF16 (s) or as MXFP8 rows (s_q, s_sf)."""
+def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_sf=None, dsum=None, stream=None,
+                     labels=None, V=0):
+    """Gradients of rmsnorm from the forward's sum, in BF16 (s) or as MXFP8 rows (s_q, s_sf). labels [T] (int32 or
+    int64, with s): rows whose label is outside 0..V-1 count as zeros, whatever they hold."""
     T, H = dy.shape
     _dense("dy", dy, torch.bfloat16, T, H)
     _dense("dx", dx, torch.bfloat16, T, H)
@@ -526,8 +529,13 @@ def rmsnorm_backward(dy, gain, rstd, dx, dgain, workspace, s=None, s_q=None, s_s
     _dense("gain", gain, torch.float32, H)
     _dense("dgain", dgain, torch.float32, H)
     _dense("rstd", rstd, torch.float32, T)
+    i64 = False
+    if labels is not None:
+        i64 = labels.dtype is torch.int64
+        _dense("labels", labels, torch.int64 if i64 else torch.int32, T)
     a = RmsNormBwdArgs(dy.data_ptr(), _addr(s), _addr(s_q), _addr(s_sf), _addr(dsum), rstd.data_ptr(),
-                       gain.data_ptr(), dx.data_ptr(), dgain.data_ptr(), workspace.data_ptr(), workspace.numel())
+                       gain.data_ptr(), dx.data_ptr(), dgain.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                       _addr(labels), i64, V)
     _check(lib().mok_rmsnorm_backward(T, H, ctypes.byref(a), _stream(stream)), "mok_rmsnorm_backward")
 
 

@@ -475,6 +475,9 @@ typedef struct {
     float* dgain;          /* [H] */
     void* workspace;       /* mok_rmsnorm_bwd_workspace_size bytes, 16-byte aligned */
     size_t ws_bytes;
+    const void* labels;    /* [T] i32 or i64, or NULL: see below */
+    int32_t labels_i64;
+    int32_t V;             /* of the labels, >= 1 */
 } mok_rmsnorm_bwd_args;
 
 /* Workspace bytes of mok_rmsnorm_backward on the current device (0: invalid). */
@@ -483,7 +486,9 @@ size_t mok_rmsnorm_bwd_workspace_size(int32_t T, int32_t H);
 /* With xh = sum * rstd and a = gain * dy:
  * dx = bf16(dsum + rstd * (a - xh * mean(a * xh))), dgain = sum_t dy * xh, in
  * fp32 and in a fixed order (bitwise the same in every run on one device).
- * The sum comes in BF16 or as the 8-bit checkpoint, exactly one of the two.
+ * The sum comes in BF16 or as the 8-bit checkpoint, exactly one of the two. With
+ * labels (BF16 sum only) the rows of tokens whose label is outside 0..V-1 count as
+ * zeros in dy and sum, whatever they hold: dx is dsum there, dgain gets nothing.
  * Sizes and alignment as mok_rmsnorm. T == 0 zeroes dgain. */
 mok_status mok_rmsnorm_backward(int32_t T, int32_t H, const mok_rmsnorm_bwd_args* a, mok_stream_t stream);
 
