@@ -80,18 +80,31 @@ __device__ __forceinline__ bool is_live(const void* labels, int i64, int64_t t, 
 // Programmatic dependent launch. A kernel launched by launch_after (below)
 // may become resident while the kernel before it on the stream is still
 // running. pdl_wait() blocks until that kernel has completed and its memory
-// writes are visible (a no-op for a plain launch), so everything before it
-// may touch only shared memory, tensor memory, barriers and kernel
-// parameters; pdl_allow_next() lets the next kernel on the stream start its
-// own launch. The next kernel's CTAs take an SM only once every CTA of this
-// grid has started, so a grid larger than one wave is never starved.
+// writes are visible (a no-op for a plain launch); pdl_allow_next() lets the
+// next kernel on the stream start its own launch. The next kernel's CTAs take an
+// SM only once every CTA of this grid has started, so a grid larger than one
+// wave is never starved.
+//
+// What may stand before pdl_wait():
+// - shared memory, tensor memory, barriers and kernel parameters: always. A call's
+//   first kernel keeps to these, as it does not know what runs ahead of it.
+// - reads of what was complete before the kernel AHEAD began. That holds only if
+//   the kernel ahead is of the same call and calls pdl_allow_next() after its own
+//   pdl_wait() (in every CTA), and for what was written by kernels before that one, or
+//   is the caller's. head.cu's and grads.cu's later kernels read on this ground.
+// - never a write to global memory.
+// A kernel that allows the next one before it has waited (head_loss_kernel,
+// head_dl_kernel, head_join_kernel, grad_scale_kernel) passes the ground on only to
+// what was complete for itself: the one behind it must not read what the kernel
+// ahead of it writes, and either waits first or reads older data only. Every kernel
+// waits before it ends, so that a chain of them completes in order.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // kern<<<grid, block, smem, s>>>(args...) with the programmatic
-// stream-serialization attribute (the kernel must call pdl_wait() before it
-// reads or writes global memory that earlier work on the stream uses).
+// stream-serialization attribute (the kernel keeps to what is said above of the
+// time before its pdl_wait()).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          Args&&... args) {

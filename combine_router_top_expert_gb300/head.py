@@ -20,8 +20,8 @@ from .block import _on_stream
 
 class VocabHead:
     def __init__(self, W: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, piece: int = 0):
-        """W: [V, H] bf16, gain: [H] fp32. piece: tokens of which the training call's [piece, V] buffer is held at once
-        (0: at most 4 GB of it)."""
+        """W: [V, H] bf16, gain: [H] fp32. piece: tokens of which the training call's [piece, V] bf16 buffer is held at
+        once, in whole tiles of 256 above 256 tokens (0: as many as 4 GB hold, but 256 at least)."""
         if W.dim() != 2 or W.dtype is not torch.bfloat16 or gain.shape != (W.shape[1],):
             raise AssertionError("W: [V, H] bf16 and gain: [H] expected")
         self.W, self.gain, self.eps, self.piece = W, gain, eps, piece

@@ -578,7 +578,9 @@ typedef struct {
     const void* W;         /* [V,H] bf16: the vocabulary's rows */
     const void* labels;    /* [T] i32 or i64; outside 0..V-1: the token is ignored */
     int32_t labels_i64;
-    int32_t piece;         /* tokens of which the gradient's [piece, V] bf16 buffer is held at once; 0: at most 4 GB */
+    int32_t piece;         /* tokens of which the gradient's [piece, V] bf16 buffer is held at once, 65536 at most; 0:
+                              as many as 4 GB hold, but 256 at least (8.6 GB at V = 2^24). In a call of more than 256
+                              tokens the buffer has whole tiles of 256 rows */
     float* loss;           /* [T] */
     float* lse;            /* [T]: the log of the summed exponentials; see each call */
     /* gradient */

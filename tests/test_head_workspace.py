@@ -25,6 +25,20 @@ def test_the_running_sum_is_held_for_a_bf16_gradient_in_pieces_alone(T, H, V, pi
     assert 0 < size(False) < size(KINDS["dW_f32"]) <= size(KINDS["dW"]) <= most
 
 
+@pytest.mark.parametrize("T,V,piece,rows", [(10000, 1 << 24, 0, 256), (10000, 1 << 23, 0, 256), (10000, 1 << 22, 0, 512),
+                                            (200000, 8, 0, 65536), (200000, 8, 1 << 20, 65536), (5000, 8000, 1, 256),
+                                            (5000, 8000, 300, 512), (256, 8000, 1, 1), (256, 8000, 100, 100),
+                                            (5000, 131072, 0, 5120)])
+def test_tokens_of_a_piece(T, V, piece, rows):
+    """dl is the only part that grows with V's columns by rows x 2 bytes (beside 16 bytes a row and 256 columns)."""
+    size = lambda V: mok.head_workspace_size(T, 8, V, KINDS["dx,dW_f32"], piece)
+    tiles = -(-V // 256)
+    dl, stats = rows * -(-V // 64) * 64 * 2, rows * 2 * tiles * 8
+    rest = size(V) - dl
+    parts = -(-V // 64) // 8 * rows * 8 * 4          # dX's, at most
+    assert 0 <= rest <= stats + parts + rows * 64 + (1 << 14)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kinds", KINDS)
 @pytest.mark.parametrize("T,piece", [(5, 0), (100, 40), (300, 0), (300, 128)])
