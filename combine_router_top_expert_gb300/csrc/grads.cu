@@ -263,8 +263,9 @@ grad_scale_kernel(const __grid_constant__ GradTable t, const double* part, int p
         if (threadIdx.x == 0) {
             if (blockIdx.x == 0) *norm = (float)v;
             const double ratio = max_norm / (v + MOK_CLIP_EPS);
-            // NaN stays NaN; an infinite norm is not above an infinite bound
-            factor = ratio >= 1.0 || (isinf(v) && isinf(max_norm)) ? 1.0f : (float)ratio;
+            float f = ratio >= 1.0 ? 1.0f : (float)ratio;
+            if (isnan(f) && !isnan(v)) f = 1.0f;   // an infinite norm is not above an infinite bound; NaN stays NaN
+            factor = f;
         }
     }
     __syncthreads();
