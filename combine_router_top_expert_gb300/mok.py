@@ -475,10 +475,10 @@ def _here(name, t, device, dtype, *shape):
 
 
 def _scratch(t, device):
-    """(address, bytes) of a workspace on this device."""
-    if t.get_device() != device or not t.is_contiguous():
-        raise AssertionError(f"workspace: contiguous tensor on CUDA device {device} expected")
-    return t.data_ptr(), t.numel()
+    """The address of a workspace on this device."""
+    if t.get_device() != device:
+        raise AssertionError(f"workspace: tensor on CUDA device {device} expected")
+    return t.data_ptr()
 
 
 def _rows(name, t, T, H):
@@ -610,14 +610,15 @@ _ELEMS = {torch.bfloat16: BF16_ROWS, torch.float16: F16_ROWS, torch.float32: F32
 
 def _elem(name, t):
     """(mok_elem, device) of a tensor on the current device."""
-    if t.dtype not in _ELEMS or not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+    elem, dev = _ELEMS.get(t.dtype), t.get_device()
+    if elem is None or dev < 0 or dev != torch._C._cuda_getDevice():
         raise AssertionError(f"{name}: bf16, fp16 or fp32 tensor on the current CUDA device expected")
-    return _ELEMS[t.dtype], t.get_device()
+    return elem, dev
 
 
 class SortLayout(dict):
     """sort_layout's arrays by name, and the tokens and entries per token that they are of."""
-    tokens = k = None
+    __slots__ = ("tokens", "k")
 
 
 def sort_workspace_size(T, E, k) -> int:
@@ -630,10 +631,9 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     token names an expert twice. Returns a SortLayout (a dict) of counts [E], offsets [E+1], row_src [T*k], slot_row [T*k] (see
     mok_sort_layout); new ones are `stream`'s in the allocator."""
     T, k = topk_idx.shape
-    _dense("topk_idx", topk_idx, torch.int32, T, k)
     dev = topk_idx.get_device()
-    if dev != torch._C._cuda_getDevice():
-        raise AssertionError("topk_idx: on the current CUDA device expected")
+    if dev < 0 or dev != torch._C._cuda_getDevice() or topk_idx.dtype is not torch.int32 or not topk_idx.is_contiguous():
+        raise AssertionError("topk_idx: contiguous int32 tensor on the current CUDA device expected")
     n = T * k
     if out is None or workspace is None:
         with _allocating(stream):
@@ -648,11 +648,12 @@ def sort_layout(topk_idx, E, out=None, workspace=None, stream=None):
     _here("row_src", row_src, dev, torch.int32, n)
     _here("slot_row", slot_row, dev, torch.int32, n)
     _check(lib().mok_sort_layout(topk_idx.data_ptr(), T, E, k, counts.data_ptr(), offsets.data_ptr(),
-                                 row_src.data_ptr(), slot_row.data_ptr(), *_scratch(workspace, dev),
+                                 row_src.data_ptr(), slot_row.data_ptr(), _scratch(workspace, dev), workspace.numel(),
                                  _stream(stream)), "mok_sort_layout")
-    if not isinstance(out, SortLayout):
+    if out.__class__ is not SortLayout:
         out = SortLayout(out)
-    out.tokens, out.k = T, k
+    out.tokens = T
+    out.k = k
     return out
 
 
@@ -660,7 +661,7 @@ def _slots(layout, T, device, w=None):
     """(slot_row, k) of a layout of T tokens on this device. Of no tokens, k is the layout's or the weights'."""
     s = layout["slot_row"]
     n = s.numel()
-    if isinstance(layout, SortLayout) and layout.tokens != T:
+    if layout.__class__ is SortLayout and layout.tokens != T:
         raise AssertionError(f"layout: of {T} tokens expected, not of {layout.tokens}")
     if T <= 0:
         if n or T:
@@ -743,7 +744,7 @@ def _head_args(x, W, labels, workspace, piece, loss=None, lse=None, dloss=None, 
     _here("dW", dW, dev, torch.float32 if f32 else torch.bfloat16, V, H)
     return T, H, V, HeadArgs(x.data_ptr(), pitch, W.data_ptr(), labels.data_ptr(), labels.dtype is torch.int64, piece,
                              _addr(loss), _addr(lse), _addr(dloss), scale, f32, bool(accumulate), _addr(dx), _addr(dW),
-                             *_scratch(workspace, dev))
+                             _scratch(workspace, dev), workspace.numel())
 
 
 def _head_call(name, a, cfg, stream):
@@ -815,18 +816,19 @@ def grad_workspace_size() -> int:
     return int(lib().mok_grad_workspace_size())
 
 
-def _norm(norm, workspace):
-    """Addresses of the norm and the workspace, on the current device."""
-    _dense("norm", norm, torch.float32)
-    dev = torch._C._cuda_getDevice()
-    _here("norm", norm, dev, torch.float32)
-    return norm.data_ptr(), *_scratch(workspace, dev)
+def _norm_device(norm):
+    """The current device, on which the norm has to be."""
+    dev = norm.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or norm.dtype is not torch.float32 or norm.dim():
+        raise AssertionError("norm: fp32 tensor [] on the current CUDA device expected")
+    return dev
 
 
 def grad_norm(grads, norm, workspace, stream=None):
     """norm [] (fp32) = 2-norm of all elements of a list of bf16, fp16 and fp32 tensors."""
     g = grads.check() if isinstance(grads, GradList) else GradList(grads)
-    _check(lib().mok_grad_norm(g.count, g.array, *_norm(norm, workspace), _stream(stream)), "mok_grad_norm")
+    _check(lib().mok_grad_norm(g.count, g.array, norm.data_ptr(), _scratch(workspace, _norm_device(norm)),
+                               workspace.numel(), _stream(stream)), "mok_grad_norm")
     return norm
 
 
@@ -834,7 +836,8 @@ def grad_clip(grads, max_norm, norm, workspace, stream=None):
     """norm as grad_norm, and all gradients times min(1, max_norm / (norm + 1e-6)): in place, or into a grad_list's
     outputs."""
     g = grads.check() if isinstance(grads, GradList) else GradList(grads)
-    _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), *_norm(norm, workspace), _stream(stream)),
+    _check(lib().mok_grad_clip(g.count, g.array, float(max_norm), norm.data_ptr(),
+                               _scratch(workspace, _norm_device(norm)), workspace.numel(), _stream(stream)),
            "mok_grad_clip")
     return norm
 
