@@ -24,10 +24,10 @@
 //   dX      dl W     A K-major, B MN-major (the vocabulary is K)
 //   dW      dl^T x   both MN-major (the tokens are K)
 // Few tokens are bound by the bytes of W (H = 7168, V = 131072, call after call: T = 64
-// 294 us, 6.4 TB/s; T = 1 278 us), many by the tensor cores and what the power limit
-// leaves of their clock (T = 2560, H = 7168, V = 50001, scoring: 975 us when the GPU is
-// cool, 1110 call after call, 1.9 and 1.65 PFLOP/s; T = 4096, V = 131072, training: 12.9
-// and 14.5 ms, 1.8 and 1.6 PFLOP/s).
+// 294 to 312 us by the GPU at hand, 6.4 to 6.0 TB/s; T = 1 278 us), many by the tensor
+// cores and what the power limit leaves of their clock (T = 2560, H = 7168, V = 50001,
+// scoring: 975 us when the GPU is cool, 1110 to 1140 call after call, 1.9 and 1.6 PFLOP/s;
+// T = 4096, V = 131072, training: 12.9 ms, and 14.3 to 15.6, 1.8 and 1.6 to 1.5 PFLOP/s).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
