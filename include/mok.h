@@ -541,7 +541,7 @@ size_t mok_sort_workspace_size(int32_t T, int32_t E, int32_t k);
  * may name an expert more than once. counts [E]; offsets [E+1], offsets[E] =
  * entries kept; row_src [T*k]: t*k+j of each row, -1 from row offsets[E] on;
  * slot_row [T*k]: each entry's row, -1 for dropped ones. 1 <= E <= 1024, k >= 1,
- * T*k < 2^30. workspace 4-byte aligned, any content. */
+ * T*k < 2^30. workspace 4-byte aligned, any content. Buffers do not overlap. */
 mok_status mok_sort_layout(const int32_t* topk_idx, int32_t T, int32_t E, int32_t k, int32_t* counts,
                            int32_t* offsets, int32_t* row_src, int32_t* slot_row, void* workspace,
                            size_t ws_bytes, mok_stream_t stream);

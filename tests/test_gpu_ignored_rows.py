@@ -49,7 +49,7 @@ def test_norm_backward_with_labels(T, H, dtype, dsum):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 9, 300])
+@pytest.mark.parametrize("T", [0, 1, 9, 300])
 @pytest.mark.parametrize("bad", [NAN, INF, -INF, 3e38])
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
